@@ -205,6 +205,137 @@ int mla_decode_up_project_fp8w(const mla_decode_dims* dims, const uint8_t* w_uv_
                                const float* w_uv_scale, void* out, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The 8-bit latent cache.  The method's pages describe a bf16 cache; this is
+ * this library's own addition for contexts that bf16 does not hold, or does
+ * not read fast enough: half the bytes per token.
+ *   kv_fp8      uint8 [num_pages, 64, 576]  FP8 E4M3 codes of [c_kv || k_pe]
+ *   kv_scale    fp32  [num_pages]           one scale per page, > 0
+ * A cached value is code * scale of its page.  Pages are found through the
+ * same block_table and seq_lens as in the bf16 cache.
+ *
+ * `status` of the calls in this part: device int32 or null; the first
+ * device-side error (DEVICE_BOUNDS) is written there if it holds 0.  The
+ * pages of a call that are in range are processed whatever the others are. */
+
+/* Appends new tokens: quantises rows of the bf16 cache's layout into the pages.
+ *   rows        bf16 [B, max_new, 576]: row i < n_b of sequence b goes to
+ *               position seq_lens[b] - n_b + i; the rows behind are not read
+ *   new_lens    int32 [B], n_b in [0, max_new]; null: max_new everywhere
+ *   seq_lens    int32 [B]: lengths INCLUDING the new tokens (0 for an unused
+ *               line of the batch)
+ * A page's scale is the smallest power of two s with |value| <= 448 s for every
+ * finite new value, within [2^-32, 2^32] (values beyond 448 * 2^32 saturate,
+ * infinities too; NaN stays NaN).  A page whose first token is among the new
+ * ones starts afresh: its scale is that of the new tokens, and its rows past
+ * them are cleared.  In any other page the scale only grows; when it does, the
+ * rows that stay are re-coded under the new scale (round to nearest even).
+ * Positions past max_pages_per_seq * 64, n_b outside [0, min(max_new, length)]
+ * or a block_table entry outside the pool: DEVICE_BOUNDS, and the sequence (the
+ * page) is left as it was.  A page that receives tokens must belong to one
+ * sequence of the batch.  Uses batch, num_pages and max_pages_per_seq of dims;
+ * the others are checked too.  One kernel; max_new >= 1. */
+int mla_decode_append_fp8kv(const mla_decode_dims* dims, const void* rows, int32_t max_new,
+                            const int32_t* new_lens, const int32_t* block_table,
+                            const int32_t* seq_lens, uint8_t* kv_fp8, float* kv_scale,
+                            int32_t* status, void* stream);
+
+/* Bytes of the buffer of query terms (below) for `dims`.  Needs no device. */
+int mla_decode_fp8kv_terms_size(const mla_decode_dims* dims, size_t* bytes);
+
+/* mla_decode_run over the 8-bit cache, after mla_decode_plan on the same
+ * workspace (a plan serves both kinds of cache).  Arguments as there, and
+ *   terms       device scratch of mla_decode_fp8kv_terms_size bytes, 16-byte
+ *               aligned: the absorbed query as 8-bit terms.  Like the
+ *               workspace it belongs to one call at a time.
+ * Rows past a sequence's length in its last page must not be NaN codes (0x7f,
+ * 0xff); mla_decode_append_fp8kv clears them.  A page's scale outside [2^-32,
+ * 2^32] is reported as DEVICE_BOUNDS by mla_decode_check and taken as 1.  The
+ * query must be finite.  The absorbed query enters as its bf16 part, exactly
+ * (to 2^-22 of its row's largest value), and the lse gets the same first-order
+ * correction as over the bf16 cache; the softmax weights are rounded to two
+ * 3-bit terms (at most 2^-7 of a weight), and the output is normalised by the
+ * sum of the weights as rounded.  One kernel more than mla_decode_run. */
+int mla_decode_run_fp8kv(const mla_decode_dims* dims, const void* q, const uint8_t* kv_fp8,
+                         const float* kv_scale, const int32_t* block_table,
+                         const int32_t* seq_lens, const void* w_uk, const void* w_uv,
+                         float softmax_scale, void* out, float* lse, void* terms,
+                         size_t terms_bytes, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/* Its attention step, in the place of mla_decode_attend between the absorb
+ * and combine steps (with bf16 or FP8 weights). */
+int mla_decode_attend_fp8kv(const mla_decode_dims* dims, const uint8_t* kv_fp8,
+                            const float* kv_scale, const int32_t* block_table,
+                            const int32_t* seq_lens, float softmax_scale, float* lse,
+                            void* terms, size_t terms_bytes, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Block-sparse decode: each query token attends to top_k pages of its
+ * sequence.  Every page has a key (the mean of its rows); a query's score for
+ * a page is its largest head's product with the key; the pages selected form a
+ * batch of B * T sequences with one query token each, on which the calls above
+ * run as on any other:
+ *   append or write tokens; page_keys          (per layer)
+ *   absorb -> q_lat; score_pages(q_lat); select_pages -> sel_table, sel_lens
+ *   plan, run or run_fp8kv with dims {batch = B * T, q_len = 1,
+ *     max_pages_per_seq = top_k}, sel_table and sel_lens
+ * (q [B, T, H, 192] is [B * T, 1, H, 192] as it stands.)  Not described by the
+ * method's pages; for either kind of cache. */
+
+/* Keys of the pages that hold any of each sequence's newest n_b tokens
+ * (new_lens, max_new and seq_lens as for mla_decode_append_fp8kv):
+ *   page_keys   bf16 [num_pages, 576] (written at those pages): the mean of
+ *               the page's rows up to the sequence's length, summed in fp32
+ * Recomputed from the cache, so a page may be filled in any number of steps
+ * and shortened again.  One kernel. */
+int mla_decode_page_keys(const mla_decode_dims* dims, const void* kv_cache,
+                         const int32_t* block_table, const int32_t* seq_lens, int32_t max_new,
+                         const int32_t* new_lens, void* page_keys, int32_t* status,
+                         void* stream);
+int mla_decode_page_keys_fp8kv(const mla_decode_dims* dims, const uint8_t* kv_fp8,
+                               const float* kv_scale, const int32_t* block_table,
+                               const int32_t* seq_lens, int32_t max_new,
+                               const int32_t* new_lens, void* page_keys, int32_t* status,
+                               void* stream);
+
+/* Scores of every page for every query token.
+ *   query       bf16 [B, T, H, 576]: absorbed queries (mla_decode_absorb's
+ *               q_lat, see mla_decode_workspace_offsets) or others of that form
+ *   scores      fp32 [B, T, max_pages_per_seq] (written): max over heads of
+ *               query . page_key, -infinity for pages that query t does not see
+ *               (it sees keys [0, seq_len - T + t]).  A NaN product counts as
+ *               -infinity.
+ * Lengths outside [T, max_pages_per_seq * 64] are clamped, and block_table
+ * entries outside the pool replaced by page 0, with DEVICE_BOUNDS.  One
+ * kernel. */
+int mla_decode_score_pages(const mla_decode_dims* dims, const void* query,
+                           const void* page_keys, const int32_t* block_table,
+                           const int32_t* seq_lens, float* scores, int32_t* status,
+                           void* stream);
+
+/* Selects pages for every query token (line b * T + t of the outputs): all that
+ * it sees if those are at most top_k; otherwise the first keep_first, the last
+ * keep_last (one at least: the last page may be partly filled) and, of the
+ * others, those with the highest scores; of equal scores the page that comes
+ * first in the sequence, NaN behind everything.
+ *   scores      fp32 [B, T, max_pages_per_seq]
+ *   sel_table   int32 [B * T, top_k] (written): physical pages in the
+ *               sequence's order, then -1
+ *   sel_pages   the same as logical pages; may be null
+ *   sel_lens    int32 [B * T] (written): keys in the selected pages that the
+ *               query sees
+ * INVALID_ARG unless 1 <= keep_last, 0 <= keep_first, keep_first + keep_last <=
+ * top_k.  Lengths outside [T, max_pages_per_seq * 64] are clamped, with
+ * DEVICE_BOUNDS; block_table entries are copied as they are (the decode step
+ * checks them).  One kernel. */
+int mla_decode_select_pages(const mla_decode_dims* dims, const float* scores,
+                            const int32_t* block_table, const int32_t* seq_lens, int32_t top_k,
+                            int32_t keep_first, int32_t keep_last, int32_t* sel_table,
+                            int32_t* sel_pages, int32_t* sel_lens, int32_t* status,
+                            void* stream);
+
 /* Waits for `stream`, then returns the first device-side status recorded in
  * the workspace since the last plan (OK, DEVICE_BOUNDS or TIMEOUT), or
  * CUDA_ERROR if the stream reports an error.  INVALID_ARG for a null

@@ -24,7 +24,10 @@ ENTRY_POINTS = (
     "mla_decode_combine", "mla_decode_up_project", "mla_decode_check", "mla_decode_status_string",
     "mla_decode_workspace_offsets", "mla_decode_kernels_per_run",
     "mla_decode_run_static_scratch", "mla_decode_selftest_wait_timeout",
-    "mla_decode_run_fp8w", "mla_decode_absorb_fp8w", "mla_decode_up_project_fp8w")
+    "mla_decode_run_fp8w", "mla_decode_absorb_fp8w", "mla_decode_up_project_fp8w",
+    "mla_decode_append_fp8kv", "mla_decode_fp8kv_terms_size", "mla_decode_run_fp8kv",
+    "mla_decode_attend_fp8kv", "mla_decode_page_keys", "mla_decode_page_keys_fp8kv",
+    "mla_decode_score_pages", "mla_decode_select_pages")
 
 
 class Dims(ctypes.Structure):
@@ -72,6 +75,15 @@ def lib():
         L.mla_decode_run_fp8w.argtypes = [D, P, P, P, P, P, P, P, P, ctypes.c_float, P, P, P, S, P]
         L.mla_decode_absorb_fp8w.argtypes = [D, P, P, P, P, S, P]
         L.mla_decode_up_project_fp8w.argtypes = [D, P, P, P, P, S, P]
+        L.mla_decode_append_fp8kv.argtypes = [D, P, i32, P, P, P, P, P, P, P]
+        L.mla_decode_fp8kv_terms_size.argtypes = [D, sz]
+        L.mla_decode_run_fp8kv.argtypes = [D, P, P, P, P, P, P, P, ctypes.c_float, P, P, P, S, P,
+                                           S, P]
+        L.mla_decode_attend_fp8kv.argtypes = [D, P, P, P, P, ctypes.c_float, P, P, S, P, S, P]
+        L.mla_decode_page_keys.argtypes = [D, P, P, P, i32, P, P, P, P]
+        L.mla_decode_page_keys_fp8kv.argtypes = [D, P, P, P, P, i32, P, P, P, P]
+        L.mla_decode_score_pages.argtypes = [D, P, P, P, P, P, P, P]
+        L.mla_decode_select_pages.argtypes = [D, P, P, P, i32, i32, i32, P, P, P, P, P]
         for n in ENTRY_POINTS:
             if n != "mla_decode_status_string":
                 getattr(L, n).restype = ctypes.c_int
@@ -120,16 +132,29 @@ def kernels_per_run(d: Dims, fp8_weights: bool = False) -> int:
     return n.value
 
 
+def fp8kv_terms_size(d: Dims) -> int:
+    """Bytes of the query-term scratch that decoding over the 8-bit cache needs."""
+    n = ctypes.c_size_t(0)
+    _ok(lib().mla_decode_fp8kv_terms_size(ctypes.byref(d), ctypes.byref(n)),
+        "mla_decode_fp8kv_terms_size")
+    return n.value
+
+
 class MlaDecode:
     """Owns a device workspace for one set of dims; plan() once per decode step,
-    run() once per layer.  All tensors must be CUDA, contiguous."""
+    run() once per layer.  All tensors must be CUDA, contiguous.  With fp8_kv
+    it also owns the query-term scratch, and run_fp8kv() decodes over the
+    8-bit cache (one plan serves both)."""
 
-    def __init__(self, d: Dims, device=None, num_ranges: int = 0):
+    def __init__(self, d: Dims, device=None, num_ranges: int = 0, fp8_kv: bool = False):
         self.dims = d
         self.num_ranges = num_ranges
         self.ws_bytes = workspace_size(d, num_ranges)
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8,
                                      device=device or torch.device("cuda"))
+        self.terms_bytes = fp8kv_terms_size(d) if fp8_kv else 0
+        self.terms = torch.empty(self.terms_bytes, dtype=torch.uint8,
+                                 device=self.workspace.device) if fp8_kv else None
 
     def plan(self, seq_lens):
         _ok(lib().mla_decode_plan_ex(ctypes.byref(self.dims), _ptr(seq_lens), self.num_ranges,
@@ -150,6 +175,23 @@ class MlaDecode:
                                       float(scale), _ptr(out), _ptr(lse), _ptr(self.workspace),
                                       self.ws_bytes, _stream()),
             "mla_decode_run_fp8w")
+
+    def run_fp8kv(self, q, kv8, kv_scale, block_table, seq_lens, w_uk, w_uv, scale, out, lse):
+        _fp8kv_tensors(self.dims, kv8, kv_scale)
+        _ok(lib().mla_decode_run_fp8kv(ctypes.byref(self.dims), _ptr(q), _ptr(kv8),
+                                       _ptr(kv_scale), _ptr(block_table), _ptr(seq_lens),
+                                       _ptr(w_uk), _ptr(w_uv), float(scale), _ptr(out),
+                                       _ptr(lse), _ptr(self.terms), self.terms_bytes,
+                                       _ptr(self.workspace), self.ws_bytes, _stream()),
+            "mla_decode_run_fp8kv")
+
+    def attend_fp8kv(self, kv8, kv_scale, block_table, seq_lens, scale, lse):
+        _fp8kv_tensors(self.dims, kv8, kv_scale)
+        _ok(lib().mla_decode_attend_fp8kv(ctypes.byref(self.dims), _ptr(kv8), _ptr(kv_scale),
+                                          _ptr(block_table), _ptr(seq_lens), float(scale),
+                                          _ptr(lse), _ptr(self.terms), self.terms_bytes,
+                                          _ptr(self.workspace), self.ws_bytes, _stream()),
+            "mla_decode_attend_fp8kv")
 
     def absorb_fp8w(self, q, w_uk8, w_uk_scale):
         _ok(lib().mla_decode_absorb_fp8w(ctypes.byref(self.dims), _ptr(q), _ptr(w_uk8),
@@ -220,3 +262,97 @@ def decode(q, cache, block_table, seq_lens, w_uk, w_uv, scale, num_ranges: int =
     m.plan(seq_lens)
     m.run(q, cache, block_table, seq_lens, w_uk, w_uv, scale, out, lse)
     return out, lse
+
+
+# ---------------------------------------------------------------- 8-bit cache, sparse decode
+def _need(name, t, dtype, *shape):
+    """The C ABI sees pointers only: type, shape and layout are checked here."""
+    if t is None or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        got = None if t is None else (t.dtype, tuple(t.shape), t.is_contiguous())
+        raise ValueError("%s: expected a contiguous %s tensor of shape %s, got %s"
+                         % (name, dtype, shape, got))
+
+
+def _fp8kv_tensors(d, kv8, kv_scale):
+    _need("kv8", kv8, torch.uint8, d.num_pages, 64, 576)
+    _need("kv_scale", kv_scale, torch.float32, d.num_pages)
+
+
+def _lines(d, block_table, seq_lens, new_lens=None, status=None):
+    _need("block_table", block_table, torch.int32, d.batch, d.max_pages_per_seq)
+    _need("seq_lens", seq_lens, torch.int32, d.batch)
+    if new_lens is not None:
+        _need("new_lens", new_lens, torch.int32, d.batch)
+    if status is not None:
+        _need("status", status, torch.int32, 1)
+
+
+def append_fp8kv(d: Dims, rows, kv8, kv_scale, block_table, seq_lens, new_lens=None,
+                 status=None):
+    """Quantise new rows (bf16 [B, max_new, 576]) into the 8-bit cache, in place.
+
+    Row i < new_lens[b] (default: every row) goes to position
+    seq_lens[b] - new_lens[b] + i.  status: optional int32 [1] on the device
+    that receives the first error found there."""
+    _need("rows", rows, torch.bfloat16, d.batch, rows.shape[1], 576)
+    _fp8kv_tensors(d, kv8, kv_scale)
+    _lines(d, block_table, seq_lens, new_lens, status)
+    _ok(lib().mla_decode_append_fp8kv(ctypes.byref(d), _ptr(rows), rows.shape[1], _ptr(new_lens),
+                                      _ptr(block_table), _ptr(seq_lens), _ptr(kv8),
+                                      _ptr(kv_scale), _ptr(status), _stream()),
+        "mla_decode_append_fp8kv")
+
+
+def page_keys(d: Dims, cache, block_table, seq_lens, max_new, keys, new_lens=None, status=None):
+    """Mean keys (bf16 [num_pages, 576], in place) of the pages that hold each
+    sequence's newest new_lens[b] <= max_new tokens (default: max_new), from the
+    bf16 cache."""
+    _need("cache", cache, torch.bfloat16, d.num_pages, 64, 576)
+    _need("keys", keys, torch.bfloat16, d.num_pages, 576)
+    _lines(d, block_table, seq_lens, new_lens, status)
+    _ok(lib().mla_decode_page_keys(ctypes.byref(d), _ptr(cache), _ptr(block_table),
+                                   _ptr(seq_lens), max_new, _ptr(new_lens), _ptr(keys),
+                                   _ptr(status), _stream()),
+        "mla_decode_page_keys")
+
+
+def page_keys_fp8kv(d: Dims, kv8, kv_scale, block_table, seq_lens, max_new, keys, new_lens=None,
+                    status=None):
+    """page_keys() from the 8-bit cache."""
+    _fp8kv_tensors(d, kv8, kv_scale)
+    _need("keys", keys, torch.bfloat16, d.num_pages, 576)
+    _lines(d, block_table, seq_lens, new_lens, status)
+    _ok(lib().mla_decode_page_keys_fp8kv(ctypes.byref(d), _ptr(kv8), _ptr(kv_scale),
+                                         _ptr(block_table), _ptr(seq_lens), max_new,
+                                         _ptr(new_lens), _ptr(keys), _ptr(status), _stream()),
+        "mla_decode_page_keys_fp8kv")
+
+
+def score_pages(d: Dims, query, keys, block_table, seq_lens, scores, status=None):
+    """scores (fp32 [B, T, max_pages_per_seq], written): each query token's
+    largest head product (query: bf16 [B, T, H, 576]) with every page's key."""
+    _need("query", query, torch.bfloat16, d.batch, d.q_len, d.num_heads, 576)
+    _need("keys", keys, torch.bfloat16, d.num_pages, 576)
+    _need("scores", scores, torch.float32, d.batch, d.q_len, d.max_pages_per_seq)
+    _lines(d, block_table, seq_lens, None, status)
+    _ok(lib().mla_decode_score_pages(ctypes.byref(d), _ptr(query), _ptr(keys), _ptr(block_table),
+                                     _ptr(seq_lens), _ptr(scores), _ptr(status), _stream()),
+        "mla_decode_score_pages")
+
+
+def select_pages(d: Dims, scores, block_table, seq_lens, top_k, keep_first, keep_last, sel_table,
+                 sel_lens, sel_pages=None, status=None):
+    """The top_k pages of every query token, as a block table (int32 [B * T, top_k])
+    and lengths (int32 [B * T]) to decode on with one query token per line."""
+    lines = d.batch * d.q_len
+    _need("scores", scores, torch.float32, d.batch, d.q_len, d.max_pages_per_seq)
+    _need("sel_table", sel_table, torch.int32, lines, top_k)
+    _need("sel_lens", sel_lens, torch.int32, lines)
+    if sel_pages is not None:
+        _need("sel_pages", sel_pages, torch.int32, lines, top_k)
+    _lines(d, block_table, seq_lens, None, status)
+    _ok(lib().mla_decode_select_pages(ctypes.byref(d), _ptr(scores), _ptr(block_table),
+                                      _ptr(seq_lens), top_k, keep_first, keep_last,
+                                      _ptr(sel_table), _ptr(sel_pages), _ptr(sel_lens),
+                                      _ptr(status), _stream()),
+        "mla_decode_select_pages")

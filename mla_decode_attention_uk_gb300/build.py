@@ -14,7 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libmla_decode.so")
-SOURCES = ["api.cu", "plan.cu", "bmm.cu", "decode.cu", "combine.cu", "noalloc.cu"]
+SOURCES = ["api.cu", "plan.cu", "bmm.cu", "decode.cu", "combine.cu", "noalloc.cu",
+           "decode_fp8kv.cu", "append.cu", "select.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", CSRC, "-I", INCLUDE]

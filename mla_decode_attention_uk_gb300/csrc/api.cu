@@ -55,6 +55,30 @@ cudaError_t launch_combine_up(const CUtensorMap& tm_wuv, int B, int T, int H, co
                               const __nv_bfloat16* olat, float* lse, float scale,
                               __nv_bfloat16* out, int32_t* status, int splits_per_seq,
                               const float* wuv_scale, cudaStream_t st);
+size_t fp8kv_terms_bytes(int B, int T, int H);
+cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_c, int sm_count,
+                                const __nv_bfloat16* qlat, uint8_t* terms,
+                                const int32_t* block_table, const float* kv_scale,
+                                const int32_t* seq_len_eff, const PlanHeader* header, void* ws,
+                                const int32_t* seq_first, const int32_t* seq_nsplit,
+                                const int32_t* seq_slot, __nv_bfloat16* olat, float* lse,
+                                int32_t* status, int B, int T, int H, int max_pages,
+                                int num_pages, float scale, cudaStream_t st);
+cudaError_t launch_append(const void* rows, int max_new, const int32_t* new_lens,
+                          const int32_t* block_table, const int32_t* seq_lens, int B,
+                          int num_pages, int max_pages, uint8_t* kv8, float* kv_scale,
+                          int32_t* status, cudaStream_t st);
+cudaError_t launch_page_keys(const void* cache, const float* kv_scale,
+                             const int32_t* block_table, const int32_t* seq_lens, int max_new,
+                             const int32_t* new_lens, int B, int num_pages, int max_pages,
+                             __nv_bfloat16* keys, int32_t* status, cudaStream_t st);
+cudaError_t launch_score(const void* query, const void* page_keys, const int32_t* block_table,
+                         const int32_t* seq_lens, int B, int T, int H, int num_pages,
+                         int max_pages, float* scores, int32_t* status, cudaStream_t st);
+cudaError_t launch_select(const float* scores, const int32_t* block_table,
+                          const int32_t* seq_lens, int B, int T, int max_pages, int top_k,
+                          int keep_first, int keep_last, int32_t* sel_table, int32_t* sel_pages,
+                          int32_t* sel_lens, int32_t* status, cudaStream_t st);
 }  // namespace mla
 
 namespace {
@@ -154,6 +178,7 @@ int cuda_rc(cudaError_t e) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int check_dims(const mla_decode_dims* d) {
   if (!d) return MLA_DECODE_INVALID_ARG;
@@ -228,7 +253,6 @@ int check_run_inputs(const mla_decode_dims* d, const void* q, const void* kv_cac
                      float scale, const void* out, const float* lse) {
   int rc = check_dims(d);
   if (rc) return rc;
-  auto aligned4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; };
   if (!softmax_scale_ok(scale)) return MLA_DECODE_INVALID_ARG;
   if (!q || !kv_cache || !block_table || !seq_lens || !w_uk || !w_uv || !out || !lse ||
       !aligned16(q) || !aligned16(kv_cache) || !aligned16(w_uk) || !aligned16(w_uv) ||
@@ -582,6 +606,30 @@ static int check_run(const mla_decode_dims* d, const void* q, const void* kv_cac
   return layout_for(d, ws_bytes, &L);
 }
 
+// Steps a4 and a5 of a whole run, with bf16 weights (w_uv) or FP8 weights (w8
+// with block scales).
+static int finish_run(const mla_decode_dims* d, const void* w_uv, const uint8_t* w8,
+                      const float* w8_scale, float scale, void* out, float* lse, void* ws,
+                      size_t ws_bytes, void* stream) {
+  // Small batches: the combine's merges build the up-projection's operand in
+  // shared memory (one launch, no o_lat round trip).
+  bool fused = false;
+  int rc = run_uses_combine_up(d, &fused);
+  if (rc) return rc;
+  if (fused) return combine_up_impl(d, w_uv, w8, w8_scale, scale, out, lse, ws, ws_bytes, stream);
+  // Large batches: the combine merges split sequences only and the
+  // up-projection corrects the lse of the others from the o_lat and q_lo
+  // tiles it stages anyway (one read of each instead of two).
+  bool rows = false;
+  rc = run_uses_up_rows(d, &rows);
+  if (rc) return rc;
+  rc = combine_impl(d, scale, lse, ws, ws_bytes, stream, rows);
+  if (rc) return rc;
+  if (rows)
+    return up_project_rows_impl(d, w_uv, w8, w8_scale, scale, out, lse, ws, ws_bytes, stream);
+  return up_project_impl(d, w_uv, w8, w8_scale, out, ws, ws_bytes, stream);
+}
+
 int mla_decode_run(const mla_decode_dims* d, const void* q, const void* kv_cache,
                    const int32_t* block_table, const int32_t* seq_lens, const void* w_uk,
                    const void* w_uv, float scale, void* out, float* lse, void* ws, size_t ws_bytes,
@@ -593,25 +641,7 @@ int mla_decode_run(const mla_decode_dims* d, const void* q, const void* kv_cache
   if (rc) return rc;
   rc = mla_decode_attend(d, kv_cache, block_table, seq_lens, scale, lse, ws, ws_bytes, stream);
   if (rc) return rc;
-  // Small batches: the combine's merges build the up-projection's operand in
-  // shared memory (one launch, no o_lat round trip).
-  bool fused = false;
-  rc = run_uses_combine_up(d, &fused);
-  if (rc) return rc;
-  if (fused)
-    return combine_up_impl(d, w_uv, nullptr, nullptr, scale, out, lse, ws, ws_bytes, stream);
-  // Large batches: the combine merges split sequences only and the
-  // up-projection corrects the lse of the others from the o_lat and q_lo
-  // tiles it stages anyway (one read of each instead of two).
-  bool rows = false;
-  rc = run_uses_up_rows(d, &rows);
-  if (rc) return rc;
-  rc = combine_impl(d, scale, lse, ws, ws_bytes, stream, rows);
-  if (rc) return rc;
-  if (rows)
-    return up_project_rows_impl(d, w_uv, nullptr, nullptr, scale, out, lse, ws, ws_bytes,
-                                stream);
-  return mla_decode_up_project(d, w_uv, out, ws, ws_bytes, stream);
+  return finish_run(d, w_uv, nullptr, nullptr, scale, out, lse, ws, ws_bytes, stream);
 }
 
 int mla_decode_run_fp8w(const mla_decode_dims* d, const void* q, const void* kv_cache,
@@ -626,21 +656,156 @@ int mla_decode_run_fp8w(const mla_decode_dims* d, const void* q, const void* kv_
   if (rc) return rc;
   rc = mla_decode_attend(d, kv_cache, block_table, seq_lens, scale, lse, ws, ws_bytes, stream);
   if (rc) return rc;
-  bool fused = false;  // as in mla_decode_run
-  rc = run_uses_combine_up(d, &fused);
+  return finish_run(d, nullptr, w_uv_fp8, w_uv_scale, scale, out, lse, ws, ws_bytes, stream);
+}
+
+int mla_decode_fp8kv_terms_size(const mla_decode_dims* d, size_t* bytes) {
+  const int rc = check_dims(d);
   if (rc) return rc;
-  if (fused)
-    return combine_up_impl(d, nullptr, w_uv_fp8, w_uv_scale, scale, out, lse, ws, ws_bytes,
-                           stream);
-  bool rows = false;
-  rc = run_uses_up_rows(d, &rows);
+  if (!bytes) return MLA_DECODE_INVALID_ARG;
+  *bytes = fp8kv_terms_bytes(d->batch, d->q_len, d->num_heads);
+  return MLA_DECODE_OK;
+}
+
+int mla_decode_attend_fp8kv(const mla_decode_dims* d, const uint8_t* kv_fp8,
+                            const float* kv_scale, const int32_t* block_table,
+                            const int32_t* seq_lens, float scale, float* lse, void* terms,
+                            size_t terms_bytes, void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_dims(d);
   if (rc) return rc;
-  rc = combine_impl(d, scale, lse, ws, ws_bytes, stream, rows);
+  if (!softmax_scale_ok(scale) || !kv_fp8 || !kv_scale || !block_table || !seq_lens || !lse ||
+      !terms || !ws || !aligned16(kv_fp8) || !aligned16(terms) || !aligned16(ws) ||
+      !aligned4(kv_scale) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(lse))
+    return MLA_DECODE_INVALID_ARG;
+  WsLayout L;
+  rc = layout_for(d, ws_bytes, &L);
   if (rc) return rc;
-  if (rows)
-    return up_project_rows_impl(d, nullptr, w_uv_fp8, w_uv_scale, scale, out, lse, ws, ws_bytes,
-                                stream);
-  return mla_decode_up_project_fp8w(d, w_uv_fp8, w_uv_scale, out, ws, ws_bytes, stream);
+  if (terms_bytes < fp8kv_terms_bytes(d->batch, d->q_len, d->num_heads))
+    return MLA_DECODE_WORKSPACE_TOO_SMALL;
+  // Boxes of 128 codes; the fifth's second half lies past the row and is
+  // filled with zeros.
+  CUtensorMap tm_c;
+  if (!make_map(&tm_c, kv_fp8, static_cast<uint64_t>(d->num_pages) * kPage, kDqk, kDqk, 128,
+                kPage, true, 1))
+    return MLA_DECODE_CUDA_ERROR;
+  int sms = 0;
+  rc = sm_count(&sms);
+  if (rc) return rc;
+  return cuda_rc(launch_decode_fp8kv(
+      tm_c, sms, at<__nv_bfloat16>(ws, L.qlat), static_cast<uint8_t*>(terms), block_table,
+      kv_scale, at<int32_t>(ws, L.seq_len_eff), at<PlanHeader>(ws, L.header), ws,
+      at<int32_t>(ws, L.seq_first), at<int32_t>(ws, L.seq_nsplit), at<int32_t>(ws, L.seq_slot),
+      at<__nv_bfloat16>(ws, L.olat), lse, at<int32_t>(ws, L.status), d->batch, d->q_len,
+      d->num_heads, d->max_pages_per_seq, d->num_pages, scale,
+      static_cast<cudaStream_t>(stream)));
+}
+
+int mla_decode_run_fp8kv(const mla_decode_dims* d, const void* q, const uint8_t* kv_fp8,
+                         const float* kv_scale, const int32_t* block_table,
+                         const int32_t* seq_lens, const void* w_uk, const void* w_uv,
+                         float scale, void* out, float* lse, void* terms, size_t terms_bytes,
+                         void* ws, size_t ws_bytes, void* stream) {
+  int rc = check_run(d, q, kv_fp8, block_table, seq_lens, w_uk, w_uv, false, nullptr, nullptr,
+                     scale, out, lse, ws, ws_bytes);
+  if (rc) return rc;
+  if (!kv_scale || !aligned4(kv_scale) || !terms || !aligned16(terms))
+    return MLA_DECODE_INVALID_ARG;
+  if (terms_bytes < fp8kv_terms_bytes(d->batch, d->q_len, d->num_heads))
+    return MLA_DECODE_WORKSPACE_TOO_SMALL;
+  rc = mla_decode_absorb(d, q, w_uk, ws, ws_bytes, stream);
+  if (rc) return rc;
+  rc = mla_decode_attend_fp8kv(d, kv_fp8, kv_scale, block_table, seq_lens, scale, lse, terms,
+                               terms_bytes, ws, ws_bytes, stream);
+  if (rc) return rc;
+  return finish_run(d, w_uv, nullptr, nullptr, scale, out, lse, ws, ws_bytes, stream);
+}
+
+int mla_decode_append_fp8kv(const mla_decode_dims* d, const void* rows, int32_t max_new,
+                            const int32_t* new_lens, const int32_t* block_table,
+                            const int32_t* seq_lens, uint8_t* kv_fp8, float* kv_scale,
+                            int32_t* status, void* stream) {
+  const int rc = check_dims(d);
+  if (rc) return rc;
+  if (!rows || !aligned16(rows) || max_new < 1 || !aligned4(new_lens) || !block_table ||
+      !aligned4(block_table) || !seq_lens || !aligned4(seq_lens) || !kv_fp8 ||
+      !aligned16(kv_fp8) || !kv_scale || !aligned4(kv_scale) || !aligned4(status))
+    return MLA_DECODE_INVALID_ARG;
+  if (max_new > INT32_MAX - kPage) return MLA_DECODE_INVALID_ARG;
+  return cuda_rc(launch_append(rows, max_new, new_lens, block_table, seq_lens, d->batch,
+                               d->num_pages, d->max_pages_per_seq, kv_fp8, kv_scale, status,
+                               static_cast<cudaStream_t>(stream)));
+}
+
+static int page_keys_impl(const mla_decode_dims* d, const void* cache, const float* kv_scale,
+                          const int32_t* block_table, const int32_t* seq_lens, int32_t max_new,
+                          const int32_t* new_lens, void* page_keys, int32_t* status,
+                          void* stream) {
+  const int rc = check_dims(d);
+  if (rc) return rc;
+  if (!cache || !aligned16(cache) || !aligned4(kv_scale) || !block_table ||
+      !aligned4(block_table) || !seq_lens || !aligned4(seq_lens) || max_new < 1 ||
+      max_new > INT32_MAX - kPage || !aligned4(new_lens) || !page_keys ||
+      !aligned16(page_keys) || !aligned4(status))
+    return MLA_DECODE_INVALID_ARG;
+  return cuda_rc(launch_page_keys(cache, kv_scale, block_table, seq_lens, max_new, new_lens,
+                                  d->batch, d->num_pages, d->max_pages_per_seq,
+                                  static_cast<__nv_bfloat16*>(page_keys), status,
+                                  static_cast<cudaStream_t>(stream)));
+}
+
+int mla_decode_page_keys(const mla_decode_dims* d, const void* kv_cache,
+                         const int32_t* block_table, const int32_t* seq_lens, int32_t max_new,
+                         const int32_t* new_lens, void* page_keys, int32_t* status,
+                         void* stream) {
+  return page_keys_impl(d, kv_cache, nullptr, block_table, seq_lens, max_new, new_lens,
+                        page_keys, status, stream);
+}
+
+int mla_decode_page_keys_fp8kv(const mla_decode_dims* d, const uint8_t* kv_fp8,
+                               const float* kv_scale, const int32_t* block_table,
+                               const int32_t* seq_lens, int32_t max_new,
+                               const int32_t* new_lens, void* page_keys, int32_t* status,
+                               void* stream) {
+  const int rc = check_dims(d);
+  if (rc) return rc;
+  if (!kv_scale) return MLA_DECODE_INVALID_ARG;
+  return page_keys_impl(d, kv_fp8, kv_scale, block_table, seq_lens, max_new, new_lens, page_keys,
+                        status, stream);
+}
+
+int mla_decode_score_pages(const mla_decode_dims* d, const void* query, const void* page_keys,
+                           const int32_t* block_table, const int32_t* seq_lens, float* scores,
+                           int32_t* status, void* stream) {
+  const int rc = check_dims(d);
+  if (rc) return rc;
+  if (!query || !aligned16(query) || !page_keys || !aligned16(page_keys) || !block_table ||
+      !aligned4(block_table) || !seq_lens || !aligned4(seq_lens) || !scores ||
+      !aligned4(scores) || !aligned4(status))
+    return MLA_DECODE_INVALID_ARG;
+  return cuda_rc(launch_score(query, page_keys, block_table, seq_lens, d->batch, d->q_len,
+                              d->num_heads, d->num_pages, d->max_pages_per_seq, scores, status,
+                              static_cast<cudaStream_t>(stream)));
+}
+
+int mla_decode_select_pages(const mla_decode_dims* d, const float* scores,
+                            const int32_t* block_table, const int32_t* seq_lens, int32_t top_k,
+                            int32_t keep_first, int32_t keep_last, int32_t* sel_table,
+                            int32_t* sel_pages, int32_t* sel_lens, int32_t* status,
+                            void* stream) {
+  const int rc = check_dims(d);
+  if (rc) return rc;
+  if (!scores || !aligned4(scores) || !block_table || !aligned4(block_table) || !seq_lens ||
+      !aligned4(seq_lens) || !sel_table || !aligned4(sel_table) || !aligned4(sel_pages) ||
+      !sel_lens || !aligned4(sel_lens) || !aligned4(status))
+    return MLA_DECODE_INVALID_ARG;
+  // The last page is always kept: it may be partly filled, and the selected
+  // pages in order then hold keys without a gap.
+  if (top_k < 1 || keep_first < 0 || keep_last < 1 || keep_first > top_k - keep_last ||
+      static_cast<int64_t>(top_k) * kPage > INT32_MAX / 2)
+    return MLA_DECODE_INVALID_ARG;
+  return cuda_rc(launch_select(scores, block_table, seq_lens, d->batch, d->q_len,
+                               d->max_pages_per_seq, top_k, keep_first, keep_last, sel_table,
+                               sel_pages, sel_lens, status, static_cast<cudaStream_t>(stream)));
 }
 
 int mla_decode_kernels_per_run(const mla_decode_dims* d, int32_t fp8_weights,

@@ -1,0 +1,764 @@
+// decode_fp8kv.cu -- the attention step over the 8-bit latent cache.
+//
+// The cache holds E4M3 codes and one scale s per page (fp8kv.cuh).  With the
+// absorbed query q and codes c_j of a page:
+//   x_j   = scale log2(e) s (q . c_j)        p_j = 2^(x_j - m)
+//   o_lat = sum_j (p_j s) c_j[0:512] / sum_j p_j,   lse = (m + log2 sum p_j) ln 2
+// Split-KV ranges, the plan, the merge of partial results and the lse's
+// first-order correction are those of the bf16 cache's step (decode.cu).
+//
+// GB300 mapping: both products run on the 8-bit tensor-core path (kind::f8f6f4,
+// K = 32 per instruction), so the codes go from memory to the tensor core as
+// they are, half the bytes of a bf16 page at every level.  What the other
+// operand loses in 8 bits is given back by a second term:
+//   * Q = scale_row (hi + mid / 16), both E4M3: hi is the value rounded to four
+//     bits, mid the rest times 16.  A bf16 value has eight significant bits and
+//     the two terms hold it exactly (down to 2^-13 of the row's largest value
+//     and, below that, to 2^-22 of it), so the product is that of the bf16
+//     query.  The terms are stacked as the M = 128 rows of one MMA: the full
+//     rate of the tensor core for 64 query rows, where a 64-row MMA would run at
+//     half of it.
+//   * P = hi + mid, both E5M2, eight bits wide of fp16: as both accumulate into
+//     the same columns they cannot have scales of their own, and E5M2's range
+//     (2^-16 to 2^15) keeps the small weights of a long context next to a large
+//     one, which E4M3's would drop.  Two terms leave at most 2^-7 of a weight;
+//     the row is divided by the sum of the weights as rounded, so a rounding
+//     that all weights share cancels, and the lse takes the unrounded sum.
+// Per page and 64 query rows: QK^T 18 MMAs of 128 x 64 x 32, PV 16 of
+// 128 x N x 32 (N: the tile's rows).  The rest is as in decode.cu: the
+// producer warp brings pages box by box into a ring of slots (three of 40 KB
+// next to the query's 80 KB), the softmax runs on TMEM rows with a running
+// maximum that is raised lazily, P^T goes into the page's RoPE box, and O^T
+// stays in TMEM.  The page's scale joins the exponent (p_j s = 2^(x_j + log2 s
+// - m), m the running maximum of that sum), so that P never leaves E5M2's
+// range however the scales of a sequence's pages differ.
+// Warp roles: 0 TMA producer, 1 QK^T issuer, 2 TMEM, 3 and 8 PV issuers (latent
+// halves), 4-7 softmax and epilogue.  (QK^T has one issuer: two that took turns
+// would each see only every second phase of a slot's barriers.)
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "fp8kv.cuh"
+#include "ptx.cuh"
+
+namespace mla {
+
+int decode_tiles(int T, int H);
+
+namespace {
+
+// ---------------------------------------------------------------- query terms
+constexpr int kSplitThreads = 256;  // one warp per tile row
+
+// q_lat (bf16) -> the attention step's tiles of E4M3 terms, in the shared-
+// memory image that the tensor core reads (128-byte swizzle), and each row's
+// scale.  Rows past the sequence's T * H are zero.
+__global__ void __launch_bounds__(kSplitThreads)
+split_q_kernel(const uint4* __restrict__ qlat, int TH, int tiles, uint8_t* __restrict__ terms,
+               float* __restrict__ row_scale) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.x * (kSplitThreads / 32) + warp;  // row of the tile
+  const int tile = blockIdx.y;                             // b * tiles + tile of the sequence
+  const int b = tile / tiles, rs = (tile % tiles) * kTileRows + r;
+  const bool ok = rs < TH;
+  // Lane l holds columns 16 l .. + 15; lanes 0-3 also the 64 RoPE columns.
+  uint32_t v[2][8] = {};
+  if (ok) {
+    const uint4* src = qlat + (static_cast<size_t>(b) * TH + rs) * (kDqk / 8);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (i == 1 && lane >= 4) break;
+      const uint4 x = src[2 * (lane + 32 * i)], y = src[2 * (lane + 32 * i) + 1];
+      v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
+      v[i][4] = y.x; v[i][5] = y.y; v[i][6] = y.z; v[i][7] = y.w;
+    }
+  }
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[i][k] << 16)),
+                             fabsf(__uint_as_float(v[i][k] & 0xffff0000u))));
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float scale = exp2_int(page_scale_exp(top));
+  const float inv = 1.0f / scale;
+  uint8_t* const img = terms + static_cast<size_t>(tile) * kQTile8;
+  const int row = 32 * (r >> 4) + (r & 15);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (i == 1 && lane >= 4) break;
+    uint32_t hi[4], mid[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float x0 = __uint_as_float(v[i][2 * k] << 16) * inv;
+      const float x1 = __uint_as_float(v[i][2 * k] & 0xffff0000u) * inv;
+      const float x2 = __uint_as_float(v[i][2 * k + 1] << 16) * inv;
+      const float x3 = __uint_as_float(v[i][2 * k + 1] & 0xffff0000u) * inv;
+      hi[k] = e4m3x4(x0, x1, x2, x3);
+      const float2 h0 = e4m3x2_to_float2(hi[k]), h1 = e4m3x2_to_float2(hi[k] >> 16);
+      mid[k] = e4m3x4((x0 - h0.x) * kQMidScale, (x1 - h0.y) * kQMidScale,
+                      (x2 - h1.x) * kQMidScale, (x3 - h1.y) * kQMidScale);
+    }
+    const int chunk = lane + 32 * i;  // 16 columns: chunk (mod 8) of box chunk / 8
+    uint8_t* const box = img + (chunk >> 3) * kQBox8;
+    const int at = ((chunk & 7) ^ (row & 7)) << 4;  // rows row and row + 16: the same swizzle
+    *reinterpret_cast<uint4*>(box + row * 128 + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(box + (row + 16) * 128 + at) =
+        make_uint4(mid[0], mid[1], mid[2], mid[3]);
+  }
+  if (lane == 0) row_scale[static_cast<size_t>(tile) * kTileRows + r] = scale;
+}
+
+// ---------------------------------------------------------------- attention
+constexpr int kThreads = 288;                     // 9 warps
+constexpr int kBox = kPage * 128;                 // 64 keys x 128 codes: 8 KB
+constexpr int kSlot = kBoxes8 * kBox;             // 40 KB (the last box half empty)
+constexpr int kSlots = 3;
+constexpr int kSBufs = 4;                         // S buffers of 64 columns
+constexpr int kRopeBox8 = kBoxes8 - 1;
+constexpr int kSmemBytes = 1024 + kQTile8 + kSlots * kSlot;
+// Boxes in the order in which the PV issuers release them (blocks 0 and 2, then
+// 1 and 3, then the RoPE box, which holds P^T); loaded and read by QK^T so too.
+constexpr uint32_t kOrder = 0x43120u;             // 0, 2, 1, 3, 4
+__device__ __forceinline__ int box_at(int t) { return static_cast<int>((kOrder >> (4 * t)) & 15); }
+constexpr int kAhead = 2;                         // pages looked up (and prefetched) ahead
+constexpr uint32_t kTmemAll = 512;
+constexpr uint32_t kTmemOut = 256;                // O^T blocks at 256 + 64 m
+constexpr float kRaise = 8.0f;                    // log2 units
+// The running maximum's weight is 2^kTopExp; it may grow by 2^kRaise before
+// the maximum is raised, to 2^15 (E5M2 ends at 1.75 * 2^15).
+constexpr float kTopExp = 7.0f;
+// Weights from here on count as rounded in the row's normalising sum.  Smaller
+// ones count as they are: near the end of E5M2's range their rounding is no
+// longer small against them, and in a page of a small scale such weights may
+// make up the sum while they add nothing to the output.
+constexpr float kRoundedFrom = 1.0f / 512.0f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Params {
+  const int32_t* block_table;
+  const float* kv_scale;
+  const int32_t* seq_len_eff;
+  const PlanHeader* header;
+  uint8_t* ws;
+  const int32_t* range_b;  // these two are filled in on the device
+  const int32_t* range_p;
+  const int32_t* seq_first;
+  const int32_t* seq_nsplit;
+  const int32_t* seq_slot;
+  const uint8_t* terms;
+  const float* row_scale;
+  __nv_bfloat16* olat;
+  float* lse;
+  __nv_bfloat16* opart;
+  float* lpart;
+  int32_t* status;
+  int B, T, H, max_pages, num_pages;
+  int tiles, tpg, sets;
+  float scale_log2;
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+__device__ __forceinline__ bool bar_any(uint32_t id, uint32_t n, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(pred ? 1u : 0u), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+
+// Two fp32 values to two E5M2 codes in the high bytes of an fp16 pair: E5M2 is
+// fp16's upper byte, so rounding is an addition and a mask (ties away from
+// zero; |x| <= 2^15 and its rounding stay finite).
+__device__ __forceinline__ __half2 e5m2_in_half2(__half2 x) {
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(&x);
+  const uint32_t r = (u + 0x00800080u) & 0xff00ff00u;
+  return *reinterpret_cast<const __half2*>(&r);
+}
+__device__ __forceinline__ uint32_t bits(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+
+struct Piece {
+  int task, b, pbeg, pend, len;
+};
+
+// The pieces (sequence, page range) of a CTA's tasks v = v0, v0 + stride, ...
+// < nv, in the order that all roles walk.  Task v is work range v / sets.
+struct Pieces {
+  int v, stride, nv, sets;
+  int b, p, b1, p1;
+  __device__ Pieces(const Params& P, int v0, int stride_, int nv_)
+      : v(v0), stride(stride_), nv(nv_), sets(P.sets) { open(P); }
+  __device__ void open(const Params& P) {
+    if (v >= nv) return;
+    const int k = v / sets;
+    b = P.range_b[k];
+    p = P.range_p[k];
+    b1 = P.range_b[k + 1];
+    p1 = P.range_p[k + 1];
+  }
+  __device__ bool next(const Params& P, Piece& out) {
+    while (v < nv) {
+      while (b < b1 || (b == b1 && p < p1)) {
+        const int L = P.seq_len_eff[b];
+        const int end = b == b1 ? p1 : (L + kPage - 1) / kPage;
+        out = Piece{v, b, p, end, L};
+        ++b;
+        p = 0;
+        if (out.pend > out.pbeg) return true;
+      }
+      v += stride;
+      open(P);
+    }
+    return false;
+  }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
+  extern __shared__ uint8_t smem_raw[];
+  // slot_full: one barrier per box of a slot; slot_free: one per box, after
+  // PV block m (RoPE box: after both PV issuers).  p_full / p_free follow the
+  // slot of the page.
+  __shared__ __align__(8) uint64_t q_full, q_free, slot_full[kSlots][kBoxes8],
+      slot_free[kSlots][kBoxes8], s_full[kSBufs], s_free[kSBufs], p_full[kSlots], p_free[kSlots],
+      o_full, o_free, drain_bar[3];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+  __shared__ float page_scale_sh[kSlots];
+  __shared__ float alpha_sh[kTileRows];
+  __shared__ __align__(16) float inv_l_sh[kTileRows];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Tasks v = range * sets + set are dealt round robin to groups of tpg CTAs;
+  // a group's CTA ti takes tile set * tpg + ti (as in decode.cu).
+  const int tpg = P.tpg, sets = P.sets;
+  const int ti = blockIdx.x % tpg, gi = blockIdx.x / tpg, groups = gridDim.x / tpg;
+  const int TH = P.T * P.H;
+  const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sSlot0 = sQ + kQTile8;
+
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&q_full), 1);
+    mbar_init(smem_u32(&q_free), 1);
+    for (int i = 0; i < kSlots; ++i) {
+      for (int j = 0; j < kBoxes8; ++j) {
+        mbar_init(smem_u32(&slot_full[i][j]), 1);
+        mbar_init(smem_u32(&slot_free[i][j]), j == kRopeBox8 ? 2 : 1);
+      }
+      mbar_init(smem_u32(&p_full[i]), 1);
+      mbar_init(smem_u32(&p_free[i]), 2);
+    }
+    for (int i = 0; i < kSBufs; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&s_free[i]), 4);
+    }
+    mbar_init(smem_u32(&o_full), 2);
+    mbar_init(smem_u32(&o_free), 4);
+    for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&drain_bar[i]), 1);
+    abort_sh = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_c);
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  const int R = P.header->num_ranges;
+  {
+    const WsLayout L = make_layout(P.B, P.T, P.H, R);
+    P.range_b = reinterpret_cast<const int32_t*>(P.ws + L.range_b);
+    P.range_p = reinterpret_cast<const int32_t*>(P.ws + L.range_p);
+    P.lpart = reinterpret_cast<float*>(P.ws + L.lpart);
+    P.opart = reinterpret_cast<__nv_bfloat16*>(P.ws + L.opart);
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(&tmem_base_sh), kTmemAll);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  Pieces walk(P, gi, groups, R * sets);
+  Piece pc;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (elect_one()) {
+      int g = 0, n = 0, nq = 0;  // pages, pieces, query copies issued
+      bool ok = true;
+      while (ok && walk.next(P, pc)) {
+        if (n > 0 && !mbar_wait(smem_u32(&q_free), (n - 1) & 1, &abort_sh, P.status)) break;
+        const int tile = (pc.task % sets) * tpg + ti;
+        mbar_expect_tx(smem_u32(&q_full), kQTile8);
+        bulk_load(sQ, P.terms + (static_cast<size_t>(pc.b) * P.tiles + tile) * kQTile8, kQTile8,
+                  smem_u32(&q_full));
+        ++nq;
+        const int nc = pc.pend - pc.pbeg;
+        const int32_t* row = P.block_table + static_cast<size_t>(pc.b) * P.max_pages + pc.pbeg;
+        // Page numbers and scales are read, and pages prefetched into L2,
+        // kAhead pages before their load into shared memory.
+        int page[kAhead];
+        float scale[kAhead];
+        auto look = [&](int i, int& pg, float& sc) {
+          if (i >= nc) return;
+          pg = __ldg(row + i);
+          if (pg < 0 || pg >= P.num_pages) {
+            record_status(P.status, MLA_STATUS_BOUNDS);
+            pg = 0;
+          }
+          sc = P.kv_scale[pg];
+          for (int j = 0; j < kBoxes8; ++j) tma_prefetch_l2_2d(&tm_c, j * 128, pg * kPage);
+        };
+#pragma unroll
+        for (int a = 0; a < kAhead; ++a) look(a, page[a], scale[a]);
+        for (int i = 0; i < nc; ++i, ++g) {
+          const int s = g % kSlots, u = g / kSlots;
+          float sc = scale[0];
+          if (!(sc >= exp2_int(kScaleExpMin) && sc <= exp2_int(kScaleExpMax))) {
+            record_status(P.status, MLA_STATUS_BOUNDS);
+            sc = 1.0f;
+          }
+          int t = 0;
+          for (; t < kBoxes8; ++t) {
+            const int j = box_at(t);
+            if (u > 0 && !mbar_wait(smem_u32(&slot_free[s][j]), (u - 1) & 1, &abort_sh, P.status)) {
+              ok = false;
+              break;
+            }
+            // The softmax is done with the slot's last page once any of its
+            // boxes is free (PV follows it).
+            if (t == 0) *static_cast<volatile float*>(&page_scale_sh[s]) = sc;
+            const uint32_t fb = smem_u32(&slot_full[s][j]);
+            mbar_expect_tx(fb, kBox);
+            tma_load_2d(sSlot0 + s * kSlot + j * kBox, &tm_c, j * 128, page[0] * kPage, fb);
+          }
+          if (!ok) {
+            for (int t2 = 0; t2 < t; ++t2)
+              mbar_wait_drain(smem_u32(&slot_full[s][box_at(t2)]), u & 1, P.status);
+            break;
+          }
+#pragma unroll
+          for (int a = 0; a + 1 < kAhead; ++a) {
+            page[a] = page[a + 1];
+            scale[a] = scale[a + 1];
+          }
+          look(i + kAhead, page[kAhead - 1], scale[kAhead - 1]);
+        }
+        ++n;
+      }
+      // Every copy lands before the CTA exits, after an abort too.
+      if (nq > 0) mbar_wait_drain(smem_u32(&q_full), (nq - 1) & 1, P.status);
+      for (int s = 0; s < kSlots; ++s) {
+        const int k = (g - s + kSlots - 1) / kSlots;  // pages loaded into slot s
+        if (k > 0)
+          for (int j = 0; j < kBoxes8; ++j)
+            mbar_wait_drain(smem_u32(&slot_full[s][j]), (k - 1) & 1, P.status);
+      }
+    }
+  } else if (warp == 1 || warp == 3 || warp == 8) {
+    // ------------------------------------------------------------ MMA issuers
+    if (elect_one()) {
+      const uint64_t dq0 = sdesc_sw128(sQ, 16, 1024);
+      const uint64_t dslot0 = sdesc_sw128(sSlot0, 16, 1024);
+      const uint64_t dpv0 = sdesc_sw128(sSlot0, kBox, 1024);
+      int g = 0, n = 0;
+      bool ok = true;
+      if (warp == 1) {
+        constexpr uint32_t idesc = idesc_f8_f32(kQTermRows, kPage, 0, 0, false, false);
+        while (ok && walk.next(P, pc)) {
+          if (!mbar_wait(smem_u32(&q_full), n & 1, &abort_sh, P.status)) break;
+          for (int i = pc.pbeg; i < pc.pend; ++i, ++g) {
+            const int s = g % kSlots, sb = g % kSBufs;
+            if (g >= kSBufs && !mbar_wait(smem_u32(&s_free[sb]), (g / kSBufs - 1) & 1, &abort_sh,
+                                          P.status)) {
+              ok = false;
+              break;
+            }
+            const uint64_t bd0 = dslot0 + static_cast<uint64_t>((s * kSlot) >> 4);
+            for (int t = 0; t < kBoxes8 && ok; ++t) {
+              const int j = box_at(t);
+              if (!mbar_wait(smem_u32(&slot_full[s][j]), (g / kSlots) & 1, &abort_sh, P.status)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const int steps = j == kRopeBox8 ? 2 : 4;  // 32 columns each
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                if (kk < steps)
+                  umma_f8(tmem + 64 * sb, dq0 + ((j * kQBox8) >> 4) + kk * 2,
+                          bd0 + ((j * kBox) >> 4) + kk * 2, idesc, t != 0 || kk != 0);
+            }
+            if (!ok) break;
+            umma_commit(smem_u32(&s_full[sb]));
+          }
+          if (!ok) break;
+          umma_commit(smem_u32(&q_free));
+          ++n;
+        }
+      } else {
+        const int half = warp == 3 ? 0 : 1;
+        while (ok && walk.next(P, pc)) {
+          const int tile = (pc.task % sets) * tpg + ti;
+          const int nrows = min(kTileRows, (TH - tile * kTileRows + 15) & ~15);
+          const uint32_t idesc = idesc_f8_f32(128, nrows, 0, 1, true, false);
+          for (int i = pc.pbeg; i < pc.pend; ++i, ++g) {
+            const int s = g % kSlots;
+            const bool first = i == pc.pbeg;
+            if (!mbar_wait(smem_u32(&p_full[s]), (g / kSlots) & 1, &abort_sh, P.status) ||
+                (first && n > 0 &&
+                 !mbar_wait(smem_u32(&o_free), (n - 1) & 1, &abort_sh, P.status))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t ad0 = dpv0 + static_cast<uint64_t>((s * kSlot) >> 4);
+            const uint64_t bd0 = dslot0 + static_cast<uint64_t>((s * kSlot + kRopeBox8 * kBox) >> 4);
+#pragma unroll
+            for (int m = 2 * half; m < 2 * half + 2; ++m) {
+              // Steps 0, 1: the hi terms of keys 0-31 and 32-63; 2, 3: mid.
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_f8(tmem + kTmemOut + 64 * m, ad0 + ((m * kBox + (kk & 1) * 4096) >> 4),
+                        bd0 + kk * 2, idesc, !(first && kk == 0));
+              umma_commit(smem_u32(&slot_free[s][m]));
+            }
+            umma_commit(smem_u32(&slot_free[s][kRopeBox8]));
+            umma_commit(smem_u32(&p_free[s]));
+          }
+          if (!ok) break;
+          umma_commit(smem_u32(&o_full));
+          ++n;
+        }
+      }
+      const uint32_t db = smem_u32(&drain_bar[warp == 1 ? 0 : (warp == 3 ? 1 : 2)]);
+      umma_commit(db);
+      mbar_wait_drain(db, 0, P.status);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax + epilogue
+    const int wq = warp - 4;  // TMEM lane quarter
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    // This thread: row srow of the tile (its hi term in lane rig of the
+    // quarter, its mid term in lane 16 + rig), keys of parity par.
+    const int rig = (lane >> 2) + 8 * (lane & 1);
+    const int par = (lane >> 1) & 1;
+    const int srow = 16 * wq + rig;
+    const bool owner = par == 0;
+    int g = 0, n = 0;
+    bool fail = false;
+    bool have = walk.next(P, pc);
+    while (!fail && have) {
+      const int k = pc.task / sets, tile = (pc.task % sets) * tpg + ti;
+      const int b = pc.b;
+      const int r = tile * kTileRows + srow;
+      const bool row_ok = r < TH;
+      const int nsplit = P.seq_nsplit[b];
+      const int split = k - P.seq_first[b];
+      const int slot = P.seq_slot[b];
+      const float q_scale =
+          P.row_scale[(static_cast<size_t>(b) * P.tiles + tile) * kTileRows + srow] * P.scale_log2;
+      const int n_row = row_ok ? pc.len - P.T + r / P.H + 1 : 0;
+      float m_used = -INFINITY;
+      float l = 0.0f, l_r = 0.0f;  // this thread's halves of the row's sums: exact, as rounded
+      for (int i = pc.pbeg; i < pc.pend; ++i, ++g) {
+        const int sb = g % kSBufs, s = g % kSlots;
+        bool need = false;
+        // (The slot's first box is complete long before; its barrier orders
+        // the producer's page_scale_sh.)
+        bool bad = !mbar_wait(smem_u32(&slot_full[s][0]), (g / kSlots) & 1, &abort_sh, P.status) ||
+                   !mbar_wait(smem_u32(&s_full[sb]), (g / kSBufs) & 1, &abort_sh, P.status);
+        bad = __any_sync(0xffffffffu, bad);
+        const float page_scale = *static_cast<volatile float*>(&page_scale_sh[s]);
+        uint32_t v[32];
+        if (!bad) {
+          tc_fence_after();
+          uint32_t v2[32];
+          tmem_ld_16x64b_x32(tmem + lane_off + 64 * sb, v);
+          tmem_ld_16x64b_x32(tmem + lane_off + (16u << 16) + 64 * sb, v2);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            v[j] = __float_as_uint(
+                fmaf(__uint_as_float(v2[j]), 1.0f / kQMidScale, __uint_as_float(v[j])));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s_free[sb]));
+        if (!bad) {
+          const int kb = i * kPage + par;  // key of v[0]; v[j] is key kb + 2 j
+          if (kb + 62 >= n_row) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (kb + 2 * j >= n_row) v[j] = __float_as_uint(-INFINITY);
+          }
+          float a3[11];
+#pragma unroll
+          for (int t = 0; t < 10; ++t)
+            a3[t] = max3(__uint_as_float(v[3 * t]), __uint_as_float(v[3 * t + 1]),
+                         __uint_as_float(v[3 * t + 2]));
+          a3[10] = fmaxf(__uint_as_float(v[30]), __uint_as_float(v[31]));
+          float vmax = fmaxf(max3(max3(a3[0], a3[1], a3[2]), max3(a3[3], a3[4], a3[5]),
+                                  max3(a3[6], a3[7], a3[8])),
+                             fmaxf(a3[9], a3[10]));
+          vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+          // Not zero, so that a hidden key's -inf times it stays -inf (a
+          // product below 2^-100 is 0 to the exponent either way).
+          const float mul = fmaxf(q_scale * page_scale, 7.9e-31f);
+          const float shift = __log2f(page_scale);
+          const float pmax = fmaf(vmax, mul, shift);
+          float alpha = 1.0f;
+          if (pmax > m_used + kRaise) {
+            alpha = m_used == -INFINITY ? 0.0f : ex2_approx(m_used - pmax);
+            m_used = pmax;
+            need = i > pc.pbeg;
+          }
+          __half2 hi[16], mid[16];
+          float sum = 0.0f, sum_r = 0.0f;
+          if (m_used == -INFINITY) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) hi[j] = mid[j] = __float2half2_rn(0.0f);
+          } else {
+            const float add = shift + kTopExp - m_used;
+            float se[4] = {};
+            __half2 err = __float2half2_rn(0.0f);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float p0 = ex2_approx(fmaf(__uint_as_float(v[2 * j]), mul, add));
+              const float p1 = ex2_approx(fmaf(__uint_as_float(v[2 * j + 1]), mul, add));
+              se[(2 * j) & 3] += p0;
+              se[(2 * j + 1) & 3] += p1;
+              const __half2 h = __floats2half2_rn(p0, p1);
+              hi[j] = e5m2_in_half2(h);
+              mid[j] = e5m2_in_half2(__hsub2(h, hi[j]));
+              err = __hfma2(__hsub2(__hadd2(hi[j], mid[j]), h),
+                            __hge2(h, __float2half2_rn(kRoundedFrom)), err);
+            }
+            sum = (se[0] + se[1]) + (se[2] + se[3]);
+            const float2 e = __half22float2(err);
+            sum_r = sum + (e.x + e.y);
+          }
+          const float inv_scale = __frcp_rn(page_scale);
+          l = fmaf(sum, inv_scale, l * alpha);
+          l_r = fmaf(sum_r, inv_scale, l_r * alpha);
+          if (owner) alpha_sh[srow] = alpha;
+          // The codes are the upper bytes.  The even-key thread writes keys
+          // 0-31, the odd-key thread keys 32-63: half of each thread's codes
+          // cross to its partner, four to a word.
+          uint32_t hw[8], mw[8];
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            hw[t] = __byte_perm(bits(hi[2 * t]), bits(hi[2 * t + 1]), 0x7531);
+            mw[t] = __byte_perm(bits(mid[2 * t]), bits(mid[2 * t + 1]), 0x7531);
+          }
+          uint32_t ph[8], pm[8];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t keep_h = par ? hw[4 + t] : hw[t], keep_m = par ? mw[4 + t] : mw[t];
+            const uint32_t got_h =
+                __shfl_xor_sync(0xffffffffu, par ? hw[t] : hw[4 + t], 2);
+            const uint32_t got_m =
+                __shfl_xor_sync(0xffffffffu, par ? mw[t] : mw[4 + t], 2);
+            const uint32_t eh = par ? got_h : keep_h, oh = par ? keep_h : got_h;
+            const uint32_t em = par ? got_m : keep_m, om = par ? keep_m : got_m;
+            ph[2 * t] = __byte_perm(eh, oh, 0x5140);
+            ph[2 * t + 1] = __byte_perm(eh, oh, 0x7362);
+            pm[2 * t] = __byte_perm(em, om, 0x5140);
+            pm[2 * t + 1] = __byte_perm(em, om, 0x7362);
+          }
+          // P^T row: 64 bytes of hi codes (chunks 0-3), 64 of mid codes (4-7),
+          // into the page's RoPE box, which QK^T is done with.  Rows r and
+          // r + 8 of a quarter-warp's store share their swizzle, so the
+          // latter's threads write mid before hi: eight distinct positions.
+          const uint32_t rowaddr = sSlot0 + s * kSlot + kRopeBox8 * kBox + srow * 128;
+          const bool late = (srow >> 3) & 1;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int h4 = 4 * (q & 1);
+            const bool is_mid = (q >= 2) != late;
+            const int chunk = (is_mid ? 4 : 0) + 2 * par + (q & 1);
+            st_shared_v4(rowaddr + ((chunk ^ (srow & 7)) << 4), is_mid ? pm[h4] : ph[h4],
+                         is_mid ? pm[h4 + 1] : ph[h4 + 1], is_mid ? pm[h4 + 2] : ph[h4 + 2],
+                         is_mid ? pm[h4 + 3] : ph[h4 + 3]);
+          }
+          fence_proxy_async_smem();
+        }
+        // One barrier per page: a timeout anywhere, or a raised maximum.
+        if (bar_any(1, 128, bad || need)) {
+          bool f = *static_cast<volatile int*>(&abort_sh) != 0;
+          if (!f && g >= 1 &&
+              !mbar_wait(smem_u32(&p_free[(g - 1) % kSlots]), ((g - 1) / kSlots) & 1, &abort_sh,
+                         P.status))
+            f = true;
+          if (bar_any(1, 128, f)) { fail = true; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int m = 0; m < 4; ++m) {
+#pragma unroll 1
+            for (int h2 = 0; h2 < 2; ++h2) {
+              uint32_t vv[32];
+              const uint32_t ta = tmem + lane_off + kTmemOut + 64 * m + 32 * h2;
+              tmem_ld_x32(ta, vv);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                vv[j] = __float_as_uint(__uint_as_float(vv[j]) * alpha_sh[32 * h2 + j]);
+              tmem_st_x32(ta, vv);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          named_bar_sync(1, 128);
+        }
+        if (threadIdx.x == 128) mbar_arrive(smem_u32(&p_full[s]));
+      }
+      if (fail) break;
+      have = walk.next(P, pc);
+
+      // ---------------- epilogue of this piece
+      const bool bad = !mbar_wait(smem_u32(&o_full), n & 1, &abort_sh, P.status);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      l_r += __shfl_xor_sync(0xffffffffu, l_r, 2);
+      if (owner) inv_l_sh[srow] = row_ok && l_r > 0.0f ? 1.0f / l_r : 0.0f;
+      if (bar_any(1, 128, bad)) { fail = true; break; }
+      tc_fence_after();
+      const size_t row_base = static_cast<size_t>(b) * TH + tile * kTileRows;
+      const size_t part_base =
+          nsplit > 1 ? static_cast<size_t>(slot + split) * TH + tile * kTileRows : 0;
+      const int rows_here = min(kTileRows, TH - tile * kTileRows);
+#pragma unroll 1
+      for (int h2 = 0; h2 < 2 && 32 * h2 < rows_here; ++h2) {
+        float il[32];
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(&inv_l_sh[32 * h2 + j]);
+          il[j] = x.x;
+          il[j + 1] = x.y;
+          il[j + 2] = x.z;
+          il[j + 3] = x.w;
+        }
+        const int nrow = min(32, rows_here - 32 * h2);
+#pragma unroll 1
+        for (int m = 0; m < 4; ++m) {
+          const int lat = 128 * m + 32 * wq + lane;
+          uint32_t v[32];
+          tmem_ld_x32(tmem + lane_off + kTmemOut + 64 * m + 32 * h2, v);
+          tmem_wait_ld();
+          __nv_bfloat16* dst = (nsplit > 1 ? P.opart : P.olat) +
+                               ((nsplit > 1 ? part_base : row_base) + 32 * h2) * kLora + lat;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (j < nrow) dst[j * kLora] = __float2bfloat16_rn(__uint_as_float(v[j]) * il[j]);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&o_free));
+      named_bar_sync(1, 128);
+      if (owner && row_ok) {
+        const float lse2 = l > 0.0f ? m_used - kTopExp + __log2f(l) : -INFINITY;
+        if (nsplit > 1)
+          P.lpart[part_base + srow] = lse2 * kLn2;
+        else
+          P.lse[row_base + srow] = lse2 * kLn2;
+      }
+      named_bar_sync(1, 128);
+      ++n;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemAll);
+  }
+}
+
+}  // namespace
+
+// How the step spreads over the SMs: as decode.cu's, whose plan it runs on.  A
+// CTA group holds all tiles of a sequence, or gcd(tiles, SMs) of them where all
+// would leave 3 % or more of the SMs idle.
+struct Shape {
+  int tiles, tpg, sets, groups;
+};
+static Shape shape_for(int T, int H, int sm_count) {
+  Shape d;
+  d.tiles = decode_tiles(T, H);
+  const int sms = sm_count > 0 ? sm_count : 1;
+  const int idle = d.tiles <= sms ? sms % d.tiles : 0;
+  d.tpg = d.tiles;
+  if (100 * idle >= 3 * sms)
+    for (d.tpg = d.tiles; d.tiles % d.tpg || sms % d.tpg;) --d.tpg;
+  d.sets = d.tiles / d.tpg;
+  d.groups = sms / d.tpg > 0 ? sms / d.tpg : 1;
+  return d;
+}
+
+// Bytes of the query terms of B sequences: the tiles, then the rows' scales.
+size_t fp8kv_terms_bytes(int B, int T, int H) {
+  const size_t tiles = static_cast<size_t>(B) * decode_tiles(T, H);
+  return tiles * (kQTile8 + kTileRows * sizeof(float));
+}
+
+cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_c, int sm_count,
+                                const __nv_bfloat16* qlat, uint8_t* terms,
+                                const int32_t* block_table, const float* kv_scale,
+                                const int32_t* seq_len_eff, const PlanHeader* header, void* ws,
+                                const int32_t* seq_first, const int32_t* seq_nsplit,
+                                const int32_t* seq_slot, __nv_bfloat16* olat, float* lse,
+                                int32_t* status, int B, int T, int H, int max_pages,
+                                int num_pages, float scale, cudaStream_t st) {
+  Params P{};
+  const Shape shape = shape_for(T, H, sm_count);
+  P.tiles = shape.tiles;
+  float* row_scale = reinterpret_cast<float*>(terms + static_cast<size_t>(B) * P.tiles * kQTile8);
+  cudaError_t e = launch_pdl(split_q_kernel, dim3(kTileRows / (kSplitThreads / 32), B * P.tiles),
+                             dim3(kSplitThreads), 0, st, reinterpret_cast<const uint4*>(qlat),
+                             T * H, P.tiles, terms, row_scale);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(decode_fp8kv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmemBytes);
+  if (e != cudaSuccess) return e;
+  P.block_table = block_table;
+  P.kv_scale = kv_scale;
+  P.seq_len_eff = seq_len_eff;
+  P.header = header;
+  P.ws = static_cast<uint8_t*>(ws);
+  P.seq_first = seq_first;
+  P.seq_nsplit = seq_nsplit;
+  P.seq_slot = seq_slot;
+  P.terms = terms;
+  P.row_scale = row_scale;
+  P.olat = olat;
+  P.lse = lse;
+  P.status = status;
+  P.B = B;
+  P.T = T;
+  P.H = H;
+  P.max_pages = max_pages;
+  P.num_pages = num_pages;
+  P.tpg = shape.tpg;
+  P.sets = shape.sets;
+  P.scale_log2 = scale * 1.4426950408889634f;
+  return launch_pdl(decode_fp8kv_kernel, dim3(shape.groups * shape.tpg), dim3(kThreads),
+                    kSmemBytes, st, tm_c, P);
+}
+
+}  // namespace mla

@@ -1,0 +1,99 @@
+// fp8kv.cuh -- what the kernels of the 8-bit latent cache share: its layout,
+// its scales, and the PTX of 8-bit tensor-core operands.
+//
+// The cache holds a page of 64 tokens as 64 x 576 E4M3 codes ([c_kv 512 ||
+// k_pe 64] per token, as the bf16 cache) and one fp32 scale per page: a value
+// is code * scale.  E4M3 keeps four significant bits down to 2^-6, so a page
+// whose largest value takes the top of the range (448) holds values to 2^-15
+// of it at full precision, and one scale for the block of 64 tokens loses
+// nothing against finer ones.  The scales that the library writes are powers
+// of two: scaling and rescaling are then exact, and a code depends only on the
+// value and the scale, not on how a quotient was rounded.
+#pragma once
+#include <cstdint>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "ptx.cuh"
+
+namespace mla {
+
+constexpr int kPageBytes8 = kPage * kDqk;  // one page of codes: 36,864 bytes
+// Exponents of a page's scale.  bf16 latents of practical size lie far inside;
+// the bound keeps every product of the attention step in fp32's range.
+constexpr int kScaleExpMin = -32;
+constexpr int kScaleExpMax = 32;
+
+// The query's two E4M3 terms (attention step): q = scale * (hi + mid / 16).
+constexpr float kQMidScale = 16.0f;
+// One tile of query terms: five 128-byte-wide boxes (the last half empty) of
+// 128 rows: rows 32 w + i and 32 w + 16 + i are the hi and mid terms of tile
+// row 16 w + i, so that the two land in TMEM lanes of the same warp.
+constexpr int kBoxes8 = 5;
+constexpr int kQTermRows = 2 * kTileRows;
+constexpr int kQBox8 = kQTermRows * 128;
+constexpr int kQTile8 = kBoxes8 * kQBox8;  // 80 KB
+
+// Exponent of the smallest power of two s with amax <= 448 s, within the
+// bounds.  amax: finite, >= 0; exact (bit operations only).
+__device__ __forceinline__ int page_scale_exp(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int k = static_cast<int>(u >> 23) - 127;  // amax = m 2^k, 1 <= m < 2 (normal numbers)
+  const int e = k - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // 448 = 1.75 * 2^8
+  return max(kScaleExpMin, min(kScaleExpMax, e));
+}
+__device__ __forceinline__ float exp2_int(int e) {
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Four values to four E4M3 codes, round to nearest even, finite values beyond
+// 448 (infinities too) saturated; NaN keeps NaN's code.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
+}
+// Two E4M3 codes (low 16 bits) to fp32, exact.
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
+  return __half22float2(static_cast<__half2>(__nv_cvt_fp8x2_to_halfraw2(
+      static_cast<__nv_fp8x2_storage_t>(codes & 0xffffu), __NV_E4M3)));
+}
+
+// Records the first device-side error, where the caller asked for it.
+__device__ __forceinline__ void record_status(int32_t* status, int code) {
+  if (status) atomicCAS(status, 0, code);
+}
+
+// Instruction descriptor for kind::f8f6f4 with fp32 accumulation.  Formats: 0
+// E4M3, 1 E5M2; a_mn / b_mn select MN-major (transposed) operands.
+__host__ __device__ constexpr uint32_t idesc_f8_f32(int M, int N, uint32_t a_fmt, uint32_t b_fmt,
+                                                    bool a_mn, bool b_mn) {
+  return (1u << 4) | (a_fmt << 7) | (b_fmt << 10) | ((a_mn ? 1u : 0u) << 15) |
+         ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+// D[tmem] (+)= A[smem] * B[smem]^T of 8-bit operands (K = 32), one thread.
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Bulk copy of `bytes` from global to shared memory, completing on an
+// mbarrier; both addresses and the size are multiples of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
+}  // namespace mla
