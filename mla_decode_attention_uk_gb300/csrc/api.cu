@@ -72,9 +72,10 @@ cudaError_t launch_page_keys(const void* cache, const float* kv_scale,
                              const int32_t* block_table, const int32_t* seq_lens, int max_new,
                              const int32_t* new_lens, int B, int num_pages, int max_pages,
                              __nv_bfloat16* keys, int32_t* status, cudaStream_t st);
-cudaError_t launch_score(const void* query, const void* page_keys, const int32_t* block_table,
-                         const int32_t* seq_lens, int B, int T, int H, int num_pages,
-                         int max_pages, float* scores, int32_t* status, cudaStream_t st);
+cudaError_t launch_score(const CUtensorMap& tm_q, const void* page_keys,
+                         const int32_t* block_table, const int32_t* seq_lens, int B, int T, int H,
+                         int num_pages, int max_pages, float* scores, int32_t* status,
+                         cudaStream_t st);
 cudaError_t launch_select(const float* scores, const int32_t* block_table,
                           const int32_t* seq_lens, int B, int T, int max_pages, int top_k,
                           int keep_first, int keep_last, int32_t* sel_table, int32_t* sel_pages,
@@ -782,7 +783,11 @@ int mla_decode_score_pages(const mla_decode_dims* d, const void* query, const vo
       !aligned4(block_table) || !seq_lens || !aligned4(seq_lens) || !scores ||
       !aligned4(scores) || !aligned4(status))
     return MLA_DECODE_INVALID_ARG;
-  return cuda_rc(launch_score(query, page_keys, block_table, seq_lens, d->batch, d->q_len,
+  CUtensorMap tm_q;
+  if (!make_map(&tm_q, query, static_cast<uint64_t>(d->batch) * d->q_len * d->num_heads, kDqk,
+                kDqk, kBoxCols, d->num_heads, false))
+    return MLA_DECODE_CUDA_ERROR;
+  return cuda_rc(launch_score(tm_q, page_keys, block_table, seq_lens, d->batch, d->q_len,
                               d->num_heads, d->num_pages, d->max_pages_per_seq, scores, status,
                               static_cast<cudaStream_t>(stream)));
 }

@@ -7,6 +7,7 @@
 // The selection is a block table and lengths of its own, one line per query
 // token: the decode step then runs on it as on any batch of sequences with one
 // query token each.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -27,104 +28,185 @@ __device__ __forceinline__ int clamp_len(int L, int T, int cap, bool report, int
   return L;
 }
 
-// D += A B on the warp-level tensor pipe: 16 pages x 8 heads x 16 columns.
-__device__ __forceinline__ void mma_16x8x16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                            uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+// ---------------------------------------------------------------- scores
+// One CTA scores kScorePages pages for one query token: D[page, head] = K Q^T
+// on tcgen05, M = 128 pages, N = H heads, over 576 columns in nine stages of
+// 64.  With the pages as TMEM lanes the maximum over the heads is one thread's
+// own.  Page keys lie scattered through the pool, so threads gather them row by
+// row (16-byte asynchronous copies, eight threads to a 128-byte piece of a row)
+// into the swizzled layout that the tensor core reads; the queries come by TMA.
+// Every stage is in flight at once where shared memory holds all nine (H <= 64),
+// the first seven or eight else.
+constexpr int kScoreThreads = 160;            // warps 0-3 gather and reduce, 4 drives
+constexpr int kGatherThreads = 128;
+constexpr int kScorePages = 128;
+constexpr int kScoreABytes = kScorePages * 128;  // 128 pages x 64 columns: 16 KB
+constexpr int kScoreSmemMax = 224 * 1024;
+
+__host__ __device__ constexpr int score_stage_bytes(int H) { return kScoreABytes + H * 128; }
+__host__ __device__ constexpr int score_stages(int H) {
+  const int n = kScoreSmemMax / score_stage_bytes(H);
+  return n < kBoxes ? n : kBoxes;
 }
 
-constexpr int kScoreThreads = 128;
-constexpr int kScorePages = 64;               // 16 per warp
-constexpr int kScoreRows = 16;                // query rows staged at a time
-constexpr int kScoreStride = kDqk * 2 + 64;   // bytes; odd multiple of 64: no bank conflicts
-constexpr int kSteps = kDqk / 32;             // 32 columns (16 bytes per thread) at a time
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
 
 __global__ void __launch_bounds__(kScoreThreads)
-score_kernel(const uint4* __restrict__ query, const uint4* __restrict__ keys,
+score_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t* __restrict__ keys,
              const int32_t* __restrict__ block_table, const int32_t* __restrict__ seq_lens,
              int T, int H, int num_pages, int max_pages, float* __restrict__ scores,
              int32_t* __restrict__ status) {
-  __shared__ __align__(16) uint8_t q_sh[kScoreRows * kScoreStride];
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[kBoxes], free_[kBoxes], done;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh, timeout_sh;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.z, t = blockIdx.y, page0 = blockIdx.x * kScorePages;
+  const int stages = score_stages(H);
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t stage_bytes = score_stage_bytes(H);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kBoxes; ++i) {
+      mbar_init(smem_u32(&full[i]), kGatherThreads + 1);
+      mbar_init(smem_u32(&free_[i]), 1);
+    }
+    mbar_init(smem_u32(&done), 1);
+    abort_sh = timeout_sh = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_q);
+  }
   griddep_wait();
   griddep_launch_dependents();
-  const int b = blockIdx.y;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int L = clamp_len(seq_lens[b], T, max_pages * kPage, threadIdx.x == 0 && blockIdx.x == 0,
-                          status);
-  const int page0 = blockIdx.x * kScorePages;
-  const int held = (L + kPage - 1) / kPage;  // pages in use
-  if (page0 >= held) {
-    for (int i = threadIdx.x; i < T * kScorePages; i += kScoreThreads) {
-      const int t = i / kScorePages, j = page0 + i % kScorePages;
-      if (j < max_pages) scores[(static_cast<size_t>(b) * T + t) * max_pages + j] = -INFINITY;
-    }
+  const int L = clamp_len(seq_lens[b], T, max_pages * kPage,
+                          threadIdx.x == 0 && t == 0 && page0 == 0, status);
+  const int seen = (L - T + t + kPage) / kPage;  // pages that query t sees
+  float* const out = scores + (static_cast<size_t>(b) * T + t) * max_pages;
+  if (page0 >= seen) {  // the whole CTA: nothing to compute
+    const int j = page0 + threadIdx.x;
+    if (threadIdx.x < kScorePages && j < max_pages) out[j] = -INFINITY;
     return;
   }
-  // This warp's 16 page keys stay in registers: thread (g, c) holds columns
-  // 32 k + 8 c .. + 7 of pages g and g + 8 for every k.  (The order of the
-  // columns inside a product does not matter as long as queries use the same.)
-  const int g = lane >> 2, c = lane & 3;
-  uint32_t a[kSteps][2][4];
-  {
-    int row[2];
+  if (warp == 4) {
+    tmem_alloc(smem_u32(&tmem_base_sh), 128);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  bool ok = true;
+  if (warp < 4) {
+    // Thread (row group, chunk): 16-byte chunk `chunk` of rows rg, rg + 16, ...
+    const int chunk = threadIdx.x & 7, rg = threadIdx.x >> 3;
+    const uint8_t* src[8];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int j = page0 + 16 * warp + g + 8 * r;
-      int p = j < held ? block_table[static_cast<size_t>(b) * max_pages + j] : 0;
+    for (int i = 0; i < 8; ++i) {
+      const int j = page0 + rg + 16 * i;
+      int p = j < seen ? block_table[static_cast<size_t>(b) * max_pages + j] : 0;
       if (p < 0 || p >= num_pages) {
         record_status(status, MLA_STATUS_BOUNDS);
         p = 0;
       }
-      row[r] = p;
+      src[i] = keys + static_cast<size_t>(p) * (kDqk * 2) + chunk * 16;
     }
+    const uint32_t at = rg * 128 + ((chunk ^ (rg & 7)) << 4);  // (rows 16 apart share it)
+    auto copy = [&](int k) {
+      const uint32_t dst = base + (k % stages) * stage_bytes + at;
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      const uint4 x = keys[static_cast<size_t>(row[0]) * (kDqk / 8) + 4 * k + c];
-      const uint4 y = keys[static_cast<size_t>(row[1]) * (kDqk / 8) + 4 * k + c];
-      a[k][0][0] = x.x; a[k][0][1] = y.x; a[k][0][2] = x.y; a[k][0][3] = y.y;
-      a[k][1][0] = x.z; a[k][1][1] = y.z; a[k][1][2] = x.w; a[k][1][3] = y.w;
+      for (int i = 0; i < 8; ++i)
+        cp_async16(dst + i * 16 * 128, src[i] + k * 128);
+    };
+#pragma unroll
+    for (int k = 0; k < kBoxes; ++k) {
+      if (k < stages) copy(k);
+      cp_async_commit();
     }
-  }
-  for (int t = 0; t < T; ++t) {
-    float top[2] = {-INFINITY, -INFINITY};
-    for (int h0 = 0; h0 < H; h0 += kScoreRows) {
-      __syncthreads();
-      const uint4* src =
-          query + (static_cast<size_t>(b) * T * H + static_cast<size_t>(t) * H + h0) * (kDqk / 8);
-      for (int i = threadIdx.x; i < kScoreRows * (kDqk / 8); i += kScoreThreads)
-        *reinterpret_cast<uint4*>(q_sh + (i / (kDqk / 8)) * kScoreStride + (i % (kDqk / 8)) * 16) =
-            src[i];
-      __syncthreads();
+    // Group k is complete once at most kBoxes - 1 - k younger ones are not.
+    auto landed = [&](int k) {
+      fence_proxy_async_smem();
+      mbar_arrive(smem_u32(&full[k]));
+    };
+    cp_async_wait<8>(); landed(0);
+    cp_async_wait<7>(); landed(1);
+    cp_async_wait<6>(); landed(2);
+    cp_async_wait<5>(); landed(3);
+    cp_async_wait<4>(); landed(4);
+    cp_async_wait<3>(); landed(5);
+    cp_async_wait<2>(); landed(6);  // (seven stages at least, at H = 128)
+    if (stages > 7) { cp_async_wait<1>(); landed(7); }
+    if (stages > 8) { cp_async_wait<0>(); landed(8); }
+    for (int k = stages; k < kBoxes && ok; ++k) {
+      ok = mbar_wait(smem_u32(&free_[k - stages]), 0, &abort_sh, &timeout_sh);
+      if (!ok) break;
+      copy(k);
+      cp_async_commit();
+    }
+    cp_async_wait<0>();
+    for (int k = stages; k < kBoxes && ok; ++k) landed(k);
+    ok = ok && mbar_wait(smem_u32(&done), 0, &abort_sh, &timeout_sh);
+    if (__all_sync(0xffffffffu, ok)) {
+      tc_fence_after();
+      float top = -INFINITY;
+      for (int h = 0; h < H; h += 16) {
+        uint32_t v[16];
+        tmem_ld_x16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + h, v);
+        tmem_wait_ld();
 #pragma unroll
-      for (int n = 0; n < kScoreRows / 8; ++n) {
-        float d[4] = {};
-        const uint8_t* q = q_sh + (8 * n + g) * kScoreStride + c * 16;
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+      }
+      const int j = page0 + threadIdx.x;
+      if (j < max_pages) out[j] = j < seen ? top : -INFINITY;
+    }
+  } else if (elect_one()) {
+    // One thread brings the queries and issues the MMAs.
+    const int row = (b * T + t) * H;
+    auto load = [&](int k) {
+      const uint32_t dst = base + (k % stages) * stage_bytes + kScoreABytes;
+      mbar_expect_tx(smem_u32(&full[k]), H * 128);
+      tma_load_2d(dst, &tm_q, k * kBoxCols, row, smem_u32(&full[k]));
+    };
+    int loaded = 0;
+    for (; loaded < stages; ++loaded) load(loaded);
+    const uint32_t idesc = idesc_bf16_f32(kScorePages, H, false, false);
+    for (int k = 0; k < kBoxes && ok; ++k) {
+      ok = mbar_wait(smem_u32(&full[k]), 0, &abort_sh, &timeout_sh);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t a = base + (k % stages) * stage_bytes;
+      const uint64_t da = sdesc_sw128(a, 16, 1024), dq = sdesc_sw128(a + kScoreABytes, 16, 1024);
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          const uint4 v = *reinterpret_cast<const uint4*>(q + 64 * k);
-          mma_16x8x16(d, a[k][0], v.x, v.y);
-          mma_16x8x16(d, a[k][1], v.z, v.w);
-        }
-        top[0] = fmaxf(top[0], fmaxf(d[0], d[1]));
-        top[1] = fmaxf(top[1], fmaxf(d[2], d[3]));
+      for (int kk = 0; kk < 4; ++kk) umma_bf16(tmem, da + 2 * kk, dq + 2 * kk, idesc, k | kk);
+      umma_commit(smem_u32(&free_[k]));
+      if (k + stages < kBoxes) {
+        ok = mbar_wait(smem_u32(&free_[k]), 0, &abort_sh, &timeout_sh);
+        if (ok) load(loaded++);
       }
     }
-    const int seen = (L - T + t + kPage) / kPage;  // pages that query t sees
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-      top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-      const int j = page0 + 16 * warp + g + 8 * r;
-      if (c == 0 && j < max_pages)
-        scores[(static_cast<size_t>(b) * T + t) * max_pages + j] = j < seen ? top[r] : -INFINITY;
-    }
+    umma_commit(smem_u32(&done));
+    // Nothing is in flight when the CTA ends, after a timeout either.
+    mbar_wait_drain(smem_u32(&done), 0, &timeout_sh);
+    if (!ok)
+      for (int k = 0; k < loaded; ++k) mbar_wait_drain(smem_u32(&full[k]), 0, &timeout_sh);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 128);
+    if (lane == 0 && timeout_sh) record_status(status, MLA_STATUS_TIMEOUT);
   }
 }
 
+// ---------------------------------------------------------------- selection
 constexpr int kSelThreads = 256;
 
 // Keys in the order of the scores: larger is better, NaN below everything,
@@ -247,13 +329,18 @@ select_kernel(const float* __restrict__ scores, const int32_t* __restrict__ bloc
 
 }  // namespace
 
-cudaError_t launch_score(const void* query, const void* page_keys, const int32_t* block_table,
-                         const int32_t* seq_lens, int B, int T, int H, int num_pages,
-                         int max_pages, float* scores, int32_t* status, cudaStream_t st) {
-  const dim3 grid((max_pages + kScorePages - 1) / kScorePages, B);
-  return launch_pdl(score_kernel, grid, dim3(kScoreThreads), 0, st,
-                    static_cast<const uint4*>(query), static_cast<const uint4*>(page_keys),
-                    block_table, seq_lens, T, H, num_pages, max_pages, scores, status);
+cudaError_t launch_score(const CUtensorMap& tm_q, const void* page_keys,
+                         const int32_t* block_table, const int32_t* seq_lens, int B, int T, int H,
+                         int num_pages, int max_pages, float* scores, int32_t* status,
+                         cudaStream_t st) {
+  const int smem = 1024 + score_stages(H) * score_stage_bytes(H);
+  const cudaError_t e =
+      cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((max_pages + kScorePages - 1) / kScorePages, T, B);
+  return launch_pdl(score_kernel, grid, dim3(kScoreThreads), smem, st, tm_q,
+                    static_cast<const uint8_t*>(page_keys), block_table, seq_lens, T, H,
+                    num_pages, max_pages, scores, status);
 }
 
 cudaError_t launch_select(const float* scores, const int32_t* block_table,
