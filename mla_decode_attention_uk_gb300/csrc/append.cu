@@ -40,8 +40,13 @@ __device__ __forceinline__ float finite_max2(float top, uint32_t w) {
   return fmaxf(top, __uint_as_float(m << 16));
 }
 
-// One CTA per (sequence, page that receives new tokens).
-__global__ void __launch_bounds__(kAppThreads)
+// One CTA per (sequence, page that receives new tokens).  The new rows are read
+// once, into registers (a full page: 18 16-byte loads per thread, all in
+// flight), so that their maximum, hence the scale, is known before any code is
+// formed.
+constexpr int kPerThread = kPage * kChunks / kAppThreads;  // 18
+
+__global__ void __launch_bounds__(kAppThreads, 2)
 append_kernel(const uint4* __restrict__ rows, int max_new, const int32_t* __restrict__ new_lens,
               const int32_t* __restrict__ block_table, const int32_t* __restrict__ seq_lens,
               int num_pages, int max_pages, uint8_t* __restrict__ kv8,
@@ -65,52 +70,56 @@ append_kernel(const uint4* __restrict__ rows, int max_new, const int32_t* __rest
   const int n = (r1 - r0) * kChunks;
   const uint4* src =
       rows + (static_cast<size_t>(b) * max_new + (logical * kPage + r0 - nt.first)) * kChunks;
+  uint4 v[kPerThread];
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k) {
+    const int i = threadIdx.x + k * kAppThreads;
+    v[k] = i < n ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+  }
   // Read before the barrier below: one thread replaces it at the end.
   const float old = r0 > 0 ? kv_scale[page] : 0.0f;
   float top = 0.0f;
-  for (int i = threadIdx.x; i < n; i += kAppThreads) {
-    const uint4 v = src[i];
-    top = finite_max2(finite_max2(finite_max2(finite_max2(top, v.x), v.y), v.z), v.w);
-  }
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k)
+    top = finite_max2(finite_max2(finite_max2(finite_max2(top, v[k].x), v[k].y), v[k].z), v[k].w);
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
   __syncthreads();
   for (int w = 0; w < kAppThreads / 32; ++w) top = fmaxf(top, warp_top[w]);
   float scale = exp2_int(page_scale_exp(top));
-  uint8_t* const dst = kv8 + static_cast<size_t>(page) * kPageBytes8;
   if (r0 > 0) scale = fmaxf(scale, old);
-  // Rows that stay: cleared in a page that starts here, re-coded if the scale
-  // grew.
-  if (r0 == 0 || scale != old) {
-    const float ratio = old / scale;
-    uint2* const d = reinterpret_cast<uint2*>(dst);
-    for (int i = threadIdx.x; i < kPage * kChunks; i += kAppThreads) {
-      const int r = i / kChunks;
-      if (r >= r0 && r < r1) continue;
-      uint2 c = make_uint2(0u, 0u);
-      if (r0 > 0) {
-        c = d[i];
-        uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float2 p = e4m3x2_to_float2(w[k]), q = e4m3x2_to_float2(w[k] >> 16);
-          w[k] = e4m3x4(p.x * ratio, p.y * ratio, q.x * ratio, q.y * ratio);
-        }
-        c = make_uint2(w[0], w[1]);
-      }
-      d[i] = c;
-    }
-  }
+  uint2* const dst = reinterpret_cast<uint2*>(kv8 + static_cast<size_t>(page) * kPageBytes8);
   const float inv = 1.0f / scale;  // exact: a power of two
-  uint2* const d = reinterpret_cast<uint2*>(dst + r0 * kDqk);
-  for (int i = threadIdx.x; i < n; i += kAppThreads) {
-    const uint4 v = src[i];
-    d[i] = make_uint2(e4m3x4(bf16_lo(v.x) * inv, bf16_hi(v.x) * inv, bf16_lo(v.y) * inv,
-                             bf16_hi(v.y) * inv),
-                      e4m3x4(bf16_lo(v.z) * inv, bf16_hi(v.z) * inv, bf16_lo(v.w) * inv,
-                             bf16_hi(v.w) * inv));
+#pragma unroll
+  for (int k = 0; k < kPerThread; ++k) {
+    const int i = threadIdx.x + k * kAppThreads;
+    if (i < n)
+      dst[r0 * kChunks + i] =
+          make_uint2(e4m3x4(bf16_lo(v[k].x) * inv, bf16_hi(v[k].x) * inv, bf16_lo(v[k].y) * inv,
+                            bf16_hi(v[k].y) * inv),
+                     e4m3x4(bf16_lo(v[k].z) * inv, bf16_hi(v[k].z) * inv, bf16_lo(v[k].w) * inv,
+                            bf16_hi(v[k].w) * inv));
   }
   if (threadIdx.x == 0) kv_scale[page] = scale;
+  // Rows that stay: cleared in a page that starts here, re-coded if the scale
+  // grew.
+  if (r0 > 0 && scale == old) return;
+  const float ratio = old / scale;
+  for (int i = threadIdx.x; i < kPage * kChunks; i += kAppThreads) {
+    if (i >= r0 * kChunks && i < r1 * kChunks) continue;
+    uint2 c = make_uint2(0u, 0u);
+    if (r0 > 0) {
+      c = dst[i];
+      uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 p = e4m3x2_to_float2(w[k]), q = e4m3x2_to_float2(w[k] >> 16);
+        w[k] = e4m3x4(p.x * ratio, p.y * ratio, q.x * ratio, q.y * ratio);
+      }
+      c = make_uint2(w[0], w[1]);
+    }
+    dst[i] = c;
+  }
 }
 
 constexpr int kKeyThreads = 288;

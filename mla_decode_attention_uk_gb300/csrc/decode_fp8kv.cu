@@ -32,8 +32,10 @@
 // stays in TMEM.  The page's scale joins the exponent (p_j s = 2^(x_j + log2 s
 // - m), m the running maximum of that sum), so that P never leaves E5M2's
 // range however the scales of a sequence's pages differ.
-// Warp roles: 0 TMA producer, 1 QK^T issuer, 2 TMEM, 3 and 8 PV issuers (latent
-// halves), 4-7 softmax and epilogue.  (QK^T has one issuer: two that took turns
+// Warp roles: 0 TMA producer, 1 QK^T issuer, 2 and 3 PV issuers (latent halves;
+// warp 2 also owns TMEM), 4-11 softmax and epilogue, two warps to the rows of a
+// TMEM lane quarter, each with half of a page's keys (one warp each: 2,800
+// cycles a page whatever the heads, its 64 exponentials' chain).  (QK^T has one issuer: two that took turns
 // would each see only every second phase of a slot's barriers.)
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -116,7 +118,8 @@ split_q_kernel(const uint4* __restrict__ qlat, int TH, int tiles, uint8_t* __res
 }
 
 // ---------------------------------------------------------------- attention
-constexpr int kThreads = 288;                     // 9 warps
+constexpr int kThreads = 384;                     // 12 warps
+constexpr int kSoftThreads = 256;                 // of them softmax and epilogue
 constexpr int kBox = kPage * 128;                 // 64 keys x 128 codes: 8 KB
 constexpr int kSlot = kBoxes8 * kBox;             // 40 KB (the last box half empty)
 constexpr int kSlots = 3;
@@ -241,8 +244,8 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
   __shared__ float page_scale_sh[kSlots];
-  __shared__ float alpha_sh[kTileRows];
-  __shared__ __align__(16) float inv_l_sh[kTileRows];
+  __shared__ float alpha_sh[2][kTileRows], max_sh[2][2][kTileRows];
+  __shared__ float l_sh[2][kTileRows], l_r_sh[2][kTileRows];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Tasks v = range * sets + set are dealt round robin to groups of tpg CTAs;
@@ -261,15 +264,15 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
         mbar_init(smem_u32(&slot_full[i][j]), 1);
         mbar_init(smem_u32(&slot_free[i][j]), j == kRopeBox8 ? 2 : 1);
       }
-      mbar_init(smem_u32(&p_full[i]), 1);
+      mbar_init(smem_u32(&p_full[i]), kSoftThreads / 32);
       mbar_init(smem_u32(&p_free[i]), 2);
     }
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&s_free[i]), 4);
+      mbar_init(smem_u32(&s_free[i]), kSoftThreads / 32);
     }
     mbar_init(smem_u32(&o_full), 2);
-    mbar_init(smem_u32(&o_free), 4);
+    mbar_init(smem_u32(&o_free), kSoftThreads / 32);
     for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&drain_bar[i]), 1);
     abort_sh = 0;
     fence_mbar_init();
@@ -370,7 +373,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
             mbar_wait_drain(smem_u32(&slot_full[s][j]), (k - 1) & 1, P.status);
       }
     }
-  } else if (warp == 1 || warp == 3 || warp == 8) {
+  } else if (warp < 4) {
     // ------------------------------------------------------------ MMA issuers
     if (elect_one()) {
       const uint64_t dq0 = sdesc_sw128(sQ, 16, 1024);
@@ -412,7 +415,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
           ++n;
         }
       } else {
-        const int half = warp == 3 ? 0 : 1;
+        const int half = warp - 2;
         while (ok && walk.next(P, pc)) {
           const int tile = (pc.task % sets) * tpg + ti;
           const int nrows = min(kTileRows, (TH - tile * kTileRows + 15) & ~15);
@@ -446,13 +449,15 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
           ++n;
         }
       }
-      const uint32_t db = smem_u32(&drain_bar[warp == 1 ? 0 : (warp == 3 ? 1 : 2)]);
+      const uint32_t db = smem_u32(&drain_bar[warp - 1]);
       umma_commit(db);
       mbar_wait_drain(db, 0, P.status);
     }
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------ softmax + epilogue
-    const int wq = warp - 4;  // TMEM lane quarter
+    // Warps 4 + w and 8 + w share the rows of TMEM lane quarter w; `half` of them
+    // takes keys 16 half .. + 15 and 32 + 16 half .. + 15 of every page.
+    const int wq = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     // This thread: row srow of the tile (its hi term in lane rig of the
     // quarter, its mid term in lane 16 + rig), keys of parity par.
@@ -475,157 +480,157 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
           P.row_scale[(static_cast<size_t>(b) * P.tiles + tile) * kTileRows + srow] * P.scale_log2;
       const int n_row = row_ok ? pc.len - P.T + r / P.H + 1 : 0;
       float m_used = -INFINITY;
-      float l = 0.0f, l_r = 0.0f;  // this thread's halves of the row's sums: exact, as rounded
+      float l = 0.0f, l_r = 0.0f;  // this thread's shares of the row's sums: exact, as rounded
       for (int i = pc.pbeg; i < pc.pend; ++i, ++g) {
         const int sb = g % kSBufs, s = g % kSlots;
-        bool need = false;
         // (The slot's first box is complete long before; its barrier orders
         // the producer's page_scale_sh.)
         bool bad = !mbar_wait(smem_u32(&slot_full[s][0]), (g / kSlots) & 1, &abort_sh, P.status) ||
                    !mbar_wait(smem_u32(&s_full[sb]), (g / kSBufs) & 1, &abort_sh, P.status);
         bad = __any_sync(0xffffffffu, bad);
         const float page_scale = *static_cast<volatile float*>(&page_scale_sh[s]);
-        uint32_t v[32];
+        uint32_t v[16];  // v[j]: key kb + 2 j, from j = 8 on kb + 16 + 2 j
         if (!bad) {
           tc_fence_after();
-          uint32_t v2[32];
-          tmem_ld_16x64b_x32(tmem + lane_off + 64 * sb, v);
-          tmem_ld_16x64b_x32(tmem + lane_off + (16u << 16) + 64 * sb, v2);
+          uint32_t v2[16];
+          const uint32_t ta = tmem + lane_off + 64 * sb + 16 * half;
+          tmem_ld_16x64b_x8(ta, v);
+          tmem_ld_16x64b_x8(ta + 32, v + 8);
+          tmem_ld_16x64b_x8(ta + (16u << 16), v2);
+          tmem_ld_16x64b_x8(ta + (16u << 16) + 32, v2 + 8);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
+          for (int j = 0; j < 16; ++j)
             v[j] = __float_as_uint(
                 fmaf(__uint_as_float(v2[j]), 1.0f / kQMidScale, __uint_as_float(v[j])));
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s_free[sb]));
-        if (!bad) {
-          const int kb = i * kPage + par;  // key of v[0]; v[j] is key kb + 2 j
-          if (kb + 62 >= n_row) {
+        const int kb = i * kPage + 16 * half + par;
+        if (kb + 32 + 14 >= n_row) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (kb + 2 * j >= n_row) v[j] = __float_as_uint(-INFINITY);
-          }
-          float a3[11];
-#pragma unroll
-          for (int t = 0; t < 10; ++t)
-            a3[t] = max3(__uint_as_float(v[3 * t]), __uint_as_float(v[3 * t + 1]),
-                         __uint_as_float(v[3 * t + 2]));
-          a3[10] = fmaxf(__uint_as_float(v[30]), __uint_as_float(v[31]));
-          float vmax = fmaxf(max3(max3(a3[0], a3[1], a3[2]), max3(a3[3], a3[4], a3[5]),
-                                  max3(a3[6], a3[7], a3[8])),
-                             fmaxf(a3[9], a3[10]));
-          vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
-          // Not zero, so that a hidden key's -inf times it stays -inf (a
-          // product below 2^-100 is 0 to the exponent either way).
-          const float mul = fmaxf(q_scale * page_scale, 7.9e-31f);
-          const float shift = __log2f(page_scale);
-          const float pmax = fmaf(vmax, mul, shift);
-          float alpha = 1.0f;
-          if (pmax > m_used + kRaise) {
-            alpha = m_used == -INFINITY ? 0.0f : ex2_approx(m_used - pmax);
-            m_used = pmax;
-            need = i > pc.pbeg;
-          }
-          __half2 hi[16], mid[16];
-          float sum = 0.0f, sum_r = 0.0f;
-          if (m_used == -INFINITY) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) hi[j] = mid[j] = __float2half2_rn(0.0f);
-          } else {
-            const float add = shift + kTopExp - m_used;
-            float se[4] = {};
-            __half2 err = __float2half2_rn(0.0f);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float p0 = ex2_approx(fmaf(__uint_as_float(v[2 * j]), mul, add));
-              const float p1 = ex2_approx(fmaf(__uint_as_float(v[2 * j + 1]), mul, add));
-              se[(2 * j) & 3] += p0;
-              se[(2 * j + 1) & 3] += p1;
-              const __half2 h = __floats2half2_rn(p0, p1);
-              hi[j] = e5m2_in_half2(h);
-              mid[j] = e5m2_in_half2(__hsub2(h, hi[j]));
-              err = __hfma2(__hsub2(__hadd2(hi[j], mid[j]), h),
-                            __hge2(h, __float2half2_rn(kRoundedFrom)), err);
-            }
-            sum = (se[0] + se[1]) + (se[2] + se[3]);
-            const float2 e = __half22float2(err);
-            sum_r = sum + (e.x + e.y);
-          }
-          const float inv_scale = __frcp_rn(page_scale);
-          l = fmaf(sum, inv_scale, l * alpha);
-          l_r = fmaf(sum_r, inv_scale, l_r * alpha);
-          if (owner) alpha_sh[srow] = alpha;
-          // The codes are the upper bytes.  The even-key thread writes keys
-          // 0-31, the odd-key thread keys 32-63: half of each thread's codes
-          // cross to its partner, four to a word.
-          uint32_t hw[8], mw[8];
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            hw[t] = __byte_perm(bits(hi[2 * t]), bits(hi[2 * t + 1]), 0x7531);
-            mw[t] = __byte_perm(bits(mid[2 * t]), bits(mid[2 * t + 1]), 0x7531);
-          }
-          uint32_t ph[8], pm[8];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint32_t keep_h = par ? hw[4 + t] : hw[t], keep_m = par ? mw[4 + t] : mw[t];
-            const uint32_t got_h =
-                __shfl_xor_sync(0xffffffffu, par ? hw[t] : hw[4 + t], 2);
-            const uint32_t got_m =
-                __shfl_xor_sync(0xffffffffu, par ? mw[t] : mw[4 + t], 2);
-            const uint32_t eh = par ? got_h : keep_h, oh = par ? keep_h : got_h;
-            const uint32_t em = par ? got_m : keep_m, om = par ? keep_m : got_m;
-            ph[2 * t] = __byte_perm(eh, oh, 0x5140);
-            ph[2 * t + 1] = __byte_perm(eh, oh, 0x7362);
-            pm[2 * t] = __byte_perm(em, om, 0x5140);
-            pm[2 * t + 1] = __byte_perm(em, om, 0x7362);
-          }
-          // P^T row: 64 bytes of hi codes (chunks 0-3), 64 of mid codes (4-7),
-          // into the page's RoPE box, which QK^T is done with.  Rows r and
-          // r + 8 of a quarter-warp's store share their swizzle, so the
-          // latter's threads write mid before hi: eight distinct positions.
-          const uint32_t rowaddr = sSlot0 + s * kSlot + kRopeBox8 * kBox + srow * 128;
-          const bool late = (srow >> 3) & 1;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int h4 = 4 * (q & 1);
-            const bool is_mid = (q >= 2) != late;
-            const int chunk = (is_mid ? 4 : 0) + 2 * par + (q & 1);
-            st_shared_v4(rowaddr + ((chunk ^ (srow & 7)) << 4), is_mid ? pm[h4] : ph[h4],
-                         is_mid ? pm[h4 + 1] : ph[h4 + 1], is_mid ? pm[h4 + 2] : ph[h4 + 2],
-                         is_mid ? pm[h4 + 3] : ph[h4 + 3]);
-          }
-          fence_proxy_async_smem();
+          for (int j = 0; j < 16; ++j)
+            if (kb + 2 * j + (j < 8 ? 0 : 16) >= n_row) v[j] = __float_as_uint(-INFINITY);
         }
-        // One barrier per page: a timeout anywhere, or a raised maximum.
-        if (bar_any(1, 128, bad || need)) {
+        float a3[5];
+#pragma unroll
+        for (int t = 0; t < 5; ++t)
+          a3[t] = max3(__uint_as_float(v[3 * t]), __uint_as_float(v[3 * t + 1]),
+                       __uint_as_float(v[3 * t + 2]));
+        float vmax = max3(max3(a3[0], a3[1], a3[2]), max3(a3[3], a3[4], __uint_as_float(v[15])),
+                          -INFINITY);
+        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+        // Not zero, so that a hidden key's -inf times it stays -inf (a
+        // product below 2^-100 is 0 to the exponent either way).
+        const float mul = fmaxf(q_scale * page_scale, 7.9e-31f);
+        const float shift = __log2f(page_scale);
+        const float pmax = fmaf(vmax, mul, shift);
+        if (owner) max_sh[g & 1][half][srow] = pmax;
+        // One barrier per page: does any row's maximum pass the one in use by
+        // enough, or has a wait given up?  Only then do the halves exchange
+        // their maxima (the arrays alternate: a warp may be a page ahead).
+        if (bar_any(1, kSoftThreads, bad || pmax > m_used + kRaise)) {
           bool f = *static_cast<volatile int*>(&abort_sh) != 0;
-          if (!f && g >= 1 &&
+          const float both = fmaxf(pmax, max_sh[g & 1][half ^ 1][srow]);
+          float alpha = 1.0f;
+          if (both > m_used + kRaise) {
+            alpha = m_used == -INFINITY ? 0.0f : ex2_approx(m_used - both);
+            m_used = both;
+          }
+          l *= alpha;
+          l_r *= alpha;
+          if (owner && half == 0) alpha_sh[g & 1][srow] = alpha;
+          if (!f && i > pc.pbeg &&
               !mbar_wait(smem_u32(&p_free[(g - 1) % kSlots]), ((g - 1) / kSlots) & 1, &abort_sh,
                          P.status))
             f = true;
-          if (bar_any(1, 128, f)) { fail = true; break; }
-          tc_fence_after();
+          if (bar_any(1, kSoftThreads, f)) { fail = true; break; }
+          if (i > pc.pbeg) {  // rescale O^T (its rows are columns), a half of it each
+            tc_fence_after();
 #pragma unroll 1
-          for (int m = 0; m < 4; ++m) {
+            for (int m = 2 * half; m < 2 * half + 2; ++m) {
 #pragma unroll 1
-            for (int h2 = 0; h2 < 2; ++h2) {
-              uint32_t vv[32];
-              const uint32_t ta = tmem + lane_off + kTmemOut + 64 * m + 32 * h2;
-              tmem_ld_x32(ta, vv);
-              tmem_wait_ld();
+              for (int h2 = 0; h2 < 2; ++h2) {
+                uint32_t vv[32];
+                const uint32_t ta = tmem + lane_off + kTmemOut + 64 * m + 32 * h2;
+                tmem_ld_x32(ta, vv);
+                tmem_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                vv[j] = __float_as_uint(__uint_as_float(vv[j]) * alpha_sh[32 * h2 + j]);
-              tmem_st_x32(ta, vv);
+                for (int j = 0; j < 32; ++j)
+                  vv[j] =
+                      __float_as_uint(__uint_as_float(vv[j]) * alpha_sh[g & 1][32 * h2 + j]);
+                tmem_st_x32(ta, vv);
+              }
             }
+            tmem_wait_st();
+            tc_fence_before();
           }
-          tmem_wait_st();
-          tc_fence_before();
-          named_bar_sync(1, 128);
         }
-        if (threadIdx.x == 128) mbar_arrive(smem_u32(&p_full[s]));
+        __half2 hi[8], mid[8];
+        if (m_used == -INFINITY) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) hi[j] = mid[j] = __float2half2_rn(0.0f);
+        } else {
+          const float add = shift + kTopExp - m_used;
+          float se[4] = {};
+          __half2 err = __float2half2_rn(0.0f);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float p0 = ex2_approx(fmaf(__uint_as_float(v[2 * j]), mul, add));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(v[2 * j + 1]), mul, add));
+            se[(2 * j) & 3] += p0;
+            se[(2 * j + 1) & 3] += p1;
+            const __half2 h = __floats2half2_rn(p0, p1);
+            hi[j] = e5m2_in_half2(h);
+            mid[j] = e5m2_in_half2(__hsub2(h, hi[j]));
+            err = __hfma2(__hsub2(__hadd2(hi[j], mid[j]), h),
+                          __hge2(h, __float2half2_rn(kRoundedFrom)), err);
+          }
+          const float sum = (se[0] + se[1]) + (se[2] + se[3]);
+          const float2 e = __half22float2(err);
+          const float inv_scale = __frcp_rn(page_scale);
+          l = fmaf(sum, inv_scale, l);
+          l_r = fmaf(sum + (e.x + e.y), inv_scale, l_r);
+        }
+        // The codes are the upper bytes, four to a word (words 0, 1: the lower
+        // 16 keys).  The even-key thread writes the lower keys, the odd-key
+        // thread the upper ones: half of each thread's codes cross over.
+        uint32_t hw[4], mw[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          hw[t] = __byte_perm(bits(hi[2 * t]), bits(hi[2 * t + 1]), 0x7531);
+          mw[t] = __byte_perm(bits(mid[2 * t]), bits(mid[2 * t + 1]), 0x7531);
+        }
+        uint32_t ph[4], pm[4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t keep_h = par ? hw[2 + t] : hw[t], keep_m = par ? mw[2 + t] : mw[t];
+          const uint32_t got_h = __shfl_xor_sync(0xffffffffu, par ? hw[t] : hw[2 + t], 2);
+          const uint32_t got_m = __shfl_xor_sync(0xffffffffu, par ? mw[t] : mw[2 + t], 2);
+          const uint32_t eh = par ? got_h : keep_h, oh = par ? keep_h : got_h;
+          const uint32_t em = par ? got_m : keep_m, om = par ? keep_m : got_m;
+          ph[2 * t] = __byte_perm(eh, oh, 0x5140);
+          ph[2 * t + 1] = __byte_perm(eh, oh, 0x7362);
+          pm[2 * t] = __byte_perm(em, om, 0x5140);
+          pm[2 * t + 1] = __byte_perm(em, om, 0x7362);
+        }
+        // P^T row: 64 bytes of hi codes (chunks 0-3), 64 of mid codes (4-7),
+        // into the page's RoPE box, which QK^T is done with.  Rows r and r + 8
+        // of a quarter-warp's store share their swizzle, so the latter's
+        // threads write mid before hi: eight distinct positions.
+        const uint32_t rowaddr = sSlot0 + s * kSlot + kRopeBox8 * kBox + srow * 128;
+        const bool late = (srow >> 3) & 1;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const bool is_mid = (q == 1) != late;
+          const int chunk = (is_mid ? 4 : 0) + 2 * par + half;
+          st_shared_v4(rowaddr + ((chunk ^ (srow & 7)) << 4), is_mid ? pm[0] : ph[0],
+                       is_mid ? pm[1] : ph[1], is_mid ? pm[2] : ph[2], is_mid ? pm[3] : ph[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[s]));
       }
       if (fail) break;
       have = walk.next(P, pc);
@@ -634,8 +639,11 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
       const bool bad = !mbar_wait(smem_u32(&o_full), n & 1, &abort_sh, P.status);
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       l_r += __shfl_xor_sync(0xffffffffu, l_r, 2);
-      if (owner) inv_l_sh[srow] = row_ok && l_r > 0.0f ? 1.0f / l_r : 0.0f;
-      if (bar_any(1, 128, bad)) { fail = true; break; }
+      if (owner) {
+        l_sh[half][srow] = l;
+        l_r_sh[half][srow] = l_r;
+      }
+      if (bar_any(1, kSoftThreads, bad)) { fail = true; break; }
       tc_fence_after();
       const size_t row_base = static_cast<size_t>(b) * TH + tile * kTileRows;
       const size_t part_base =
@@ -643,18 +651,12 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
       const int rows_here = min(kTileRows, TH - tile * kTileRows);
 #pragma unroll 1
       for (int h2 = 0; h2 < 2 && 32 * h2 < rows_here; ++h2) {
-        float il[32];
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(&inv_l_sh[32 * h2 + j]);
-          il[j] = x.x;
-          il[j + 1] = x.y;
-          il[j + 2] = x.z;
-          il[j + 3] = x.w;
-        }
+        // Lane j holds the reciprocal of row 32 h2 + j.
+        const float total = l_r_sh[0][32 * h2 + lane] + l_r_sh[1][32 * h2 + lane];
+        const float inv = total > 0.0f ? 1.0f / total : 0.0f;
         const int nrow = min(32, rows_here - 32 * h2);
 #pragma unroll 1
-        for (int m = 0; m < 4; ++m) {
+        for (int m = 2 * half; m < 2 * half + 2; ++m) {
           const int lat = 128 * m + 32 * wq + lane;
           uint32_t v[32];
           tmem_ld_x32(tmem + lane_off + kTmemOut + 64 * m + 32 * h2, v);
@@ -662,22 +664,24 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
           __nv_bfloat16* dst = (nsplit > 1 ? P.opart : P.olat) +
                                ((nsplit > 1 ? part_base : row_base) + 32 * h2) * kLora + lat;
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (j < nrow) dst[j * kLora] = __float2bfloat16_rn(__uint_as_float(v[j]) * il[j]);
+          for (int j = 0; j < 32; ++j) {
+            const float il = __shfl_sync(0xffffffffu, inv, j);
+            if (j < nrow) dst[j * kLora] = __float2bfloat16_rn(__uint_as_float(v[j]) * il);
+          }
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&o_free));
-      named_bar_sync(1, 128);
-      if (owner && row_ok) {
-        const float lse2 = l > 0.0f ? m_used - kTopExp + __log2f(l) : -INFINITY;
+      if (owner && half == 0 && row_ok) {
+        const float total = l + l_sh[1][srow];
+        const float lse2 = total > 0.0f ? m_used - kTopExp + __log2f(total) : -INFINITY;
         if (nsplit > 1)
           P.lpart[part_base + srow] = lse2 * kLn2;
         else
           P.lse[row_base + srow] = lse2 * kLn2;
       }
-      named_bar_sync(1, 128);
+      named_bar_sync(1, kSoftThreads);  // the sums are read before the next piece's
       ++n;
     }
   }
