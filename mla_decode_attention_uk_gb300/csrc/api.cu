@@ -56,7 +56,7 @@ cudaError_t launch_combine_up(const CUtensorMap& tm_wuv, int B, int T, int H, co
                               __nv_bfloat16* out, int32_t* status, int splits_per_seq,
                               const float* wuv_scale, cudaStream_t st);
 size_t fp8kv_terms_bytes(int B, int T, int H);
-cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_c, int sm_count,
+cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, int sm_count,
                                 const __nv_bfloat16* qlat, uint8_t* terms,
                                 const int32_t* block_table, const float* kv_scale,
                                 const int32_t* seq_len_eff, const PlanHeader* header, void* ws,
@@ -170,6 +170,22 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, ui
                                : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+// The latent columns of an 8-bit cache of `rows` rows as [4, rows, 128] codes
+// (a row's four 128-column chunks; the outermost stride is the smallest), box =
+// a page's 64 rows of all four, 128-byte swizzle.
+bool make_map_chunks(CUtensorMap* m, const void* base, uint64_t rows) {
+  EncodeTiledFn enc = encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {128, rows, kLora / 128};
+  cuuint64_t strides[2] = {kDqk, 128};
+  cuuint32_t box[3] = {128, kPage, kLora / 128};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
 }
 
 int cuda_rc(cudaError_t e) {
@@ -683,17 +699,19 @@ int mla_decode_attend_fp8kv(const mla_decode_dims* d, const uint8_t* kv_fp8,
   if (rc) return rc;
   if (terms_bytes < fp8kv_terms_bytes(d->batch, d->q_len, d->num_heads))
     return MLA_DECODE_WORKSPACE_TOO_SMALL;
-  // Boxes of 128 codes; the fifth's second half lies past the row and is
-  // filled with zeros.
-  CUtensorMap tm_c;
-  if (!make_map(&tm_c, kv_fp8, static_cast<uint64_t>(d->num_pages) * kPage, kDqk, kDqk, 128,
+  // A page is one copy of its latent columns, as four 128-column boxes one after
+  // the other, and one of its RoPE columns: a box of 128 whose second half lies
+  // past the row and is filled with zeros.
+  CUtensorMap tm_lat, tm_rope;
+  if (!make_map_chunks(&tm_lat, kv_fp8, static_cast<uint64_t>(d->num_pages) * kPage) ||
+      !make_map(&tm_rope, kv_fp8, static_cast<uint64_t>(d->num_pages) * kPage, kDqk, kDqk, 128,
                 kPage, true, 1))
     return MLA_DECODE_CUDA_ERROR;
   int sms = 0;
   rc = sm_count(&sms);
   if (rc) return rc;
   return cuda_rc(launch_decode_fp8kv(
-      tm_c, sms, at<__nv_bfloat16>(ws, L.qlat), static_cast<uint8_t*>(terms), block_table,
+      tm_lat, tm_rope, sms, at<__nv_bfloat16>(ws, L.qlat), static_cast<uint8_t*>(terms), block_table,
       kv_scale, at<int32_t>(ws, L.seq_len_eff), at<PlanHeader>(ws, L.header), ws,
       at<int32_t>(ws, L.seq_first), at<int32_t>(ws, L.seq_nsplit), at<int32_t>(ws, L.seq_slot),
       at<__nv_bfloat16>(ws, L.olat), lse, at<int32_t>(ws, L.status), d->batch, d->q_len,

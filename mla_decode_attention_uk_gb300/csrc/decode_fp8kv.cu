@@ -17,7 +17,9 @@
 //     and, below that, to 2^-22 of it), so the product is that of the bf16
 //     query.  The terms are stacked as the M = 128 rows of one MMA: the full
 //     rate of the tensor core for 64 query rows, where a 64-row MMA would run at
-//     half of it.
+//     half of it.  The 512 latent columns of the terms live in TMEM (128
+//     columns), so that QK^T reads only the page from shared memory, and the 64
+//     KB that they would take there hold two more pages.
 //   * P = hi + mid, both E5M2, eight bits wide of fp16: as both accumulate into
 //     the same columns they cannot have scales of their own, and E5M2's range
 //     (2^-16 to 2^15) keeps the small weights of a long context next to a large
@@ -26,17 +28,23 @@
 //     that all weights share cancels, and the lse takes the unrounded sum.
 // Per page and 64 query rows: QK^T 18 MMAs of 128 x 64 x 32, PV 16 of
 // 128 x N x 32 (N: the tile's rows).  The rest is as in decode.cu: the
-// producer warp brings pages box by box into a ring of slots (three of 40 KB
-// next to the query's 80 KB), the softmax runs on TMEM rows with a running
+// producer warp brings pages into a ring of slots (five of 40 KB next to the
+// query's RoPE terms; a page is two copies, and five pages in flight need no
+// prefetch into L2), the softmax runs on TMEM rows with a running
 // maximum that is raised lazily, P^T goes into the page's RoPE box, and O^T
 // stays in TMEM.  The page's scale joins the exponent (p_j s = 2^(x_j + log2 s
 // - m), m the running maximum of that sum), so that P never leaves E5M2's
 // range however the scales of a sequence's pages differ.
 // Warp roles: 0 TMA producer, 1 QK^T issuer, 2 and 3 PV issuers (latent halves;
-// warp 2 also owns TMEM), 4-11 softmax and epilogue, two warps to the rows of a
-// TMEM lane quarter, each with half of a page's keys (one warp each: 2,800
-// cycles a page whatever the heads, its 64 exponentials' chain).  (QK^T has one issuer: two that took turns
-// would each see only every second phase of a slot's barriers.)
+// warp 2 also owns TMEM), 4-7 and 8-11 softmax and epilogue, 12-15 query terms.
+// The two softmax groups take turns, page by page: a page's chain of waits,
+// exponentials and stores is about 1,700 cycles long however many warps share
+// it (measured with four and with eight), while the tensor core is done in
+// 1,400, so two pages are in work at once.  They share the rows' running
+// maxima: a group looks at a row's maximum once the other is through with it
+// for the page before, and the sums, which each keeps for itself, follow it.
+// (QK^T has one issuer: two that took turns would each see only some phases of a
+// slot's barriers.)
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -55,9 +63,8 @@ namespace {
 // ---------------------------------------------------------------- query terms
 constexpr int kSplitThreads = 256;  // one warp per tile row
 
-// q_lat (bf16) -> the attention step's tiles of E4M3 terms, in the shared-
-// memory image that the tensor core reads (128-byte swizzle), and each row's
-// scale.  Rows past the sequence's T * H are zero.
+// q_lat (bf16) -> the attention step's tiles of E4M3 terms (layout: fp8kv.cuh)
+// and each row's scale.  Rows past the sequence's T * H are zero.
 __global__ void __launch_bounds__(kSplitThreads)
 split_q_kernel(const uint4* __restrict__ qlat, int TH, int tiles, uint8_t* __restrict__ terms,
                float* __restrict__ row_scale) {
@@ -107,31 +114,27 @@ split_q_kernel(const uint4* __restrict__ qlat, int TH, int tiles, uint8_t* __res
       mid[k] = e4m3x4((x0 - h0.x) * kQMidScale, (x1 - h0.y) * kQMidScale,
                       (x2 - h1.x) * kQMidScale, (x3 - h1.y) * kQMidScale);
     }
-    const int chunk = lane + 32 * i;  // 16 columns: chunk (mod 8) of box chunk / 8
-    uint8_t* const box = img + (chunk >> 3) * kQBox8;
-    const int at = ((chunk & 7) ^ (row & 7)) << 4;  // rows row and row + 16: the same swizzle
-    *reinterpret_cast<uint4*>(box + row * 128 + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(box + (row + 16) * 128 + at) =
+    // 16 columns: chunk `lane` of the latent part, or chunk `lane` of the RoPE
+    // box (rows row and row + 16 share their swizzle).
+    uint8_t* const at = i == 0 ? img + lane * (kQTermRows * 16) + row * 16
+                               : img + kQLat8 + row * 128 + ((lane ^ (row & 7)) << 4);
+    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(at + 16 * (i == 0 ? 16 : 128)) =
         make_uint4(mid[0], mid[1], mid[2], mid[3]);
   }
   if (lane == 0) row_scale[static_cast<size_t>(tile) * kTileRows + r] = scale;
 }
 
 // ---------------------------------------------------------------- attention
-constexpr int kThreads = 384;                     // 12 warps
-constexpr int kSoftThreads = 256;                 // of them softmax and epilogue
+constexpr int kThreads = 512;                     // 16 warps
 constexpr int kBox = kPage * 128;                 // 64 keys x 128 codes: 8 KB
 constexpr int kSlot = kBoxes8 * kBox;             // 40 KB (the last box half empty)
-constexpr int kSlots = 3;
-constexpr int kSBufs = 4;                         // S buffers of 64 columns
+constexpr int kSlots = 5;
+constexpr int kSBufs = 2;                         // S buffers of 64 columns
 constexpr int kRopeBox8 = kBoxes8 - 1;
-constexpr int kSmemBytes = 1024 + kQTile8 + kSlots * kSlot;
-// Boxes in the order in which the PV issuers release them (blocks 0 and 2, then
-// 1 and 3, then the RoPE box, which holds P^T); loaded and read by QK^T so too.
-constexpr uint32_t kOrder = 0x43120u;             // 0, 2, 1, 3, 4
-__device__ __forceinline__ int box_at(int t) { return static_cast<int>((kOrder >> (4 * t)) & 15); }
-constexpr int kAhead = 2;                         // pages looked up (and prefetched) ahead
+constexpr int kSmemBytes = 1024 + kQBox8 + kSlots * kSlot;
 constexpr uint32_t kTmemAll = 512;
+constexpr uint32_t kTmemQ = 128;                  // the query's latent terms: 128 columns
 constexpr uint32_t kTmemOut = 256;                // O^T blocks at 256 + 64 m
 constexpr float kRaise = 8.0f;                    // log2 units
 // The running maximum's weight is 2^kTopExp; it may grow by 2^kRaise before
@@ -233,19 +236,19 @@ struct Pieces {
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
-decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
+decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
+                    const __grid_constant__ CUtensorMap tm_rope, Params P) {
   extern __shared__ uint8_t smem_raw[];
-  // slot_full: one barrier per box of a slot; slot_free: one per box, after
-  // PV block m (RoPE box: after both PV issuers).  p_full / p_free follow the
-  // slot of the page.
-  __shared__ __align__(8) uint64_t q_full, q_free, slot_full[kSlots][kBoxes8],
-      slot_free[kSlots][kBoxes8], s_full[kSBufs], s_free[kSBufs], p_full[kSlots], p_free[kSlots],
-      o_full, o_free, drain_bar[3];
+  // slot_full: a page has landed; p_full: its P^T is written; slot_free: PV has
+  // read both.
+  __shared__ __align__(8) uint64_t q_full, q_free, slot_full[kSlots], slot_free[kSlots],
+      s_full[kSBufs], s_free[kSBufs], p_full[kSlots], o_full, o_free, m_final[2][4], sums_full,
+      epi_done, drain_bar[3];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
   __shared__ float page_scale_sh[kSlots];
-  __shared__ float alpha_sh[2][kTileRows], max_sh[2][2][kTileRows];
-  __shared__ float l_sh[2][kTileRows], l_r_sh[2][kTileRows];
+  __shared__ float alpha_sh[2][kTileRows], m_sh[kTileRows];
+  __shared__ float l_sh[2][kTileRows], l_r_sh[2][kTileRows], m_l_sh[2][kTileRows];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Tasks v = range * sets + set are dealt round robin to groups of tpg CTAs;
@@ -254,29 +257,30 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
   const int ti = blockIdx.x % tpg, gi = blockIdx.x / tpg, groups = gridDim.x / tpg;
   const int TH = P.T * P.H;
   const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t sSlot0 = sQ + kQTile8;
+  const uint32_t sSlot0 = sQ + kQBox8;
 
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&q_full), 1);
+    mbar_init(smem_u32(&q_full), 1 + 4);  // the RoPE box; the four warps of the latent terms
     mbar_init(smem_u32(&q_free), 1);
     for (int i = 0; i < kSlots; ++i) {
-      for (int j = 0; j < kBoxes8; ++j) {
-        mbar_init(smem_u32(&slot_full[i][j]), 1);
-        mbar_init(smem_u32(&slot_free[i][j]), j == kRopeBox8 ? 2 : 1);
-      }
-      mbar_init(smem_u32(&p_full[i]), kSoftThreads / 32);
-      mbar_init(smem_u32(&p_free[i]), 2);
+      mbar_init(smem_u32(&slot_full[i]), 1);
+      mbar_init(smem_u32(&slot_free[i]), 2);
+      mbar_init(smem_u32(&p_full[i]), 4);
     }
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
-      mbar_init(smem_u32(&s_free[i]), kSoftThreads / 32);
+      mbar_init(smem_u32(&s_free[i]), 4);
     }
     mbar_init(smem_u32(&o_full), 2);
-    mbar_init(smem_u32(&o_free), kSoftThreads / 32);
+    mbar_init(smem_u32(&o_free), 8);
+    mbar_init(smem_u32(&sums_full), 8);
+    mbar_init(smem_u32(&epi_done), 8);
+    for (int i = 0; i < 8; ++i) mbar_init(smem_u32(&m_final[i >> 2][i & 3]), 1);
     for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&drain_bar[i]), 1);
     abort_sh = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_c);
+    tma_prefetch_desc(&tm_lat);
+    tma_prefetch_desc(&tm_rope);
   }
   griddep_wait();
   griddep_launch_dependents();
@@ -301,76 +305,78 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    if (elect_one()) {
-      int g = 0, n = 0, nq = 0;  // pages, pieces, query copies issued
-      bool ok = true;
-      while (ok && walk.next(P, pc)) {
-        if (n > 0 && !mbar_wait(smem_u32(&q_free), (n - 1) & 1, &abort_sh, P.status)) break;
-        const int tile = (pc.task % sets) * tpg + ti;
-        mbar_expect_tx(smem_u32(&q_full), kQTile8);
-        bulk_load(sQ, P.terms + (static_cast<size_t>(pc.b) * P.tiles + tile) * kQTile8, kQTile8,
-                  smem_u32(&q_full));
-        ++nq;
-        const int nc = pc.pend - pc.pbeg;
-        const int32_t* row = P.block_table + static_cast<size_t>(pc.b) * P.max_pages + pc.pbeg;
-        // Page numbers and scales are read, and pages prefetched into L2,
-        // kAhead pages before their load into shared memory.
-        int page[kAhead];
-        float scale[kAhead];
-        auto look = [&](int i, int& pg, float& sc) {
-          if (i >= nc) return;
-          pg = __ldg(row + i);
-          if (pg < 0 || pg >= P.num_pages) {
-            record_status(P.status, MLA_STATUS_BOUNDS);
-            pg = 0;
-          }
-          sc = P.kv_scale[pg];
-          for (int j = 0; j < kBoxes8; ++j) tma_prefetch_l2_2d(&tm_c, j * 128, pg * kPage);
-        };
-#pragma unroll
-        for (int a = 0; a < kAhead; ++a) look(a, page[a], scale[a]);
-        for (int i = 0; i < nc; ++i, ++g) {
-          const int s = g % kSlots, u = g / kSlots;
-          float sc = scale[0];
-          if (!(sc >= exp2_int(kScaleExpMin) && sc <= exp2_int(kScaleExpMax))) {
-            record_status(P.status, MLA_STATUS_BOUNDS);
-            sc = 1.0f;
-          }
-          int t = 0;
-          for (; t < kBoxes8; ++t) {
-            const int j = box_at(t);
-            if (u > 0 && !mbar_wait(smem_u32(&slot_free[s][j]), (u - 1) & 1, &abort_sh, P.status)) {
-              ok = false;
-              break;
-            }
-            // The softmax is done with the slot's last page once any of its
-            // boxes is free (PV follows it).
-            if (t == 0) *static_cast<volatile float*>(&page_scale_sh[s]) = sc;
-            const uint32_t fb = smem_u32(&slot_full[s][j]);
-            mbar_expect_tx(fb, kBox);
-            tma_load_2d(sSlot0 + s * kSlot + j * kBox, &tm_c, j * 128, page[0] * kPage, fb);
-          }
-          if (!ok) {
-            for (int t2 = 0; t2 < t; ++t2)
-              mbar_wait_drain(smem_u32(&slot_full[s][box_at(t2)]), u & 1, P.status);
-            break;
-          }
-#pragma unroll
-          for (int a = 0; a + 1 < kAhead; ++a) {
-            page[a] = page[a + 1];
-            scale[a] = scale[a + 1];
-          }
-          look(i + kAhead, page[kAhead - 1], scale[kAhead - 1]);
+    // Lane 0 issues the copies.  The lanes look pages and scales up 32 at a
+    // time, a block ahead, so that those dependent loads are off the path from
+    // a free box to its copy (looked up page by page they bounded the kernel,
+    // at 1,700 cycles a page, together with eight more copies and prefetches).
+    int g = 0, n = 0, loaded = 0, nq = 0;  // pages, pieces; pages, query copies issued
+    bool ok = true;
+    while (ok && walk.next(P, pc)) {
+      const int nc = pc.pend - pc.pbeg;
+      const int32_t* row = P.block_table + static_cast<size_t>(pc.b) * P.max_pages + pc.pbeg;
+      int pg = 0, pg_next = 0;
+      float sc = 1.0f, sc_next = 1.0f;
+      auto look = [&](int i, int& page, float& scale) {
+        if (i >= nc) return;
+        page = __ldg(row + i);
+        if (page < 0 || page >= P.num_pages) {
+          record_status(P.status, MLA_STATUS_BOUNDS);
+          page = 0;
         }
-        ++n;
+        scale = P.kv_scale[page];
+        if (!(scale >= exp2_int(kScaleExpMin) && scale <= exp2_int(kScaleExpMax))) {
+          record_status(P.status, MLA_STATUS_BOUNDS);
+          scale = 1.0f;
+        }
+      };
+      look(lane, pg_next, sc_next);
+      for (int i = 0; i < nc; ++i, ++g) {
+        if ((i & 31) == 0) {
+          pg = pg_next;
+          sc = sc_next;
+          look(i + 32 + lane, pg_next, sc_next);
+        }
+        const int page = __shfl_sync(0xffffffffu, pg, i & 31);
+        const float scale = __shfl_sync(0xffffffffu, sc, i & 31);
+        if (lane == 0) {
+          const int s = g % kSlots, u = g / kSlots;
+          ok = u == 0 || mbar_wait(smem_u32(&slot_free[s]), (u - 1) & 1, &abort_sh, P.status);
+          if (ok) {
+            // (The softmax is done with the slot's last page: PV followed it.)
+            *static_cast<volatile float*>(&page_scale_sh[s]) = scale;
+            const uint32_t fb = smem_u32(&slot_full[s]), dst = sSlot0 + s * kSlot;
+            mbar_expect_tx(fb, kSlot);
+            tma_load_3d(dst, &tm_lat, 0, page * kPage, 0, fb);
+            tma_load_2d(dst + kRopeBox8 * kBox, &tm_rope, kLora, page * kPage, fb);
+            ++loaded;
+          }
+          // The query's RoPE terms follow the piece's first page: their buffer
+          // is free once QK^T of the piece before is done.
+          if (ok && i == 0) {
+            ok = n == 0 || mbar_wait(smem_u32(&q_free), (n - 1) & 1, &abort_sh, P.status);
+            if (ok) {
+              const int tile = (pc.task % sets) * tpg + ti;
+              mbar_expect_tx(smem_u32(&q_full), kQBox8);
+              ++nq;
+              bulk_load(sQ,
+                        P.terms + (static_cast<size_t>(pc.b) * P.tiles + tile) * kQTile8 + kQLat8,
+                        kQBox8, smem_u32(&q_full));
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
       }
-      // Every copy lands before the CTA exits, after an abort too.
+      ++n;
+    }
+    if (lane == 0) {
+      // Every copy lands before the CTA exits, after an abort too (the query's
+      // barrier may then never complete, for its other arrivals: the copy has
+      // landed long before that wait gives up).
       if (nq > 0) mbar_wait_drain(smem_u32(&q_full), (nq - 1) & 1, P.status);
       for (int s = 0; s < kSlots; ++s) {
-        const int k = (g - s + kSlots - 1) / kSlots;  // pages loaded into slot s
-        if (k > 0)
-          for (int j = 0; j < kBoxes8; ++j)
-            mbar_wait_drain(smem_u32(&slot_full[s][j]), (k - 1) & 1, P.status);
+        const int k = (loaded - s + kSlots - 1) / kSlots;  // pages loaded into slot s
+        if (k > 0) mbar_wait_drain(smem_u32(&slot_full[s]), (k - 1) & 1, P.status);
       }
     }
   } else if (warp < 4) {
@@ -385,6 +391,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
         constexpr uint32_t idesc = idesc_f8_f32(kQTermRows, kPage, 0, 0, false, false);
         while (ok && walk.next(P, pc)) {
           if (!mbar_wait(smem_u32(&q_full), n & 1, &abort_sh, P.status)) break;
+          tc_fence_after();
           for (int i = pc.pbeg; i < pc.pend; ++i, ++g) {
             const int s = g % kSlots, sb = g % kSBufs;
             if (g >= kSBufs && !mbar_wait(smem_u32(&s_free[sb]), (g / kSBufs - 1) & 1, &abort_sh,
@@ -392,22 +399,20 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
               ok = false;
               break;
             }
-            const uint64_t bd0 = dslot0 + static_cast<uint64_t>((s * kSlot) >> 4);
-            for (int t = 0; t < kBoxes8 && ok; ++t) {
-              const int j = box_at(t);
-              if (!mbar_wait(smem_u32(&slot_full[s][j]), (g / kSlots) & 1, &abort_sh, P.status)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const int steps = j == kRopeBox8 ? 2 : 4;  // 32 columns each
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                if (kk < steps)
-                  umma_f8(tmem + 64 * sb, dq0 + ((j * kQBox8) >> 4) + kk * 2,
-                          bd0 + ((j * kBox) >> 4) + kk * 2, idesc, t != 0 || kk != 0);
+            if (!mbar_wait(smem_u32(&slot_full[s]), (g / kSlots) & 1, &abort_sh, P.status)) {
+              ok = false;
+              break;
             }
-            if (!ok) break;
+            tc_fence_after();
+            const uint64_t bd = dslot0 + static_cast<uint64_t>((s * kSlot) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kLora / 32; ++kk)  // four steps to a box
+              umma_f8_ta(tmem + 64 * sb, tmem + kTmemQ + 8 * kk,
+                         bd + (((kk >> 2) * kBox) >> 4) + (kk & 3) * 2, idesc, kk != 0);
+#pragma unroll
+            for (int kk = 0; kk < kRope / 32; ++kk)
+              umma_f8(tmem + 64 * sb, dq0 + kk * 2, bd + ((kRopeBox8 * kBox) >> 4) + kk * 2, idesc,
+                      1);
             umma_commit(smem_u32(&s_full[sb]));
           }
           if (!ok) break;
@@ -439,10 +444,8 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
               for (int kk = 0; kk < 4; ++kk)
                 umma_f8(tmem + kTmemOut + 64 * m, ad0 + ((m * kBox + (kk & 1) * 4096) >> 4),
                         bd0 + kk * 2, idesc, !(first && kk == 0));
-              umma_commit(smem_u32(&slot_free[s][m]));
             }
-            umma_commit(smem_u32(&slot_free[s][kRopeBox8]));
-            umma_commit(smem_u32(&p_free[s]));
+            umma_commit(smem_u32(&slot_free[s]));
           }
           if (!ok) break;
           umma_commit(smem_u32(&o_full));
@@ -453,11 +456,49 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
       umma_commit(db);
       mbar_wait_drain(db, 0, P.status);
     }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------ query terms to TMEM
+    // Lane i of TMEM quarter w takes row 32 w + i, in two halves of 64 columns;
+    // the first is on its way while the last piece's QK^T still runs.
+    const uint32_t ta = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kTmemQ;
+    int n = 0;
+    while (walk.next(P, pc)) {
+      const int tile = (pc.task % sets) * tpg + ti;
+      const uint4* src = reinterpret_cast<const uint4*>(
+                             P.terms + (static_cast<size_t>(pc.b) * P.tiles + tile) * kQTile8) +
+                         (warp & 3) * 32 + lane;
+      bool ok = true;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t v[64];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const uint4 x = src[(16 * h + c) * kQTermRows];
+          v[4 * c] = x.x;
+          v[4 * c + 1] = x.y;
+          v[4 * c + 2] = x.z;
+          v[4 * c + 3] = x.w;
+        }
+        if (h == 0) {
+          ok = n == 0 || mbar_wait(smem_u32(&q_free), (n - 1) & 1, &abort_sh, P.status);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          tc_fence_after();
+        }
+        tmem_st_x32(ta + 64 * h, v);
+        tmem_st_x32(ta + 64 * h + 32, v + 32);
+      }
+      if (!ok) break;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&q_full));
+      ++n;
+    }
   } else {
     // ------------------------------------------------------------ softmax + epilogue
-    // Warps 4 + w and 8 + w share the rows of TMEM lane quarter w; `half` of them
-    // takes keys 16 half .. + 15 and 32 + 16 half .. + 15 of every page.
-    const int wq = warp & 3, half = (warp - 4) >> 2;
+    // Two groups of four warps take turns: group q has the pages g with g mod 2 =
+    // q, and S buffer q.  A warp has the rows of its TMEM lane quarter.
+    const int wq = warp & 3, q = (warp - 4) >> 2;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     // This thread: row srow of the tile (its hi term in lane rig of the
     // quarter, its mid term in lane 16 + rig), keys of parity par.
@@ -479,113 +520,133 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
       const float q_scale =
           P.row_scale[(static_cast<size_t>(b) * P.tiles + tile) * kTileRows + srow] * P.scale_log2;
       const int n_row = row_ok ? pc.len - P.T + r / P.H + 1 : 0;
-      float m_used = -INFINITY;
+      // The running maximum of a row is m_sh (one group raises it, the other
+      // finds it raised); m_mine is the one that this thread's sums are in.
+      float m_mine = -INFINITY;
       float l = 0.0f, l_r = 0.0f;  // this thread's shares of the row's sums: exact, as rounded
+      // The last piece's epilogue has read m_sh and the sums.
+      bool bad = n > 0 && !mbar_wait(smem_u32(&epi_done), (n - 1) & 1, &abort_sh, P.status);
       for (int i = pc.pbeg; i < pc.pend; ++i, ++g) {
-        const int sb = g % kSBufs, s = g % kSlots;
-        // (The slot's first box is complete long before; its barrier orders
-        // the producer's page_scale_sh.)
-        bool bad = !mbar_wait(smem_u32(&slot_full[s][0]), (g / kSlots) & 1, &abort_sh, P.status) ||
-                   !mbar_wait(smem_u32(&s_full[sb]), (g / kSBufs) & 1, &abort_sh, P.status);
+        if ((g & 1) != q) continue;
+        const int s = g % kSlots;
+        // (The page has landed, QK^T has read it; its barrier orders the
+        // producer's page_scale_sh.)
+        bad = bad || !mbar_wait(smem_u32(&s_full[q]), (g >> 1) & 1, &abort_sh, P.status) ||
+              !mbar_wait(smem_u32(&slot_full[s]), (g / kSlots) & 1, &abort_sh, P.status);
         bad = __any_sync(0xffffffffu, bad);
         const float page_scale = *static_cast<volatile float*>(&page_scale_sh[s]);
-        uint32_t v[16];  // v[j]: key kb + 2 j, from j = 8 on kb + 16 + 2 j
+        uint32_t v[32];  // v[j]: key kb + 2 j
         if (!bad) {
           tc_fence_after();
-          uint32_t v2[16];
-          const uint32_t ta = tmem + lane_off + 64 * sb + 16 * half;
-          tmem_ld_16x64b_x8(ta, v);
-          tmem_ld_16x64b_x8(ta + 32, v + 8);
-          tmem_ld_16x64b_x8(ta + (16u << 16), v2);
-          tmem_ld_16x64b_x8(ta + (16u << 16) + 32, v2 + 8);
+          uint32_t v2[32];
+          tmem_ld_16x64b_x32(tmem + lane_off + 64 * q, v);
+          tmem_ld_16x64b_x32(tmem + lane_off + (16u << 16) + 64 * q, v2);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
+          for (int j = 0; j < 32; ++j)
             v[j] = __float_as_uint(
                 fmaf(__uint_as_float(v2[j]), 1.0f / kQMidScale, __uint_as_float(v[j])));
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s_free[sb]));
-        const int kb = i * kPage + 16 * half + par;
-        if (kb + 32 + 14 >= n_row) {
+        if (lane == 0) mbar_arrive(smem_u32(&s_free[q]));
+        const int kb = i * kPage + par;
+        if (kb + 62 >= n_row) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (kb + 2 * j + (j < 8 ? 0 : 16) >= n_row) v[j] = __float_as_uint(-INFINITY);
+          for (int j = 0; j < 32; ++j)
+            if (kb + 2 * j >= n_row) v[j] = __float_as_uint(-INFINITY);
         }
-        float a3[5];
+        float a3[11];
 #pragma unroll
-        for (int t = 0; t < 5; ++t)
+        for (int t = 0; t < 10; ++t)
           a3[t] = max3(__uint_as_float(v[3 * t]), __uint_as_float(v[3 * t + 1]),
                        __uint_as_float(v[3 * t + 2]));
-        float vmax = max3(max3(a3[0], a3[1], a3[2]), max3(a3[3], a3[4], __uint_as_float(v[15])),
-                          -INFINITY);
+        a3[10] = fmaxf(__uint_as_float(v[30]), __uint_as_float(v[31]));
+        float vmax = fmaxf(max3(max3(a3[0], a3[1], a3[2]), max3(a3[3], a3[4], a3[5]),
+                                max3(a3[6], a3[7], a3[8])),
+                           fmaxf(a3[9], a3[10]));
         vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
         // Not zero, so that a hidden key's -inf times it stays -inf (a
         // product below 2^-100 is 0 to the exponent either way).
         const float mul = fmaxf(q_scale * page_scale, 7.9e-31f);
         const float shift = __log2f(page_scale);
         const float pmax = fmaf(vmax, mul, shift);
-        if (owner) max_sh[g & 1][half][srow] = pmax;
-        // One barrier per page: does any row's maximum pass the one in use by
-        // enough, or has a wait given up?  Only then do the halves exchange
-        // their maxima (the arrays alternate: a warp may be a page ahead).
-        if (bar_any(1, kSoftThreads, bad || pmax > m_used + kRaise)) {
+        // The page before, the other group's, is through with the maximum.
+        if (g > 0)
+          bad = !mbar_wait(smem_u32(&m_final[q ^ 1][wq]), ((g - 1) >> 1) & 1, &abort_sh,
+                           P.status) || bad;
+        const bool first = i == pc.pbeg;
+        const float m_old = first ? -INFINITY : m_sh[srow];
+        const bool raise = pmax > m_old + kRaise;
+        const float m_used = raise ? pmax : m_old;
+        __syncwarp();
+        if (owner && (raise || first)) m_sh[srow] = m_used;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&m_final[q][wq]));
+        if (m_used != m_mine) {
+          const float f = ex2_approx(m_mine - m_used);
+          l *= f;
+          l_r *= f;
+          m_mine = m_used;
+        }
+        // One barrier of the group per page: a raised maximum (the group then
+        // rescales O^T, rows are its columns), or a wait that gave up.
+        if (bar_any(1 + q, 128, bad || raise)) {
           bool f = *static_cast<volatile int*>(&abort_sh) != 0;
-          const float both = fmaxf(pmax, max_sh[g & 1][half ^ 1][srow]);
-          float alpha = 1.0f;
-          if (both > m_used + kRaise) {
-            alpha = m_used == -INFINITY ? 0.0f : ex2_approx(m_used - both);
-            m_used = both;
-          }
-          l *= alpha;
-          l_r *= alpha;
-          if (owner && half == 0) alpha_sh[g & 1][srow] = alpha;
-          if (!f && i > pc.pbeg &&
-              !mbar_wait(smem_u32(&p_free[(g - 1) % kSlots]), ((g - 1) / kSlots) & 1, &abort_sh,
+          if (owner) alpha_sh[q][srow] = raise ? ex2_approx(m_old - pmax) : 1.0f;
+          if (!f && !first &&
+              !mbar_wait(smem_u32(&slot_free[(g - 1) % kSlots]), ((g - 1) / kSlots) & 1, &abort_sh,
                          P.status))
             f = true;
-          if (bar_any(1, kSoftThreads, f)) { fail = true; break; }
-          if (i > pc.pbeg) {  // rescale O^T (its rows are columns), a half of it each
+          if (bar_any(1 + q, 128, f)) { fail = true; break; }
+          if (!first) {
             tc_fence_after();
 #pragma unroll 1
-            for (int m = 2 * half; m < 2 * half + 2; ++m) {
+            for (int m = 0; m < 4; ++m) {
 #pragma unroll 1
-              for (int h2 = 0; h2 < 2; ++h2) {
-                uint32_t vv[32];
-                const uint32_t ta = tmem + lane_off + kTmemOut + 64 * m + 32 * h2;
-                tmem_ld_x32(ta, vv);
+              for (int h2 = 0; h2 < 4; ++h2) {
+                uint32_t vv[16];
+                const uint32_t ta = tmem + lane_off + kTmemOut + 64 * m + 16 * h2;
+                tmem_ld_x16(ta, vv);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  vv[j] =
-                      __float_as_uint(__uint_as_float(vv[j]) * alpha_sh[g & 1][32 * h2 + j]);
-                tmem_st_x32(ta, vv);
+                for (int j = 0; j < 16; ++j)
+                  vv[j] = __float_as_uint(__uint_as_float(vv[j]) * alpha_sh[q][16 * h2 + j]);
+                tmem_st_x16(ta, vv);
               }
             }
             tmem_wait_st();
             tc_fence_before();
           }
         }
-        __half2 hi[8], mid[8];
+        // Codes are the upper bytes of fp16 pairs, four to a word.
+        uint32_t hw[8], mw[8];
         if (m_used == -INFINITY) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) hi[j] = mid[j] = __float2half2_rn(0.0f);
+          for (int t = 0; t < 8; ++t) hw[t] = mw[t] = 0u;
         } else {
           const float add = shift + kTopExp - m_used;
           float se[4] = {};
           __half2 err = __float2half2_rn(0.0f);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float p0 = ex2_approx(fmaf(__uint_as_float(v[2 * j]), mul, add));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(v[2 * j + 1]), mul, add));
-            se[(2 * j) & 3] += p0;
-            se[(2 * j + 1) & 3] += p1;
-            const __half2 h = __floats2half2_rn(p0, p1);
-            hi[j] = e5m2_in_half2(h);
-            mid[j] = e5m2_in_half2(__hsub2(h, hi[j]));
-            err = __hfma2(__hsub2(__hadd2(hi[j], mid[j]), h),
-                          __hge2(h, __float2half2_rn(kRoundedFrom)), err);
+          for (int t = 0; t < 8; ++t) {
+            uint32_t hb[2], mb[2];
+#pragma unroll
+            for (int j = 2 * t; j < 2 * t + 2; ++j) {
+              const float p0 = ex2_approx(fmaf(__uint_as_float(v[2 * j]), mul, add));
+              const float p1 = ex2_approx(fmaf(__uint_as_float(v[2 * j + 1]), mul, add));
+              se[(2 * j) & 3] += p0;
+              se[(2 * j + 1) & 3] += p1;
+              const __half2 h = __floats2half2_rn(p0, p1);
+              const __half2 hi = e5m2_in_half2(h);
+              const __half2 mid = e5m2_in_half2(__hsub2(h, hi));
+              err = __hfma2(__hsub2(__hadd2(hi, mid), h),
+                            __hge2(h, __float2half2_rn(kRoundedFrom)), err);
+              hb[j & 1] = bits(hi);
+              mb[j & 1] = bits(mid);
+            }
+            hw[t] = __byte_perm(hb[0], hb[1], 0x7531);
+            mw[t] = __byte_perm(mb[0], mb[1], 0x7531);
           }
           const float sum = (se[0] + se[1]) + (se[2] + se[3]);
           const float2 e = __half22float2(err);
@@ -593,21 +654,14 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
           l = fmaf(sum, inv_scale, l);
           l_r = fmaf(sum + (e.x + e.y), inv_scale, l_r);
         }
-        // The codes are the upper bytes, four to a word (words 0, 1: the lower
-        // 16 keys).  The even-key thread writes the lower keys, the odd-key
-        // thread the upper ones: half of each thread's codes cross over.
-        uint32_t hw[4], mw[4];
+        // The even-key thread writes keys 0-31, the odd-key thread keys 32-63:
+        // half of each thread's codes cross to its partner.
+        uint32_t ph[8], pm[8];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          hw[t] = __byte_perm(bits(hi[2 * t]), bits(hi[2 * t + 1]), 0x7531);
-          mw[t] = __byte_perm(bits(mid[2 * t]), bits(mid[2 * t + 1]), 0x7531);
-        }
-        uint32_t ph[4], pm[4];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint32_t keep_h = par ? hw[2 + t] : hw[t], keep_m = par ? mw[2 + t] : mw[t];
-          const uint32_t got_h = __shfl_xor_sync(0xffffffffu, par ? hw[t] : hw[2 + t], 2);
-          const uint32_t got_m = __shfl_xor_sync(0xffffffffu, par ? mw[t] : mw[2 + t], 2);
+          const uint32_t keep_h = par ? hw[4 + t] : hw[t], keep_m = par ? mw[4 + t] : mw[t];
+          const uint32_t got_h = __shfl_xor_sync(0xffffffffu, par ? hw[t] : hw[4 + t], 2);
+          const uint32_t got_m = __shfl_xor_sync(0xffffffffu, par ? mw[t] : mw[4 + t], 2);
           const uint32_t eh = par ? got_h : keep_h, oh = par ? keep_h : got_h;
           const uint32_t em = par ? got_m : keep_m, om = par ? keep_m : got_m;
           ph[2 * t] = __byte_perm(eh, oh, 0x5140);
@@ -622,11 +676,13 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
         const uint32_t rowaddr = sSlot0 + s * kSlot + kRopeBox8 * kBox + srow * 128;
         const bool late = (srow >> 3) & 1;
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const bool is_mid = (q == 1) != late;
-          const int chunk = (is_mid ? 4 : 0) + 2 * par + half;
-          st_shared_v4(rowaddr + ((chunk ^ (srow & 7)) << 4), is_mid ? pm[0] : ph[0],
-                       is_mid ? pm[1] : ph[1], is_mid ? pm[2] : ph[2], is_mid ? pm[3] : ph[3]);
+        for (int t = 0; t < 4; ++t) {
+          const int h4 = 4 * (t & 1);
+          const bool is_mid = (t >= 2) != late;
+          const int chunk = (is_mid ? 4 : 0) + 2 * par + (t & 1);
+          st_shared_v4(rowaddr + ((chunk ^ (srow & 7)) << 4), is_mid ? pm[h4] : ph[h4],
+                       is_mid ? pm[h4 + 1] : ph[h4 + 1], is_mid ? pm[h4 + 2] : ph[h4 + 2],
+                       is_mid ? pm[h4 + 3] : ph[h4 + 3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -635,53 +691,66 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_c, Params P) {
       if (fail) break;
       have = walk.next(P, pc);
 
-      // ---------------- epilogue of this piece
-      const bool bad = !mbar_wait(smem_u32(&o_full), n & 1, &abort_sh, P.status);
+      // ---------------- epilogue of this piece, a half of the columns each
       l += __shfl_xor_sync(0xffffffffu, l, 2);
       l_r += __shfl_xor_sync(0xffffffffu, l_r, 2);
       if (owner) {
-        l_sh[half][srow] = l;
-        l_r_sh[half][srow] = l_r;
+        l_sh[q][srow] = l;
+        l_r_sh[q][srow] = l_r;
+        m_l_sh[q][srow] = m_mine;
       }
-      if (bar_any(1, kSoftThreads, bad)) { fail = true; break; }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sums_full));
+      bad = bad || !mbar_wait(smem_u32(&sums_full), n & 1, &abort_sh, P.status) ||
+            !mbar_wait(smem_u32(&o_full), n & 1, &abort_sh, P.status);
+      if (__any_sync(0xffffffffu, bad)) break;
       tc_fence_after();
       const size_t row_base = static_cast<size_t>(b) * TH + tile * kTileRows;
       const size_t part_base =
           nsplit > 1 ? static_cast<size_t>(slot + split) * TH + tile * kTileRows : 0;
       const int rows_here = min(kTileRows, TH - tile * kTileRows);
+      __nv_bfloat16* const out =
+          nsplit > 1 ? P.opart + part_base * kLora : P.olat + row_base * kLora;
 #pragma unroll 1
       for (int h2 = 0; h2 < 2 && 32 * h2 < rows_here; ++h2) {
-        // Lane j holds the reciprocal of row 32 h2 + j.
-        const float total = l_r_sh[0][32 * h2 + lane] + l_r_sh[1][32 * h2 + lane];
-        const float inv = total > 0.0f ? 1.0f / total : 0.0f;
-        const int nrow = min(32, rows_here - 32 * h2);
+        // Lane j: row 32 h2 + j's sums, in its last maximum, and the reciprocal.
+        const int row = 32 * h2 + lane;
+        const float m = m_sh[row];
+        const float w0 = m_l_sh[0][row] == -INFINITY ? 0.0f : ex2_approx(m_l_sh[0][row] - m);
+        const float w1 = m_l_sh[1][row] == -INFINITY ? 0.0f : ex2_approx(m_l_sh[1][row] - m);
+        const float total_r = fmaf(l_r_sh[0][row], w0, l_r_sh[1][row] * w1);
+        const float inv = total_r > 0.0f ? 1.0f / total_r : 0.0f;
+        const int nrow = min(32, rows_here - 32 * h2);  // 16 or 32
+        if (q == 0 && wq == h2 && lane < nrow) {
+          const float total = fmaf(l_sh[0][row], w0, l_sh[1][row] * w1);
+          const float lse2 = total > 0.0f ? m - kTopExp + __log2f(total) : -INFINITY;
+          (nsplit > 1 ? P.lpart + part_base : P.lse + row_base)[row] = lse2 * kLn2;
+        }
 #pragma unroll 1
-        for (int m = 2 * half; m < 2 * half + 2; ++m) {
-          const int lat = 128 * m + 32 * wq + lane;
+        for (int m4 = 2 * q; m4 < 2 * q + 2; ++m4) {
           uint32_t v[32];
-          tmem_ld_x32(tmem + lane_off + kTmemOut + 64 * m + 32 * h2, v);
+          tmem_ld_x32(tmem + lane_off + kTmemOut + 64 * m4 + 32 * h2, v);
           tmem_wait_ld();
-          __nv_bfloat16* dst = (nsplit > 1 ? P.opart : P.olat) +
-                               ((nsplit > 1 ? part_base : row_base) + 32 * h2) * kLora + lat;
+          // Lane = latent column, v[j] = row j.  Of two rows the even lane
+          // stores one and the odd lane the other, two columns each.
+          uint32_t* const dst = reinterpret_cast<uint32_t*>(
+              out + (32 * h2 + (lane & 1)) * kLora + 128 * m4 + 32 * wq + (lane & ~1));
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float il = __shfl_sync(0xffffffffu, inv, j);
-            if (j < nrow) dst[j * kLora] = __float2bfloat16_rn(__uint_as_float(v[j]) * il);
+          for (int j = 0; j < 32; j += 2) {
+            if (j == 16 && nrow == 16) break;
+            const float x = __uint_as_float(v[j]) * __shfl_sync(0xffffffffu, inv, j);
+            const float y = __uint_as_float(v[j + 1]) * __shfl_sync(0xffffffffu, inv, j + 1);
+            const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? x : y, 1);
+            dst[j * (kLora / 2)] = lane & 1 ? pack_bf16x2(got, y) : pack_bf16x2(x, got);
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&o_free));
-      if (owner && half == 0 && row_ok) {
-        const float total = l + l_sh[1][srow];
-        const float lse2 = total > 0.0f ? m_used - kTopExp + __log2f(total) : -INFINITY;
-        if (nsplit > 1)
-          P.lpart[part_base + srow] = lse2 * kLn2;
-        else
-          P.lse[row_base + srow] = lse2 * kLn2;
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&o_free));
+        mbar_arrive(smem_u32(&epi_done));
       }
-      named_bar_sync(1, kSoftThreads);  // the sums are read before the next piece's
       ++n;
     }
   }
@@ -721,7 +790,7 @@ size_t fp8kv_terms_bytes(int B, int T, int H) {
   return tiles * (kQTile8 + kTileRows * sizeof(float));
 }
 
-cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_c, int sm_count,
+cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, int sm_count,
                                 const __nv_bfloat16* qlat, uint8_t* terms,
                                 const int32_t* block_table, const float* kv_scale,
                                 const int32_t* seq_len_eff, const PlanHeader* header, void* ws,
@@ -762,7 +831,7 @@ cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_c, int sm_count,
   P.sets = shape.sets;
   P.scale_log2 = scale * 1.4426950408889634f;
   return launch_pdl(decode_fp8kv_kernel, dim3(shape.groups * shape.tpg), dim3(kThreads),
-                    kSmemBytes, st, tm_c, P);
+                    kSmemBytes, st, tm_lat, tm_rope, P);
 }
 
 }  // namespace mla

@@ -28,13 +28,16 @@ constexpr int kScaleExpMax = 32;
 
 // The query's two E4M3 terms (attention step): q = scale * (hi + mid / 16).
 constexpr float kQMidScale = 16.0f;
-// One tile of query terms: five 128-byte-wide boxes (the last half empty) of
-// 128 rows: rows 32 w + i and 32 w + 16 + i are the hi and mid terms of tile
-// row 16 w + i, so that the two land in TMEM lanes of the same warp.
-constexpr int kBoxes8 = 5;
+// One tile of query terms, 128 rows: rows 32 w + i and 32 w + 16 + i are the hi
+// and mid terms of tile row 16 w + i, so that the two land in TMEM lanes of the
+// same warp.  First the 512 latent columns as 32 chunks of 16 columns x 128 rows
+// (a TMEM lane's loads are then coalesced with its neighbours'), then the 64
+// RoPE columns as the shared-memory image of a 128-byte-wide box (half empty).
+constexpr int kBoxes8 = 5;                       // 128-byte-wide boxes of a cached row
 constexpr int kQTermRows = 2 * kTileRows;
-constexpr int kQBox8 = kQTermRows * 128;
-constexpr int kQTile8 = kBoxes8 * kQBox8;  // 80 KB
+constexpr int kQLat8 = kQTermRows * kLora;       // 64 KB
+constexpr int kQBox8 = kQTermRows * 128;         // 16 KB
+constexpr int kQTile8 = kQLat8 + kQBox8;
 
 // Exponent of the smallest power of two s with amax <= 448 s, within the
 // bounds.  amax: finite, >= 0; exact (bit operations only).
@@ -85,14 +88,36 @@ __device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_
       : "memory");
 }
 
-// 16 lanes x 64 bits, 8 repetitions (16 columns): the lane and column mapping
-// of tmem_ld_16x64b_x16.
-__device__ __forceinline__ void tmem_ld_16x64b_x8(uint32_t taddr, uint32_t* r) {
+// The same with A in tensor memory: lane = row, four codes to a column.
+__device__ __forceinline__ void umma_f8_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x64b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr));
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// 32 lanes x 32 bits, 16 consecutive columns (as tmem_ld_x16).
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15])
+      : "memory");
+}
+
+// 3-D tiled load of one box into shared memory (see tma_load_2d).
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, int32_t c0,
+                                            int32_t c1, int32_t c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
 }
 
 // Bulk copy of `bytes` from global to shared memory, completing on an
