@@ -240,14 +240,15 @@ int mla_decode_append_fp8kv(const mla_decode_dims* dims, const void* rows, int32
                             const int32_t* seq_lens, uint8_t* kv_fp8, float* kv_scale,
                             int32_t* status, void* stream);
 
-/* Bytes of the buffer of query terms (below) for `dims`.  Needs no device. */
-int mla_decode_fp8kv_terms_size(const mla_decode_dims* dims, size_t* bytes);
+/* mla_decode_plan_ex balanced for the 8-bit cache, where a piece's start and
+ * end weigh more against its pages.  Any plan serves either cache and gives the
+ * same results to within the split-KV merge's rounding. */
+int mla_decode_plan_fp8kv(const mla_decode_dims* dims, const int32_t* seq_lens,
+                          int32_t num_ranges, void* workspace, size_t workspace_bytes,
+                          void* stream);
 
-/* mla_decode_run over the 8-bit cache, after mla_decode_plan on the same
- * workspace (a plan serves both kinds of cache).  Arguments as there, and
- *   terms       device scratch of mla_decode_fp8kv_terms_size bytes, 16-byte
- *               aligned: the absorbed query as 8-bit terms.  Like the
- *               workspace it belongs to one call at a time.
+/* mla_decode_run over the 8-bit cache, after mla_decode_plan or
+ * mla_decode_plan_fp8kv on the same workspace; arguments as there.
  * Rows past a sequence's length in its last page must not be NaN codes (0x7f,
  * 0xff); mla_decode_append_fp8kv clears them.  A page's scale outside [2^-32,
  * 2^32] is reported as DEVICE_BOUNDS by mla_decode_check and taken as 1.  The
@@ -255,21 +256,19 @@ int mla_decode_fp8kv_terms_size(const mla_decode_dims* dims, size_t* bytes);
  * (to 2^-22 of its row's largest value), and the lse gets the same first-order
  * correction as over the bf16 cache; the softmax weights are rounded to two
  * 3-bit terms (at most 2^-7 of a weight), and the output is normalised by the
- * sum of the weights as rounded.  One kernel more than mla_decode_run. */
+ * sum of the weights as rounded.  As many kernels as mla_decode_run. */
 int mla_decode_run_fp8kv(const mla_decode_dims* dims, const void* q, const uint8_t* kv_fp8,
                          const float* kv_scale, const int32_t* block_table,
                          const int32_t* seq_lens, const void* w_uk, const void* w_uv,
-                         float softmax_scale, void* out, float* lse, void* terms,
-                         size_t terms_bytes, void* workspace, size_t workspace_bytes,
-                         void* stream);
+                         float softmax_scale, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
 
 /* Its attention step, in the place of mla_decode_attend between the absorb
  * and combine steps (with bf16 or FP8 weights). */
 int mla_decode_attend_fp8kv(const mla_decode_dims* dims, const uint8_t* kv_fp8,
                             const float* kv_scale, const int32_t* block_table,
                             const int32_t* seq_lens, float softmax_scale, float* lse,
-                            void* terms, size_t terms_bytes, void* workspace,
-                            size_t workspace_bytes, void* stream);
+                            void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Block-sparse decode: each query token attends to top_k pages of its

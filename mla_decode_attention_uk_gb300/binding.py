@@ -25,7 +25,7 @@ ENTRY_POINTS = (
     "mla_decode_workspace_offsets", "mla_decode_kernels_per_run",
     "mla_decode_run_static_scratch", "mla_decode_selftest_wait_timeout",
     "mla_decode_run_fp8w", "mla_decode_absorb_fp8w", "mla_decode_up_project_fp8w",
-    "mla_decode_append_fp8kv", "mla_decode_fp8kv_terms_size", "mla_decode_run_fp8kv",
+    "mla_decode_append_fp8kv", "mla_decode_plan_fp8kv", "mla_decode_run_fp8kv",
     "mla_decode_attend_fp8kv", "mla_decode_page_keys", "mla_decode_page_keys_fp8kv",
     "mla_decode_score_pages", "mla_decode_select_pages")
 
@@ -76,10 +76,9 @@ def lib():
         L.mla_decode_absorb_fp8w.argtypes = [D, P, P, P, P, S, P]
         L.mla_decode_up_project_fp8w.argtypes = [D, P, P, P, P, S, P]
         L.mla_decode_append_fp8kv.argtypes = [D, P, i32, P, P, P, P, P, P, P]
-        L.mla_decode_fp8kv_terms_size.argtypes = [D, sz]
-        L.mla_decode_run_fp8kv.argtypes = [D, P, P, P, P, P, P, P, ctypes.c_float, P, P, P, S, P,
-                                           S, P]
-        L.mla_decode_attend_fp8kv.argtypes = [D, P, P, P, P, ctypes.c_float, P, P, S, P, S, P]
+        L.mla_decode_plan_fp8kv.argtypes = [D, P, i32, P, S, P]
+        L.mla_decode_run_fp8kv.argtypes = [D, P, P, P, P, P, P, P, ctypes.c_float, P, P, P, S, P]
+        L.mla_decode_attend_fp8kv.argtypes = [D, P, P, P, P, ctypes.c_float, P, P, S, P]
         L.mla_decode_page_keys.argtypes = [D, P, P, P, i32, P, P, P, P]
         L.mla_decode_page_keys_fp8kv.argtypes = [D, P, P, P, P, i32, P, P, P, P]
         L.mla_decode_score_pages.argtypes = [D, P, P, P, P, P, P, P]
@@ -134,19 +133,11 @@ def kernels_per_run(d: Dims, fp8_weights: bool = False) -> int:
     return n.value
 
 
-def fp8kv_terms_size(d: Dims) -> int:
-    """Bytes of the query-term scratch that decoding over the 8-bit cache needs."""
-    n = ctypes.c_size_t(0)
-    _ok(lib().mla_decode_fp8kv_terms_size(ctypes.byref(d), ctypes.byref(n)),
-        "mla_decode_fp8kv_terms_size")
-    return n.value
-
-
 class MlaDecode:
     """Owns a device workspace for one set of dims; plan() once per decode step,
-    run() once per layer.  All tensors must be CUDA, contiguous.  With fp8_kv
-    it also owns the query-term scratch, and run_fp8kv() decodes over the
-    8-bit cache (one plan serves both)."""
+    run() or run_fp8kv() once per layer.  All tensors must be CUDA, contiguous.
+    With fp8_kv plan() balances the work for the 8-bit cache (a plan of either
+    kind serves both)."""
 
     def __init__(self, d: Dims, device=None, num_ranges: int = 0, fp8_kv: bool = False):
         self.dims = d
@@ -154,11 +145,15 @@ class MlaDecode:
         self.ws_bytes = workspace_size(d, num_ranges)
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8,
                                      device=device or torch.device("cuda"))
-        self.terms_bytes = fp8kv_terms_size(d) if fp8_kv else 0
-        self.terms = torch.empty(self.terms_bytes, dtype=torch.uint8,
-                                 device=self.workspace.device) if fp8_kv else None
+        self.fp8_kv = fp8_kv
 
     def plan(self, seq_lens):
+        if self.fp8_kv:
+            _ok(lib().mla_decode_plan_fp8kv(ctypes.byref(self.dims), _ptr(seq_lens),
+                                            self.num_ranges, _ptr(self.workspace), self.ws_bytes,
+                                            _stream()),
+                "mla_decode_plan_fp8kv")
+            return
         _ok(lib().mla_decode_plan_ex(ctypes.byref(self.dims), _ptr(seq_lens), self.num_ranges,
                                      _ptr(self.workspace), self.ws_bytes, _stream()),
             "mla_decode_plan_ex")
@@ -183,8 +178,7 @@ class MlaDecode:
         _ok(lib().mla_decode_run_fp8kv(ctypes.byref(self.dims), _ptr(q), _ptr(kv8),
                                        _ptr(kv_scale), _ptr(block_table), _ptr(seq_lens),
                                        _ptr(w_uk), _ptr(w_uv), float(scale), _ptr(out),
-                                       _ptr(lse), _ptr(self.terms), self.terms_bytes,
-                                       _ptr(self.workspace), self.ws_bytes,
+                                       _ptr(lse), _ptr(self.workspace), self.ws_bytes,
                                        _stream_of(q, kv8, kv_scale, block_table, seq_lens, w_uk,
                                                   w_uv, out, lse, self.workspace)),
             "mla_decode_run_fp8kv")
@@ -193,8 +187,7 @@ class MlaDecode:
         _fp8kv_tensors(self.dims, kv8, kv_scale)
         _ok(lib().mla_decode_attend_fp8kv(ctypes.byref(self.dims), _ptr(kv8), _ptr(kv_scale),
                                           _ptr(block_table), _ptr(seq_lens), float(scale),
-                                          _ptr(lse), _ptr(self.terms), self.terms_bytes,
-                                          _ptr(self.workspace), self.ws_bytes,
+                                          _ptr(lse), _ptr(self.workspace), self.ws_bytes,
                                           _stream_of(kv8, kv_scale, block_table, seq_lens, lse,
                                                      self.workspace)),
             "mla_decode_attend_fp8kv")

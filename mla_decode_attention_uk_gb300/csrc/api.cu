@@ -16,7 +16,7 @@
 
 namespace mla {
 cudaError_t launch_plan(const int32_t* seq_lens, int B, int T, int max_pages, int R,
-                        int32_t* status, PlanHeader* header, int32_t* range_b, int32_t* range_p,
+                        int piece_cost, int32_t* status, PlanHeader* header, int32_t* range_b, int32_t* range_p,
                         int32_t* seq_first, int32_t* seq_nsplit, int32_t* seq_slot,
                         int32_t* seq_len_eff, int32_t* prefix, cudaStream_t stream);
 int bmm_token_tile(int BT, bool absorb);
@@ -55,9 +55,8 @@ cudaError_t launch_combine_up(const CUtensorMap& tm_wuv, int B, int T, int H, co
                               const __nv_bfloat16* olat, float* lse, float scale,
                               __nv_bfloat16* out, int32_t* status, int splits_per_seq,
                               const float* wuv_scale, cudaStream_t st);
-size_t fp8kv_terms_bytes(int B, int T, int H);
-cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, int sm_count,
-                                const __nv_bfloat16* qlat, uint8_t* terms,
+cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope,
+                                const CUtensorMap& tm_q, int sm_count,
                                 const int32_t* block_table, const float* kv_scale,
                                 const int32_t* seq_len_eff, const PlanHeader* header, void* ws,
                                 const int32_t* seq_first, const int32_t* seq_nsplit,
@@ -106,6 +105,13 @@ using namespace mla;
 namespace {
 
 constexpr int kMaxDevices = 64;
+
+// Cost of starting and ending a piece over the 8-bit cache, in its pages: 5 to 6
+// us against 0.75-0.8 us a page.  (kPieceCost, 2, is the bf16 cache's, whose pages
+// take longer.)  Measured, attention step with 2 / 4 / 6 / 8 / 10: 61 sequences of
+// 4 to 12,001 tokens x 4 queries x 128 heads 127 / 110 / 99 / 102 / 106 us, 128 of
+// 1,000-10,000 x 128 heads 119 / 116 / 113 / 113 / 113 us.
+constexpr int kPieceCost8 = 6;
 int g_sm_count[kMaxDevices];
 std::once_flag g_sm_once[kMaxDevices];
 
@@ -325,8 +331,8 @@ int mla_decode_workspace_size(const mla_decode_dims* d, size_t* bytes) {
 
 extern "C" {
 
-int mla_decode_plan_ex(const mla_decode_dims* d, const int32_t* seq_lens, int32_t num_ranges,
-                       void* ws, size_t ws_bytes, void* stream) {
+static int plan_impl(const mla_decode_dims* d, const int32_t* seq_lens, int32_t num_ranges,
+                     int piece_cost, void* ws, size_t ws_bytes, void* stream) {
   int rc = check_dims(d);
   if (rc) return rc;
   if (!seq_lens || !ws || !aligned16(ws) || num_ranges < 0 || num_ranges > 65536)
@@ -339,12 +345,22 @@ int mla_decode_plan_ex(const mla_decode_dims* d, const int32_t* seq_lens, int32_
   const WsLayout L = make_layout(d->batch, d->q_len, d->num_heads, R);
   if (ws_bytes < L.total) return MLA_DECODE_WORKSPACE_TOO_SMALL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return cuda_rc(launch_plan(seq_lens, d->batch, d->q_len, d->max_pages_per_seq, R,
+  return cuda_rc(launch_plan(seq_lens, d->batch, d->q_len, d->max_pages_per_seq, R, piece_cost,
                              at<int32_t>(ws, L.status), at<PlanHeader>(ws, L.header),
                              at<int32_t>(ws, L.range_b), at<int32_t>(ws, L.range_p),
                              at<int32_t>(ws, L.seq_first), at<int32_t>(ws, L.seq_nsplit),
                              at<int32_t>(ws, L.seq_slot), at<int32_t>(ws, L.seq_len_eff),
                              at<int32_t>(ws, L.prefix), st));
+}
+
+int mla_decode_plan_ex(const mla_decode_dims* d, const int32_t* seq_lens, int32_t num_ranges,
+                       void* ws, size_t ws_bytes, void* stream) {
+  return plan_impl(d, seq_lens, num_ranges, kPieceCost, ws, ws_bytes, stream);
+}
+
+int mla_decode_plan_fp8kv(const mla_decode_dims* d, const int32_t* seq_lens, int32_t num_ranges,
+                          void* ws, size_t ws_bytes, void* stream) {
+  return plan_impl(d, seq_lens, num_ranges, kPieceCost8, ws, ws_bytes, stream);
 }
 
 int mla_decode_plan(const mla_decode_dims* d, const int32_t* seq_lens, void* ws, size_t ws_bytes,
@@ -676,34 +692,26 @@ int mla_decode_run_fp8w(const mla_decode_dims* d, const void* q, const void* kv_
   return finish_run(d, nullptr, w_uv_fp8, w_uv_scale, scale, out, lse, ws, ws_bytes, stream);
 }
 
-int mla_decode_fp8kv_terms_size(const mla_decode_dims* d, size_t* bytes) {
-  const int rc = check_dims(d);
-  if (rc) return rc;
-  if (!bytes) return MLA_DECODE_INVALID_ARG;
-  *bytes = fp8kv_terms_bytes(d->batch, d->q_len, d->num_heads);
-  return MLA_DECODE_OK;
-}
-
 int mla_decode_attend_fp8kv(const mla_decode_dims* d, const uint8_t* kv_fp8,
                             const float* kv_scale, const int32_t* block_table,
-                            const int32_t* seq_lens, float scale, float* lse, void* terms,
-                            size_t terms_bytes, void* ws, size_t ws_bytes, void* stream) {
+                            const int32_t* seq_lens, float scale, float* lse, void* ws,
+                            size_t ws_bytes, void* stream) {
   int rc = check_dims(d);
   if (rc) return rc;
   if (!softmax_scale_ok(scale) || !kv_fp8 || !kv_scale || !block_table || !seq_lens || !lse ||
-      !terms || !ws || !aligned16(kv_fp8) || !aligned16(terms) || !aligned16(ws) ||
-      !aligned4(kv_scale) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(lse))
+      !ws || !aligned16(kv_fp8) || !aligned16(ws) || !aligned4(kv_scale) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(lse))
     return MLA_DECODE_INVALID_ARG;
   WsLayout L;
   rc = layout_for(d, ws_bytes, &L);
   if (rc) return rc;
-  if (terms_bytes < fp8kv_terms_bytes(d->batch, d->q_len, d->num_heads))
-    return MLA_DECODE_WORKSPACE_TOO_SMALL;
   // A page is one copy of its latent columns, as four 128-column boxes one after
   // the other, and one of its RoPE columns: a box of 128 whose second half lies
   // past the row and is filled with zeros.
-  CUtensorMap tm_lat, tm_rope;
-  if (!make_map_chunks(&tm_lat, kv_fp8, static_cast<uint64_t>(d->num_pages) * kPage) ||
+  CUtensorMap tm_lat, tm_rope, tm_q;
+  if (!make_map(&tm_q, at<void>(ws, L.qlat),
+                static_cast<uint64_t>(d->batch) * d->q_len * d->num_heads, kDqk, kDqk, kBoxCols,
+                decode_q_box_rows(d->q_len, d->num_heads), false) ||
+      !make_map_chunks(&tm_lat, kv_fp8, static_cast<uint64_t>(d->num_pages) * kPage) ||
       !make_map(&tm_rope, kv_fp8, static_cast<uint64_t>(d->num_pages) * kPage, kDqk, kDqk, 128,
                 kPage, true, 1))
     return MLA_DECODE_CUDA_ERROR;
@@ -711,8 +719,7 @@ int mla_decode_attend_fp8kv(const mla_decode_dims* d, const uint8_t* kv_fp8,
   rc = sm_count(&sms);
   if (rc) return rc;
   return cuda_rc(launch_decode_fp8kv(
-      tm_lat, tm_rope, sms, at<__nv_bfloat16>(ws, L.qlat), static_cast<uint8_t*>(terms), block_table,
-      kv_scale, at<int32_t>(ws, L.seq_len_eff), at<PlanHeader>(ws, L.header), ws,
+      tm_lat, tm_rope, tm_q, sms, block_table, kv_scale, at<int32_t>(ws, L.seq_len_eff), at<PlanHeader>(ws, L.header), ws,
       at<int32_t>(ws, L.seq_first), at<int32_t>(ws, L.seq_nsplit), at<int32_t>(ws, L.seq_slot),
       at<__nv_bfloat16>(ws, L.olat), lse, at<int32_t>(ws, L.status), d->batch, d->q_len,
       d->num_heads, d->max_pages_per_seq, d->num_pages, scale,
@@ -722,19 +729,16 @@ int mla_decode_attend_fp8kv(const mla_decode_dims* d, const uint8_t* kv_fp8,
 int mla_decode_run_fp8kv(const mla_decode_dims* d, const void* q, const uint8_t* kv_fp8,
                          const float* kv_scale, const int32_t* block_table,
                          const int32_t* seq_lens, const void* w_uk, const void* w_uv,
-                         float scale, void* out, float* lse, void* terms, size_t terms_bytes,
-                         void* ws, size_t ws_bytes, void* stream) {
+                         float scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                         void* stream) {
   int rc = check_run(d, q, kv_fp8, block_table, seq_lens, w_uk, w_uv, false, nullptr, nullptr,
                      scale, out, lse, ws, ws_bytes);
   if (rc) return rc;
-  if (!kv_scale || !aligned4(kv_scale) || !terms || !aligned16(terms))
-    return MLA_DECODE_INVALID_ARG;
-  if (terms_bytes < fp8kv_terms_bytes(d->batch, d->q_len, d->num_heads))
-    return MLA_DECODE_WORKSPACE_TOO_SMALL;
+  if (!kv_scale || !aligned4(kv_scale)) return MLA_DECODE_INVALID_ARG;
   rc = mla_decode_absorb(d, q, w_uk, ws, ws_bytes, stream);
   if (rc) return rc;
-  rc = mla_decode_attend_fp8kv(d, kv_fp8, kv_scale, block_table, seq_lens, scale, lse, terms,
-                               terms_bytes, ws, ws_bytes, stream);
+  rc = mla_decode_attend_fp8kv(d, kv_fp8, kv_scale, block_table, seq_lens, scale, lse, ws,
+                               ws_bytes, stream);
   if (rc) return rc;
   return finish_run(d, w_uv, nullptr, nullptr, scale, out, lse, ws, ws_bytes, stream);
 }

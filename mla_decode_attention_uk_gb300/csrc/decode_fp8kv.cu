@@ -30,7 +30,7 @@
 // 128 x N x 32 (N: the tile's rows).  The rest is as in decode.cu: the
 // producer warp brings pages into a ring of slots (five of 40 KB next to the
 // query's RoPE terms; a page is two copies, and five pages in flight need no
-// prefetch into L2), the softmax runs on TMEM rows with a running
+// prefetch into L2; a piece's query tile passes through two of the slots), the softmax runs on TMEM rows with a running
 // maximum that is raised lazily, P^T goes into the page's RoPE box, and O^T
 // stays in TMEM.  The page's scale joins the exponent (p_j s = 2^(x_j + log2 s
 // - m), m the running maximum of that sum), so that P never leaves E5M2's
@@ -57,75 +57,10 @@
 namespace mla {
 
 int decode_tiles(int T, int H);
+int decode_q_box_rows(int T, int H);
 
 namespace {
 
-// ---------------------------------------------------------------- query terms
-constexpr int kSplitThreads = 256;  // one warp per tile row
-
-// q_lat (bf16) -> the attention step's tiles of E4M3 terms (layout: fp8kv.cuh)
-// and each row's scale.  Rows past the sequence's T * H are zero.
-__global__ void __launch_bounds__(kSplitThreads)
-split_q_kernel(const uint4* __restrict__ qlat, int TH, int tiles, uint8_t* __restrict__ terms,
-               float* __restrict__ row_scale) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r = blockIdx.x * (kSplitThreads / 32) + warp;  // row of the tile
-  const int tile = blockIdx.y;                             // b * tiles + tile of the sequence
-  const int b = tile / tiles, rs = (tile % tiles) * kTileRows + r;
-  const bool ok = rs < TH;
-  // Lane l holds columns 16 l .. + 15; lanes 0-3 also the 64 RoPE columns.
-  uint32_t v[2][8] = {};
-  if (ok) {
-    const uint4* src = qlat + (static_cast<size_t>(b) * TH + rs) * (kDqk / 8);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (i == 1 && lane >= 4) break;
-      const uint4 x = src[2 * (lane + 32 * i)], y = src[2 * (lane + 32 * i) + 1];
-      v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
-      v[i][4] = y.x; v[i][5] = y.y; v[i][6] = y.z; v[i][7] = y.w;
-    }
-  }
-  float top = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[i][k] << 16)),
-                             fabsf(__uint_as_float(v[i][k] & 0xffff0000u))));
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float scale = exp2_int(page_scale_exp(top));
-  const float inv = 1.0f / scale;
-  uint8_t* const img = terms + static_cast<size_t>(tile) * kQTile8;
-  const int row = 32 * (r >> 4) + (r & 15);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (i == 1 && lane >= 4) break;
-    uint32_t hi[4], mid[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float x0 = __uint_as_float(v[i][2 * k] << 16) * inv;
-      const float x1 = __uint_as_float(v[i][2 * k] & 0xffff0000u) * inv;
-      const float x2 = __uint_as_float(v[i][2 * k + 1] << 16) * inv;
-      const float x3 = __uint_as_float(v[i][2 * k + 1] & 0xffff0000u) * inv;
-      hi[k] = e4m3x4(x0, x1, x2, x3);
-      const float2 h0 = e4m3x2_to_float2(hi[k]), h1 = e4m3x2_to_float2(hi[k] >> 16);
-      mid[k] = e4m3x4((x0 - h0.x) * kQMidScale, (x1 - h0.y) * kQMidScale,
-                      (x2 - h1.x) * kQMidScale, (x3 - h1.y) * kQMidScale);
-    }
-    // 16 columns: chunk `lane` of the latent part, or chunk `lane` of the RoPE
-    // box (rows row and row + 16 share their swizzle).
-    uint8_t* const at = i == 0 ? img + lane * (kQTermRows * 16) + row * 16
-                               : img + kQLat8 + row * 128 + ((lane ^ (row & 7)) << 4);
-    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    *reinterpret_cast<uint4*>(at + 16 * (i == 0 ? 16 : 128)) =
-        make_uint4(mid[0], mid[1], mid[2], mid[3]);
-  }
-  if (lane == 0) row_scale[static_cast<size_t>(tile) * kTileRows + r] = scale;
-}
-
-// ---------------------------------------------------------------- attention
 constexpr int kThreads = 512;                     // 16 warps
 constexpr int kBox = kPage * 128;                 // 64 keys x 128 codes: 8 KB
 constexpr int kSlot = kBoxes8 * kBox;             // 40 KB (the last box half empty)
@@ -153,21 +88,24 @@ struct Params {
   const int32_t* seq_len_eff;
   const PlanHeader* header;
   uint8_t* ws;
-  const int32_t* range_b;  // these two are filled in on the device
-  const int32_t* range_p;
   const int32_t* seq_first;
   const int32_t* seq_nsplit;
   const int32_t* seq_slot;
-  const uint8_t* terms;
-  const float* row_scale;
   __nv_bfloat16* olat;
   float* lse;
-  __nv_bfloat16* opart;
-  float* lpart;
   int32_t* status;
   int B, T, H, max_pages, num_pages;
-  int tiles, tpg, sets;
+  int tpg, sets, q_box_rows;
   float scale_log2;
+};
+// What depends on the plan's number of ranges, found out on the device.  (In
+// shared memory, as every thread would hold it in registers else.)
+struct PlanView {
+  const int32_t* range_b;
+  const int32_t* range_p;
+  __nv_bfloat16* opart;
+  float* lpart;
+  int tasks;  // ranges * sets
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -203,23 +141,22 @@ struct Piece {
   int task, b, pbeg, pend, len;
 };
 
-// The pieces (sequence, page range) of a CTA's tasks v = v0, v0 + stride, ...
-// < nv, in the order that all roles walk.  Task v is work range v / sets.
+// The pieces (sequence, page range) of a CTA's tasks v = v0, v0 + groups, ...,
+// in the order that all roles walk.  Task v is work range v / sets.
+// (Few fields: every thread of the kernel has one.)
 struct Pieces {
-  int v, stride, nv, sets;
-  int b, p, b1, p1;
-  __device__ Pieces(const Params& P, int v0, int stride_, int nv_)
-      : v(v0), stride(stride_), nv(nv_), sets(P.sets) { open(P); }
-  __device__ void open(const Params& P) {
-    if (v >= nv) return;
-    const int k = v / sets;
-    b = P.range_b[k];
-    p = P.range_p[k];
-    b1 = P.range_b[k + 1];
-    p1 = P.range_p[k + 1];
+  int v, b, p, b1, p1;
+  __device__ Pieces(const Params& P, const PlanView& V, int v0) : v(v0) { open(P, V); }
+  __device__ void open(const Params& P, const PlanView& V) {
+    if (v >= V.tasks) return;
+    const int k = v / P.sets;
+    b = V.range_b[k];
+    p = V.range_p[k];
+    b1 = V.range_b[k + 1];
+    p1 = V.range_p[k + 1];
   }
-  __device__ bool next(const Params& P, Piece& out) {
-    while (v < nv) {
+  __device__ bool next(const Params& P, const PlanView& V, Piece& out) {
+    while (v < V.tasks) {
       while (b < b1 || (b == b1 && p < p1)) {
         const int L = P.seq_len_eff[b];
         const int end = b == b1 ? p1 : (L + kPage - 1) / kPage;
@@ -228,8 +165,8 @@ struct Pieces {
         p = 0;
         if (out.pend > out.pbeg) return true;
       }
-      v += stride;
-      open(P);
+      v += gridDim.x / P.tpg;
+      open(P, V);
     }
     return false;
   }
@@ -237,36 +174,41 @@ struct Pieces {
 
 __global__ void __launch_bounds__(kThreads, 1)
 decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
-                    const __grid_constant__ CUtensorMap tm_rope, Params P) {
+                    const __grid_constant__ CUtensorMap tm_rope,
+                    const __grid_constant__ CUtensorMap tm_q, Params P) {
   extern __shared__ uint8_t smem_raw[];
-  // slot_full: a page has landed; p_full: its P^T is written; slot_free: PV has
-  // read both.
+  // By slot: slot_full, a page has landed; slot_free, PV has read it and its P^T.
+  // p_full[g mod kSlots]: P^T of page g is written (a page kSlots further on
+  // is not in a slot before PV has read this one).
   __shared__ __align__(8) uint64_t q_full, q_free, slot_full[kSlots], slot_free[kSlots],
-      s_full[kSBufs], s_free[kSBufs], p_full[kSlots], o_full, o_free, m_final[2][4], sums_full,
+      s_full[kSBufs], s_free[kSBufs], p_full[kSlots], q_raw, o_full, o_free, m_final[2][4], sums_full,
       epi_done, drain_bar[3];
+  __shared__ PlanView view;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
-  __shared__ float page_scale_sh[kSlots];
+  __shared__ float page_scale_sh[kSlots], q_scale_sh[kTileRows];
   __shared__ float alpha_sh[2][kTileRows], m_sh[kTileRows];
-  __shared__ float l_sh[2][kTileRows], l_r_sh[2][kTileRows], m_l_sh[2][kTileRows];
+  __shared__ __align__(16) float inv_sh[8][kTileRows];
+  __shared__ float amax_sh[3][kTileRows], l_sh[2][kTileRows], l_r_sh[2][kTileRows], m_l_sh[2][kTileRows];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Tasks v = range * sets + set are dealt round robin to groups of tpg CTAs;
   // a group's CTA ti takes tile set * tpg + ti (as in decode.cu).
   const int tpg = P.tpg, sets = P.sets;
-  const int ti = blockIdx.x % tpg, gi = blockIdx.x / tpg, groups = gridDim.x / tpg;
+  const int ti = blockIdx.x % tpg, gi = blockIdx.x / tpg;
   const int TH = P.T * P.H;
   const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sSlot0 = sQ + kQBox8;
 
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&q_full), 1 + 4);  // the RoPE box; the four warps of the latent terms
-    mbar_init(smem_u32(&q_free), 1);
+    mbar_init(smem_u32(&q_full), 12);
+    mbar_init(smem_u32(&q_free), 1 + 8);  // QK^T, and the softmax warps (the rows' scales)
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(smem_u32(&slot_full[i]), 1);
       mbar_init(smem_u32(&slot_free[i]), 2);
       mbar_init(smem_u32(&p_full[i]), 4);
     }
+    mbar_init(smem_u32(&q_raw), 1);
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&s_free[i]), 4);
@@ -281,16 +223,18 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
     fence_mbar_init();
     tma_prefetch_desc(&tm_lat);
     tma_prefetch_desc(&tm_rope);
+    tma_prefetch_desc(&tm_q);
   }
   griddep_wait();
   griddep_launch_dependents();
-  const int R = P.header->num_ranges;
-  {
+  if (threadIdx.x == 0) {
+    const int R = P.header->num_ranges;
     const WsLayout L = make_layout(P.B, P.T, P.H, R);
-    P.range_b = reinterpret_cast<const int32_t*>(P.ws + L.range_b);
-    P.range_p = reinterpret_cast<const int32_t*>(P.ws + L.range_p);
-    P.lpart = reinterpret_cast<float*>(P.ws + L.lpart);
-    P.opart = reinterpret_cast<__nv_bfloat16*>(P.ws + L.opart);
+    view.range_b = reinterpret_cast<const int32_t*>(P.ws + L.range_b);
+    view.range_p = reinterpret_cast<const int32_t*>(P.ws + L.range_p);
+    view.lpart = reinterpret_cast<float*>(P.ws + L.lpart);
+    view.opart = reinterpret_cast<__nv_bfloat16*>(P.ws + L.opart);
+    view.tasks = R * P.sets;
   }
   if (warp == 2) {
     tmem_alloc(smem_u32(&tmem_base_sh), kTmemAll);
@@ -300,7 +244,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
-  Pieces walk(P, gi, groups, R * sets);
+  Pieces walk(P, view, gi);
   Piece pc;
 
   if (warp == 0) {
@@ -309,9 +253,9 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
     // time, a block ahead, so that those dependent loads are off the path from
     // a free box to its copy (looked up page by page they bounded the kernel,
     // at 1,700 cycles a page, together with eight more copies and prefetches).
-    int g = 0, n = 0, loaded = 0, nq = 0;  // pages, pieces; pages, query copies issued
+    int ring = 0, n = 0;  // slots filled, pieces
     bool ok = true;
-    while (ok && walk.next(P, pc)) {
+    while (ok && walk.next(P, view, pc)) {
       const int nc = pc.pend - pc.pbeg;
       const int32_t* row = P.block_table + static_cast<size_t>(pc.b) * P.max_pages + pc.pbeg;
       int pg = 0, pg_next = 0;
@@ -329,8 +273,31 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
           scale = 1.0f;
         }
       };
+      // The query tile comes first, through two slots.
+      if (lane == 0) {
+        const int row = pc.b * TH + ((pc.task % sets) * tpg + ti) * kTileRows;
+        // (One tile at a time: the last one's terms are made, so its barrier's
+        // phase is over and seen.)
+        ok = n == 0 || mbar_wait(smem_u32(&q_full), (n - 1) & 1, &abort_sh, P.status);
+        for (int r = ring; r < ring + 2 && ok; ++r)
+          ok = r < kSlots || mbar_wait(smem_u32(&slot_free[r % kSlots]), (r / kSlots - 1) & 1,
+                                       &abort_sh, P.status);
+        if (ok) {
+          // (Every fill of a slot is a phase of its barrier.)
+          mbar_arrive(smem_u32(&slot_full[ring % kSlots]));
+          mbar_arrive(smem_u32(&slot_full[(ring + 1) % kSlots]));
+          mbar_expect_tx(smem_u32(&q_raw), kBoxes * P.q_box_rows * 128);
+          for (int j = 0; j < kBoxes; ++j)
+            tma_load_2d(sSlot0 + ((ring + j / kBoxes8) % kSlots) * kSlot + (j % kBoxes8) * kBox,
+                        &tm_q, j * kBoxCols, row, smem_u32(&q_raw));
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
+      ring += 2;
+      ++n;
       look(lane, pg_next, sc_next);
-      for (int i = 0; i < nc; ++i, ++g) {
+      for (int i = 0; i < nc; ++i, ++ring) {
         if ((i & 31) == 0) {
           pg = pg_next;
           sc = sc_next;
@@ -339,7 +306,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
         const int page = __shfl_sync(0xffffffffu, pg, i & 31);
         const float scale = __shfl_sync(0xffffffffu, sc, i & 31);
         if (lane == 0) {
-          const int s = g % kSlots, u = g / kSlots;
+          const int s = ring % kSlots, u = ring / kSlots;
           ok = u == 0 || mbar_wait(smem_u32(&slot_free[s]), (u - 1) & 1, &abort_sh, P.status);
           if (ok) {
             // (The softmax is done with the slot's last page: PV followed it.)
@@ -348,34 +315,17 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
             mbar_expect_tx(fb, kSlot);
             tma_load_3d(dst, &tm_lat, 0, page * kPage, 0, fb);
             tma_load_2d(dst + kRopeBox8 * kBox, &tm_rope, kLora, page * kPage, fb);
-            ++loaded;
-          }
-          // The query's RoPE terms follow the piece's first page: their buffer
-          // is free once QK^T of the piece before is done.
-          if (ok && i == 0) {
-            ok = n == 0 || mbar_wait(smem_u32(&q_free), (n - 1) & 1, &abort_sh, P.status);
-            if (ok) {
-              const int tile = (pc.task % sets) * tpg + ti;
-              mbar_expect_tx(smem_u32(&q_full), kQBox8);
-              ++nq;
-              bulk_load(sQ,
-                        P.terms + (static_cast<size_t>(pc.b) * P.tiles + tile) * kQTile8 + kQLat8,
-                        kQBox8, smem_u32(&q_full));
-            }
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
       }
-      ++n;
     }
     if (lane == 0) {
-      // Every copy lands before the CTA exits, after an abort too (the query's
-      // barrier may then never complete, for its other arrivals: the copy has
-      // landed long before that wait gives up).
-      if (nq > 0) mbar_wait_drain(smem_u32(&q_full), (nq - 1) & 1, P.status);
+      // Every copy lands before the CTA exits, after an abort too.
+      if (n > 0) mbar_wait_drain(smem_u32(&q_raw), (n - 1) & 1, P.status);
       for (int s = 0; s < kSlots; ++s) {
-        const int k = (loaded - s + kSlots - 1) / kSlots;  // pages loaded into slot s
+        const int k = (ring - s + kSlots - 1) / kSlots;  // fills of slot s
         if (k > 0) mbar_wait_drain(smem_u32(&slot_full[s]), (k - 1) & 1, P.status);
       }
     }
@@ -389,17 +339,17 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
       bool ok = true;
       if (warp == 1) {
         constexpr uint32_t idesc = idesc_f8_f32(kQTermRows, kPage, 0, 0, false, false);
-        while (ok && walk.next(P, pc)) {
+        while (ok && walk.next(P, view, pc)) {
           if (!mbar_wait(smem_u32(&q_full), n & 1, &abort_sh, P.status)) break;
           tc_fence_after();
           for (int i = pc.pbeg; i < pc.pend; ++i, ++g) {
-            const int s = g % kSlots, sb = g % kSBufs;
+            const int ring = g + 2 * (n + 1), s = ring % kSlots, sb = g % kSBufs;
             if (g >= kSBufs && !mbar_wait(smem_u32(&s_free[sb]), (g / kSBufs - 1) & 1, &abort_sh,
                                           P.status)) {
               ok = false;
               break;
             }
-            if (!mbar_wait(smem_u32(&slot_full[s]), (g / kSlots) & 1, &abort_sh, P.status)) {
+            if (!mbar_wait(smem_u32(&slot_full[s]), (ring / kSlots) & 1, &abort_sh, P.status)) {
               ok = false;
               break;
             }
@@ -421,14 +371,14 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
         }
       } else {
         const int half = warp - 2;
-        while (ok && walk.next(P, pc)) {
+        while (ok && walk.next(P, view, pc)) {
           const int tile = (pc.task % sets) * tpg + ti;
           const int nrows = min(kTileRows, (TH - tile * kTileRows + 15) & ~15);
           const uint32_t idesc = idesc_f8_f32(128, nrows, 0, 1, true, false);
           for (int i = pc.pbeg; i < pc.pend; ++i, ++g) {
-            const int s = g % kSlots;
+            const int s = (g + 2 * (n + 1)) % kSlots;
             const bool first = i == pc.pbeg;
-            if (!mbar_wait(smem_u32(&p_full[s]), (g / kSlots) & 1, &abort_sh, P.status) ||
+            if (!mbar_wait(smem_u32(&p_full[g % kSlots]), (g / kSlots) & 1, &abort_sh, P.status) ||
                 (first && n > 0 &&
                  !mbar_wait(smem_u32(&o_free), (n - 1) & 1, &abort_sh, P.status))) {
               ok = false;
@@ -456,96 +406,143 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
       umma_commit(db);
       mbar_wait_drain(db, 0, P.status);
     }
-  } else if (warp >= 12) {
-    // ------------------------------------------------------------ query terms to TMEM
-    // Lane i of TMEM quarter w takes row 32 w + i, in two halves of 64 columns;
-    // the first is on its way while the last piece's QK^T still runs.
-    const uint32_t ta = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kTmemQ;
-    int n = 0;
-    while (walk.next(P, pc)) {
-      const int tile = (pc.task % sets) * tpg + ti;
-      const uint4* src = reinterpret_cast<const uint4*>(
-                             P.terms + (static_cast<size_t>(pc.b) * P.tiles + tile) * kQTile8) +
-                         (warp & 3) * 32 + lane;
-      bool ok = true;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t v[64];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const uint4 x = src[(16 * h + c) * kQTermRows];
-          v[4 * c] = x.x;
-          v[4 * c + 1] = x.y;
-          v[4 * c + 2] = x.z;
-          v[4 * c + 3] = x.w;
-        }
-        if (h == 0) {
-          ok = n == 0 || mbar_wait(smem_u32(&q_free), (n - 1) & 1, &abort_sh, P.status);
-          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-          tc_fence_after();
-        }
-        tmem_st_x32(ta + 64 * h, v);
-        tmem_st_x32(ta + 64 * h + 32, v + 32);
-      }
-      if (!ok) break;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&q_full));
-      ++n;
-    }
   } else {
-    // ------------------------------------------------------------ softmax + epilogue
-    // Two groups of four warps take turns: group q has the pages g with g mod 2 =
-    // q, and S buffer q.  A warp has the rows of its TMEM lane quarter.
-    const int wq = warp & 3, q = (warp - 4) >> 2;
+    // ------------------------------------------------------------ query terms
+    // Warps 12-15 turn the query tile into its terms, warp 12 + w tile rows 16 w
+    // .. + 15, between the end of a piece's QK^T and that of its epilogue.  (A
+    // kernel of its own took 3 to 14 us.)  The terms of a CTA's first piece, which
+    // waits for them, are the work of all twelve warps, three of the nine blocks
+    // of 64 columns each (the last block is the RoPE columns).
+    //
+    // Lane layout of TMEM loads and stores of 16 lanes x 64 bits: this thread has
+    // row rig of the quarter's 16, and the words (four codes) or keys of parity
+    // par.
+    const int wq = warp & 3;
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-    // This thread: row srow of the tile (its hi term in lane rig of the
-    // quarter, its mid term in lane 16 + rig), keys of parity par.
     const int rig = (lane >> 2) + 8 * (lane & 1);
     const int par = (lane >> 1) & 1;
     const int srow = 16 * wq + rig;
-    const bool owner = par == 0;
+    const bool softmax = warp < 12;
     int g = 0, n = 0;
     bool fail = false;
-    bool have = walk.next(P, pc);
+    bool have = walk.next(P, view, pc);
     while (!fail && have) {
-      const int k = pc.task / sets, tile = (pc.task % sets) * tpg + ti;
-      const int b = pc.b;
-      const int r = tile * kTileRows + srow;
-      const bool row_ok = r < TH;
-      const int nsplit = P.seq_nsplit[b];
-      const int split = k - P.seq_first[b];
-      const int slot = P.seq_slot[b];
-      const float q_scale =
-          P.row_scale[(static_cast<size_t>(b) * P.tiles + tile) * kTileRows + srow] * P.scale_log2;
-      const int n_row = row_ok ? pc.len - P.T + r / P.H + 1 : 0;
+      if (n == 0 || !softmax) {
+        // Columns 64 block + 8 j + 4 par .. + 3 of this row.
+        auto word = [&](int block, int j) {
+          const int ring = g + 2 * n + (block >= kBoxes8 ? 1 : 0);
+          return ld_shared_v2(sSlot0 + (ring % kSlots) * kSlot + (block % kBoxes8) * kBox +
+                              srow * 128 + ((j ^ (srow & 7)) << 4) + 8 * par);
+        };
+        const int b0 = n == 0 ? 3 * ((warp - 4) >> 2) : 0, b1 = n == 0 ? b0 + 3 : kBoxes;
+        bool ok = mbar_wait(smem_u32(&q_raw), n & 1, &abort_sh, P.status);
+        // The row's scale: its largest value takes the top but one of E4M3's
+        // binades.
+        __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
+#pragma unroll 1
+        for (int block = b0; block < b1; ++block)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint2 x = word(block, j);
+            top = __hmax2(__hmax2(top, __habs2(as_bf162(x.x))), __habs2(as_bf162(x.y)));
+          }
+        float amax = fmaxf(__low2float(top), __high2float(top));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        if (n == 0) {
+          if (par == 0) amax_sh[(warp - 4) >> 2][srow] = amax;
+          named_bar_sync(3, 384);
+          amax = fmaxf(amax_sh[0][srow], fmaxf(amax_sh[1][srow], amax_sh[2][srow]));
+        }
+        const int e = page_scale_exp(amax) + 1;  // amax <= 224 * 2^e
+        const __nv_bfloat162 down = __float2bfloat162_rn(exp2_int(max(-126, -e - 120)));
+        ok = ok && (n == 0 || mbar_wait(smem_u32(&q_free), (n - 1) & 1, &abort_sh, P.status));
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        if (par == 0 && !softmax) q_scale_sh[srow] = exp2_int(e);
+#pragma unroll 1
+        for (int block = b0; block < b1; ++block) {
+          uint32_t hi[8], mid[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) split_terms(word(block, j), down, hi[j], mid[j]);
+          if (block < kLatBoxes) {
+            const uint32_t ta = tmem + lane_off + kTmemQ + 16 * block;
+            tmem_st_16x64b_x8(ta, hi);
+            tmem_st_16x64b_x8(ta + (16u << 16), mid);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {  // word 2 j + par (row + 16: the same swizzle)
+              const uint32_t a = sQ + (32 * wq + rig) * 128 +
+                                 (((j >> 1) ^ (rig & 7)) << 4) + 8 * (j & 1) + 4 * par;
+              st_shared_b32(a, hi[j]);
+              st_shared_b32(a + 16 * 128, mid[j]);
+            }
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_n(smem_u32(&q_full), n == 0 ? 1 : 3);
+        if (!softmax) {
+          // Everyone is done with the tile: its slots are free.
+          if (warp == 12 && !mbar_wait(smem_u32(&q_full), n & 1, &abort_sh, P.status)) break;
+          if (threadIdx.x == 12 * 32) {
+            mbar_arrive_n(smem_u32(&slot_free[(g + 2 * n) % kSlots]), 2);
+            mbar_arrive_n(smem_u32(&slot_free[(g + 2 * n + 1) % kSlots]), 2);
+          }
+          g += pc.pend - pc.pbeg;
+          ++n;
+          have = walk.next(P, view, pc);
+          continue;
+        }
+      }
+      // ---------------------------------------------------------- softmax + epilogue
+      // Two groups of four warps take turns: group q has the pages g with g mod 2
+      // = q, and S buffer q.  A warp has the rows of its TMEM lane quarter; this
+      // thread row srow of the tile (its hi term in lane rig of the quarter, its
+      // mid term in lane 16 + rig) and keys of parity par.
+      const int q = (warp - 4) >> 2;
+      const bool owner = par == 0;
+      const int row0 = ((pc.task % sets) * tpg + ti) * kTileRows;  // of the sequence's T * H
+      const int rows_here = min(kTileRows, TH - row0);
+      // Where the rows' results go: row of o_lat, or ~row of the partial results.
+      const int dest = P.seq_nsplit[pc.b] > 1
+                           ? ~((P.seq_slot[pc.b] + pc.task / sets - P.seq_first[pc.b]) * TH + row0)
+                           : pc.b * TH + row0;
+      const int n_row = srow < rows_here ? pc.len - P.T + (row0 + srow) / P.H + 1 : 0;
       // The running maximum of a row is m_sh (one group raises it, the other
       // finds it raised); m_mine is the one that this thread's sums are in.
       float m_mine = -INFINITY;
       float l = 0.0f, l_r = 0.0f;  // this thread's shares of the row's sums: exact, as rounded
-      // The last piece's epilogue has read m_sh and the sums.
-      bool bad = n > 0 && !mbar_wait(smem_u32(&epi_done), (n - 1) & 1, &abort_sh, P.status);
+      // The last piece's epilogue has read m_sh and the sums; the query is there.
+      bool bad = (n > 0 && !mbar_wait(smem_u32(&epi_done), (n - 1) & 1, &abort_sh, P.status)) ||
+                 !mbar_wait(smem_u32(&q_full), n & 1, &abort_sh, P.status);
+      const float q_scale = q_scale_sh[srow] * P.scale_log2;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&q_free));
       for (int i = pc.pbeg; i < pc.pend; ++i, ++g) {
         if ((g & 1) != q) continue;
-        const int s = g % kSlots;
+        const int ring = g + 2 * (n + 1), s = ring % kSlots;
         // (The page has landed, QK^T has read it; its barrier orders the
         // producer's page_scale_sh.)
         bad = bad || !mbar_wait(smem_u32(&s_full[q]), (g >> 1) & 1, &abort_sh, P.status) ||
-              !mbar_wait(smem_u32(&slot_full[s]), (g / kSlots) & 1, &abort_sh, P.status);
+              !mbar_wait(smem_u32(&slot_full[s]), (ring / kSlots) & 1, &abort_sh, P.status);
         bad = __any_sync(0xffffffffu, bad);
         const float page_scale = *static_cast<volatile float*>(&page_scale_sh[s]);
         uint32_t v[32];  // v[j]: key kb + 2 j
         if (!bad) {
           tc_fence_after();
-          uint32_t v2[32];
           tmem_ld_16x64b_x32(tmem + lane_off + 64 * q, v);
-          tmem_ld_16x64b_x32(tmem + lane_off + (16u << 16) + 64 * q, v2);
-          tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            v[j] = __float_as_uint(
-                fmaf(__uint_as_float(v2[j]), 1.0f / kQMidScale, __uint_as_float(v[j])));
+          for (int h = 0; h < 2; ++h) {  // (in halves for the registers)
+            uint32_t v2[16];
+            tmem_ld_16x64b_x16(tmem + lane_off + (16u << 16) + 64 * q + 32 * h, v2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              v[16 * h + j] = __float_as_uint(fmaf(__uint_as_float(v2[j]), 1.0f / kQMidScale,
+                                                   __uint_as_float(v[16 * h + j])));
+          }
         }
         tc_fence_before();
         __syncwarp();
@@ -595,8 +592,8 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
           bool f = *static_cast<volatile int*>(&abort_sh) != 0;
           if (owner) alpha_sh[q][srow] = raise ? ex2_approx(m_old - pmax) : 1.0f;
           if (!f && !first &&
-              !mbar_wait(smem_u32(&slot_free[(g - 1) % kSlots]), ((g - 1) / kSlots) & 1, &abort_sh,
-                         P.status))
+              !mbar_wait(smem_u32(&slot_free[(ring - 1) % kSlots]), ((ring - 1) / kSlots) & 1,
+                         &abort_sh, P.status))
             f = true;
           if (bar_any(1 + q, 128, f)) { fail = true; break; }
           if (!first) {
@@ -604,7 +601,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
 #pragma unroll 1
             for (int m = 0; m < 4; ++m) {
 #pragma unroll 1
-              for (int h2 = 0; h2 < 4; ++h2) {
+              for (int h2 = 0; 16 * h2 < rows_here; ++h2) {
                 uint32_t vv[16];
                 const uint32_t ta = tmem + lane_off + kTmemOut + 64 * m + 16 * h2;
                 tmem_ld_x16(ta, vv);
@@ -686,10 +683,10 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&p_full[s]));
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[g % kSlots]));
       }
       if (fail) break;
-      have = walk.next(P, pc);
+      have = walk.next(P, view, pc);
 
       // ---------------- epilogue of this piece, a half of the columns each
       l += __shfl_xor_sync(0xffffffffu, l, 2);
@@ -705,43 +702,44 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
             !mbar_wait(smem_u32(&o_full), n & 1, &abort_sh, P.status);
       if (__any_sync(0xffffffffu, bad)) break;
       tc_fence_after();
-      const size_t row_base = static_cast<size_t>(b) * TH + tile * kTileRows;
-      const size_t part_base =
-          nsplit > 1 ? static_cast<size_t>(slot + split) * TH + tile * kTileRows : 0;
-      const int rows_here = min(kTileRows, TH - tile * kTileRows);
-      __nv_bfloat16* const out =
-          nsplit > 1 ? P.opart + part_base * kLora : P.olat + row_base * kLora;
+      const size_t row_base = dest < 0 ? ~dest : dest;
+      __nv_bfloat16* const out = (dest < 0 ? view.opart : P.olat) + row_base * kLora;
 #pragma unroll 1
-      for (int h2 = 0; h2 < 2 && 32 * h2 < rows_here; ++h2) {
-        // Lane j: row 32 h2 + j's sums, in its last maximum, and the reciprocal.
-        const int row = 32 * h2 + lane;
+      for (int row = lane; row < rows_here; row += 32) {
+        // The row's sums, in its last maximum.
         const float m = m_sh[row];
         const float w0 = m_l_sh[0][row] == -INFINITY ? 0.0f : ex2_approx(m_l_sh[0][row] - m);
         const float w1 = m_l_sh[1][row] == -INFINITY ? 0.0f : ex2_approx(m_l_sh[1][row] - m);
         const float total_r = fmaf(l_r_sh[0][row], w0, l_r_sh[1][row] * w1);
-        const float inv = total_r > 0.0f ? 1.0f / total_r : 0.0f;
-        const int nrow = min(32, rows_here - 32 * h2);  // 16 or 32
-        if (q == 0 && wq == h2 && lane < nrow) {
+        inv_sh[warp - 4][row] = total_r > 0.0f ? 1.0f / total_r : 0.0f;
+        if (q == 0 && wq == 0) {
           const float total = fmaf(l_sh[0][row], w0, l_sh[1][row] * w1);
           const float lse2 = total > 0.0f ? m - kTopExp + __log2f(total) : -INFINITY;
-          (nsplit > 1 ? P.lpart + part_base : P.lse + row_base)[row] = lse2 * kLn2;
+          (dest < 0 ? view.lpart : P.lse)[row_base + row] = lse2 * kLn2;
         }
+      }
+      __syncwarp();
 #pragma unroll 1
-        for (int m4 = 2 * q; m4 < 2 * q + 2; ++m4) {
-          uint32_t v[32];
-          tmem_ld_x32(tmem + lane_off + kTmemOut + 64 * m4 + 32 * h2, v);
-          tmem_wait_ld();
-          // Lane = latent column, v[j] = row j.  Of two rows the even lane
-          // stores one and the odd lane the other, two columns each.
-          uint32_t* const dst = reinterpret_cast<uint32_t*>(
-              out + (32 * h2 + (lane & 1)) * kLora + 128 * m4 + 32 * wq + (lane & ~1));
+      for (int h = 0; 16 * h < rows_here; ++h) {
+        uint32_t v[2][16];
+        const uint32_t ta = tmem + lane_off + kTmemOut + 128 * q + 16 * h;
+        tmem_ld_x16(ta, v[0]);
+        tmem_ld_x16(ta + 64, v[1]);
+        tmem_wait_ld();
+        // Lane = latent column, v[.][j] = row j.  Of two rows the even lane
+        // stores one and the odd lane the other, two columns each.
+        uint32_t* const dst = reinterpret_cast<uint32_t*>(
+            out + (16 * h + (lane & 1)) * kLora + 256 * q + 32 * wq + (lane & ~1));
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            if (j == 16 && nrow == 16) break;
-            const float x = __uint_as_float(v[j]) * __shfl_sync(0xffffffffu, inv, j);
-            const float y = __uint_as_float(v[j + 1]) * __shfl_sync(0xffffffffu, inv, j + 1);
+        for (int j = 0; j < 16; j += 2) {
+          const float2 il = *reinterpret_cast<const float2*>(&inv_sh[warp - 4][16 * h + j]);
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            const float x = __uint_as_float(v[m][j]) * il.x;
+            const float y = __uint_as_float(v[m][j + 1]) * il.y;
             const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? x : y, 1);
-            dst[j * (kLora / 2)] = lane & 1 ? pack_bf16x2(got, y) : pack_bf16x2(x, got);
+            dst[j * (kLora / 2) + 64 * m] =
+                lane & 1 ? pack_bf16x2(got, y) : pack_bf16x2(x, got);
           }
         }
       }
@@ -784,14 +782,8 @@ static Shape shape_for(int T, int H, int sm_count) {
   return d;
 }
 
-// Bytes of the query terms of B sequences: the tiles, then the rows' scales.
-size_t fp8kv_terms_bytes(int B, int T, int H) {
-  const size_t tiles = static_cast<size_t>(B) * decode_tiles(T, H);
-  return tiles * (kQTile8 + kTileRows * sizeof(float));
-}
-
-cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope, int sm_count,
-                                const __nv_bfloat16* qlat, uint8_t* terms,
+cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope,
+                                const CUtensorMap& tm_q, int sm_count,
                                 const int32_t* block_table, const float* kv_scale,
                                 const int32_t* seq_len_eff, const PlanHeader* header, void* ws,
                                 const int32_t* seq_first, const int32_t* seq_nsplit,
@@ -800,14 +792,8 @@ cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm
                                 int num_pages, float scale, cudaStream_t st) {
   Params P{};
   const Shape shape = shape_for(T, H, sm_count);
-  P.tiles = shape.tiles;
-  float* row_scale = reinterpret_cast<float*>(terms + static_cast<size_t>(B) * P.tiles * kQTile8);
-  cudaError_t e = launch_pdl(split_q_kernel, dim3(kTileRows / (kSplitThreads / 32), B * P.tiles),
-                             dim3(kSplitThreads), 0, st, reinterpret_cast<const uint4*>(qlat),
-                             T * H, P.tiles, terms, row_scale);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(decode_fp8kv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kSmemBytes);
+  const cudaError_t e = cudaFuncSetAttribute(
+      decode_fp8kv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   P.block_table = block_table;
   P.kv_scale = kv_scale;
@@ -817,8 +803,7 @@ cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm
   P.seq_first = seq_first;
   P.seq_nsplit = seq_nsplit;
   P.seq_slot = seq_slot;
-  P.terms = terms;
-  P.row_scale = row_scale;
+  P.q_box_rows = decode_q_box_rows(T, H);
   P.olat = olat;
   P.lse = lse;
   P.status = status;
@@ -831,7 +816,7 @@ cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm
   P.sets = shape.sets;
   P.scale_log2 = scale * 1.4426950408889634f;
   return launch_pdl(decode_fp8kv_kernel, dim3(shape.groups * shape.tpg), dim3(kThreads),
-                    kSmemBytes, st, tm_lat, tm_rope, P);
+                    kSmemBytes, st, tm_lat, tm_rope, tm_q, P);
 }
 
 }  // namespace mla

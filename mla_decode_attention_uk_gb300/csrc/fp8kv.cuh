@@ -11,6 +11,7 @@
 // value and the scale, not on how a quotient was rounded.
 #pragma once
 #include <cstdint>
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -30,14 +31,10 @@ constexpr int kScaleExpMax = 32;
 constexpr float kQMidScale = 16.0f;
 // One tile of query terms, 128 rows: rows 32 w + i and 32 w + 16 + i are the hi
 // and mid terms of tile row 16 w + i, so that the two land in TMEM lanes of the
-// same warp.  First the 512 latent columns as 32 chunks of 16 columns x 128 rows
-// (a TMEM lane's loads are then coalesced with its neighbours'), then the 64
-// RoPE columns as the shared-memory image of a 128-byte-wide box (half empty).
-constexpr int kBoxes8 = 5;                       // 128-byte-wide boxes of a cached row
+// same warp.
 constexpr int kQTermRows = 2 * kTileRows;
-constexpr int kQLat8 = kQTermRows * kLora;       // 64 KB
-constexpr int kQBox8 = kQTermRows * 128;         // 16 KB
-constexpr int kQTile8 = kQLat8 + kQBox8;
+constexpr int kQBox8 = kQTermRows * 128;  // 128 rows of 128 bytes: 16 KB
+constexpr int kBoxes8 = 5;                // 128-byte-wide boxes of a cached row
 
 // Exponent of the smallest power of two s with amax <= 448 s, within the
 // bounds.  amax: finite, >= 0; exact (bit operations only).
@@ -62,6 +59,37 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
   return __half22float2(static_cast<__half2>(__nv_cvt_fp8x2_to_halfraw2(
       static_cast<__nv_fp8x2_storage_t>(codes & 0xffffu), __NV_E4M3)));
+}
+
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) {
+  return *reinterpret_cast<const __nv_bfloat162*>(&w);
+}
+// Four bf16 values as two words of E4M3 codes: value = 2^e (hi + mid / 16) for |value|
+// < 256 * 2^e, exactly down to |value| = 2^(e - 6) (and to 2^(e - 14) below).
+// down = 2^(-e - 120) brings E4M3's exponent field and steps (bias 7) onto
+// bf16's (bias 127), subnormals too, so that a code is a bit field of the bf16
+// number: hi is the value cut to four significant bits, mid 16 times the rest,
+// which has at most four.  (Conversion instructions took twice as many.)
+__device__ __forceinline__ uint32_t e4m3_field(uint32_t w) {  // of two, in bytes 0 and 2
+  constexpr uint32_t kMagnitude = 0x007f007fu;
+  return ((w >> 4) & kMagnitude) | ((w >> 8) & ~kMagnitude);
+}
+__device__ __forceinline__ void split_terms(uint2 x, __nv_bfloat162 down, uint32_t& hi,
+                                            uint32_t& mid) {
+  const __nv_bfloat162 down16 = __hmul2(down, __float2bfloat162_rn(kQMidScale));
+  const uint32_t in[2] = {x.x, x.y};
+  uint32_t h[2], m[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __nv_bfloat162 v = __hmul2(as_bf162(in[i]), down);
+    const uint32_t cut = *reinterpret_cast<const uint32_t*>(&v) & 0xfff0fff0u;
+    const __nv_bfloat162 rest = __hfma2(as_bf162(cut), __float2bfloat162_rn(-kQMidScale),
+                                        __hmul2(as_bf162(in[i]), down16));
+    h[i] = e4m3_field(cut);
+    m[i] = e4m3_field(*reinterpret_cast<const uint32_t*>(&rest));
+  }
+  hi = __byte_perm(h[0], h[1], 0x6420);
+  mid = __byte_perm(m[0], m[1], 0x6420);
 }
 
 // Records the first device-side error, where the caller asked for it.
@@ -99,6 +127,14 @@ __device__ __forceinline__ void umma_f8_ta(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
+// 16 lanes x 64 bits, 8 repetitions (16 columns): the lane and column mapping
+// of tmem_ld_16x64b_x16.
+__device__ __forceinline__ void tmem_st_16x64b_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x64b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
 // 32 lanes x 32 bits, 16 consecutive columns (as tmem_ld_x16).
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -120,15 +156,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* m, 
       : "memory");
 }
 
-// Bulk copy of `bytes` from global to shared memory, completing on an
-// mbarrier; both addresses and the size are multiples of 16 bytes.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          dst),
-      "l"(src), "r"(bytes), "r"(bar)
-      : "memory");
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared_b32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
 }
 
 }  // namespace mla

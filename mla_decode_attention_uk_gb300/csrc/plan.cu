@@ -3,7 +3,7 @@
 // FlashMLA is described as optimised for serving variable-length sequences
 // ("DeepSeek publica FlashMLA como codigo abierto", feature list).  This
 // planner realises that with an equal-cost partition: every sequence b costs
-// pages_b + kPieceCost units (pages to stream plus a fixed per-piece charge
+// pages_b + piece_cost units (pages to stream plus a fixed per-piece charge
 // for loading the query tile and writing results), the costs are laid end to
 // end, and the line is cut into num_ranges equal pieces.  Decode CTA group k
 // streams range k; a sequence cut by a range boundary is split, and its pieces
@@ -50,6 +50,7 @@ __device__ int block_inclusive_scan(int v, int* warp_tot) {
 
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(const int32_t* __restrict__ seq_lens, int B, int T, int max_pages, int R,
+            int piece_cost,
             int32_t* __restrict__ status, PlanHeader* __restrict__ header,
             int32_t* __restrict__ range_b, int32_t* __restrict__ range_p,
             int32_t* __restrict__ seq_first, int32_t* __restrict__ seq_nsplit,
@@ -85,7 +86,7 @@ plan_kernel(const int32_t* __restrict__ seq_lens, int B, int T, int max_pages, i
       seq_len_eff[b] = L;
       const int pages = (L + kPage - 1) / kPage;
       if (in_smem) s_pages[b] = pages;
-      cost = pages + kPieceCost;
+      cost = pages + piece_cost;
     }
     const int incl = block_inclusive_scan(cost, warp_tot);
     if (b < B) pref[b] = carry + incl - cost;
@@ -149,11 +150,11 @@ plan_kernel(const int32_t* __restrict__ seq_lens, int B, int T, int max_pages, i
 }  // namespace
 
 cudaError_t launch_plan(const int32_t* seq_lens, int B, int T, int max_pages, int R,
-                        int32_t* status, PlanHeader* header, int32_t* range_b, int32_t* range_p,
+                        int piece_cost, int32_t* status, PlanHeader* header, int32_t* range_b, int32_t* range_p,
                         int32_t* seq_first, int32_t* seq_nsplit, int32_t* seq_slot,
                         int32_t* seq_len_eff, int32_t* prefix, cudaStream_t stream) {
   cudaError_t e = launch_pdl(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, seq_lens, B,
-                             T, max_pages, R, status, header, range_b, range_p, seq_first,
+                             T, max_pages, R, piece_cost, status, header, range_b, range_p, seq_first,
                              seq_nsplit, seq_slot, seq_len_eff, prefix);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

@@ -50,33 +50,27 @@ def test_append_refuses_bad_arguments():
 
 def test_run_and_attend_refuse_bad_arguments():
     sc = ctypes.c_float(0.07)
-    #      q kv8 kvs table lens wuk wuv scale out lse terms tbytes ws wbytes stream
-    run = [OK, OK, OK, OK, OK, OK, OK, sc, OK, OK, OK, 1 << 30, OK, 1 << 30, None]
+    #      q kv8 kvs table lens wuk wuv scale out lse ws wbytes stream
+    run = [OK, OK, OK, OK, OK, OK, OK, sc, OK, OK, OK, 1 << 30, None]
     for change in ({0: None}, {1: None}, {1: ODD8}, {2: None}, {2: ODD2}, {3: ODD2}, {4: None},
-                   {5: ODD8}, {6: None}, {8: ODD8}, {9: None}, {10: None}, {10: ODD8}, {12: None},
-                   {12: ODD8}, {7: ctypes.c_float(0.0)}, {7: ctypes.c_float(-1.0)},
+                   {5: ODD8}, {6: None}, {8: ODD8}, {9: None}, {10: None}, {10: ODD8},
+                   {7: ctypes.c_float(0.0)}, {7: ctypes.c_float(-1.0)},
                    {7: ctypes.c_float(math.nan)}, {7: ctypes.c_float(math.inf)}):
         assert call("mla_decode_run_fp8kv", run, change) == 1, change
-    need = binding.fp8kv_terms_size(good_dims())
-    assert call("mla_decode_run_fp8kv", run, {11: need - 1}) == 3
-    assert call("mla_decode_run_fp8kv", run, {13: 64}) == 3
+    assert call("mla_decode_run_fp8kv", run, {11: 64}) == 3
     assert call("mla_decode_run_fp8kv", run, d=good_dims(q_len=9)) == 2
-    #      kv8 kvs table lens scale lse terms tbytes ws wbytes stream
-    att = [OK, OK, OK, OK, sc, OK, OK, 1 << 30, OK, 1 << 30, None]
+    #      kv8 kvs table lens scale lse ws wbytes stream
+    att = [OK, OK, OK, OK, sc, OK, OK, 1 << 30, None]
     for change in ({0: None}, {0: ODD8}, {1: None}, {1: ODD2}, {2: None}, {3: ODD2}, {5: None},
-                   {6: None}, {6: ODD8}, {8: ODD8}, {4: ctypes.c_float(math.nan)}):
+                   {6: None}, {6: ODD8}, {4: ctypes.c_float(math.nan)}):
         assert call("mla_decode_attend_fp8kv", att, change) == 1, change
-    assert call("mla_decode_attend_fp8kv", att, {7: need - 1}) == 3
-    assert call("mla_decode_attend_fp8kv", att, {9: 64}) == 3
-
-
-@pytest.mark.parametrize("B,T,H", [(1, 1, 16), (3, 1, 128), (5, 8, 128), (7, 3, 48)])
-def test_terms_size_holds_two_byte_terms_per_value(B, T, H):
-    d = good_dims(batch=B, q_len=T, num_heads=H)
-    n = binding.fp8kv_terms_size(d)
-    assert n >= B * T * H * (2 * 576 + 4)
-    assert n % 16 == 0
-    assert binding.lib().mla_decode_fp8kv_terms_size(ctypes.byref(d), None) == 1
+    assert call("mla_decode_attend_fp8kv", att, {7: 64}) == 3
+    #       lens ranges ws wbytes stream
+    plan = [OK, 5, OK, 1 << 30, None]
+    for change in ({0: None}, {1: -1}, {1: 65537}, {2: None}, {2: ODD8}):
+        assert call("mla_decode_plan_fp8kv", plan, change) == 1, change
+    assert call("mla_decode_plan_fp8kv", plan, {3: 64}) == 3
+    assert call("mla_decode_plan_fp8kv", plan, d=good_dims(page_size=16)) == 2
 
 
 def test_python_calls_check_types_and_shapes():
