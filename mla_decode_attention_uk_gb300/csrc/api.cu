@@ -66,7 +66,7 @@ cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm
 cudaError_t launch_append(const void* rows, int max_new, const int32_t* new_lens,
                           const int32_t* block_table, const int32_t* seq_lens, int B,
                           int num_pages, int max_pages, uint8_t* kv8, float* kv_scale,
-                          int32_t* status, cudaStream_t st);
+                          int32_t* status, int sm_count, cudaStream_t st);
 cudaError_t launch_page_keys(const void* cache, const float* kv_scale,
                              const int32_t* block_table, const int32_t* seq_lens, int max_new,
                              const int32_t* new_lens, int B, int num_pages, int max_pages,
@@ -747,15 +747,18 @@ int mla_decode_append_fp8kv(const mla_decode_dims* d, const void* rows, int32_t 
                             const int32_t* new_lens, const int32_t* block_table,
                             const int32_t* seq_lens, uint8_t* kv_fp8, float* kv_scale,
                             int32_t* status, void* stream) {
-  const int rc = check_dims(d);
+  int rc = check_dims(d);
   if (rc) return rc;
   if (!rows || !aligned16(rows) || max_new < 1 || !aligned4(new_lens) || !block_table ||
       !aligned4(block_table) || !seq_lens || !aligned4(seq_lens) || !kv_fp8 ||
       !aligned16(kv_fp8) || !kv_scale || !aligned4(kv_scale) || !aligned4(status))
     return MLA_DECODE_INVALID_ARG;
   if (max_new > INT32_MAX - kPage) return MLA_DECODE_INVALID_ARG;
+  int sms = 0;
+  rc = sm_count(&sms);
+  if (rc) return rc;
   return cuda_rc(launch_append(rows, max_new, new_lens, block_table, seq_lens, d->batch,
-                               d->num_pages, d->max_pages_per_seq, kv_fp8, kv_scale, status,
+                               d->num_pages, d->max_pages_per_seq, kv_fp8, kv_scale, status, sms,
                                static_cast<cudaStream_t>(stream)));
 }
 

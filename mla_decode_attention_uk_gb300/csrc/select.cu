@@ -29,23 +29,28 @@ __device__ __forceinline__ int clamp_len(int L, int T, int cap, bool report, int
 }
 
 // ---------------------------------------------------------------- scores
-// One CTA scores kScorePages pages for one query token: D[page, head] = K Q^T
-// on tcgen05, M = 128 pages, N = H heads, over 576 columns in nine stages of
-// 64.  With the pages as TMEM lanes the maximum over the heads is one thread's
-// own.  Page keys lie scattered through the pool, so threads gather them row by
-// row (16-byte asynchronous copies, eight threads to a 128-byte piece of a row)
-// into the swizzled layout that the tensor core reads; the queries come by TMA.
-// Every stage is in flight at once where shared memory holds all nine (H <= 64),
-// the first seven or eight else.
+// One CTA scores kScorePages pages for up to 256 query rows, whole query tokens
+// of H rows: D[page, row] = K Q^T on tcgen05, M = 128 pages, N = rows, over 576
+// columns in nine stages of 64.  With the pages as TMEM lanes the maximum over
+// the heads is one thread's own.  Page keys lie scattered through the pool, so
+// threads gather them row by row (16-byte asynchronous copies, eight threads to
+// a 128-byte piece of a row) into the swizzled layout that the tensor core
+// reads; the queries come by TMA.  As many stages as shared memory holds are in
+// flight: all nine up to 64 rows, four at 256.
 constexpr int kScoreThreads = 160;            // warps 0-3 gather and reduce, 4 drives
 constexpr int kGatherThreads = 128;
 constexpr int kScorePages = 128;
 constexpr int kScoreABytes = kScorePages * 128;  // 128 pages x 64 columns: 16 KB
+constexpr int kScoreRowsMax = 256;               // N of one MMA
 constexpr int kScoreSmemMax = 224 * 1024;
+constexpr int kStagesMin = 4;
 
-__host__ __device__ constexpr int score_stage_bytes(int H) { return kScoreABytes + H * 128; }
-__host__ __device__ constexpr int score_stages(int H) {
-  const int n = kScoreSmemMax / score_stage_bytes(H);
+__host__ __device__ constexpr int score_tokens(int T, int H) {
+  return T < kScoreRowsMax / H ? T : kScoreRowsMax / H;
+}
+__host__ __device__ constexpr int score_stage_bytes(int rows) { return kScoreABytes + rows * 128; }
+__host__ __device__ constexpr int score_stages(int rows) {
+  const int n = kScoreSmemMax / score_stage_bytes(rows);
   return n < kBoxes ? n : kBoxes;
 }
 
@@ -70,10 +75,12 @@ score_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t* __restrict
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh, timeout_sh;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.z, t = blockIdx.y, page0 = blockIdx.x * kScorePages;
-  const int stages = score_stages(H);
+  const int b = blockIdx.z, page0 = blockIdx.x * kScorePages;
+  const int t0 = blockIdx.y * score_tokens(T, H), t1 = min(T, t0 + score_tokens(T, H));
+  const int rows = (t1 - t0) * H;  // of this CTA; stages are sized for the most
+  const int stages = score_stages(score_tokens(T, H) * H);
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t stage_bytes = score_stage_bytes(H);
+  const uint32_t stage_bytes = score_stage_bytes(score_tokens(T, H) * H);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBoxes; ++i) {
       mbar_init(smem_u32(&full[i]), kGatherThreads + 1);
@@ -87,16 +94,18 @@ score_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t* __restrict
   griddep_wait();
   griddep_launch_dependents();
   const int L = clamp_len(seq_lens[b], T, max_pages * kPage,
-                          threadIdx.x == 0 && t == 0 && page0 == 0, status);
-  const int seen = (L - T + t + kPage) / kPage;  // pages that query t sees
-  float* const out = scores + (static_cast<size_t>(b) * T + t) * max_pages;
-  if (page0 >= seen) {  // the whole CTA: nothing to compute
+                          threadIdx.x == 0 && t0 == 0 && page0 == 0, status);
+  // Query t sees (L - T + t + kPage) / kPage pages; the last one here the most.
+  const int most = (L - T + t1 - 1 + kPage) / kPage;
+  float* const out = scores + static_cast<size_t>(b) * T * max_pages;
+  if (page0 >= most) {  // the whole CTA: nothing to compute
     const int j = page0 + threadIdx.x;
-    if (threadIdx.x < kScorePages && j < max_pages) out[j] = -INFINITY;
+    if (threadIdx.x < kScorePages && j < max_pages)
+      for (int t = t0; t < t1; ++t) out[static_cast<size_t>(t) * max_pages + j] = -INFINITY;
     return;
   }
   if (warp == 4) {
-    tmem_alloc(smem_u32(&tmem_base_sh), 128);
+    tmem_alloc(smem_u32(&tmem_base_sh), kScoreRowsMax);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -111,7 +120,7 @@ score_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t* __restrict
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int j = page0 + rg + 16 * i;
-      int p = j < seen ? block_table[static_cast<size_t>(b) * max_pages + j] : 0;
+      int p = j < most ? block_table[static_cast<size_t>(b) * max_pages + j] : 0;
       if (p < 0 || p >= num_pages) {
         record_status(status, MLA_STATUS_BOUNDS);
         p = 0;
@@ -138,45 +147,56 @@ score_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t* __restrict
     cp_async_wait<8>(); landed(0);
     cp_async_wait<7>(); landed(1);
     cp_async_wait<6>(); landed(2);
-    cp_async_wait<5>(); landed(3);
-    cp_async_wait<4>(); landed(4);
-    cp_async_wait<3>(); landed(5);
-    cp_async_wait<2>(); landed(6);  // (seven stages at least, at H = 128)
+    cp_async_wait<5>(); landed(3);  // (four stages at least)
+    if (stages > 4) { cp_async_wait<4>(); landed(4); }
+    if (stages > 5) { cp_async_wait<3>(); landed(5); }
+    if (stages > 6) { cp_async_wait<2>(); landed(6); }
     if (stages > 7) { cp_async_wait<1>(); landed(7); }
     if (stages > 8) { cp_async_wait<0>(); landed(8); }
+    // The others go out as their stage is free, and are waited for one behind
+    // (with four stages the last five are a chain of loads else).
     for (int k = stages; k < kBoxes && ok; ++k) {
       ok = mbar_wait(smem_u32(&free_[k - stages]), 0, &abort_sh, &timeout_sh);
       if (!ok) break;
       copy(k);
       cp_async_commit();
+      if (k > stages) {
+        cp_async_wait<1>();
+        landed(k - 1);
+      }
     }
     cp_async_wait<0>();
-    for (int k = stages; k < kBoxes && ok; ++k) landed(k);
+    if (ok && stages < kBoxes) landed(kBoxes - 1);
     ok = ok && mbar_wait(smem_u32(&done), 0, &abort_sh, &timeout_sh);
     if (__all_sync(0xffffffffu, ok)) {
       tc_fence_after();
-      float top = -INFINITY;
-      for (int h = 0; h < H; h += 16) {
-        uint32_t v[16];
-        tmem_ld_x16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + h, v);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, __uint_as_float(v[i]));
-      }
       const int j = page0 + threadIdx.x;
-      if (j < max_pages) out[j] = j < seen ? top : -INFINITY;
+      for (int t = t0; t < t1; ++t) {
+        float top = -INFINITY;
+        for (int h = (t - t0) * H; h < (t - t0 + 1) * H; h += 16) {
+          uint32_t v[16];
+          tmem_ld_x16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + h, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+        }
+        if (j < max_pages)
+          out[static_cast<size_t>(t) * max_pages + j] =
+              j < (L - T + t + kPage) / kPage ? top : -INFINITY;
+      }
     }
   } else if (elect_one()) {
     // One thread brings the queries and issues the MMAs.
-    const int row = (b * T + t) * H;
+    const int row = (b * T + t0) * H;
     auto load = [&](int k) {
       const uint32_t dst = base + (k % stages) * stage_bytes + kScoreABytes;
-      mbar_expect_tx(smem_u32(&full[k]), H * 128);
-      tma_load_2d(dst, &tm_q, k * kBoxCols, row, smem_u32(&full[k]));
+      mbar_expect_tx(smem_u32(&full[k]), rows * 128);
+      for (int r = 0; r < rows; r += H)
+        tma_load_2d(dst + r * 128, &tm_q, k * kBoxCols, row + r, smem_u32(&full[k]));
     };
     int loaded = 0;
     for (; loaded < stages; ++loaded) load(loaded);
-    const uint32_t idesc = idesc_bf16_f32(kScorePages, H, false, false);
+    const uint32_t idesc = idesc_bf16_f32(kScorePages, rows, false, false);
     for (int k = 0; k < kBoxes && ok; ++k) {
       ok = mbar_wait(smem_u32(&full[k]), 0, &abort_sh, &timeout_sh);
       if (!ok) break;
@@ -201,7 +221,7 @@ score_kernel(const __grid_constant__ CUtensorMap tm_q, const uint8_t* __restrict
   __syncthreads();
   if (warp == 4) {
     tc_fence_after();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, kScoreRowsMax);
     if (lane == 0 && timeout_sh) record_status(status, MLA_STATUS_TIMEOUT);
   }
 }
@@ -234,14 +254,19 @@ __device__ __forceinline__ int block_rank(bool flag, int* warp_cnt, int* total) 
   return before + __popc(m & ((1u << lane) - 1u));
 }
 
-// One CTA per query token.
+// One CTA per query token: a radix selection of the key of the last page taken,
+// eight bits at a time, then one ordered pass over the pages.  A line's keys are
+// read once into shared memory where they fit (131k tokens).
+constexpr int kSelKeys = 2048;
+
 __global__ void __launch_bounds__(kSelThreads)
 select_kernel(const float* __restrict__ scores, const int32_t* __restrict__ block_table,
               const int32_t* __restrict__ seq_lens, int T, int max_pages, int top_k,
               int keep_first, int keep_last, int32_t* __restrict__ sel_table,
               int32_t* __restrict__ sel_pages, int32_t* __restrict__ sel_lens,
               int32_t* __restrict__ status) {
-  __shared__ int hist[256];
+  __shared__ int hist[4][256];
+  __shared__ uint32_t keys_sh[kSelKeys];
   __shared__ int warp_cnt[kSelThreads / 32];
   __shared__ uint32_t prefix_sh;
   __shared__ int need_sh;
@@ -260,15 +285,20 @@ select_kernel(const float* __restrict__ scores, const int32_t* __restrict__ bloc
   // with just that key are selected (those of the lowest numbers).
   uint32_t last_key = 0;
   int need = 0;
+  const bool held = seen <= kSelKeys;
+  auto key = [&](int j) { return held ? keys_sh[j] : order_key(s[j]); };
   if (seen > top_k) {
     need = top_k - keep_first - keep_last;
+    for (int i = threadIdx.x; i < 4 * 256; i += kSelThreads) (&hist[0][0])[i] = 0;
+    if (held)
+      for (int j = threadIdx.x; j < seen; j += kSelThreads) keys_sh[j] = order_key(s[j]);
+    __syncthreads();
     uint32_t mask = 0;
     for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
-      for (int i = threadIdx.x; i < 256; i += kSelThreads) hist[i] = 0;
-      __syncthreads();
+      int* const h = hist[shift >> 3];
       for (int j = keep_first + threadIdx.x; j < seen - keep_last; j += kSelThreads) {
-        const uint32_t u = order_key(s[j]);
-        if ((u & mask) == last_key) atomicAdd(&hist[(u >> shift) & 255], 1);
+        const uint32_t u = key(j);
+        if ((u & mask) == last_key) atomicAdd(&h[(u >> shift) & 255], 1);
       }
       __syncthreads();
       if (threadIdx.x < 32) {
@@ -276,8 +306,10 @@ select_kernel(const float* __restrict__ scores, const int32_t* __restrict__ bloc
         // `need`: lane i owns bins 255 - 8 i downwards.
         const int lane = threadIdx.x;
         int own = 0;
-        for (int k = 0; k < 8; ++k) own += hist[255 - 8 * lane - k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) own += h[255 - 8 * lane - k];
         int upto = own;
+#pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int v = __shfl_up_sync(0xffffffffu, upto, o);
           if (lane >= o) upto += v;
@@ -285,7 +317,7 @@ select_kernel(const float* __restrict__ scores, const int32_t* __restrict__ bloc
         const int before = upto - own;
         if (before < need && need <= upto) {
           int left = need - before, bin = 255 - 8 * lane;
-          while (left > hist[bin]) left -= hist[bin--];
+          while (left > h[bin]) left -= h[bin--];
           prefix_sh = last_key | (static_cast<uint32_t>(bin) << shift);
           need_sh = left;
         }
@@ -294,7 +326,6 @@ select_kernel(const float* __restrict__ scores, const int32_t* __restrict__ bloc
       last_key = prefix_sh;
       need = need_sh;
       mask |= 255u << shift;
-      __syncthreads();
     }
     if (top_k == keep_first + keep_last) last_key = 0xffffffffu;  // none by score
   }
@@ -303,7 +334,7 @@ select_kernel(const float* __restrict__ scores, const int32_t* __restrict__ bloc
     const int j = j0 + threadIdx.x;
     bool take = j < seen, tie = false;
     if (seen > top_k && take && j >= keep_first && j < seen - keep_last) {
-      const uint32_t u = order_key(s[j]);
+      const uint32_t u = key(j);
       take = u > last_key;
       tie = u == last_key;
     }
@@ -333,11 +364,13 @@ cudaError_t launch_score(const CUtensorMap& tm_q, const void* page_keys,
                          const int32_t* block_table, const int32_t* seq_lens, int B, int T, int H,
                          int num_pages, int max_pages, float* scores, int32_t* status,
                          cudaStream_t st) {
-  const int smem = 1024 + score_stages(H) * score_stage_bytes(H);
+  const int tokens = score_tokens(T, H), rows = tokens * H;
+  const int smem = 1024 + score_stages(rows) * score_stage_bytes(rows);
+  static_assert(score_stages(kScoreRowsMax) >= kStagesMin, "the gather waits for four stages");
   const cudaError_t e =
       cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const dim3 grid((max_pages + kScorePages - 1) / kScorePages, T, B);
+  const dim3 grid((max_pages + kScorePages - 1) / kScorePages, (T + tokens - 1) / tokens, B);
   return launch_pdl(score_kernel, grid, dim3(kScoreThreads), smem, st, tm_q,
                     static_cast<const uint8_t*>(page_keys), block_table, seq_lens, T, H,
                     num_pages, max_pages, scores, status);

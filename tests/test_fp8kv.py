@@ -132,6 +132,10 @@ def run_append(rows, new_lens, table, lens, kv8, kvs, pages, pass_new=True):
     ([130, 130, 130], [130, 67, 2], 131),                # whole, from inside a page, two rows
     ([0, 17, 0, 300], [0, 17, 0, 3], 40),                # unused lines of the batch
     ([1000, 513], [999, 512], 1000),
+    ([128, 100], [128, 33], 128),                        # a table of two pages
+    ([32 + 40, 33 + 40, 95], [32, 0, 31], 32),           # the two kernels' border
+    ([33 + 40, 20], [33, 20], 33),
+    ([1 + i % 70 for i in range(300)], [(1 + i % 70) // 2 for i in range(300)], 35),
 ])
 def test_append_equals_the_definition(lens, new, max_new):
     # The definition is exact (powers of two, one rounding): codes and scales
