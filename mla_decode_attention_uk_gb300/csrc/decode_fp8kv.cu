@@ -29,8 +29,8 @@
 // Per page and 64 query rows: QK^T 18 MMAs of 128 x 64 x 32, PV 16 of
 // 128 x N x 32 (N: the tile's rows).  The rest is as in decode.cu: the
 // producer warp brings pages into a ring of slots (five of 40 KB next to the
-// query's RoPE terms; a page is two copies, and five pages in flight need no
-// prefetch into L2; a piece's query tile passes through two of the slots), the softmax runs on TMEM rows with a running
+// query's RoPE terms; a page is two copies, and with five in flight prefetching
+// into L2 only costs: 35 -> 39 us on 64 x 4096 x 16 heads, eight pages ahead; a piece's query tile passes through two of the slots), the softmax runs on TMEM rows with a running
 // maximum that is raised lazily, P^T goes into the page's RoPE box, and O^T
 // stays in TMEM.  The page's scale joins the exponent (p_j s = 2^(x_j + log2 s
 // - m), m the running maximum of that sum), so that P never leaves E5M2's

@@ -91,6 +91,8 @@ def test_python_calls_check_types_and_shapes():
         binding.append_fp8kv(d, **good, new_lens=lens.long())
     with pytest.raises(ValueError):
         binding.append_fp8kv(d, **good, status=torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="CUDA device"):
+        binding.append_fp8kv(d, **good)  # right shapes, but in host memory
 
 
 # ---------------------------------------------------------------- append
@@ -278,6 +280,44 @@ def test_attention_any_split(H, T, ranges):
 
 
 @gpu
+@pytest.mark.parametrize("H,T,ranges", [(16, 1, 1), (128, 1, 1), (16, 1, 0), (128, 2, 0), (32, 8, 3)])
+def test_attention_many_pieces_of_a_page_or_two(H, T, ranges):
+    # Sequences of one to three pages, several (with one range: all) of them to a
+    # CTA: query tiles and pages of the next pieces enter the ring while the
+    # first are still in work, from the first round of its slots on.
+    lens = [max(T, 1 + (37 * i) % 190) for i in range(40 if ranges else 400)]
+    lens[0] = T
+    inp, kv8, kvs = fp8_inputs(make_inputs(len(lens), lens, T, H, seed=43))
+    out, lse = run_fp8(inp, kv8, kvs, num_ranges=ranges)
+    assert_parity(compare(inp, out, lse), "ranges %d" % ranges)
+    out2, lse2 = run_fp8(inp, kv8, kvs, num_ranges=ranges)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+@gpu
+def test_attention_repeated_runs_give_the_same_bits_while_memory_is_busy():
+    # 64 sequences of 64 pages: every SM streams, loads are slow and the pipeline
+    # runs out of pages.  Ten runs between copies that evict the cache from L2.
+    inp, kv8, kvs = fp8_inputs(make_inputs(64, [4096 - 7 * i for i in range(64)], 1, 16, seed=44))
+    g = inp.to(torch.device("cuda"))
+    k, s = kv8.cuda(), kvs.cuda()
+    m = binding.MlaDecode(binding.dims_for(g.q, g.cache, g.block_table), fp8_kv=True)
+    big = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    results = []
+    for i in range(10):
+        out = torch.empty(64, 1, 16, 128, dtype=BF, device="cuda")
+        lse = torch.empty(64, 1, 16, device="cuda")
+        big.fill_(i)
+        m.plan(g.seq_lens)
+        m.run_fp8kv(g.q, k, s, g.block_table, g.seq_lens, g.w_uk, g.w_uv, g.scale, out, lse)
+        results.append((out, lse))
+    assert m.check() == 0
+    for out, lse in results[1:]:
+        assert torch.equal(out, results[0][0]) and torch.equal(lse, results[0][1])
+    assert_parity(compare(inp, results[0][0].cpu(), results[0][1].cpu()), "64 x 4096")
+
+
+@gpu
 def test_attention_large_batch_takes_the_large_paths():
     lens = torch.randint(1, 400, (300,), generator=torch.Generator().manual_seed(22)).tolist()
     lens = [max(2, n) for n in lens]
@@ -385,6 +425,30 @@ def test_lengths_out_of_range_are_clamped_and_reported():
     inp.seq_lens = torch.tensor([100, 0], dtype=torch.int32)
     out, lse = run_fp8(inp, kv8, kvs, expect=5)
     assert torch.equal(out[0], out0[0]) and torch.equal(lse[0], lse0[0])
+
+
+@gpu
+def test_the_plans_for_either_cache_differ_and_serve_both():
+    lens = [1 + 13 * i % 700 for i in range(200)]
+    inp, kv8, kvs = fp8_inputs(make_inputs(200, lens, 1, 64, seed=45))
+    g = inp.to(torch.device("cuda"))
+    d = binding.dims_for(g.q, g.cache, g.block_table)
+    results = []
+    for fp8_kv in (False, True):
+        m = binding.MlaDecode(d, fp8_kv=fp8_kv)
+        m.plan(g.seq_lens)
+        pages = sum((n + 63) // 64 for n in lens)
+        assert m.plan_header()[2] == pages + 200 * (6 if fp8_kv else 2)
+        for kind in ("bf16", "fp8"):
+            out = torch.empty(200, 1, 64, 128, dtype=BF, device="cuda")
+            lse = torch.empty(200, 1, 64, device="cuda")
+            if kind == "fp8":
+                m.run_fp8kv(g.q, kv8.cuda(), kvs.cuda(), g.block_table, g.seq_lens, g.w_uk,
+                            g.w_uv, g.scale, out, lse)
+            else:
+                m.run(g.q, g.cache, g.block_table, g.seq_lens, g.w_uk, g.w_uv, g.scale, out, lse)
+            assert m.check() == 0
+            assert_parity(compare(inp, out.cpu(), lse.cpu()), kind)
 
 
 @gpu

@@ -81,6 +81,8 @@ def test_python_calls_check_types_and_shapes():
         binding.select_pages(d, scores, table, lens, 3, 1, 1, sel, sl, sel_pages=sel.long())
     with pytest.raises(ValueError):
         binding.page_keys(d, torch.zeros(4, 64, 576), table, lens, 1, keys)
+    with pytest.raises(ValueError, match="CUDA device"):
+        binding.score_pages(d, q, keys, table, lens, scores)  # in host memory
     with pytest.raises(ValueError):
         binding.page_keys_fp8kv(d, torch.zeros(4, 64, 576, dtype=torch.uint8), torch.ones(3),
                                 table, lens, 1, keys)
