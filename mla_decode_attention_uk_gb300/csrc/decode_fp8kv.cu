@@ -11,30 +11,30 @@
 // K = 32 per instruction), so the codes go from memory to the tensor core as
 // they are, half the bytes of a bf16 page at every level.  What the other
 // operand loses in 8 bits is given back by a second term:
-//   * Q = scale_row (hi + mid / 16), both E4M3: hi is the value rounded to four
-//     bits, mid the rest times 16.  A bf16 value has eight significant bits and
-//     the two terms hold it exactly (down to 2^-13 of the row's largest value
-//     and, below that, to 2^-22 of it), so the product is that of the bf16
-//     query.  The terms are stacked as the M = 128 rows of one MMA: the full
-//     rate of the tensor core for 64 query rows, where a 64-row MMA would run at
-//     half of it.  The 512 latent columns of the terms live in TMEM (128
-//     columns), so that QK^T reads only the page from shared memory, and the 64
-//     KB that they would take there hold two more pages.
-//   * P = hi + mid, both E5M2, eight bits wide of fp16: as both accumulate into
+//   * Q = scale_row (hi + mid / 16), both E4M3: hi is the value cut to four
+//     significant bits, mid the rest times 16.  A bf16 value has eight and the
+//     two terms hold it exactly (down to 2^-13 of the row's largest value; below
+//     that to 2^-21 of it), so the product is that of the bf16 query.  The terms
+//     are stacked as the M = 128 rows of one MMA: the full rate of the tensor
+//     core for 64 query rows, where a 64-row MMA would run at half of it.  The
+//     512 latent columns of the terms live in TMEM (128 columns), so that QK^T
+//     reads only the page from shared memory (32 cycles an MMA instead of 48),
+//     and the 64 KB that they would take there hold two more pages.
+//   * P = hi + mid, both E5M2, the upper bytes of fp16: as both accumulate into
 //     the same columns they cannot have scales of their own, and E5M2's range
 //     (2^-16 to 2^15) keeps the small weights of a long context next to a large
 //     one, which E4M3's would drop.  Two terms leave at most 2^-7 of a weight;
 //     the row is divided by the sum of the weights as rounded, so a rounding
 //     that all weights share cancels, and the lse takes the unrounded sum.
-// Per page and 64 query rows: QK^T 18 MMAs of 128 x 64 x 32, PV 16 of
-// 128 x N x 32 (N: the tile's rows).  The rest is as in decode.cu: the
-// producer warp brings pages into a ring of slots (five of 40 KB next to the
-// query's RoPE terms; a page is two copies, and with five in flight prefetching
-// into L2 only costs: 35 -> 39 us on 64 x 4096 x 16 heads, eight pages ahead; a piece's query tile passes through two of the slots), the softmax runs on TMEM rows with a running
-// maximum that is raised lazily, P^T goes into the page's RoPE box, and O^T
-// stays in TMEM.  The page's scale joins the exponent (p_j s = 2^(x_j + log2 s
-// - m), m the running maximum of that sum), so that P never leaves E5M2's
-// range however the scales of a sequence's pages differ.
+// Per page and 64 query rows: QK^T 18 MMAs of 128 x 64 x 32, PV 16 of 128 x N x 32
+// (N: the tile's rows; O^T = C^T P^T, M = 128 latent columns).  A page comes in two
+// copies into a ring of five 40 KB slots; a piece's query tile passes through
+// two of them on its way to the terms.  The softmax runs on TMEM rows with a
+// running maximum that is raised lazily, P^T goes into the page's RoPE box, O^T
+// stays in TMEM.  The page's scale joins the exponent (p_j s = 2^(x_j + log2 s -
+// m), m the running maximum of that sum), so that P never leaves E5M2's range
+// however the scales of a sequence's pages differ.
+//
 // Warp roles: 0 TMA producer, 1 QK^T issuer, 2 and 3 PV issuers (latent halves;
 // warp 2 also owns TMEM), 4-7 and 8-11 softmax and epilogue, 12-15 query terms.
 // The two softmax groups take turns, page by page: a page's chain of waits,
@@ -45,6 +45,16 @@
 // for the page before, and the sums, which each keeps for itself, follow it.
 // (QK^T has one issuer: two that took turns would each see only some phases of a
 // slot's barriers.)
+//
+// What bounds it: with 64 rows the tensor pipe, whose 34 MMAs take 1,376 cycles of
+// the 1,500 that a page takes (PV 768, bound by shared-memory reads: 6 KB per
+// MMA of 4 KB worth); with 16 heads memory, 6.1 TB/s while pages stream.  Beside
+// the pages a piece costs 5 to 6 us (its query terms and its epilogue are not
+// hidden by each other's pages) and a launch 8 us.  Measured (one GB300, with the
+// query terms' tile, without absorb and merge): 64 sequences of 4,096 tokens x 16
+// heads 35 us; 128 of 1,000-10,000 (500k tokens) x 128 heads 113 us; 61 ragged
+// drafts of 4 queries x 128 heads (133k tokens) 100 us.  Prefetching pages into
+// L2 ahead of the ring only cost: 35 -> 39 us on the first, eight pages ahead.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -157,13 +167,13 @@ struct Pieces {
   }
   __device__ bool next(const Params& P, const PlanView& V, Piece& out) {
     while (v < V.tasks) {
-      while (b < b1 || (b == b1 && p < p1)) {
+      if (b < b1 || (b == b1 && p < p1)) {  // (never empty: a range starts inside a sequence)
         const int L = P.seq_len_eff[b];
         const int end = b == b1 ? p1 : (L + kPage - 1) / kPage;
         out = Piece{v, b, p, end, L};
         ++b;
         p = 0;
-        if (out.pend > out.pbeg) return true;
+        return true;
       }
       v += gridDim.x / P.tpg;
       open(P, V);
@@ -588,7 +598,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
         }
         // One barrier of the group per page: a raised maximum (the group then
         // rescales O^T, rows are its columns), or a wait that gave up.
-        if (bar_any(1 + q, 128, bad || raise)) {
+        if (bar_any(1 + q, 128, bad || (raise && !first))) {
           bool f = *static_cast<volatile int*>(&abort_sh) != 0;
           if (owner) alpha_sh[q][srow] = raise ? ex2_approx(m_old - pmax) : 1.0f;
           if (!f && !first &&
