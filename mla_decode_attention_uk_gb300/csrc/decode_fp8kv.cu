@@ -199,7 +199,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
   __shared__ float page_scale_sh[kSlots], q_scale_sh[kTileRows];
   __shared__ float alpha_sh[2][kTileRows], m_sh[kTileRows];
   __shared__ __align__(16) float inv_sh[8][kTileRows];
-  __shared__ float amax_sh[3][kTileRows], l_sh[2][kTileRows], l_r_sh[2][kTileRows], m_l_sh[2][kTileRows];
+  __shared__ float l_sh[2][kTileRows], l_r_sh[2][kTileRows], m_l_sh[2][kTileRows];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Tasks v = range * sets + set are dealt round robin to groups of tpg CTAs;
@@ -438,42 +438,77 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
     bool have = walk.next(P, view, pc);
     while (!fail && have) {
       if (n == 0 || !softmax) {
-        // Columns 64 block + 8 j + 4 par .. + 3 of this row.
-        auto word = [&](int block, int j) {
+        // Where columns 64 block + 8 j + 4 half .. + 3 of a row are: four bf16
+        // values, or in their place a word of hi codes and one of mid codes.
+        auto word = [&](int row, int block, int j, int half) {
           const int ring = g + 2 * n + (block >= kBoxes8 ? 1 : 0);
-          return ld_shared_v2(sSlot0 + (ring % kSlots) * kSlot + (block % kBoxes8) * kBox +
-                              srow * 128 + ((j ^ (srow & 7)) << 4) + 8 * par);
+          return sSlot0 + (ring % kSlots) * kSlot + (block % kBoxes8) * kBox + row * 128 +
+                 ((j ^ (row & 7)) << 4) + 8 * half;
         };
-        const int b0 = n == 0 ? 3 * ((warp - 4) >> 2) : 0, b1 = n == 0 ? b0 + 3 : kBoxes;
+        const int rows_here = min(kTileRows, TH - ((pc.task % sets) * tpg + ti) * kTileRows);
         bool ok = mbar_wait(smem_u32(&q_raw), n & 1, &abort_sh, P.status);
-        // The row's scale: its largest value takes the top but one of E4M3's
-        // binades.
-        __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
-#pragma unroll 1
-        for (int block = b0; block < b1; ++block)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint2 x = word(block, j);
-            top = __hmax2(__hmax2(top, __habs2(as_bf162(x.x))), __habs2(as_bf162(x.y)));
-          }
-        float amax = fmaxf(__low2float(top), __high2float(top));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        // A row's largest value takes the top but one of E4M3's binades.
+        int e = 0;
         if (n == 0) {
-          if (par == 0) amax_sh[(warp - 4) >> 2][srow] = amax;
+          // All warps share the rows out, whatever TMEM lanes they belong to (16
+          // heads would leave three quarters of the SM idle else), and make the
+          // terms in place.
+          for (int row = warp - 4; row < rows_here; row += 12) {
+            uint2 x[5];  // words lane, lane + 32, ... of the row's 144
+            __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+              const int w = lane + 32 * i;
+              x[i] = make_uint2(0u, 0u);
+              if (i < 4 || lane < 16) x[i] = ld_shared_v2(word(row, w >> 4, (w >> 1) & 7, w & 1));
+              top = __hmax2(__hmax2(top, __habs2(as_bf162(x[i].x))), __habs2(as_bf162(x[i].y)));
+            }
+            float amax = fmaxf(__low2float(top), __high2float(top));
+            amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+            const int er = page_scale_exp(amax) + 1;  // amax <= 224 * 2^er
+            const __nv_bfloat162 down = __float2bfloat162_rn(exp2_int(max(-126, -er - 120)));
+            if (lane == 0) q_scale_sh[row] = exp2_int(er);
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+              const int w = lane + 32 * i;
+              uint32_t hi, mid;
+              split_terms(x[i], down, hi, mid);
+              if (i < 4 || lane < 16) st_shared_v2(word(row, w >> 4, (w >> 1) & 7, w & 1), hi, mid);
+            }
+          }
           named_bar_sync(3, 384);
-          amax = fmaxf(amax_sh[0][srow], fmaxf(amax_sh[1][srow], amax_sh[2][srow]));
+        } else {
+          __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
+#pragma unroll 1
+          for (int block = 0; block < kBoxes; ++block)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint2 x = ld_shared_v2(word(srow, block, j, par));
+              top = __hmax2(__hmax2(top, __habs2(as_bf162(x.x))), __habs2(as_bf162(x.y)));
+            }
+          float amax = fmaxf(__low2float(top), __high2float(top));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          e = page_scale_exp(amax) + 1;
+          ok = ok && mbar_wait(smem_u32(&q_free), (n - 1) & 1, &abort_sh, P.status);
         }
-        const int e = page_scale_exp(amax) + 1;  // amax <= 224 * 2^e
         const __nv_bfloat162 down = __float2bfloat162_rn(exp2_int(max(-126, -e - 120)));
-        ok = ok && (n == 0 || mbar_wait(smem_u32(&q_free), (n - 1) & 1, &abort_sh, P.status));
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        if (par == 0 && !softmax) q_scale_sh[srow] = exp2_int(e);
+        if (par == 0 && n > 0) q_scale_sh[srow] = exp2_int(e);
+        const int b0 = n == 0 ? 3 * ((warp - 4) >> 2) : 0, b1 = n == 0 ? b0 + 3 : kBoxes;
 #pragma unroll 1
         for (int block = b0; block < b1; ++block) {
           uint32_t hi[8], mid[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) split_terms(word(block, j), down, hi[j], mid[j]);
+          for (int j = 0; j < 8; ++j) {
+            const uint2 x = ld_shared_v2(word(srow, block, j, par));
+            hi[j] = x.x;
+            mid[j] = x.y;
+          }
+          if (n > 0)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              split_terms(make_uint2(hi[j], mid[j]), down, hi[j], mid[j]);
           if (block < kLatBoxes) {
             const uint32_t ta = tmem + lane_off + kTmemQ + 16 * block;
             tmem_st_16x64b_x8(ta, hi);
