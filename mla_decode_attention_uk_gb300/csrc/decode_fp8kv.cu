@@ -420,9 +420,11 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
     // ------------------------------------------------------------ query terms
     // Warps 12-15 turn the query tile into its terms, warp 12 + w tile rows 16 w
     // .. + 15, between the end of a piece's QK^T and that of its epilogue.  (A
-    // kernel of its own took 3 to 14 us.)  The terms of a CTA's first piece, which
-    // waits for them, are the work of all twelve warps, three of the nine blocks
-    // of 64 columns each (the last block is the RoPE columns).
+    // kernel of its own took 3 to 14 us; the softmax warps' help, between their
+    // last page and the epilogue, made the step slower: 138 -> 144 us on 128
+    // sequences x 128 heads; making the terms in place before QK^T's end and
+    // copying them after it too: 146.)  A CTA's first piece waits for its terms,
+    // so all twelve warps make them.
     //
     // Lane layout of TMEM loads and stores of 16 lanes x 64 bits: this thread has
     // row rig of the quarter's 16, and the words (four codes) or keys of parity
