@@ -228,8 +228,10 @@ int mla_decode_up_project_fp8w(const mla_decode_dims* dims, const uint8_t* w_uv_
  * finite new value, within [2^-32, 2^32] (values beyond 448 * 2^32 saturate,
  * infinities too; NaN stays NaN).  A page whose first token is among the new
  * ones starts afresh: its scale is that of the new tokens, and its rows past
- * them are cleared.  In any other page the scale only grows; when it does, the
- * rows that stay are re-coded under the new scale (round to nearest even).
+ * them are cleared.  In any other page the scale only grows, from the page's
+ * rounded up to a power of two; when it does, the rows that stay are re-coded
+ * under the new scale (round to nearest even).  A page's scale outside [2^-32,
+ * 2^32] is taken as 1, with DEVICE_BOUNDS.
  * Positions past max_pages_per_seq * 64, n_b outside [0, min(max_new, length)]
  * or a block_table entry outside the pool: DEVICE_BOUNDS, and the sequence (the
  * page) is left as it was.  A page that receives tokens must belong to one

@@ -61,11 +61,11 @@ __device__ __forceinline__ uint2 codes8(const uint4& v, __nv_bfloat162 inv) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// Maximum of `top` over the CTA, the same to all; `bad` of any thread in *any_bad.
-__device__ __forceinline__ float block_max(float top, float* warp_top, bool bad, bool* any_bad) {
+// Maximum of `top` over the CTA, the same to all.
+__device__ __forceinline__ float block_max(float top, float* warp_top) {
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
-  *any_bad = __syncthreads_or(bad);
+  __syncthreads();
   for (int w = 0; w < kAppThreads / 32; ++w) top = fmaxf(top, warp_top[w]);
   return top;
 }
@@ -115,14 +115,16 @@ __device__ bool append_page(const AppendParams& P, AppendShared& sh, uint4* rows
               n * 16, smem_u32(&sh.landed));
   }
   // Read before the barrier below: one thread replaces it at the end.
-  const float old = r0 > 0 && in_pool ? P.kv_scale[page] : 0.0f;
-  const bool ok = mbar_wait(smem_u32(&sh.landed), phase, &sh.abort, &sh.timeout);
-  __nv_bfloat162 most = __float2bfloat162_rn(0.0f);
-  if (ok)
-    for (int i = threadIdx.x; i < n; i += kAppThreads) most = absmax8(most, rows_sh[i]);
-  bool timeout;
-  float top = block_max(fmaxf(__low2float(most), __high2float(most)), sh.warp_top, !ok, &timeout);
-  if (timeout) {
+  float old = r0 > 0 && in_pool ? P.kv_scale[page] : 1.0f;
+  if (!scale_in_range(old)) {
+    if (threadIdx.x == 0) record_status(P.status, MLA_STATUS_BOUNDS);
+    old = 1.0f;
+  }
+  // One warp polls, the others sleep at the barrier (sixteen polling warps take
+  // the issue slots of the CTAs that have their rows).
+  bool ok = true;
+  if (threadIdx.x < 32) ok = mbar_wait(smem_u32(&sh.landed), phase, &sh.abort, &sh.timeout);
+  if (!__syncthreads_and(ok)) {
     if (threadIdx.x == 0) {
       record_status(P.status, MLA_STATUS_TIMEOUT);
       mbar_wait_drain(smem_u32(&sh.landed), phase, &sh.timeout);
@@ -130,15 +132,18 @@ __device__ bool append_page(const AppendParams& P, AppendShared& sh, uint4* rows
     __syncthreads();
     return false;
   }
+  __nv_bfloat162 most = __float2bfloat162_rn(0.0f);
+  for (int i = threadIdx.x; i < n; i += kAppThreads) most = absmax8(most, rows_sh[i]);
+  float top = block_max(fmaxf(__low2float(most), __high2float(most)), sh.warp_top);
   if (top == INFINITY) {  // rare: once more, without the infinities
     __syncthreads();
     top = 0.0f;
     for (int i = threadIdx.x; i < n; i += kAppThreads) top = finite_absmax8(top, rows_sh[i]);
-    top = block_max(top, sh.warp_top, false, &timeout);
+    top = block_max(top, sh.warp_top);
   }
   if (!in_pool) return true;
   float scale = exp2_int(page_scale_exp(top));
-  if (r0 > 0) scale = fmaxf(scale, old);
+  if (r0 > 0) scale = fmaxf(scale, next_power_of_two(old));
   uint2* const dst = reinterpret_cast<uint2*>(P.kv8 + static_cast<size_t>(page) * kPageBytes8);
   const __nv_bfloat162 inv = __float2bfloat162_rn(1.0f / scale);
 #pragma unroll 3

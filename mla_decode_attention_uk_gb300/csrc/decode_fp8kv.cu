@@ -278,7 +278,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
           page = 0;
         }
         scale = P.kv_scale[page];
-        if (!(scale >= exp2_int(kScaleExpMin) && scale <= exp2_int(kScaleExpMax))) {
+        if (!scale_in_range(scale)) {
           record_status(P.status, MLA_STATUS_BOUNDS);
           scale = 1.0f;
         }

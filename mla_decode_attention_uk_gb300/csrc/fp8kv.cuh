@@ -48,6 +48,15 @@ __device__ __forceinline__ float exp2_int(int e) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
+// A page's scale within the bounds (not so for NaN).
+__device__ __forceinline__ bool scale_in_range(float s) {
+  return s >= exp2_int(kScaleExpMin) && s <= exp2_int(kScaleExpMax);
+}
+// The smallest power of two that is not below s (s: normal, positive).
+__device__ __forceinline__ float next_power_of_two(float s) {
+  return __uint_as_float((__float_as_uint(s) + 0x7fffffu) & 0x7f800000u);
+}
+
 // Four values to four E4M3 codes, round to nearest even, finite values beyond
 // 448 (infinities too) saturated; NaN keeps NaN's code.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {

@@ -50,7 +50,9 @@ def append(rows, new_lens, block_table, seq_lens, kv8, kv_scale):
             s = scale_for(float(finite.abs().max()) if finite.numel() else 0.0)
             if first > j * PAGE:
                 s_old = float(kv_scale[p])
-                s = max(s, s_old)
+                if not 2.0 ** -32 <= s_old <= 2.0 ** 32:
+                    s_old = 1.0
+                s = max(s, 2.0 ** math.ceil(math.log2(s_old)))
                 if s != s_old:
                     kv8[p] = e4m3(values(kv8[p]) * (s_old / s))
             else:

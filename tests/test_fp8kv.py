@@ -200,6 +200,22 @@ def test_append_special_values():
 
 
 @gpu
+@pytest.mark.parametrize("old,status", [
+    (1.5 * 2.0 ** -6, 0), (0.75, 0), (1.25 * 2.0 ** -20, 0), (2.0 ** 32, 0), (2.0 ** -32, 0),
+    (0.0, 5), (-1.0, 5), (math.nan, 5), (math.inf, 5), (2.0 ** 33, 5), (2.0 ** -33, 5)])
+def test_append_to_a_page_of_any_scale(old, status):
+    # A cache quantised by others, or never: any positive scale is rounded up to
+    # a power of two, one out of range counts as 1.
+    table = torch.tensor([[0, 1]], dtype=torch.int32)
+    kv8, kvs = pool(2, 16)
+    kvs[0] = old
+    rows = torch.randn(1, 30, 576, generator=torch.Generator().manual_seed(17)).to(BF)
+    k, s, st = run_append(rows, [30], table, [50], kv8, kvs, 2)
+    rk, rs = ref.append(rows, [30], table, [50], kv8, kvs)
+    assert st == status and torch.equal(s, rs) and torch.equal(k & 0x7F, rk & 0x7F)
+
+
+@gpu
 @pytest.mark.parametrize("lens,new,why", [
     ([129, 20], [1, 1], "past the table"), ([20, 20], [21, 1], "more new tokens than tokens"),
     ([20, 20], [-1, 1], "negative"), ([20, 20], [5, 1], "more than max_new"),
