@@ -223,7 +223,8 @@ def table_of(B, width, seed):
     ([1], 1, 1, 1, 0, 1), ([64, 65, 640], 1, 10, 3, 1, 1), ([640, 641, 63], 2, 11, 2, 1, 1),
     ([9000, 8, 16384], 8, 256, 16, 0, 1), ([16383, 5000, 20000], 3, 313, 33, 2, 3),
     ([64 * 1500, 64 * 257 + 1], 1, 1500, 300, 1, 2), ([40000], 1, 700, 699, 0, 1),
-    ([128, 100], 1, 2, 5, 2, 3)])
+    ([128, 100], 1, 2, 5, 2, 3),
+    ([64 * 2048, 64 * 2049, 64 * 5000 - 1], 1, 5000, 70, 1, 1)])  # keys that do not fit the CTA
 def test_selection_equals_the_definition(kind, lens, T, width, top_k, first, last):
     g = torch.Generator().manual_seed(55)
     B = len(lens)
@@ -325,3 +326,65 @@ def test_append_score_select_and_decode_together(fp8, T, H):
                               inp.seq_lens)
     for b in (1, 2):
         assert (out.view(B, T, H, 128)[b].cpu().double() - full[b]).abs().max() <= ref.OUT_MAX
+
+
+@gpu
+def test_the_whole_chain_captured_and_replayed_on_another_stream():
+    B, T, H, top_k = 3, 2, 32, 4
+    inp = make_inputs(B, [900, 300, 130], T, H, seed=70)
+    pages, width = inp.cache.shape[0], inp.block_table.shape[1]
+    g = inp.to(torch.device("cuda"))
+    d = binding.Dims(B, T, H, 128, 64, 512, 128, 64, pages, width)
+    m = binding.MlaDecode(binding.Dims(B * T, 1, H, 128, 64, 512, 128, 64, pages, top_k),
+                          fp8_kv=True)
+    kv8, kvs = (x.cuda() for x in ref.quantise(inp.cache))
+    rows = torch.zeros(B, T, 576, dtype=BF, device="cuda")
+    keys = torch.zeros(pages, 576, dtype=BF, device="cuda")
+    scores = torch.empty(B, T, width, device="cuda")
+    st = torch.empty(B * T, top_k, dtype=torch.int32, device="cuda")
+    sl = torch.empty(B * T, dtype=torch.int32, device="cuda")
+    out = torch.empty(B * T, 1, H, 128, dtype=BF, device="cuda")
+    lse = torch.empty(B * T, 1, H, device="cuda")
+    q_lat = m.q_lat().view(B, T, H, 576)
+    # The pages that were there before this step.
+    binding.page_keys_fp8kv(d, kv8, kvs, g.block_table, g.seq_lens, 900, keys, g.seq_lens)
+
+    def step():
+        binding.append_fp8kv(d, rows, kv8, kvs, g.block_table, g.seq_lens)
+        binding.page_keys_fp8kv(d, kv8, kvs, g.block_table, g.seq_lens, T, keys)
+        m.absorb(g.q.view(B * T, 1, H, 192), g.w_uk)
+        binding.score_pages(d, q_lat, keys, g.block_table, g.seq_lens, scores)
+        binding.select_pages(d, scores, g.block_table, g.seq_lens, top_k, 1, 1, st, sl)
+        m.plan(sl)
+        m.run_fp8kv(g.q, kv8, kvs, st, sl, g.w_uk, g.w_uv, g.scale, out, lse)
+
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    saved = kv8.clone(), kvs.clone(), keys.clone()
+    with torch.cuda.stream(stream):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step()
+    torch.cuda.synchronize()
+    for seed, lens in ((71, [900, 300, 130]), (72, [850, 257, 66]), (73, [64, 2, 129])):
+        gen = torch.Generator().manual_seed(seed)
+        new = torch.randn(B, T, 576, generator=gen).to(BF)
+        q = torch.randn(B, T, H, 192, generator=gen).to(BF)
+        for x, y in zip((kv8, kvs, keys), saved):
+            x.copy_(y)
+        rows.copy_(new)
+        g.q.copy_(q)
+        g.seq_lens.copy_(i32(lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert m.check() == 0
+        rk, rs = ref.append(new, [T] * B, inp.block_table, lens, saved[0].cpu(), saved[1].cpu())
+        assert torch.equal(kv8.cpu(), rk) and torch.equal(kvs.cpu(), rs)
+        rt, _, rl = ref.select(scores.cpu(), inp.block_table, lens, T, top_k, 1, 1)
+        assert torch.equal(st.cpu(), rt) and torch.equal(sl.cpu(), rl)
+        cache = (ref.values(rk) * rs.double()[:, None, None]).to(BF)
+        o, l = expected(q.view(B * T, 1, H, 192), cache, inp.w_uk, inp.w_uv, inp.scale, rt, rl)
+        err = (out.cpu().double() - o).abs()
+        assert err.max() <= ref.OUT_MAX and err.mean() <= ref.OUT_MEAN
+        assert (lse.cpu().double() - l).abs().max() <= 1e-3
