@@ -174,22 +174,26 @@ class MlaDecode:
             "mla_decode_run_fp8w")
 
     def run_fp8kv(self, q, kv8, kv_scale, block_table, seq_lens, w_uk, w_uv, scale, out, lse):
-        _fp8kv_tensors(self.dims, kv8, kv_scale)
-        _ok(lib().mla_decode_run_fp8kv(ctypes.byref(self.dims), _ptr(q), _ptr(kv8),
-                                       _ptr(kv_scale), _ptr(block_table), _ptr(seq_lens),
-                                       _ptr(w_uk), _ptr(w_uv), float(scale), _ptr(out),
-                                       _ptr(lse), _ptr(self.workspace), self.ws_bytes,
-                                       _stream_of(q, kv8, kv_scale, block_table, seq_lens, w_uk,
-                                                  w_uv, out, lse, self.workspace)),
+        d = self.dims
+        stream = _checked(("kv8", kv8, torch.uint8, (d.num_pages, 64, 576)),
+                          ("kv_scale", kv_scale, torch.float32, (d.num_pages,)),
+                          *_lines(d, block_table, seq_lens))
+        _ok(lib().mla_decode_run_fp8kv(ctypes.byref(d), _ptr(q), kv8.data_ptr(),
+                                       kv_scale.data_ptr(), block_table.data_ptr(),
+                                       seq_lens.data_ptr(), _ptr(w_uk), _ptr(w_uv), float(scale),
+                                       _ptr(out), _ptr(lse), _ptr(self.workspace), self.ws_bytes,
+                                       stream),
             "mla_decode_run_fp8kv")
 
     def attend_fp8kv(self, kv8, kv_scale, block_table, seq_lens, scale, lse):
-        _fp8kv_tensors(self.dims, kv8, kv_scale)
-        _ok(lib().mla_decode_attend_fp8kv(ctypes.byref(self.dims), _ptr(kv8), _ptr(kv_scale),
-                                          _ptr(block_table), _ptr(seq_lens), float(scale),
-                                          _ptr(lse), _ptr(self.workspace), self.ws_bytes,
-                                          _stream_of(kv8, kv_scale, block_table, seq_lens, lse,
-                                                     self.workspace)),
+        d = self.dims
+        stream = _checked(("kv8", kv8, torch.uint8, (d.num_pages, 64, 576)),
+                          ("kv_scale", kv_scale, torch.float32, (d.num_pages,)),
+                          *_lines(d, block_table, seq_lens))
+        _ok(lib().mla_decode_attend_fp8kv(ctypes.byref(d), kv8.data_ptr(), kv_scale.data_ptr(),
+                                          block_table.data_ptr(), seq_lens.data_ptr(),
+                                          float(scale), _ptr(lse), _ptr(self.workspace),
+                                          self.ws_bytes, stream),
             "mla_decode_attend_fp8kv")
 
     def absorb_fp8w(self, q, w_uk8, w_uk_scale):
@@ -264,38 +268,35 @@ def decode(q, cache, block_table, seq_lens, w_uk, w_uv, scale, num_ranges: int =
 
 
 # ---------------------------------------------------------------- 8-bit cache, sparse decode
-def _need(name, t, dtype, *shape):
-    """The C ABI sees pointers only: type, shape and layout are checked here."""
-    if t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        got = None if t is None else (t.dtype, tuple(t.shape), t.is_contiguous())
-        raise ValueError("%s: expected a contiguous %s tensor of shape %s, got %s"
-                         % (name, dtype, shape, got))
+def _refuse(name, t, dtype, shape):
+    got = None if t is None else (t.dtype, tuple(t.shape), t.is_contiguous(), str(t.device))
+    raise ValueError("%s: expected a contiguous %s tensor of shape %s on the current CUDA device, "
+                     "with the other tensors, got %s" % (name, dtype, shape, got))
 
 
-def _stream_of(*tensors):
-    """The current device's current stream; every tensor must be on that device."""
-    device = tensors[0].get_device()
+def _checked(*tensors):
+    """The current stream, once every (name, tensor, dtype, shape) is what it should
+    be: the C ABI sees pointers only.  (One loop without helpers: the checks are
+    most of a small call's time on the host.)"""
+    device = tensors[0][1].get_device()
+    for name, t, dtype, shape in tensors:
+        if (t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+                or t.get_device() != device):
+            _refuse(name, t, dtype, shape)
     if device < 0 or device != torch._C._cuda_getDevice():
-        raise ValueError("the tensors must be on the current CUDA device")
-    for t in tensors:
-        if t is not None and t.get_device() != device:
-            raise ValueError("the tensors must be on one CUDA device")
+        _refuse(*tensors[0])
     return torch._C._cuda_getCurrentRawStream(device)
 
 
-def _fp8kv_tensors(d, kv8, kv_scale):
-    _need("kv8", kv8, torch.uint8, d.num_pages, 64, 576)
-    _need("kv_scale", kv_scale, torch.float32, d.num_pages)
-
-
 def _lines(d, block_table, seq_lens, new_lens=None, status=None):
-    batch = d.batch
-    _need("block_table", block_table, torch.int32, batch, d.max_pages_per_seq)
-    _need("seq_lens", seq_lens, torch.int32, batch)
+    B = d.batch
+    lines = [("block_table", block_table, torch.int32, (B, d.max_pages_per_seq)),
+             ("seq_lens", seq_lens, torch.int32, (B,))]
     if new_lens is not None:
-        _need("new_lens", new_lens, torch.int32, batch)
+        lines.append(("new_lens", new_lens, torch.int32, (B,)))
     if status is not None:
-        _need("status", status, torch.int32, 1)
+        lines.append(("status", status, torch.int32, (1,)))
+    return lines
 
 
 def append_fp8kv(d: Dims, rows, kv8, kv_scale, block_table, seq_lens, new_lens=None,
@@ -305,14 +306,14 @@ def append_fp8kv(d: Dims, rows, kv8, kv_scale, block_table, seq_lens, new_lens=N
     Row i < new_lens[b] (default: every row) goes to position
     seq_lens[b] - new_lens[b] + i.  status: optional int32 [1] on the device
     that receives the first error found there."""
-    _need("rows", rows, torch.bfloat16, d.batch, rows.shape[1], 576)
-    _fp8kv_tensors(d, kv8, kv_scale)
-    _lines(d, block_table, seq_lens, new_lens, status)
-    _ok(lib().mla_decode_append_fp8kv(ctypes.byref(d), _ptr(rows), rows.shape[1], _ptr(new_lens),
-                                      _ptr(block_table), _ptr(seq_lens), _ptr(kv8),
-                                      _ptr(kv_scale), _ptr(status),
-                                      _stream_of(rows, kv8, kv_scale, block_table, seq_lens,
-                                                 new_lens, status)),
+    B, pages, max_new = d.batch, d.num_pages, rows.shape[1]
+    stream = _checked(("rows", rows, torch.bfloat16, (B, max_new, 576)),
+                      ("kv8", kv8, torch.uint8, (pages, 64, 576)),
+                      ("kv_scale", kv_scale, torch.float32, (pages,)),
+                      *_lines(d, block_table, seq_lens, new_lens, status))
+    _ok(lib().mla_decode_append_fp8kv(ctypes.byref(d), rows.data_ptr(), max_new, _ptr(new_lens),
+                                      block_table.data_ptr(), seq_lens.data_ptr(), kv8.data_ptr(),
+                                      kv_scale.data_ptr(), _ptr(status), stream),
         "mla_decode_append_fp8kv")
 
 
@@ -320,42 +321,41 @@ def page_keys(d: Dims, cache, block_table, seq_lens, max_new, keys, new_lens=Non
     """Mean keys (bf16 [num_pages, 576], in place) of the pages that hold each
     sequence's newest new_lens[b] <= max_new tokens (default: max_new), from the
     bf16 cache."""
-    _need("cache", cache, torch.bfloat16, d.num_pages, 64, 576)
-    _need("keys", keys, torch.bfloat16, d.num_pages, 576)
-    _lines(d, block_table, seq_lens, new_lens, status)
-    _ok(lib().mla_decode_page_keys(ctypes.byref(d), _ptr(cache), _ptr(block_table),
-                                   _ptr(seq_lens), max_new, _ptr(new_lens), _ptr(keys),
-                                   _ptr(status),
-                                   _stream_of(cache, keys, block_table, seq_lens, new_lens,
-                                              status)),
+    pages = d.num_pages
+    stream = _checked(("cache", cache, torch.bfloat16, (pages, 64, 576)),
+                      ("keys", keys, torch.bfloat16, (pages, 576)),
+                      *_lines(d, block_table, seq_lens, new_lens, status))
+    _ok(lib().mla_decode_page_keys(ctypes.byref(d), cache.data_ptr(), block_table.data_ptr(),
+                                   seq_lens.data_ptr(), max_new, _ptr(new_lens), keys.data_ptr(),
+                                   _ptr(status), stream),
         "mla_decode_page_keys")
 
 
 def page_keys_fp8kv(d: Dims, kv8, kv_scale, block_table, seq_lens, max_new, keys, new_lens=None,
                     status=None):
     """page_keys() from the 8-bit cache."""
-    _fp8kv_tensors(d, kv8, kv_scale)
-    _need("keys", keys, torch.bfloat16, d.num_pages, 576)
-    _lines(d, block_table, seq_lens, new_lens, status)
-    _ok(lib().mla_decode_page_keys_fp8kv(ctypes.byref(d), _ptr(kv8), _ptr(kv_scale),
-                                         _ptr(block_table), _ptr(seq_lens), max_new,
-                                         _ptr(new_lens), _ptr(keys), _ptr(status),
-                                         _stream_of(kv8, kv_scale, keys, block_table, seq_lens,
-                                                    new_lens, status)),
+    pages = d.num_pages
+    stream = _checked(("kv8", kv8, torch.uint8, (pages, 64, 576)),
+                      ("kv_scale", kv_scale, torch.float32, (pages,)),
+                      ("keys", keys, torch.bfloat16, (pages, 576)),
+                      *_lines(d, block_table, seq_lens, new_lens, status))
+    _ok(lib().mla_decode_page_keys_fp8kv(ctypes.byref(d), kv8.data_ptr(), kv_scale.data_ptr(),
+                                         block_table.data_ptr(), seq_lens.data_ptr(), max_new,
+                                         _ptr(new_lens), keys.data_ptr(), _ptr(status), stream),
         "mla_decode_page_keys_fp8kv")
 
 
 def score_pages(d: Dims, query, keys, block_table, seq_lens, scores, status=None):
     """scores (fp32 [B, T, max_pages_per_seq], written): each query token's
     largest head product (query: bf16 [B, T, H, 576]) with every page's key."""
-    _need("query", query, torch.bfloat16, d.batch, d.q_len, d.num_heads, 576)
-    _need("keys", keys, torch.bfloat16, d.num_pages, 576)
-    _need("scores", scores, torch.float32, d.batch, d.q_len, d.max_pages_per_seq)
-    _lines(d, block_table, seq_lens, None, status)
-    _ok(lib().mla_decode_score_pages(ctypes.byref(d), _ptr(query), _ptr(keys), _ptr(block_table),
-                                     _ptr(seq_lens), _ptr(scores), _ptr(status),
-                                     _stream_of(query, keys, block_table, seq_lens, scores,
-                                                status)),
+    B, T = d.batch, d.q_len
+    stream = _checked(("query", query, torch.bfloat16, (B, T, d.num_heads, 576)),
+                      ("keys", keys, torch.bfloat16, (d.num_pages, 576)),
+                      ("scores", scores, torch.float32, (B, T, d.max_pages_per_seq)),
+                      *_lines(d, block_table, seq_lens, None, status))
+    _ok(lib().mla_decode_score_pages(ctypes.byref(d), query.data_ptr(), keys.data_ptr(),
+                                     block_table.data_ptr(), seq_lens.data_ptr(),
+                                     scores.data_ptr(), _ptr(status), stream),
         "mla_decode_score_pages")
 
 
@@ -364,16 +364,14 @@ def select_pages(d: Dims, scores, block_table, seq_lens, top_k, keep_first, keep
     """The top_k pages of every query token, as a block table (int32 [B * T, top_k])
     and lengths (int32 [B * T]) to decode on with one query token per line."""
     lines = d.batch * d.q_len
-    _need("scores", scores, torch.float32, d.batch, d.q_len, d.max_pages_per_seq)
-    _need("sel_table", sel_table, torch.int32, lines, top_k)
-    _need("sel_lens", sel_lens, torch.int32, lines)
+    tensors = [("scores", scores, torch.float32, (d.batch, d.q_len, d.max_pages_per_seq)),
+               ("sel_table", sel_table, torch.int32, (lines, top_k)),
+               ("sel_lens", sel_lens, torch.int32, (lines,))]
     if sel_pages is not None:
-        _need("sel_pages", sel_pages, torch.int32, lines, top_k)
-    _lines(d, block_table, seq_lens, None, status)
-    _ok(lib().mla_decode_select_pages(ctypes.byref(d), _ptr(scores), _ptr(block_table),
-                                      _ptr(seq_lens), top_k, keep_first, keep_last,
-                                      _ptr(sel_table), _ptr(sel_pages), _ptr(sel_lens),
-                                      _ptr(status),
-                                      _stream_of(scores, block_table, seq_lens, sel_table,
-                                                 sel_lens, sel_pages, status)),
+        tensors.append(("sel_pages", sel_pages, torch.int32, (lines, top_k)))
+    stream = _checked(*tensors, *_lines(d, block_table, seq_lens, None, status))
+    _ok(lib().mla_decode_select_pages(ctypes.byref(d), scores.data_ptr(), block_table.data_ptr(),
+                                      seq_lens.data_ptr(), top_k, keep_first, keep_last,
+                                      sel_table.data_ptr(), _ptr(sel_pages), sel_lens.data_ptr(),
+                                      _ptr(status), stream),
         "mla_decode_select_pages")
