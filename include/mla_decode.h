@@ -255,7 +255,7 @@ int mla_decode_plan_fp8kv(const mla_decode_dims* dims, const int32_t* seq_lens,
  * 0xff); mla_decode_append_fp8kv clears them.  A page's scale outside [2^-32,
  * 2^32] is reported as DEVICE_BOUNDS by mla_decode_check and taken as 1.  The
  * query must be finite.  The absorbed query enters as its bf16 part, exactly
- * (to 2^-22 of its row's largest value), and the lse gets the same first-order
+ * (to 2^-21 of its row's largest value), and the lse gets the same first-order
  * correction as over the bf16 cache; the softmax weights are rounded to two
  * 3-bit terms (at most 2^-7 of a weight), and the output is normalised by the
  * sum of the weights as rounded.  As many kernels as mla_decode_run. */

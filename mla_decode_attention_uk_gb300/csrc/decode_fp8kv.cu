@@ -451,6 +451,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
         bool ok = mbar_wait(smem_u32(&q_raw), n & 1, &abort_sh, P.status);
         // A row's largest value takes the top but one of E4M3's binades.
         int e = 0;
+        float amax = 0.0f;
         if (n == 0) {
           // All warps share the rows out, whatever TMEM lanes they belong to (16
           // heads would leave three quarters of the SM idle else), and make the
@@ -463,13 +464,16 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
               const int w = lane + 32 * i;
               x[i] = make_uint2(0u, 0u);
               if (i < 4 || lane < 16) x[i] = ld_shared_v2(word(row, w >> 4, (w >> 1) & 7, w & 1));
-              top = __hmax2(__hmax2(top, __habs2(as_bf162(x[i].x))), __habs2(as_bf162(x[i].y)));
+              top = max_abs(max_abs(top, x[i].x), x[i].y);
             }
-            float amax = fmaxf(__low2float(top), __high2float(top));
-            amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+            const float amax =
+                __uint_as_float(__reduce_max_sync(0xffffffffu, larger_half(top)));
             const int er = page_scale_exp(amax) + 1;  // amax <= 224 * 2^er
-            const __nv_bfloat162 down = __float2bfloat162_rn(exp2_int(max(-126, -er - 120)));
-            if (lane == 0) q_scale_sh[row] = exp2_int(er);
+            const __nv_bfloat162 down = term_factor(er);
+            if (er > kTermExpMax)
+#pragma unroll
+              for (int i = 0; i < 5; ++i) x[i] = lower_terms(x[i], er);
+            if (lane == 0) q_scale_sh[row] = row_scale(amax, er);
 #pragma unroll
             for (int i = 0; i < 5; ++i) {
               const int w = lane + 32 * i;
@@ -486,17 +490,28 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const uint2 x = ld_shared_v2(word(srow, block, j, par));
-              top = __hmax2(__hmax2(top, __habs2(as_bf162(x.x))), __habs2(as_bf162(x.y)));
+              top = max_abs(max_abs(top, x.x), x.y);
             }
-          float amax = fmaxf(__low2float(top), __high2float(top));
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          const uint32_t t = larger_half(top);
+          amax = __uint_as_float(max(t, __shfl_xor_sync(0xffffffffu, t, 2)));
           e = page_scale_exp(amax) + 1;
+          // A loop of its own, as it is rare (rows past the last hold anything).
+          const bool lower = srow < rows_here && e > kTermExpMax;
+          if (__any_sync(0xffffffffu, lower))
+#pragma unroll 1
+            for (int w = 0; w < 8 * kBoxes; ++w) {
+              const uint32_t at = word(srow, w >> 3, w & 7, par);
+              if (lower) {
+                const uint2 x = lower_terms(ld_shared_v2(at), e);
+                st_shared_v2(at, x.x, x.y);
+              }
+            }
           ok = ok && mbar_wait(smem_u32(&q_free), (n - 1) & 1, &abort_sh, P.status);
         }
-        const __nv_bfloat162 down = __float2bfloat162_rn(exp2_int(max(-126, -e - 120)));
+        const __nv_bfloat162 down = term_factor(e);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        if (par == 0 && n > 0) q_scale_sh[srow] = exp2_int(e);
+        if (par == 0 && n > 0) q_scale_sh[srow] = row_scale(amax, e);
         const int b0 = n == 0 ? 3 * ((warp - 4) >> 2) : 0, b1 = n == 0 ? b0 + 3 : kBoxes;
 #pragma unroll 1
         for (int block = b0; block < b1; ++block) {
@@ -560,11 +575,13 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
       // The running maximum of a row is m_sh (one group raises it, the other
       // finds it raised); m_mine is the one that this thread's sums are in.
       float m_mine = -INFINITY;
-      float l = 0.0f, l_r = 0.0f;  // this thread's shares of the row's sums: exact, as rounded
       // The last piece's epilogue has read m_sh and the sums; the query is there.
       bool bad = (n > 0 && !mbar_wait(smem_u32(&epi_done), (n - 1) & 1, &abort_sh, P.status)) ||
                  !mbar_wait(smem_u32(&q_full), n & 1, &abort_sh, P.status);
       const float q_scale = q_scale_sh[srow] * P.scale_log2;
+      // This thread's shares of the row's sums: exact, as rounded.  NaN from the
+      // start where the query is not finite, whatever its codes give.
+      float l = 0.0f * q_scale, l_r = l;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&q_free));
       for (int i = pc.pbeg; i < pc.pend; ++i, ++g) {
@@ -668,6 +685,8 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
         if (m_used == -INFINITY) {
 #pragma unroll
           for (int t = 0; t < 8; ++t) hw[t] = mw[t] = 0u;
+          // No key yet, or NaN alone, which a maximum passes over.
+          if (kb < n_row) l = l_r = __uint_as_float(0x7fffffffu);
         } else {
           const float add = shift + kTopExp - m_used;
           float se[4] = {};
@@ -758,10 +777,10 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
         const float w0 = m_l_sh[0][row] == -INFINITY ? 0.0f : ex2_approx(m_l_sh[0][row] - m);
         const float w1 = m_l_sh[1][row] == -INFINITY ? 0.0f : ex2_approx(m_l_sh[1][row] - m);
         const float total_r = fmaf(l_r_sh[0][row], w0, l_r_sh[1][row] * w1);
-        inv_sh[warp - 4][row] = total_r > 0.0f ? 1.0f / total_r : 0.0f;
+        inv_sh[warp - 4][row] = total_r == 0.0f ? 0.0f : 1.0f / total_r;  // (NaN stays NaN)
         if (q == 0 && wq == 0) {
           const float total = fmaf(l_sh[0][row], w0, l_sh[1][row] * w1);
-          const float lse2 = total > 0.0f ? m - kTopExp + __log2f(total) : -INFINITY;
+          const float lse2 = total == 0.0f ? -INFINITY : m - kTopExp + __log2f(total);
           (dest < 0 ? view.lpart : P.lse)[row_base + row] = lse2 * kLn2;
         }
       }

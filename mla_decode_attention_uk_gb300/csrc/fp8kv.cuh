@@ -101,6 +101,30 @@ __device__ __forceinline__ void split_terms(uint2 x, __nv_bfloat162 down, uint32
   mid = __byte_perm(m[0], m[1], 0x6420);
 }
 
+// split_terms' factor for a row's exponent, and what comes before it where 2^(-e -
+// 120) is below bf16's normal numbers (rows beyond 224 * 2^6).
+constexpr int kTermExpMax = 6;
+__device__ __forceinline__ __nv_bfloat162 term_factor(int e) {
+  return __float2bfloat162_rn(exp2_int(-min(e, kTermExpMax) - 120));
+}
+__device__ __forceinline__ uint2 lower_terms(uint2 x, int e) {
+  const __nv_bfloat162 f = __float2bfloat162_rn(exp2_int(kTermExpMax - e));
+  const __nv_bfloat162 a = __hmul2(as_bf162(x.x), f), b = __hmul2(as_bf162(x.y), f);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// The largest size among a row's values, NaN above all, as its fp32 bits.
+__device__ __forceinline__ __nv_bfloat162 max_abs(__nv_bfloat162 top, uint32_t w) {
+  return __hmax2_nan(top, __habs2(as_bf162(w)));
+}
+__device__ __forceinline__ uint32_t larger_half(__nv_bfloat162 top) {
+  return max(__float_as_uint(__low2float(top)), __float_as_uint(__high2float(top)));
+}
+// The factor of a row's terms; not a number for a row that is not finite.
+__device__ __forceinline__ float row_scale(float amax, int e) {
+  return amax < INFINITY ? exp2_int(e) : __uint_as_float(0x7fffffffu);
+}
+
 // Records the first device-side error, where the caller asked for it.
 __device__ __forceinline__ void record_status(int32_t* status, int code) {
   if (status) atomicCAS(status, 0, code);

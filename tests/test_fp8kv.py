@@ -386,6 +386,71 @@ def test_pages_of_very_different_scales(low, high):
 
 
 @gpu
+@pytest.mark.parametrize("H,lens", [(16, [300, 70]), (128, [64] * 90)])
+@pytest.mark.parametrize("e", [-12, 9, 13, 16, 24])
+def test_queries_of_any_size(e, H, lens):
+    # Queries times 2^e and a softmax scale over 2^e: the same scores.  Rows whose
+    # absorbed query is far beyond 2^14, in first pieces of a CTA and in later
+    # ones (90 sequences x two tiles: one range per CTA pair, 1.2 pieces).
+    inp = make_inputs(len(lens), lens, 1, H, seed=46)
+    inp.q = (inp.q.float() * 2.0 ** e).to(BF)
+    inp.scale = inp.scale / 2.0 ** e
+    inp, kv8, kvs = fp8_inputs(inp)
+    out, lse = run_fp8(inp, kv8, kvs, num_ranges=20 if H == 128 else 0)
+    s = compare(inp, out, lse)
+    # The lse's correction for the bf16 query q_lat is the rounding's residual r,
+    # |r| <= 2^-9 |q_lat|, stored as E4M3 of 2^10 r: it is below half of E4M3's
+    # least number (2^-9) where |q_lat| < 2^-11, and above its largest (448) where
+    # |q_lat| > 224.  Every e here is outside of that, so the lse keeps the query's
+    # rounding: 2^-9 of a score of 576 terms, whose size is about 1.7, and three
+    # times that for the largest of the rows.
+    lse_max = 1.7 * 3 * 2.0 ** -9
+    assert s["out_max"] <= ref.OUT_MAX and s["out_mean"] <= ref.OUT_MEAN, s
+    assert s["lse_max"] <= lse_max, s
+
+
+@gpu
+def test_nan_in_a_visible_token_reaches_its_sequence_only():
+    inp, kv8, kvs = fp8_inputs(make_inputs(3, [200, 70, 130], 1, 16, seed=47))
+    out0, lse0 = run_fp8(inp, kv8, kvs)
+    bad = kv8.clone()
+    bad[int(inp.block_table[1, 0]), 11, 500] = 0x7F
+    out, lse = run_fp8(inp, bad, kvs)
+    assert out[1].isnan().all() and lse[1].isnan().all()
+    for b in (0, 2):
+        assert torch.equal(out[b], out0[b]) and torch.equal(lse[b], lse0[b])
+
+
+@gpu
+@pytest.mark.parametrize("lens", [[2, 130, 90], [700, 900, 64]])
+@pytest.mark.parametrize("H,num_ranges", [(16, 0), (16, 2), (128, 2)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_a_query_that_is_not_finite_gives_nan(value, H, num_ranges, lens):
+    # In the absorbed part and in the RoPE part, in first pieces of a range and in
+    # later ones, split sequences and whole ones.
+    inp, kv8, kvs = fp8_inputs(make_inputs(3, lens, 2, H, seed=48))
+    out0, lse0 = run_fp8(inp, kv8, kvs, num_ranges=num_ranges)
+    inp.q[:, 1, 3, 5] = value
+    inp.q[:, 0, H - 1, 140] = value
+    out, lse = run_fp8(inp, kv8, kvs, num_ranges=num_ranges)
+    changed = torch.zeros_like(lse, dtype=torch.bool)
+    changed[:, 1, 3] = changed[:, 0, H - 1] = True
+    assert out[changed].isnan().all() and lse[changed].isnan().all()
+    assert torch.equal(out[~changed], out0[~changed])
+    assert torch.equal(lse[~changed], lse0[~changed])
+
+
+@gpu
+def test_nan_as_the_only_token():
+    inp, kv8, kvs = fp8_inputs(make_inputs(2, [1, 65], 1, 16, seed=49))
+    bad = kv8.clone()
+    for b, k in ((0, 0), (1, 1)):
+        bad[int(inp.block_table[b, k]), 0, 500] = 0x7F
+    out, lse = run_fp8(inp, bad, kvs)
+    assert out.isnan().all() and lse.isnan().all()
+
+
+@gpu
 @pytest.mark.parametrize("n", [4000, 32000])
 def test_many_small_weights_next_to_a_large_one(n):
     # One key has a weight of about half the row's sum, the other keys share the
