@@ -253,8 +253,10 @@ int mla_decode_plan_fp8kv(const mla_decode_dims* dims, const int32_t* seq_lens,
  * mla_decode_plan_fp8kv on the same workspace; arguments as there.
  * Rows past a sequence's length in its last page must not be NaN codes (0x7f,
  * 0xff); mla_decode_append_fp8kv clears them.  A page's scale outside [2^-32,
- * 2^32] is reported as DEVICE_BOUNDS by mla_decode_check and taken as 1.  The
- * query must be finite.  The absorbed query enters as its bf16 part, exactly
+ * 2^32] is reported as DEVICE_BOUNDS by mla_decode_check and taken as 1.  A
+ * query row that is not finite gives NaN, for the row alone; a NaN code in a
+ * token that is seen gives NaN, for its sequence.
+ * The absorbed query enters as its bf16 part, exactly
  * (to 2^-21 of its row's largest value), and the lse gets the same first-order
  * correction as over the bf16 cache; the softmax weights are rounded to two
  * 3-bit terms (at most 2^-7 of a weight), and the output is normalised by the
@@ -289,6 +291,7 @@ int mla_decode_attend_fp8kv(const mla_decode_dims* dims, const uint8_t* kv_fp8,
  * (new_lens, max_new and seq_lens as for mla_decode_append_fp8kv):
  *   page_keys   bf16 [num_pages, 576] (written at those pages): the mean of
  *               the page's rows up to the sequence's length, summed in fp32
+ * A page's scale outside [2^-32, 2^32] is taken as 1, with DEVICE_BOUNDS.
  * Recomputed from the cache, so a page may be filled in any number of steps
  * and shortened again.  One kernel. */
 int mla_decode_page_keys(const mla_decode_dims* dims, const void* kv_cache,

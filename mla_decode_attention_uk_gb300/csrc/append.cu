@@ -201,7 +201,7 @@ append_few_kernel(AppendParams P) {
 // Prompts: a grid that fills the SMs shares the pages of all sequences out, page
 // f to CTA f mod grid (with a CTA for every page that a sequence could have, the
 // empty ones of ragged prompts took a third of the time).  The CTA counts the
-// pages of 256 sequences at a time, one per thread, and finds its own among them.
+// pages of 512 sequences at a time, one per thread, and finds its own among them.
 __global__ void __launch_bounds__(kAppThreads, 3)
 append_pages_kernel(AppendParams P) {
   extern __shared__ __align__(128) uint4 rows_sh[];
@@ -224,7 +224,7 @@ append_pages_kernel(AppendParams P) {
     }
     if (lane == 31) sh.warp_sum[warp] = upto;
     __syncthreads();
-    // (At most 256 sequences of 2^24 pages: the sum may pass 32 bits.)
+    // (At most 512 sequences of 2^24 pages: the sum may pass 32 bits.)
     long long before = base, all = base;
     for (int w = 0; w < kAppThreads / 32; ++w) {
       before += w < warp ? sh.warp_sum[w] : 0;
@@ -296,7 +296,15 @@ page_keys_kernel(const uint8_t* __restrict__ cache, const float* __restrict__ kv
 #pragma unroll
   for (int k = 0; k < 8; ++k) part[r0][c * 8 + k] = s[k];
   __syncthreads();
-  const float mul = (kFp8 ? kv_scale[page] : 1.0f) / static_cast<float>(filled);
+  float scale = 1.0f;
+  if constexpr (kFp8) {
+    scale = kv_scale[page];
+    if (!scale_in_range(scale)) {
+      if (threadIdx.x == 0) record_status(status, MLA_STATUS_BOUNDS);
+      scale = 1.0f;
+    }
+  }
+  const float mul = scale / static_cast<float>(filled);
   const int k = threadIdx.x * 2;
   const float x = ((part[0][k] + part[1][k]) + (part[2][k] + part[3][k])) * mul;
   const float y = ((part[0][k + 1] + part[1][k + 1]) + (part[2][k + 1] + part[3][k + 1])) * mul;

@@ -191,8 +191,8 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
   // p_full[g mod kSlots]: P^T of page g is written (a page kSlots further on
   // is not in a slot before PV has read this one).
   __shared__ __align__(8) uint64_t q_full, q_free, slot_full[kSlots], slot_free[kSlots],
-      s_full[kSBufs], s_free[kSBufs], p_full[kSlots], q_raw, o_full, o_free, m_final[2][4], sums_full,
-      epi_done, drain_bar[3];
+      s_full[kSBufs], s_free[kSBufs], p_full[kSlots], q_raw, o_full, o_free, m_final[2][4],
+      sums_full, epi_done, drain_bar[3];
   __shared__ PlanView view;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
@@ -396,7 +396,8 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
             }
             tc_fence_after();
             const uint64_t ad0 = dpv0 + static_cast<uint64_t>((s * kSlot) >> 4);
-            const uint64_t bd0 = dslot0 + static_cast<uint64_t>((s * kSlot + kRopeBox8 * kBox) >> 4);
+            const uint64_t bd0 =
+                dslot0 + static_cast<uint64_t>((s * kSlot + kRopeBox8 * kBox) >> 4);
 #pragma unroll
             for (int m = 2 * half; m < 2 * half + 2; ++m) {
               // Steps 0, 1: the hi terms of keys 0-31 and 32-63; 2, 3: mid.

@@ -140,6 +140,23 @@ def test_page_keys_leave_a_bad_sequence_alone(lens, new):
     assert int(status.item()) == 5 and not keys[1:].any() and bool(keys[0].any())
 
 
+@gpu
+@pytest.mark.parametrize("scale", [0.0, -2.0, math.nan, math.inf, 2.0 ** 33, 2.0 ** -33])
+def test_page_keys_of_a_page_with_a_bad_scale(scale):
+    # Taken as 1 and reported, as the attention does.
+    kv8, kvs = ref.quantise(torch.randn(2, 64, 576, generator=torch.Generator().manual_seed(56)))
+    args = (i32([[0, 1]]).cuda(), i32([100]).cuda(), 100)
+    got, status = [], []
+    for first in (scale, 1.0):
+        kvs[0] = first
+        got.append(torch.zeros(2, 576, dtype=BF, device="cuda"))
+        status.append(torch.zeros(1, dtype=torch.int32, device="cuda"))
+        binding.page_keys_fp8kv(dims(1, pages=2, width=2), kv8.cuda(), kvs.cuda(), *args, got[-1],
+                                None, status[-1])
+    assert [int(x.item()) for x in status] == [5, 0]
+    assert torch.equal(got[0], got[1]) and bool(got[0][0].any())
+
+
 # ---------------------------------------------------------------- scores
 @gpu
 @pytest.mark.parametrize("B,T,H,lens,width", [
