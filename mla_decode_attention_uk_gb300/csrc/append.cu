@@ -10,7 +10,7 @@ namespace mla {
 
 namespace {
 
-constexpr int kAppThreads = 512;
+constexpr int kAppThreads = 384;  // that convert a page
 constexpr int kChunks = kDqk / 8;  // 16-byte chunks of a bf16 row: 72 (8-byte chunks of codes)
 
 // The new tokens of one sequence: positions [first, len).  False (and an error
@@ -61,20 +61,6 @@ __device__ __forceinline__ uint2 codes8(const uint4& v, __nv_bfloat162 inv) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// Maximum of `top` over the CTA, the same to all.
-__device__ __forceinline__ float block_max(float top, float* warp_top) {
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x >> 5] = top;
-  __syncthreads();
-  for (int w = 0; w < kAppThreads / 32; ++w) top = fmaxf(top, warp_top[w]);
-  return top;
-}
-
-// The new rows of a page are contiguous: one bulk copy brings them into shared
-// memory, from where they are read twice, for their maximum, hence the scale, and
-// for the codes.
-constexpr int kAppSmem = kPage * kDqk * 2;  // 73,728: three CTAs per SM
-
 struct AppendParams {
   const uint4* rows;
   int max_new;
@@ -87,74 +73,119 @@ struct AppendParams {
   int32_t* status;
 };
 
-struct AppendShared {
-  float warp_top[kAppThreads / 32];
-  alignas(8) uint64_t landed;
-  int abort, timeout;
-  int warp_sum[kAppThreads / 32];
-  int b, first, len, page;  // the page in work: sequence, its new tokens, logical page
+// A page to fill: its sequence, the new tokens there, and which of its pages.
+struct Place {
+  int b, first, len, logical;
+  // Rows [r0, r1) of the page are new.
+  __device__ int r0() const { return max(first - logical * kPage, 0); }
+  __device__ int r1() const { return min(len - logical * kPage, kPage); }
 };
 
-// Page `logical` of sequence b, whose new tokens are nt; `phase`: of sh.landed.
-// False after a timeout.
-__device__ bool append_page(const AppendParams& P, AppendShared& sh, uint4* rows_sh, int b,
-                            const NewTokens& nt, int logical, uint32_t phase) {
-  const int page = P.block_table[static_cast<size_t>(b) * P.max_pages + logical];
-  const bool in_pool = page >= 0 && page < P.num_pages;
-  if (!in_pool && threadIdx.x == 0) record_status(P.status, MLA_STATUS_BOUNDS);
-  // Rows [r0, r1) of the page are new.
-  const int r0 = max(nt.first - logical * kPage, 0);
-  const int r1 = min(nt.len - logical * kPage, kPage);
-  const int n = (r1 - r0) * kChunks;
-  if (threadIdx.x == 0) {
-    fence_proxy_async_smem();  // the last page's rows have been read
-    mbar_expect_tx(smem_u32(&sh.landed), n * 16);
-    bulk_load(smem_u32(rows_sh),
-              P.rows + (static_cast<size_t>(b) * P.max_new + (logical * kPage + r0 - nt.first)) *
-                           kChunks,
-              n * 16, smem_u32(&sh.landed));
+// kAppThreads threads that fill a page together.
+struct Group {
+  uint32_t bar;     // their named barrier
+  int tid;
+  float* warp_top;  // [kAppThreads / 32]
+  __device__ void sync() const { named_bar_sync(bar, kAppThreads); }
+  // Maximum of `top` over them, the same to all.
+  __device__ float max_of(float top) const {
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((tid & 31) == 0) warp_top[tid >> 5] = top;
+    sync();
+    for (int w = 0; w < kAppThreads / 32; ++w) top = fmaxf(top, warp_top[w]);
+    return top;
   }
-  // Read before the barrier below: one thread replaces it at the end.
-  float old = r0 > 0 && in_pool ? P.kv_scale[page] : 1.0f;
-  if (!scale_in_range(old)) {
-    if (threadIdx.x == 0) record_status(P.status, MLA_STATUS_BOUNDS);
-    old = 1.0f;
+};
+
+// The new rows of a page are contiguous: one bulk copy (of one thread) brings them
+// into shared memory, and threads take them from there.
+constexpr int kRowsBytes = kPage * kDqk * 2;  // 73,728
+
+__device__ __forceinline__ void load_rows(const AppendParams& P, const Place& at, uint4* rows_sh,
+                                          uint64_t* landed) {
+  const int r0 = at.r0(), bytes = (at.r1() - r0) * kDqk * 2;
+  fence_proxy_async_smem();  // the rows that were there have been read
+  mbar_expect_tx(smem_u32(landed), bytes);
+  bulk_load(smem_u32(rows_sh),
+            P.rows + (static_cast<size_t>(at.b) * P.max_new +
+                      (at.logical * kPage + r0 - at.first)) * kChunks,
+            bytes, smem_u32(landed));
+}
+
+// Whether the rows have landed, false after a timeout.  One warp polls, the others
+// sleep at the barrier (twelve polling warps take the issue slots of those that
+// have their rows).
+__device__ __forceinline__ bool wait_rows(const Group& grp, uint64_t* landed, uint32_t phase,
+                                          int* abort, int* timeout) {
+  bool bad = false;
+  if (grp.tid < 32) bad = !mbar_wait(smem_u32(landed), phase, abort, timeout);
+  return !bar_any(grp.bar, kAppThreads, bad);
+}
+
+// The page and, where tokens stay, its scale.
+struct Target {
+  int page;
+  float old;
+  bool in_pool;
+  __device__ Target(const AppendParams& P, const Place& at, bool report) {
+    page = P.block_table[static_cast<size_t>(at.b) * P.max_pages + at.logical];
+    in_pool = page >= 0 && page < P.num_pages;
+    old = at.r0() > 0 && in_pool ? P.kv_scale[page] : 1.0f;
+    const bool good = scale_in_range(old);
+    if (report && !(in_pool && good)) record_status(P.status, MLA_STATUS_BOUNDS);
+    if (!good) old = 1.0f;
   }
-  // One warp polls, the others sleep at the barrier (sixteen polling warps take
-  // the issue slots of the CTAs that have their rows).
-  bool ok = true;
-  if (threadIdx.x < 32) ok = mbar_wait(smem_u32(&sh.landed), phase, &sh.abort, &sh.timeout);
-  if (!__syncthreads_and(ok)) {
-    if (threadIdx.x == 0) {
-      record_status(P.status, MLA_STATUS_TIMEOUT);
-      mbar_wait_drain(smem_u32(&sh.landed), phase, &sh.timeout);
-    }
-    __syncthreads();
-    return false;
-  }
+};
+
+// Fills a page from its new rows, which a thread holds in registers between their
+// maximum and the codes; `taken` is called once all have theirs.  kFew skips what
+// a few rows do not fill, at a price for whole pages (14.2 -> 15.6 us).  (Every thread
+// has its Target before the first barrier here; one thread replaces the scale
+// behind it.)
+template <bool kFew, typename Taken>
+__device__ __forceinline__ void fill_page(const AppendParams& P, const Group& grp,
+                                          const Place& at, const Target& to,
+                                          const uint4* rows_sh, const Taken& taken) {
+  constexpr int kHeld = kPage * kChunks / kAppThreads;
+  static_assert(kHeld * kAppThreads == kPage * kChunks, "a page is whole passes");
+  const int r0 = at.r0(), r1 = at.r1(), n = (r1 - r0) * kChunks;
+  uint4 x[kHeld];
   __nv_bfloat162 most = __float2bfloat162_rn(0.0f);
-  for (int i = threadIdx.x; i < n; i += kAppThreads) most = absmax8(most, rows_sh[i]);
-  float top = block_max(fmaxf(__low2float(most), __high2float(most)), sh.warp_top);
-  if (top == INFINITY) {  // rare: once more, without the infinities
-    __syncthreads();
-    top = 0.0f;
-    for (int i = threadIdx.x; i < n; i += kAppThreads) top = finite_absmax8(top, rows_sh[i]);
-    top = block_max(top, sh.warp_top);
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int i = grp.tid + k * kAppThreads;
+    if (kFew && k * kAppThreads >= n) break;
+    x[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (i < n) x[k] = rows_sh[i];
+    most = absmax8(most, x[k]);
   }
-  if (!in_pool) return true;
+  float top = grp.max_of(fmaxf(__low2float(most), __high2float(most)));
+  taken();
+  if (top == INFINITY) {  // rare: once more, without the infinities
+    grp.sync();
+    top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (!kFew || k * kAppThreads < n) top = finite_absmax8(top, x[k]);
+    top = grp.max_of(top);
+  }
+  if (!to.in_pool) return;
   float scale = exp2_int(page_scale_exp(top));
-  if (r0 > 0) scale = fmaxf(scale, next_power_of_two(old));
-  uint2* const dst = reinterpret_cast<uint2*>(P.kv8 + static_cast<size_t>(page) * kPageBytes8);
+  if (r0 > 0) scale = fmaxf(scale, next_power_of_two(to.old));
+  uint2* const dst = reinterpret_cast<uint2*>(P.kv8 + static_cast<size_t>(to.page) * kPageBytes8);
   const __nv_bfloat162 inv = __float2bfloat162_rn(1.0f / scale);
-#pragma unroll 3
-  for (int i = threadIdx.x; i < n; i += kAppThreads)
-    dst[r0 * kChunks + i] = codes8(rows_sh[i], inv);
-  if (threadIdx.x == 0) P.kv_scale[page] = scale;
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int i = grp.tid + k * kAppThreads;
+    if (kFew && k * kAppThreads >= n) break;
+    if (i < n) dst[r0 * kChunks + i] = codes8(x[k], inv);
+  }
+  if (grp.tid == 0) P.kv_scale[to.page] = scale;
   // Rows that stay: cleared in a page that starts here, re-coded if the scale
   // grew.
-  if (r0 > 0 && scale == old) return true;
-  const float ratio = old / scale;
-  for (int i = threadIdx.x; i < kPage * kChunks; i += kAppThreads) {
+  if (r0 > 0 && scale == to.old) return;
+  const float ratio = to.old / scale;
+  for (int i = grp.tid; i < kPage * kChunks; i += kAppThreads) {
     if (i >= r0 * kChunks && i < r1 * kChunks) continue;
     uint2 c = make_uint2(0u, 0u);
     if (r0 > 0) {
@@ -169,18 +200,6 @@ __device__ bool append_page(const AppendParams& P, AppendShared& sh, uint4* rows
     }
     dst[i] = c;
   }
-  return true;
-}
-
-__device__ __forceinline__ void append_begin(AppendShared& sh) {
-  if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&sh.landed), 1);
-    sh.abort = sh.timeout = 0;
-    fence_mbar_init();
-  }
-  __syncthreads();
-  griddep_wait();
-  griddep_launch_dependents();
 }
 
 // A few new tokens per sequence: one CTA per sequence and page that they can
@@ -188,65 +207,146 @@ __device__ __forceinline__ void append_begin(AppendShared& sh) {
 __global__ void __launch_bounds__(kAppThreads)
 append_few_kernel(AppendParams P) {
   extern __shared__ __align__(128) uint4 rows_sh[];
-  __shared__ AppendShared sh;
-  append_begin(sh);
+  __shared__ float warp_top[kAppThreads / 32];
+  __shared__ alignas(8) uint64_t landed;
+  __shared__ int abort_sh, timeout_sh;
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&landed), 1);
+    abort_sh = timeout_sh = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
   NewTokens nt;
   if (!nt.load(P.seq_lens, P.new_lens, P.max_new, P.max_pages * kPage, blockIdx.y,
-               threadIdx.x == 0, P.status))
+               threadIdx.x == 0, P.status) ||
+      blockIdx.x >= nt.pages())
     return;
-  if (blockIdx.x < nt.pages())
-    append_page(P, sh, rows_sh, blockIdx.y, nt, nt.first / kPage + blockIdx.x, 0);
+  const Place at{static_cast<int>(blockIdx.y), nt.first, nt.len,
+                 nt.first / kPage + static_cast<int>(blockIdx.x)};
+  if (threadIdx.x == 0) load_rows(P, at, rows_sh, &landed);
+  const Group grp{1, static_cast<int>(threadIdx.x), warp_top};
+  const Target to(P, at, threadIdx.x == 0);
+  if (wait_rows(grp, &landed, 0, &abort_sh, &timeout_sh)) {
+    fill_page<true>(P, grp, at, to, rows_sh, [] {});
+  } else if (threadIdx.x == 0) {
+    record_status(P.status, MLA_STATUS_TIMEOUT);
+    mbar_wait_drain(smem_u32(&landed), 0, &timeout_sh);
+  }
 }
 
-// Prompts: a grid that fills the SMs shares the pages of all sequences out, page
-// f to CTA f mod grid (with a CTA for every page that a sequence could have, the
-// empty ones of ragged prompts took a third of the time).  The CTA counts the
-// pages of 512 sequences at a time, one per thread, and finds its own among them.
-__global__ void __launch_bounds__(kAppThreads, 3)
+// Prompts: one CTA per SM, page f of all sequences to CTA f mod grid (with a CTA
+// for every page that a sequence could have, the empty ones of ragged prompts took
+// a third of the time).  The CTA's pages pass through a ring of three buffers, and
+// two groups of threads take turns at filling them, so that loads and conversions
+// overlap: 13 prompts of 512 to 8190 tokens 14.1 us, 4.6 TB/s; three CTAs of one
+// buffer took 15.7, and two passes over shared memory in place of registers 15.9.
+// What is left is mostly the start (lengths, sums, first loads: 2 us with nothing in
+// flight) and the last pages' conversion.
+constexpr int kRing = 3;
+constexpr int kGroups = 2;
+constexpr int kBars = kRing * kGroups;  // a barrier is always the same group's, whose
+                                        // waits see each of its phases
+constexpr int kPlanSeqs = 512;          // sequences looked at together
+constexpr int kPagesThreads = kGroups * kAppThreads;
+
+struct AppendShared {
+  float warp_top[kGroups][kAppThreads / 32];
+  alignas(8) uint64_t landed[kBars];
+  Place place[kBars];
+  int issued[kBars];
+  int abort, timeout;
+  int warp_sum[kPlanSeqs / 32];
+  int first[kPlanSeqs], len[kPlanSeqs];
+  long long upto[kPlanSeqs];  // pages up to and with the sequence's
+};
+
+__global__ void __launch_bounds__(kPagesThreads, 1)
 append_pages_kernel(AppendParams P) {
-  extern __shared__ __align__(128) uint4 rows_sh[];
+  extern __shared__ __align__(128) uint4 ring_sh[];
   __shared__ AppendShared sh;
-  append_begin(sh);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  long long f = blockIdx.x, base = 0;
-  uint32_t phase = 0;
-  for (int b0 = 0; b0 < P.B; b0 += kAppThreads) {
-    const int b = b0 + threadIdx.x;
-    NewTokens nt;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kBars; ++i) {
+      mbar_init(smem_u32(&sh.landed[i]), 1);
+      sh.issued[i] = 0;
+    }
+    sh.abort = sh.timeout = 0;
+    fence_mbar_init();
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  const int gid = tid / kAppThreads;
+  const Group grp{1u + gid, tid % kAppThreads, sh.warp_top[gid]};
+  auto rows_of = [&](int k) { return ring_sh + (k % kRing) * (kRowsBytes / 16); };
+  long long f = blockIdx.x, base = 0;  // this CTA's next page; pages before b0
+  int k = 0;                           // this CTA's pages so far
+  bool failed = false;
+  for (int b0 = 0; b0 < P.B; b0 += kPlanSeqs) {
+    // Pages per sequence, counted by a thread each.
+    NewTokens nt{0, 0};
     int n = 0;
-    if (b < P.B && nt.load(P.seq_lens, P.new_lens, P.max_new, P.max_pages * kPage, b,
-                           blockIdx.x == 0, P.status))
-      n = nt.pages();
-    int upto = n;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += v;
-    }
-    if (lane == 31) sh.warp_sum[warp] = upto;
-    __syncthreads();
-    // (At most 512 sequences of 2^24 pages: the sum may pass 32 bits.)
-    long long before = base, all = base;
-    for (int w = 0; w < kAppThreads / 32; ++w) {
-      before += w < warp ? sh.warp_sum[w] : 0;
-      all += sh.warp_sum[w];
-    }
-    before += upto - n;
-    for (; f < all; f += gridDim.x, phase ^= 1) {
-      if (f >= before && f < before + n) {
-        sh.b = b;
-        sh.first = nt.first;
-        sh.len = nt.len;
-        sh.page = nt.first / kPage + static_cast<int>(f - before);
+    if (tid < kPlanSeqs) {
+      if (b0 + tid < P.B && nt.load(P.seq_lens, P.new_lens, P.max_new, P.max_pages * kPage,
+                                    b0 + tid, blockIdx.x == 0, P.status))
+        n = nt.pages();
+      int upto = n;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
       }
-      __syncthreads();
-      NewTokens mine;
-      mine.first = sh.first;
-      mine.len = sh.len;
-      if (!append_page(P, sh, rows_sh, sh.b, mine, sh.page, phase)) return;
-      __syncthreads();  // before the next page's rows and place
+      if (lane == 31) sh.warp_sum[warp] = upto;
+      n = upto;
+      sh.first[tid] = nt.first;
+      sh.len[tid] = nt.len;
     }
-    base = all;
     __syncthreads();
+    if (tid < kPlanSeqs) {
+      // (512 sequences of 2^25 pages: the sum may pass 32 bits.)
+      long long upto = base + n;
+      for (int w = 0; w < warp; ++w) upto += sh.warp_sum[w];
+      sh.upto[tid] = upto;
+    }
+    __syncthreads();
+    base = sh.upto[kPlanSeqs - 1];
+    const int mine = f < base ? static_cast<int>((base - 1 - f) / gridDim.x) + 1 : 0;
+    // One thread looks up the CTA's page i of these and starts its load.
+    auto issue = [&](int i) {
+      const long long page = f + static_cast<long long>(i) * gridDim.x;
+      int lo = 0;  // the first sequence with upto > page
+      for (int step = kPlanSeqs / 2; step; step >>= 1)
+        if (sh.upto[lo + step - 1] <= page) lo += step;
+      const int bar = (k + i) % kBars;
+      const Place at{b0 + lo, sh.first[lo], sh.len[lo],
+                     (sh.len[lo] - 1) / kPage - static_cast<int>(sh.upto[lo] - 1 - page)};
+      sh.place[bar] = at;
+      ++sh.issued[bar];
+      load_rows(P, at, rows_of(k + i), &sh.landed[bar]);
+    };
+    if (tid == 0)
+#pragma unroll 1
+      for (int i = 0; i < min(kRing, mine); ++i) issue(i);
+    for (int i = (k + gid) % kGroups; i < mine; i += kGroups) {
+      const int bar = (k + i) % kBars;
+      failed = !wait_rows(grp, &sh.landed[bar], ((k + i) / kBars) & 1, &sh.abort, &sh.timeout);
+      if (failed) break;
+      const Place at = sh.place[bar];  // (written before its load was issued)
+      fill_page<false>(P, grp, at, Target(P, at, grp.tid == 0), rows_of(k + i), [&] {
+        if (grp.tid == kAppThreads - 32 && i + kRing < mine) issue(i + kRing);
+      });
+    }
+    k += mine;
+    f += static_cast<long long>(mine) * gridDim.x;
+    if (__syncthreads_or(failed)) {  // every copy lands before the CTA exits
+      if (tid == 0) {
+        record_status(P.status, MLA_STATUS_TIMEOUT);
+        for (int q = 0; q < kBars; ++q)
+          if (sh.issued[q] > 0)
+            mbar_wait_drain(smem_u32(&sh.landed[q]), (sh.issued[q] - 1) & 1, &sh.timeout);
+      }
+      return;
+    }
   }
 }
 
@@ -332,10 +432,11 @@ cudaError_t launch_append(const void* rows, int max_new, const int32_t* new_lens
   if (max_new <= kFewTokens)
     return launch_pdl(append_few_kernel, dim3(touched_pages(max_new, max_pages), B),
                       dim3(kAppThreads), max_new * kDqk * 2, st, P);
+  const int smem = kRing * kRowsBytes;
   const cudaError_t e = cudaFuncSetAttribute(
-      append_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAppSmem);
+      append_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(append_pages_kernel, dim3(3 * sm_count), dim3(kAppThreads), kAppSmem, st, P);
+  return launch_pdl(append_pages_kernel, dim3(sm_count), dim3(kPagesThreads), smem, st, P);
 }
 
 cudaError_t launch_page_keys(const void* cache, const float* kv_scale,

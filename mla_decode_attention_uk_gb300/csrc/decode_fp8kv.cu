@@ -124,19 +124,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-__device__ __forceinline__ bool bar_any(uint32_t id, uint32_t n, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.or.pred q, %2, %3, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}\n"
-      : "=r"(r)
-      : "r"(pred ? 1u : 0u), "r"(id), "r"(n)
-      : "memory");
-  return r != 0;
-}
-
 // Two fp32 values to two E5M2 codes in the high bytes of an fp16 pair: E5M2 is
 // fp16's upper byte, so rounding is an addition and a mask (ties away from
 // zero; |x| <= 2^15 and its rounding stay finite).

@@ -125,6 +125,20 @@ __device__ __forceinline__ float row_scale(float amax, int e) {
   return amax < INFINITY ? exp2_int(e) : __uint_as_float(0x7fffffffu);
 }
 
+// A named barrier of n threads: whether any of them has `pred`.
+__device__ __forceinline__ bool bar_any(uint32_t id, uint32_t n, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, %2, %3, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(pred ? 1u : 0u), "r"(id), "r"(n)
+      : "memory");
+  return r != 0;
+}
+
 // Records the first device-side error, where the caller asked for it.
 __device__ __forceinline__ void record_status(int32_t* status, int code) {
   if (status) atomicCAS(status, 0, code);

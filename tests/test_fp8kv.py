@@ -158,6 +158,27 @@ def test_append_equals_the_definition(lens, new, max_new):
 
 
 @gpu
+@pytest.mark.parametrize("kind", ["long", "many", "the last ones only", "three times"])
+def test_append_of_many_pages(kind):
+    # More pages than the buffers of all SMs hold, and more sequences than are
+    # looked at together; every page once, whatever order they are filled in.
+    lens = {"long": [60000, 41, 30123], "many": [1 + 13 * i % 151 for i in range(1100)],
+            "the last ones only": [0] * 515 + [70, 0, 9, 64, 4000],
+            "three times": [5000, 700, 9000]}[kind]
+    new = [n - (i % 3) * (n // 5) if n > 3 else n for i, n in enumerate(lens)]
+    table, used = tables(lens, 21)
+    g = torch.Generator().manual_seed(22)
+    base = torch.randn(max(new), 576, generator=g).to(BF)
+    rows = torch.stack([base.roll(7 * b, 1) * 2.0 ** (b % 5) for b in range(len(lens))])
+    kv8 = torch.randint(0, 127, (used, 64, 576), generator=g, dtype=torch.uint8)
+    kvs = torch.exp2(torch.randint(-12, -4, (used,), generator=g).float())
+    rk, rs = ref.append(rows, new, table, lens, kv8, kvs)
+    for _ in range(3 if kind == "three times" else 1):
+        k, s, st = run_append(rows, new, table, lens, kv8, kvs, used)
+        assert st == 0 and torch.equal(s, rs) and torch.equal(k, rk)
+
+
+@gpu
 def test_append_token_by_token_equals_the_definition_step_by_step():
     steps, B = 70, 3
     table, used = tables([steps + 60] * B, 8)
