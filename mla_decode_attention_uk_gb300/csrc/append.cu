@@ -139,7 +139,7 @@ struct Target {
 
 // Fills a page from its new rows, which a thread holds in registers between their
 // maximum and the codes; `taken` is called once all have theirs.  kFew skips what
-// a few rows do not fill, at a price for whole pages (14.2 -> 15.6 us).  (Every thread
+// a few rows do not fill, at a price for whole pages (14 -> 15.5 us).  (Every thread
 // has its Target before the first barrier here; one thread replaces the scale
 // behind it.)
 template <bool kFew, typename Taken>
@@ -203,7 +203,8 @@ __device__ __forceinline__ void fill_page(const AppendParams& P, const Group& gr
 }
 
 // A few new tokens per sequence: one CTA per sequence and page that they can
-// touch.
+// touch.  One token for each of 128 sequences: 2.6 us in a graph, a launch and a
+// chain of three reads (lengths, block table, scale) beside the row's.
 __global__ void __launch_bounds__(kAppThreads)
 append_few_kernel(AppendParams P) {
   extern __shared__ __align__(128) uint4 rows_sh[];
@@ -240,8 +241,8 @@ append_few_kernel(AppendParams P) {
 // for every page that a sequence could have, the empty ones of ragged prompts took
 // a third of the time).  The CTA's pages pass through a ring of three buffers, and
 // two groups of threads take turns at filling them, so that loads and conversions
-// overlap: 13 prompts of 512 to 8190 tokens 14.1 us, 4.6 TB/s; three CTAs of one
-// buffer took 15.7, and two passes over shared memory in place of registers 15.9.
+// overlap: 13 prompts of 512 to 8190 tokens 14.5 us, 4.5 TB/s; three CTAs of one
+// buffer took 16.2, and two passes over shared memory in place of registers 16.
 // What is left is mostly the start (lengths, sums, first loads: 2 us with nothing in
 // flight) and the last pages' conversion.
 constexpr int kRing = 3;
@@ -354,6 +355,10 @@ constexpr int kKeyThreads = 288;
 
 // One CTA per (sequence, page that holds new tokens): the mean of its filled
 // rows.  Thread t sums columns 8 (t mod 72) .. + 7 over rows t / 72, + 4, ...
+// Four rows in flight: 13 prompts of 512 to 8190 tokens 10.6 us from a bf16 cache, 4.1
+// TB/s with the launch and the lengths' and the table's reads (eight rows in flight
+// 11.2, sixteen 14.9: registers and the ragged pages' remainders); the last pages of
+// 128 sequences 3.0 us, 8-bit.
 template <bool kFp8>
 __global__ void __launch_bounds__(kKeyThreads)
 page_keys_kernel(const uint8_t* __restrict__ cache, const float* __restrict__ kv_scale,
