@@ -282,8 +282,9 @@ int mla_decode_attend_fp8kv(const mla_decode_dims* dims, const uint8_t* kv_fp8,
  * run as on any other:
  *   append or write tokens; page_keys          (per layer)
  *   absorb -> q_lat; score_pages(q_lat); select_pages -> sel_table, sel_lens
- *   plan, run or run_fp8kv with dims {batch = B * T, q_len = 1,
- *     max_pages_per_seq = top_k}, sel_table and sel_lens
+ *   plan, then attend or attend_fp8kv, combine and up_project, with dims {batch
+ *     = B * T, q_len = 1, max_pages_per_seq = top_k}, sel_table and sel_lens (the
+ *     plan leaves q_lat as it is; run or run_fp8kv would absorb once more)
  * (q [B, T, H, 192] is [B * T, 1, H, 192] as it stands.)  Not described by the
  * method's pages; for either kind of cache. */
 

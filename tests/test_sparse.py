@@ -346,6 +346,51 @@ def test_append_score_select_and_decode_together(fp8, T, H):
 
 
 @gpu
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T,H", [(1, 16), (2, 128)])
+def test_one_absorb_serves_scores_and_attention(fp8, T, H):
+    # absorb, scores, selection, plan, attention and the rest: bit for bit a run's
+    # results, which absorbs for itself.
+    B, top_k, lens = 3, 5, [900, 64 + T, 1500]
+    inp = make_inputs(B, lens, T, H, seed=65)
+    pages, width = inp.cache.shape[0], inp.block_table.shape[1]
+    g = inp.to(torch.device("cuda"))
+    d = binding.Dims(B, T, H, 128, 64, 512, 128, 64, pages, width)
+    keys = torch.zeros(pages, 576, dtype=BF, device="cuda")
+    kv8, kvs = (x.cuda() for x in ref.quantise(inp.cache.nan_to_num(0.0)))
+    binding.page_keys_fp8kv(d, kv8, kvs, g.block_table, g.seq_lens, max(lens), keys, g.seq_lens)
+    m = binding.MlaDecode(binding.Dims(B * T, 1, H, 128, 64, 512, 128, 64, pages, top_k),
+                          fp8_kv=fp8)
+    scores = torch.empty(B, T, width, device="cuda")
+    st = torch.empty(B * T, top_k, dtype=torch.int32, device="cuda")
+    sl = torch.empty(B * T, dtype=torch.int32, device="cuda")
+    q = g.q.view(B * T, 1, H, 192)
+    got = [(torch.zeros(B * T, 1, H, 128, dtype=BF, device="cuda"),
+            torch.zeros(B * T, 1, H, device="cuda")) for _ in range(2)]
+    m.absorb(q, g.w_uk)
+    binding.score_pages(d, m.q_lat().view(B, T, H, 576), keys, g.block_table, g.seq_lens, scores)
+    binding.select_pages(d, scores, g.block_table, g.seq_lens, top_k, 1, 1, st, sl)
+    m.plan(sl)
+    out, lse = got[0]
+    if fp8:
+        m.attend_fp8kv(kv8, kvs, st, sl, g.scale, lse)
+    else:
+        m.attend(g.cache, st, sl, g.scale, lse)
+    m.combine(g.scale, lse)
+    m.up_project(g.w_uv, out)
+    assert m.check() == 0
+    out, lse = got[1]
+    args = (st, sl, g.w_uk, g.w_uv, g.scale, out, lse)
+    if fp8:
+        m.run_fp8kv(q, kv8, kvs, *args)
+    else:
+        m.run(q, g.cache, *args)
+    assert m.check() == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert bool(got[0][0].any()) and got[0][1].isfinite().all()
+
+
+@gpu
 def test_the_whole_chain_captured_and_replayed_on_another_stream():
     B, T, H, top_k = 3, 2, 32, 4
     inp = make_inputs(B, [900, 300, 130], T, H, seed=70)
