@@ -152,9 +152,11 @@ bmm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUt
 
   // Neither step waits for its predecessor up front.  The absorb step reads
   // only the caller's q and W_UK, so it overlaps the planner; it waits for
-  // its predecessor just before exiting, so that its completion still implies
-  // the planner's (the attention step relies on it).  The up-projection loads
-  // its first weight tiles, then waits (producer thread) before loading o_lat.
+  // its predecessor before its first store, as that may be the up-projection
+  // of the run before (several runs on one plan), whose attention step may
+  // still read q_lat.  Its completion thereby implies the planner's too (the
+  // attention step relies on it).  The up-projection loads its first weight
+  // tiles, then waits (producer thread) before loading o_lat.
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tok0 = blockIdx.x * NT;
@@ -306,32 +308,23 @@ bmm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUt
   __syncwarp();
   constexpr int kThreads = W8 ? kBmmThreadsW8 : kBmmThreads;
 
+  // q_pe passes through unchanged into columns 512..575 of q_lat (8 chunks
+  // of 16 B per token).  The helper warps (2 and up: idle, or done
+  // converting) load it while the MMAs run, all chunks at once, so the copy
+  // costs one memory round trip instead of one per chunk.
+  constexpr int kHelpers = kThreads - 64;
+  constexpr int kPeIters = MODE == BmmMode::kAbsorb ? (NT * 8 + kHelpers - 1) / kHelpers : 1;
+  const int pe_chunks = MODE == BmmMode::kAbsorb && blockIdx.y == 0 && warp >= 2
+                            ? min(NT, BT - tok0) * 8
+                            : 0;
+  uint4 pe[kPeIters];
   if constexpr (MODE == BmmMode::kAbsorb) {
-    // q_pe passes through unchanged into columns 512..575 of q_lat (8 chunks
-    // of 16 B per token).  The helper warps (2 and up: idle, or done
-    // converting) copy it while the MMAs run, all loads before the stores,
-    // so the copy costs one memory round trip instead of one per chunk.
-    if (blockIdx.y == 0 && warp >= 2) {
-      constexpr int kHelpers = kThreads - 64;
-      constexpr int kIters = (NT * 8 + kHelpers - 1) / kHelpers;
-      const int nchunks = min(NT, BT - tok0) * 8;
-      const int t0 = threadIdx.x - 64;
-      uint4 v[kIters];
 #pragma unroll
-      for (int it = 0; it < kIters; ++it) {
-        const int i = t0 + it * kHelpers;
-        if (i < nchunks) {
-          const size_t row = static_cast<size_t>(tok0 + (i >> 3)) * H + h;
-          v[it] = *reinterpret_cast<const uint4*>(q + row * kDq + kNope + (i & 7) * 8);
-        }
-      }
-#pragma unroll
-      for (int it = 0; it < kIters; ++it) {
-        const int i = t0 + it * kHelpers;
-        if (i < nchunks) {
-          const size_t row = static_cast<size_t>(tok0 + (i >> 3)) * H + h;
-          *reinterpret_cast<uint4*>(out_hi + row * kDqk + kLora + (i & 7) * 8) = v[it];
-        }
+    for (int it = 0; it < kPeIters; ++it) {
+      const int i = static_cast<int>(threadIdx.x) - 64 + it * kHelpers;
+      if (i < pe_chunks) {
+        const size_t row = static_cast<size_t>(tok0 + (i >> 3)) * H + h;
+        pe[it] = *reinterpret_cast<const uint4*>(q + row * kDq + kNope + (i & 7) * 8);
       }
     }
   }
@@ -369,7 +362,25 @@ bmm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUt
       }
     }
   }
+  // The tensor memory goes back before the absorb step waits: a predecessor
+  // that has yet to allocate its own on this SM must not wait for this CTA.
+  tc_fence_before();
   __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  if constexpr (MODE == BmmMode::kAbsorb) {
+    griddep_wait();  // q_lat and q_lo may still be read until here
+#pragma unroll
+    for (int it = 0; it < kPeIters; ++it) {
+      const int i = static_cast<int>(threadIdx.x) - 64 + it * kHelpers;
+      if (i < pe_chunks) {
+        const size_t row = static_cast<size_t>(tok0 + (i >> 3)) * H + h;
+        *reinterpret_cast<uint4*>(out_hi + row * kDqk + kLora + (i & 7) * 8) = pe[it];
+      }
+    }
+  }
   if (go) {
     const int ntok = min(NT, BT - tok0);
     // 16 chunks of 16 B per token row.
@@ -392,13 +403,6 @@ bmm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUt
       }
     }
   }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 2) {
-    tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
-  }
-  if constexpr (MODE == BmmMode::kAbsorb) griddep_wait();
 }
 
 // Absorb step for 128 tokens or more: the untransposed
@@ -462,8 +466,8 @@ absorb_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
   __shared__ int abort_sh;
 
   // Like the transposed absorb kernel: q and W_UK come from the caller, so
-  // nothing is waited for up front; the wait for the predecessor (the
-  // planner) comes just before exiting.
+  // nothing is waited for up front; the wait for the predecessor (the planner,
+  // or the run before) comes before the first store.
   griddep_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ntt = (BT + 127) / 128;
@@ -687,6 +691,10 @@ absorb_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
       if (lane == 0) mbar_arrive(smem_u32(&acc_empty[j]));
       fence_proxy_async_smem();
       named_bar_sync(1, kArEpiThreads);
+      // q_lat and q_lo may still be read until here.  (This CTA holds its tensor
+      // memory meanwhile: 256 columns, and no kernel that needs more than the
+      // other 256 fits next to its shared memory.)
+      if (i == 0) griddep_wait();
       if (et == 0) {
         tma_store_2d(&tm_hi, h * kDqk + n0, tok0, hi_t);
         tma_store_2d(&tm_hi, h * kDqk + n0 + 64, tok0, hi_t + 128 * 128);
@@ -713,7 +721,7 @@ absorb_rows_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_consta
     tc_fence_after();
     tmem_dealloc(tmem, 256);
   }
-  griddep_wait();
+  griddep_wait();  // (every thread once: the other warps have not waited yet)
 }
 
 // Up-projection for 128 tokens or more (bf16 weights), with the first-order

@@ -681,3 +681,39 @@ def test_cache_offsets_beyond_32_bits():
     binding.append_fp8kv(d, rows.cuda(), big, scale, table, g.seq_lens)
     rk, rs = ref.append(rows, [1, 1], inp.block_table, [200, 70], kv8, kvs)
     assert torch.equal(big[where.cuda()].cpu(), rk) and torch.equal(scale[where.cuda()].cpu(), rs)
+
+
+@gpu
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("B,H,ranges", [(24, 16, 1), (24, 128, 1), (160, 16, 2), (40, 64, 0)])
+def test_runs_of_other_queries_back_to_back_on_one_plan(fp8, B, H, ranges):
+    # A plan serves every layer of a step.  The absorb step of a run starts while
+    # the run before it is at work, whose attention reads the absorbed query of
+    # one sequence after the other (with one range on a single SM, the others
+    # being free): every run must see its own queries, bit for bit.
+    inp = make_inputs(B, [500 + 37 * i % 300 for i in range(B)], 1, H, seed=80)
+    inp, kv8, kvs = fp8_inputs(inp)
+    g = inp.to(torch.device("cuda"))
+    k, s = kv8.cuda(), kvs.cuda()
+    m = binding.MlaDecode(binding.dims_for(g.q, g.cache, g.block_table), num_ranges=ranges,
+                          fp8_kv=fp8)
+    gen = torch.Generator().manual_seed(81)
+    queries = [torch.randn(B, 1, H, 192, generator=gen).to(BF).cuda() for _ in range(4)]
+    mk = lambda: [(torch.zeros(B, 1, H, 128, dtype=BF, device="cuda"),
+                   torch.zeros(B, 1, H, device="cuda")) for _ in queries]
+
+    def run(q, out, lse):
+        tail = (g.block_table, g.seq_lens, g.w_uk, g.w_uv, g.scale, out, lse)
+        m.run_fp8kv(q, k, s, *tail) if fp8 else m.run(q, g.cache, *tail)
+
+    alone, together = mk(), mk()
+    m.plan(g.seq_lens)
+    for q, (out, lse) in zip(queries, alone):
+        run(q, out, lse)
+        torch.cuda.synchronize()
+    for _ in range(5):
+        for q, (out, lse) in zip(queries, together):
+            run(q, out, lse)
+    assert m.check() == 0
+    for (o1, l1), (o2, l2) in zip(alone, together):
+        assert torch.equal(o1, o2) and torch.equal(l1, l2)
