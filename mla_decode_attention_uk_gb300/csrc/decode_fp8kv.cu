@@ -174,12 +174,19 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
                     const __grid_constant__ CUtensorMap tm_rope,
                     const __grid_constant__ CUtensorMap tm_q, Params P) {
   extern __shared__ uint8_t smem_raw[];
-  // By slot: slot_full, a page has landed; slot_free, PV has read it and its P^T.
+  // By slot: slot_full, a page has landed; slot_free, PV has read it and its P^T,
+  // or the query terms are made of the tile that was there.
   // p_full[g mod kSlots]: P^T of page g is written (a page kSlots further on
   // is not in a slot before PV has read this one).
+  // pv_done[g mod kSlots]: PV of page g is complete.  (slot_free does not tell a
+  // softmax group: a query tile's release is one more of its phases, which may
+  // come before the group has looked, and a parity then means another phase.  A
+  // next phase here takes PV of page g + kSlots, which follows that of page g +
+  // 1, the group's own.  The phase before is over: page g + 1 is in a slot, so PV
+  // has read every page up to g + 1 - kSlots.)
   __shared__ __align__(8) uint64_t q_full, q_free, slot_full[kSlots], slot_free[kSlots],
-      s_full[kSBufs], s_free[kSBufs], p_full[kSlots], q_raw, o_full, o_free, m_final[2][4],
-      sums_full, epi_done, drain_bar[3];
+      s_full[kSBufs], s_free[kSBufs], p_full[kSlots], pv_done[kSlots], q_raw, o_full, o_free,
+      m_final[2][4], sums_full, epi_done, drain_bar[3];
   __shared__ PlanView view;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
@@ -204,6 +211,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
       mbar_init(smem_u32(&slot_full[i]), 1);
       mbar_init(smem_u32(&slot_free[i]), 2);
       mbar_init(smem_u32(&p_full[i]), 4);
+      mbar_init(smem_u32(&pv_done[i]), 2);
     }
     mbar_init(smem_u32(&q_raw), 1);
     for (int i = 0; i < kSBufs; ++i) {
@@ -393,6 +401,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
                 umma_f8(tmem + kTmemOut + 64 * m, ad0 + ((m * kBox + (kk & 1) * 4096) >> 4),
                         bd0 + kk * 2, idesc, !(first && kk == 0));
             }
+            umma_commit(smem_u32(&pv_done[g % kSlots]));
             umma_commit(smem_u32(&slot_free[s]));
           }
           if (!ok) break;
@@ -644,8 +653,8 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
           bool f = *static_cast<volatile int*>(&abort_sh) != 0;
           if (owner) alpha_sh[q][srow] = raise ? ex2_approx(m_old - pmax) : 1.0f;
           if (!f && !first &&
-              !mbar_wait(smem_u32(&slot_free[(ring - 1) % kSlots]), ((ring - 1) / kSlots) & 1,
-                         &abort_sh, P.status))
+              !mbar_wait(smem_u32(&pv_done[(g - 1) % kSlots]), ((g - 1) / kSlots) & 1, &abort_sh,
+                         P.status))
             f = true;
           if (bar_any(1 + q, 128, f)) { fail = true; break; }
           if (!first) {

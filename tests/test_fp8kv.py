@@ -717,3 +717,27 @@ def test_runs_of_other_queries_back_to_back_on_one_plan(fp8, B, H, ranges):
     assert m.check() == 0
     for (o1, l1), (o2, l2) in zip(alone, together):
         assert torch.equal(o1, o2) and torch.equal(l1, l2)
+
+
+@gpu
+@pytest.mark.parametrize("H,ranges", [(16, 1), (16, 3), (128, 1)])
+def test_a_maximum_that_rises_with_every_page_of_many_pieces(H, ranges):
+    # Scores that grow by more than the lazy maximum's slack from page to page:
+    # every page but a piece's first rescales the output, behind the product of
+    # the page before, while the next piece's query tile and its terms take the
+    # slots that this product frees.  Pieces of three to six pages, many to a CTA.
+    lens = [64 * (3 + i % 4) - i % 7 for i in range(48)]
+    inp = make_inputs(len(lens), lens, 1, H, seed=82)
+    inp.q[..., :128] = 0.0
+    inp.q[..., 128:] = 1.0
+    inp.cache[..., 512:] = 0.0
+    for b, n in enumerate(lens):
+        for j in range((n + 63) // 64):
+            # 64 products of 2 j, times 1 / sqrt(192): 9.2 a page, 8 ln 2 = 5.5.
+            inp.cache[int(inp.block_table[b, j]), :, 512:] = 2.0 * j
+    inp, kv8, kvs = fp8_inputs(inp)
+    out, lse = run_fp8(inp, kv8, kvs, num_ranges=ranges)
+    assert_parity(compare(inp, out, lse), "ranges %d" % ranges)
+    for _ in range(20):
+        out2, lse2 = run_fp8(inp, kv8, kvs, num_ranges=ranges)
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
