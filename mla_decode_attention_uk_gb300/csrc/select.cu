@@ -372,8 +372,10 @@ cudaError_t launch_score(const CUtensorMap& tm_q, const void* page_keys,
   const int tokens = score_tokens(T, H), rows = tokens * H;
   const int smem = 1024 + score_stages(rows) * score_stage_bytes(rows);
   static_assert(score_stages(kScoreRowsMax) >= kStagesMin, "the gather waits for four stages");
-  const cudaError_t e =
-      cudaFuncSetAttribute(score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // The attribute is the kernel's, not the launch's: always the same value, so
+  // that calls of other shapes on other threads do not take it away.
+  const cudaError_t e = cudaFuncSetAttribute(
+      score_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 1024 + kScoreSmemMax);
   if (e != cudaSuccess) return e;
   const dim3 grid((max_pages + kScorePages - 1) / kScorePages, (T + tokens - 1) / tokens, B);
   return launch_pdl(score_kernel, grid, dim3(kScoreThreads), smem, st, tm_q,

@@ -1,6 +1,7 @@
 """Block-sparse decode: page keys, scores, selection, and the decode on them."""
 import ctypes
 import math
+import threading
 
 import pytest
 import torch
@@ -450,3 +451,39 @@ def test_the_whole_chain_captured_and_replayed_on_another_stream():
         err = (out.cpu().double() - o).abs()
         assert err.max() <= ref.OUT_MAX and err.mean() <= ref.OUT_MEAN
         assert (lse.cpu().double() - l).abs().max() <= 1e-3
+
+
+@gpu
+def test_scores_of_other_shapes_from_several_host_threads():
+    # Shapes whose kernels take different amounts of shared memory (16, 64 and 128
+    # rows of queries), called at once from three threads.
+    g = torch.Generator().manual_seed(75)
+    table, lens = i32([[0, 1], [2, 3]]).cuda(), i32([100, 128]).cuda()
+    keys = torch.randn(4, 576, generator=g).to(BF).cuda()
+    cases = []
+    for H in (16, 64, 128):
+        q = torch.randn(2, 1, H, 576, generator=g).to(BF).cuda()
+        want = torch.empty(2, 1, 2, device="cuda")
+        binding.score_pages(dims(2, 1, H), q, keys, table, lens, want)
+        cases.append((H, q, want))
+    torch.cuda.synchronize()
+    start, errors = threading.Barrier(len(cases)), []
+
+    def work(H, q, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                got = torch.empty(2, 1, 2, device="cuda")
+                start.wait()
+                for _ in range(2000):
+                    binding.score_pages(dims(2, 1, H), q, keys, table, lens, got)
+                torch.cuda.current_stream().synchronize()
+                assert torch.equal(got, want)
+        except Exception as e:  # noqa: BLE001 (any error of a thread fails the test)
+            errors.append((H, e))
+
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
