@@ -764,12 +764,17 @@ static DecodeShape decode_shape(int T, int H, int sm_count) {
   return d;
 }
 
+// Allows the kernel the most shared memory that any shape takes.  (The limit
+// is the kernel's, not the launch's: with a limit per shape, calls of other
+// shapes on other threads would take it away between here and the launch.)
+static cudaError_t allow_smem(void (*kern)(CUtensorMap, CUtensorMap, DecodeParams)) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kDynSmemMax);
+}
+
 // Default number of work ranges for the planner (see decode_shape).
 cudaError_t decode_default_ranges(int T, int H, int sm_count, int* ranges) {
   const DecodeShape shape = decode_shape(T, H, sm_count);
-  cudaError_t e = cudaFuncSetAttribute(
-      shape.sets > 1 ? decode_kernel<true> : decode_kernel<false>,
-      cudaFuncAttributeMaxDynamicSharedMemorySize, decode_smem_bytes(T, H));
+  cudaError_t e = allow_smem(shape.sets > 1 ? decode_kernel<true> : decode_kernel<false>);
   if (e != cudaSuccess) return e;
   *ranges = shape.ranges;
   return cudaSuccess;
@@ -785,7 +790,7 @@ cudaError_t launch_decode(const CUtensorMap& tm_q, const CUtensorMap& tm_c, int 
   const int smem = decode_smem_bytes(T, H);
   const DecodeShape shape = decode_shape(T, H, sm_count);
   auto kern = shape.sets > 1 ? decode_kernel<true> : decode_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow_smem(kern);
   if (e != cudaSuccess) return e;
   DecodeParams P;
   P.block_table = block_table;

@@ -6,6 +6,7 @@ oracle is threaded over query rows; the largest, draft_q8, is about 2e8
 row-keys)."""
 import math
 import random
+import threading
 
 import numpy as np
 import pytest
@@ -457,3 +458,38 @@ def test_full_size_fp8_weights_all_rows(name):
     assert m.check() == 0
     assert_parity(compare(inp, out.cpu(), lse.cpu()), "fp8 weights " + name)
 
+
+
+def test_runs_of_other_shapes_from_several_host_threads():
+    # Shapes whose attention kernels take different amounts of shared memory,
+    # called at once from three threads, each with its own workspace.
+    dev = torch.device("cuda")
+    cases = []
+    for H in (16, 48, 64):
+        g = make_inputs(2, [70, 130], 1, H, seed=90 + H).to(dev)
+        m = binding.MlaDecode(binding.dims_for(g.q, g.cache, g.block_table), dev)
+        want = binding.decode(g.q, g.cache, g.block_table, g.seq_lens, g.w_uk, g.w_uv, g.scale)
+        cases.append((g, m, want))
+    torch.cuda.synchronize()
+    start, errors = threading.Barrier(len(cases)), []
+
+    def work(g, m, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
+                start.wait()
+                for _ in range(1000):
+                    m.plan(g.seq_lens)
+                    m.run(g.q, g.cache, g.block_table, g.seq_lens, g.w_uk, g.w_uv, g.scale, out,
+                          lse)
+                assert m.check() == 0
+                assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        except Exception as e:  # noqa: BLE001 (any error of a thread fails the test)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
