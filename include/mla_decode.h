@@ -256,8 +256,8 @@ int mla_decode_plan_fp8kv(const mla_decode_dims* dims, const int32_t* seq_lens,
  * 2^32] is reported as DEVICE_BOUNDS by mla_decode_check and taken as 1.  A
  * query row that is not finite gives NaN, for the row alone; a NaN code in a
  * token that is seen gives NaN, for its sequence.
- * The absorbed query enters as its bf16 part, exactly
- * (to 2^-21 of its row's largest value), and the lse gets the same first-order
+ * The absorbed query enters as its bf16 part, exactly (to 2^-19 of its row's
+ * largest value, whatever that is), and the lse gets the same first-order
  * correction as over the bf16 cache; the softmax weights are rounded to two
  * 3-bit terms (at most 2^-7 of a weight), and the output is normalised by the
  * sum of the weights as rounded.  As many kernels as mla_decode_run. */

@@ -13,8 +13,8 @@
 // operand loses in 8 bits is given back by a second term:
 //   * Q = scale_row (hi + mid / 16), both E4M3: hi is the value cut to four
 //     significant bits, mid the rest times 16.  A bf16 value has eight and the
-//     two terms hold it exactly (down to 2^-13 of the row's largest value; below
-//     that to 2^-21 of it), so the product is that of the bf16 query.  The terms
+//     two terms hold it exactly (down to 2^-13 of the row's largest value; smaller
+//     ones to 2^-19 of that), so the product is that of the bf16 query.  The terms
 //     are stacked as the M = 128 rows of one MMA: the full rate of the tensor
 //     core for 64 query rows, where a 64-row MMA would run at half of it.  The
 //     512 latent columns of the terms live in TMEM (128 columns), so that QK^T
@@ -446,7 +446,6 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
         };
         const int rows_here = min(kTileRows, TH - ((pc.task % sets) * tpg + ti) * kTileRows);
         bool ok = mbar_wait(smem_u32(&q_raw), n & 1, &abort_sh, P.status);
-        // A row's largest value takes the top but one of E4M3's binades.
         int e = 0;
         float amax = 0.0f;
         if (n == 0) {
@@ -465,7 +464,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
             }
             const float amax =
                 __uint_as_float(__reduce_max_sync(0xffffffffu, larger_half(top)));
-            const int er = page_scale_exp(amax) + 1;  // amax <= 224 * 2^er
+            const int er = term_exp(amax);
             const __nv_bfloat162 down = term_factor(er);
             if (er > kTermExpMax)
 #pragma unroll
@@ -493,7 +492,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
             }
           const uint32_t t = larger_half(top);
           amax = __uint_as_float(max(t, __shfl_xor_sync(0xffffffffu, t, 2)));
-          e = page_scale_exp(amax) + 1;
+          e = term_exp(amax);
           // A loop of its own, as it is rare (rows past the last hold anything).
           const bool lower = srow < rows_here && e > kTermExpMax;
           if (__any_sync(0xffffffffu, lower))

@@ -38,11 +38,14 @@ constexpr int kBoxes8 = 5;                // 128-byte-wide boxes of a cached row
 
 // Exponent of the smallest power of two s with amax <= 448 s, within the
 // bounds.  amax: finite, >= 0; exact (bit operations only).
-__device__ __forceinline__ int page_scale_exp(float amax) {
+__device__ __forceinline__ int scale_exp(float amax, int lo, int hi) {
   const uint32_t u = __float_as_uint(amax);
   const int k = static_cast<int>(u >> 23) - 127;  // amax = m 2^k, 1 <= m < 2 (normal numbers)
   const int e = k - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);  // 448 = 1.75 * 2^8
-  return max(kScaleExpMin, min(kScaleExpMax, e));
+  return max(lo, min(hi, e));
+}
+__device__ __forceinline__ int page_scale_exp(float amax) {
+  return scale_exp(amax, kScaleExpMin, kScaleExpMax);
 }
 __device__ __forceinline__ float exp2_int(int e) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
@@ -74,7 +77,7 @@ __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) {
   return *reinterpret_cast<const __nv_bfloat162*>(&w);
 }
 // Four bf16 values as two words of E4M3 codes: value = 2^e (hi + mid / 16) for |value|
-// < 256 * 2^e, exactly down to |value| = 2^(e - 6) (and to 2^(e - 14) below).
+// < 256 * 2^e, exactly down to |value| = 2^(e - 6) (cut to 2^(e - 13) below).
 // down = 2^(-e - 120) brings E4M3's exponent field and steps (bias 7) onto
 // bf16's (bias 127), subnormals too, so that a code is a bit field of the bf16
 // number: hi is the value cut to four significant bits, mid 16 times the rest,
@@ -100,6 +103,12 @@ __device__ __forceinline__ void split_terms(uint2 x, __nv_bfloat162 down, uint32
   hi = __byte_perm(h[0], h[1], 0x6420);
   mid = __byte_perm(m[0], m[1], 0x6420);
 }
+
+// A query row's exponent: amax <= 224 * 2^e, so that the row's largest value takes
+// the top but one of E4M3's binades.  Rows of every size that bf16 has: e reaches
+// 121 for the largest; below 2^-118 it stays at -126 (2^e remains a normal number)
+// and the terms hold bf16's smallest values, multiples of 2^-133, exactly.
+__device__ __forceinline__ int term_exp(float amax) { return scale_exp(amax, -127, 120) + 1; }
 
 // split_terms' factor for a row's exponent, and what comes before it where 2^(-e -
 // 120) is below bf16's normal numbers (rows beyond 224 * 2^6).

@@ -741,3 +741,19 @@ def test_a_maximum_that_rises_with_every_page_of_many_pieces(H, ranges):
     for _ in range(20):
         out2, lse2 = run_fp8(inp, kv8, kvs, num_ranges=ranges)
         assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+@gpu
+@pytest.mark.parametrize("H,lens", [(16, [300, 70]), (128, [64] * 90)])
+@pytest.mark.parametrize("e", [-100, -80, -50, -40, -36, 36, 40, 41, 44, 60, 90, 110])
+def test_queries_of_extreme_size(e, H, lens):
+    # As test_queries_of_any_size, towards the ends of bf16's range.
+    inp = make_inputs(len(lens), lens, 1, H, seed=46)
+    inp.q = (inp.q.float() * 2.0 ** e).to(BF)
+    inp.scale = inp.scale / 2.0 ** e
+    inp, kv8, kvs = fp8_inputs(inp)
+    out, lse = run_fp8(inp, kv8, kvs, num_ranges=20 if H == 128 else 0)
+    s = compare(inp, out, lse)
+    # The bound of the lse: as there.
+    assert s["out_max"] <= ref.OUT_MAX and s["out_mean"] <= ref.OUT_MEAN, s
+    assert s["lse_max"] <= 1.7 * 3 * 2.0 ** -9, s
