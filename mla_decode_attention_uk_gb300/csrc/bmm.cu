@@ -314,15 +314,14 @@ bmm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUt
   // costs one memory round trip instead of one per chunk.
   constexpr int kHelpers = kThreads - 64;
   constexpr int kPeIters = MODE == BmmMode::kAbsorb ? (NT * 8 + kHelpers - 1) / kHelpers : 1;
-  const int pe_chunks = MODE == BmmMode::kAbsorb && blockIdx.y == 0 && warp >= 2
-                            ? min(NT, BT - tok0) * 8
-                            : 0;
+  const bool pe_mine = MODE == BmmMode::kAbsorb && blockIdx.y == 0 && warp >= 2;
+  const int pe_chunks = min(NT, BT - tok0) * 8;
   uint4 pe[kPeIters];
   if constexpr (MODE == BmmMode::kAbsorb) {
 #pragma unroll
     for (int it = 0; it < kPeIters; ++it) {
       const int i = static_cast<int>(threadIdx.x) - 64 + it * kHelpers;
-      if (i < pe_chunks) {
+      if (pe_mine && i < pe_chunks) {
         const size_t row = static_cast<size_t>(tok0 + (i >> 3)) * H + h;
         pe[it] = *reinterpret_cast<const uint4*>(q + row * kDq + kNope + (i & 7) * 8);
       }
@@ -375,7 +374,7 @@ bmm_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUt
 #pragma unroll
     for (int it = 0; it < kPeIters; ++it) {
       const int i = static_cast<int>(threadIdx.x) - 64 + it * kHelpers;
-      if (i < pe_chunks) {
+      if (pe_mine && i < pe_chunks) {
         const size_t row = static_cast<size_t>(tok0 + (i >> 3)) * H + h;
         *reinterpret_cast<uint4*>(out_hi + row * kDqk + kLora + (i & 7) * 8) = pe[it];
       }

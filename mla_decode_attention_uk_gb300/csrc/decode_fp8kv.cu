@@ -480,6 +480,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
           }
           // (Here and below warps that share a named barrier leave together, or the
           // others would wait there for one that has given up.)
+          __syncwarp();
           ok = !bar_any(3, 384, !ok);
         } else {
           __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
@@ -764,6 +765,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
       if (lane == 0) mbar_arrive(smem_u32(&sums_full));
       bad = bad || !mbar_wait(smem_u32(&sums_full), n & 1, &abort_sh, P.status) ||
             !mbar_wait(smem_u32(&o_full), n & 1, &abort_sh, P.status);
+      __syncwarp();
       if (bar_any(1 + q, 128, bad)) break;
       tc_fence_after();
       const size_t row_base = dest < 0 ? ~dest : dest;
