@@ -4,6 +4,7 @@ Tolerances: max |d out| <= 2e-2, mean |d out| <= 2e-3, max |d lse| <= 1e-3.
 Every case compares every output row, the full-size workloads included (the
 oracle is threaded over query rows; the largest, draft_q8, is about 2e8
 row-keys)."""
+import ctypes
 import math
 import random
 import threading
@@ -460,36 +461,39 @@ def test_full_size_fp8_weights_all_rows(name):
 
 
 
-def test_runs_of_other_shapes_from_several_host_threads():
+def test_attention_of_other_shapes_from_several_host_threads():
     # Shapes whose attention kernels take different amounts of shared memory,
-    # called at once from three threads, each with its own workspace.
+    # called at once from six threads, each with its own workspace.  (Through the C
+    # entry: the interpreter lets go of its lock there only.)
     dev = torch.device("cuda")
     cases = []
-    for H in (16, 48, 64):
+    for H in (16, 48, 64) * 2:
         g = make_inputs(2, [70, 130], 1, H, seed=90 + H).to(dev)
-        m = binding.MlaDecode(binding.dims_for(g.q, g.cache, g.block_table), dev)
-        want = binding.decode(g.q, g.cache, g.block_table, g.seq_lens, g.w_uk, g.w_uv, g.scale)
-        cases.append((g, m, want))
+        # One range: no sequence is split, the step itself writes every row's lse.
+        m = binding.MlaDecode(binding.dims_for(g.q, g.cache, g.block_table), dev, 1)
+        lse, want = torch.zeros(2, 1, H, device=dev), torch.zeros(2, 1, H, device=dev)
+        m.plan(g.seq_lens)
+        m.absorb(g.q, g.w_uk)
+        m.attend(g.cache, g.block_table, g.seq_lens, g.scale, want)
+        cases.append((g, m, lse, want, torch.cuda.Stream()))
     torch.cuda.synchronize()
-    start, errors = threading.Barrier(len(cases)), []
+    start, codes = threading.Barrier(len(cases)), []
 
-    def work(g, m, want):
-        try:
-            with torch.cuda.stream(torch.cuda.Stream()):
-                out, lse = torch.empty_like(want[0]), torch.empty_like(want[1])
-                start.wait()
-                for _ in range(1000):
-                    m.plan(g.seq_lens)
-                    m.run(g.q, g.cache, g.block_table, g.seq_lens, g.w_uk, g.w_uv, g.scale, out,
-                          lse)
-                assert m.check() == 0
-                assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
-        except Exception as e:  # noqa: BLE001 (any error of a thread fails the test)
-            errors.append(e)
+    def work(g, m, lse, want, stream):
+        fn = binding.lib().mla_decode_attend
+        args = (ctypes.byref(m.dims), g.cache.data_ptr(), g.block_table.data_ptr(),
+                g.seq_lens.data_ptr(), g.scale, lse.data_ptr(), m.workspace.data_ptr(),
+                m.ws_bytes, stream.cuda_stream)
+        torch.cuda.set_device(0)
+        start.wait()
+        codes.extend(c for c in (fn(*args) for _ in range(5000)) if c)
 
     threads = [threading.Thread(target=work, args=c) for c in cases]
     for t in threads:
         t.start()
     for t in threads:
         t.join()
-    assert not errors, errors
+    torch.cuda.synchronize()
+    assert not codes, (len(codes), set(codes))
+    for _, m, lse, want, _ in cases:
+        assert m.check() == 0 and torch.equal(lse, want)
