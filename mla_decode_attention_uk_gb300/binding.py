@@ -146,6 +146,18 @@ class MlaDecode:
         self.workspace = torch.empty(self.ws_bytes, dtype=torch.uint8,
                                      device=device or torch.device("cuda"))
         self.fp8_kv = fp8_kv
+        # What the calls over the 8-bit cache take.  (Query, out and lse by their
+        # number of elements: [B, T, ...] serves a handle of B * T sequences.)
+        B, pages, H = d.batch, d.num_pages, d.num_heads
+        n = B * d.q_len * H
+        self._attend_spec = (
+            ("kv8", torch.uint8, (pages, 64, 576)), ("kv_scale", torch.float32, (pages,)),
+            ("block_table", torch.int32, (B, d.max_pages_per_seq)),
+            ("seq_lens", torch.int32, (B,)), ("lse", torch.float32, n),
+            ("workspace", torch.uint8, self.ws_bytes))
+        self._run_spec = self._attend_spec + (
+            ("q", torch.bfloat16, n * 192), ("w_uk", torch.bfloat16, (H, 128, 512)),
+            ("w_uv", torch.bfloat16, (H, 512, 128)), ("out", torch.bfloat16, n * 128))
 
     def plan(self, seq_lens):
         if self.fp8_kv:
@@ -174,26 +186,22 @@ class MlaDecode:
             "mla_decode_run_fp8w")
 
     def run_fp8kv(self, q, kv8, kv_scale, block_table, seq_lens, w_uk, w_uv, scale, out, lse):
-        d = self.dims
-        stream = _checked(("kv8", kv8, torch.uint8, (d.num_pages, 64, 576)),
-                          ("kv_scale", kv_scale, torch.float32, (d.num_pages,)),
-                          *_lines(d, block_table, seq_lens))
-        _ok(lib().mla_decode_run_fp8kv(ctypes.byref(d), _ptr(q), kv8.data_ptr(),
+        stream = _checked_as(self._run_spec, kv8, kv_scale, block_table, seq_lens, lse,
+                             self.workspace, q, w_uk, w_uv, out)
+        _ok(lib().mla_decode_run_fp8kv(ctypes.byref(self.dims), q.data_ptr(), kv8.data_ptr(),
                                        kv_scale.data_ptr(), block_table.data_ptr(),
-                                       seq_lens.data_ptr(), _ptr(w_uk), _ptr(w_uv), float(scale),
-                                       _ptr(out), _ptr(lse), _ptr(self.workspace), self.ws_bytes,
-                                       stream),
+                                       seq_lens.data_ptr(), w_uk.data_ptr(), w_uv.data_ptr(),
+                                       float(scale), out.data_ptr(), lse.data_ptr(),
+                                       self.workspace.data_ptr(), self.ws_bytes, stream),
             "mla_decode_run_fp8kv")
 
     def attend_fp8kv(self, kv8, kv_scale, block_table, seq_lens, scale, lse):
-        d = self.dims
-        stream = _checked(("kv8", kv8, torch.uint8, (d.num_pages, 64, 576)),
-                          ("kv_scale", kv_scale, torch.float32, (d.num_pages,)),
-                          *_lines(d, block_table, seq_lens))
-        _ok(lib().mla_decode_attend_fp8kv(ctypes.byref(d), kv8.data_ptr(), kv_scale.data_ptr(),
-                                          block_table.data_ptr(), seq_lens.data_ptr(),
-                                          float(scale), _ptr(lse), _ptr(self.workspace),
-                                          self.ws_bytes, stream),
+        stream = _checked_as(self._attend_spec, kv8, kv_scale, block_table, seq_lens, lse,
+                             self.workspace)
+        _ok(lib().mla_decode_attend_fp8kv(ctypes.byref(self.dims), kv8.data_ptr(),
+                                          kv_scale.data_ptr(), block_table.data_ptr(),
+                                          seq_lens.data_ptr(), float(scale), lse.data_ptr(),
+                                          self.workspace.data_ptr(), self.ws_bytes, stream),
             "mla_decode_attend_fp8kv")
 
     def absorb_fp8w(self, q, w_uk8, w_uk_scale):
@@ -270,8 +278,9 @@ def decode(q, cache, block_table, seq_lens, w_uk, w_uv, scale, num_ranges: int =
 # ---------------------------------------------------------------- 8-bit cache, sparse decode
 def _refuse(name, t, dtype, shape):
     got = None if t is None else (t.dtype, tuple(t.shape), t.is_contiguous(), str(t.device))
-    raise ValueError("%s: expected a contiguous %s tensor of shape %s on the current CUDA device, "
-                     "with the other tensors, got %s" % (name, dtype, shape, got))
+    size = "shape %s" % (shape,) if type(shape) is tuple else "%d elements" % shape
+    raise ValueError("%s: expected a contiguous %s tensor of %s on the current CUDA device, "
+                     "with the other tensors, got %s" % (name, dtype, size, got))
 
 
 def _checked(*tensors):
@@ -285,6 +294,21 @@ def _checked(*tensors):
             _refuse(name, t, dtype, shape)
     if device < 0 or device != torch._C._cuda_getDevice():
         _refuse(*tensors[0])
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def _checked_as(spec, *tensors):
+    """The same for (name, dtype, shape or number of elements), made once: 9 tensors
+    in the time that four take above."""
+    device = tensors[0].get_device() if tensors[0] is not None else -1
+    for t, (name, dtype, shape) in zip(tensors, spec):
+        if (t is None or t.dtype is not dtype
+                or (t.shape if type(shape) is tuple else t.numel()) != shape
+                or not t.is_contiguous() or t.get_device() != device):
+            _refuse(name, t, dtype, shape)
+    if device < 0 or device != torch._C._cuda_getDevice():
+        name, dtype, shape = spec[0]
+        _refuse(name, tensors[0], dtype, shape)
     return torch._C._cuda_getCurrentRawStream(device)
 
 

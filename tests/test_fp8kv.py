@@ -757,3 +757,57 @@ def test_queries_of_extreme_size(e, H, lens):
     # The bound of the lse: as there.
     assert s["out_max"] <= ref.OUT_MAX and s["out_mean"] <= ref.OUT_MEAN, s
     assert s["lse_max"] <= 1.7 * 3 * 2.0 ** -9, s
+
+
+def test_run_and_attend_check_every_tensor(monkeypatch):
+    # (In host memory: a call whose tensors are right is refused for that alone.)
+    monkeypatch.setattr(binding, "workspace_size", lambda d, ranges=0: 4096)
+    B, T, H = 2, 2, 16
+    m = binding.MlaDecode(good_dims(q_len=T), device=torch.device("cpu"))
+    good = dict(q=torch.zeros(B, T, H, 192, dtype=BF),
+                kv8=torch.zeros(4, 64, 576, dtype=torch.uint8), kv_scale=torch.ones(4),
+                block_table=torch.zeros(B, 2, dtype=torch.int32),
+                seq_lens=torch.ones(B, dtype=torch.int32),
+                w_uk=torch.zeros(H, 128, 512, dtype=BF), w_uv=torch.zeros(H, 512, 128, dtype=BF),
+                out=torch.zeros(B, T, H, 128, dtype=BF), lse=torch.zeros(B, T, H))
+    attend = ("kv8", "kv_scale", "block_table", "seq_lens", "lse")
+
+    def refused(name, **change):
+        a = dict(good, **change)
+        with pytest.raises(ValueError, match="^%s: " % name):
+            m.run_fp8kv(scale=0.07, **a)
+        if name in attend:
+            with pytest.raises(ValueError, match="^%s: " % name):
+                m.attend_fp8kv(scale=0.07, **{k: a[k] for k in attend})
+
+    for name, t in good.items():
+        refused(name, **{name: None})
+        refused(name, **{name: t.double()})                          # another type
+        refused(name, **{name: t[:-1]})                              # too short
+        refused(name, **{name: torch.cat([t, t])[::2]})              # strided
+        refused(name, **{name: torch.cat([t, t])})                   # too long
+    refused("w_uk", w_uk=good["w_uv"])
+    with pytest.raises(ValueError, match="^kv8: .*CUDA device"):
+        m.run_fp8kv(scale=0.07, **good)
+    with pytest.raises(ValueError, match="^kv8: .*CUDA device"):
+        m.attend_fp8kv(scale=0.07, **{k: good[k] for k in attend})
+    # [B, T, ...] for a handle of B * T sequences of one token.
+    m = binding.MlaDecode(good_dims(batch=B * T), device=torch.device("cpu"))
+    good.update(block_table=torch.zeros(B * T, 2, dtype=torch.int32),
+                seq_lens=torch.ones(B * T, dtype=torch.int32))
+    refused("kv8")
+
+
+@gpu
+def test_a_refused_run_enqueues_nothing():
+    inp, kv8, kvs = fp8_inputs(make_inputs(2, [70, 5], 1, 16, seed=83))
+    g = inp.to(torch.device("cuda"))
+    m = binding.MlaDecode(binding.dims_for(g.q, g.cache, g.block_table), fp8_kv=True)
+    out = torch.full((2, 1, 16, 128), 7.0, dtype=BF, device="cuda")
+    lse = torch.full((2, 1, 16), 7.0, device="cuda")
+    k, s = kv8.cuda(), kvs.cuda()
+    m.plan(g.seq_lens)
+    for q, o in ((g.q.float(), out), (g.q[:1], out), (g.q, out[:, :, :8]), (g.q.cpu(), out)):
+        with pytest.raises(ValueError):
+            m.run_fp8kv(q, k, s, g.block_table, g.seq_lens, g.w_uk, g.w_uv, g.scale, o, lse)
+    assert m.check() == 0 and (out == 7.0).all() and (lse == 7.0).all()
