@@ -287,7 +287,7 @@ def _checked(*tensors):
     """The current stream, once every (name, tensor, dtype, shape) is what it should
     be: the C ABI sees pointers only.  (One loop without helpers: the checks are
     most of a small call's time on the host.)"""
-    device = tensors[0][1].get_device()
+    device = tensors[0][1].get_device() if tensors[0][1] is not None else -1
     for name, t, dtype, shape in tensors:
         if (t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
                 or t.get_device() != device):
@@ -330,7 +330,8 @@ def append_fp8kv(d: Dims, rows, kv8, kv_scale, block_table, seq_lens, new_lens=N
     Row i < new_lens[b] (default: every row) goes to position
     seq_lens[b] - new_lens[b] + i.  status: optional int32 [1] on the device
     that receives the first error found there."""
-    B, pages, max_new = d.batch, d.num_pages, rows.shape[1]
+    B, pages = d.batch, d.num_pages
+    max_new = rows.shape[1] if rows is not None and rows.dim() == 3 else 0
     stream = _checked(("rows", rows, torch.bfloat16, (B, max_new, 576)),
                       ("kv8", kv8, torch.uint8, (pages, 64, 576)),
                       ("kv_scale", kv_scale, torch.float32, (pages,)),

@@ -811,3 +811,24 @@ def test_a_refused_run_enqueues_nothing():
         with pytest.raises(ValueError):
             m.run_fp8kv(q, k, s, g.block_table, g.seq_lens, g.w_uk, g.w_uv, g.scale, o, lse)
     assert m.check() == 0 and (out == 7.0).all() and (lse == 7.0).all()
+
+
+def test_missing_tensors_and_other_ranks_are_refused_by_name():
+    d = good_dims()
+    kv8, kvs = torch.zeros(4, 64, 576, dtype=torch.uint8), torch.ones(4)
+    table, lens = torch.zeros(2, 2, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    keys, query = torch.zeros(4, 576, dtype=BF), torch.zeros(2, 1, 16, 576, dtype=BF)
+    scores, sel = torch.zeros(2, 1, 2), torch.zeros(2, 2, dtype=torch.int32)
+    rows = torch.zeros(2, 3, 576, dtype=BF)
+    for bad in (None, rows[0, 0], rows[None], torch.zeros((), dtype=BF)):
+        with pytest.raises(ValueError, match="^rows: "):
+            binding.append_fp8kv(d, bad, kv8, kvs, table, lens)
+    for fn, args in ((binding.append_fp8kv, (rows, kv8, kvs, table, lens)),
+                     (binding.page_keys, (kv8.to(BF), table, lens, 1, keys)),
+                     (binding.page_keys_fp8kv, (kv8, kvs, table, lens, 1, keys)),
+                     (binding.score_pages, (query, keys, table, lens, scores)),
+                     (binding.select_pages, (scores, table, lens, 2, 1, 1, sel, lens))):
+        for i, a in enumerate(args):
+            if isinstance(a, torch.Tensor):
+                with pytest.raises(ValueError, match="got None"):
+                    fn(d, *args[:i], None, *args[i + 1:])
