@@ -100,10 +100,19 @@ def _ptr(t):
     return t.data_ptr() if t is not None else None
 
 
+def _public_raw_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# The current device and its current stream's handle.  torch.cuda.current_stream()
+# builds a Stream object, 2.9 us a call; these take 0.2, but are torch's own: a
+# torch without them serves the same through its public calls.
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _public_raw_stream)
+
+
 def _stream():
-    # The current stream's handle (torch.cuda.current_stream() builds a Stream
-    # object, 2.9 us a call against 0.2 us).
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return _raw_stream(_device())
 
 
 def _ok(code, where):
@@ -292,9 +301,9 @@ def _checked(*tensors):
         if (t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
                 or t.get_device() != device):
             _refuse(name, t, dtype, shape)
-    if device < 0 or device != torch._C._cuda_getDevice():
+    if device < 0 or device != _device():
         _refuse(*tensors[0])
-    return torch._C._cuda_getCurrentRawStream(device)
+    return _raw_stream(device)
 
 
 def _checked_as(spec, *tensors):
@@ -306,10 +315,10 @@ def _checked_as(spec, *tensors):
                 or (t.shape if type(shape) is tuple else t.numel()) != shape
                 or not t.is_contiguous() or t.get_device() != device):
             _refuse(name, t, dtype, shape)
-    if device < 0 or device != torch._C._cuda_getDevice():
+    if device < 0 or device != _device():
         name, dtype, shape = spec[0]
         _refuse(name, tensors[0], dtype, shape)
-    return torch._C._cuda_getCurrentRawStream(device)
+    return _raw_stream(device)
 
 
 def _lines(d, block_table, seq_lens, new_lens=None, status=None):

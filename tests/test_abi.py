@@ -7,6 +7,7 @@ import os
 import re
 
 import pytest
+import torch
 
 from mla_decode_attention_uk_gb300 import binding
 
@@ -237,3 +238,27 @@ def test_static_scratch_checks_every_argument_before_anything_else():
     bad_dims = good_dims(kv_lora=256)
     assert L.mla_decode_run_static_scratch(ctypes.byref(bad_dims), *args, None) == 2
     assert L.mla_decode_run_static_scratch(None, *args, None) == 1
+
+
+def test_binding_without_torchs_private_stream_calls(monkeypatch):
+    # A torch that lacks them: the public calls take their place.
+    import importlib.util
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    spec = importlib.util.spec_from_file_location("binding_copy", binding.__file__)
+    copy = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(copy)
+    stream = type("Stream", (), {"cuda_stream": 1234})()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: stream)
+    copy._device = lambda: 0
+    assert copy._stream() == 1234
+    assert copy._raw_stream is copy._public_raw_stream
+
+
+@pytest.mark.gpu
+def test_the_quick_stream_calls_equal_the_public_ones():
+    assert binding._device() == torch.cuda.current_device()
+    for stream in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(stream):
+            assert binding._stream() == stream.cuda_stream
+            assert binding._public_raw_stream(0) == stream.cuda_stream
