@@ -245,7 +245,8 @@ def test_binding_without_torchs_private_stream_calls(monkeypatch):
     import importlib.util
     for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
         monkeypatch.delattr(torch._C, name, raising=False)
-    spec = importlib.util.spec_from_file_location("binding_copy", binding.__file__)
+    spec = importlib.util.spec_from_file_location(
+        "mla_decode_attention_uk_gb300.binding_copy", binding.__file__)
     copy = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(copy)
     stream = type("Stream", (), {"cuda_stream": 1234})()
