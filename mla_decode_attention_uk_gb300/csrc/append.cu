@@ -61,6 +61,16 @@ __device__ __forceinline__ uint2 codes8(const uint4& v, __nv_bfloat162 inv) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
+// x * y rounded to odd: the nearest fp32 value with the last bit set where the
+// product is between two, so that rounding it on to a code rounds the product
+// itself (a product next to a tie of E4M3 would be rounded to the tie first).
+__device__ __forceinline__ float mul_odd(float x, float y) {
+  const float p = x * y, rest = fmaf(x, y, -p);
+  const int u = __float_as_int(p);
+  const bool even = rest != 0.0f && !(u & 1);
+  return __int_as_float(even ? ((rest > 0.0f) == (p > 0.0f) ? u + 1 : u - 1) : u);
+}
+
 struct AppendParams {
   const uint4* rows;
   int max_new;
@@ -194,7 +204,8 @@ __device__ __forceinline__ void fill_page(const AppendParams& P, const Group& gr
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const float2 p = e4m3x2_to_float2(w[k]), q = e4m3x2_to_float2(w[k] >> 16);
-        w[k] = e4m3x4(p.x * ratio, p.y * ratio, q.x * ratio, q.y * ratio);
+        w[k] = e4m3x4(mul_odd(p.x, ratio), mul_odd(p.y, ratio), mul_odd(q.x, ratio),
+                      mul_odd(q.y, ratio));
       }
       c = make_uint2(w[0], w[1]);
     }

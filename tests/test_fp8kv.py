@@ -832,3 +832,40 @@ def test_missing_tensors_and_other_ranks_are_refused_by_name():
             if isinstance(a, torch.Tensor):
                 with pytest.raises(ValueError, match="got None"):
                     fn(d, *args[:i], None, *args[i + 1:])
+
+
+@gpu
+@pytest.mark.parametrize("old", [1.5 * 2.0 ** -6, 0.75, 1.25 * 2.0 ** -20, 1.9, 0.0, math.nan])
+def test_append_under_another_scale_keeps_every_sign(old):
+    # Rows that stay are re-coded under a scale that is not a power of two: signs
+    # too, those of values that vanish among them.
+    table = torch.tensor([[0, 1]], dtype=torch.int32)
+    kv8, kvs = pool(2, 16)
+    kv8[0, 3, :256] = torch.arange(256, dtype=torch.uint8)  # every code
+    kvs[0] = old
+    rows = torch.randn(1, 30, 576, generator=torch.Generator().manual_seed(17)).to(BF)
+    rows[0, 5, :4] = torch.tensor([0.0, -0.0, 1e-30, -1e-30])
+    k, s, _ = run_append(rows, [30], table, [50], kv8, kvs, 2)
+    rk, rs = ref.append(rows, [30], table, [50], kv8, kvs)
+    nan = (rk & 0x7F) == 0x7F  # (a NaN's sign is nobody's)
+    assert torch.equal(s, rs) and torch.equal(k[~nan], rk[~nan])
+    assert ((k[nan] & 0x7F) == 0x7F).all()
+    assert bool((k[0, 25, :4] == torch.tensor([0x00, 0x80, 0x00, 0x80], dtype=torch.uint8)).all())
+
+
+@gpu
+def test_append_of_special_values_keeps_signs():
+    rows = torch.zeros(1, 6, 576)
+    rows[0, 0, :4] = torch.tensor([math.inf, -math.inf, math.nan, -1.0])
+    rows[0, 1, :2] = torch.tensor([3.0e38, -3.0e38])
+    rows[0, 2, :3] = torch.tensor([1.0e-30, -1.0e-30, -0.0])
+    rows[0, 3, :2] = torch.tensor([448.0 * 2.0 ** 32, -448.0 * 2.0 ** 32])
+    rows = rows.to(BF)
+    table = torch.tensor([[1]], dtype=torch.int32)
+    kv8, kvs = pool(2, 11)
+    k, s, st = run_append(rows, [6], table, [6], kv8, kvs, 2)
+    rk, rs = ref.append(rows, [6], table, [6], kv8, kvs)
+    nan = (rk & 0x7F) == 0x7F
+    assert st == 0 and torch.equal(s, rs) and torch.equal(k[~nan], rk[~nan])
+    assert int(nan.sum()) == 1 and (k[1, 0, 2] & 0x7F) == 0x7F
+    assert k[1, 2, :4].tolist() == [0x00, 0x80, 0x80, 0x00]
