@@ -162,8 +162,7 @@ class MlaDecode:
         self._attend_spec = (
             ("kv8", torch.uint8, (pages, 64, 576)), ("kv_scale", torch.float32, (pages,)),
             ("block_table", torch.int32, (B, d.max_pages_per_seq)),
-            ("seq_lens", torch.int32, (B,)), ("lse", torch.float32, n),
-            ("workspace", torch.uint8, self.ws_bytes))
+            ("seq_lens", torch.int32, (B,)), ("lse", torch.float32, n))
         self._run_spec = self._attend_spec + (
             ("q", torch.bfloat16, n * 192), ("w_uk", torch.bfloat16, (H, 128, 512)),
             ("w_uv", torch.bfloat16, (H, 512, 128)), ("out", torch.bfloat16, n * 128))
@@ -195,8 +194,8 @@ class MlaDecode:
             "mla_decode_run_fp8w")
 
     def run_fp8kv(self, q, kv8, kv_scale, block_table, seq_lens, w_uk, w_uv, scale, out, lse):
-        stream = _checked_as(self._run_spec, kv8, kv_scale, block_table, seq_lens, lse,
-                             self.workspace, q, w_uk, w_uv, out)
+        stream = _checked_as(self._run_spec, self.workspace, kv8, kv_scale, block_table, seq_lens,
+                             lse, q, w_uk, w_uv, out)
         _ok(lib().mla_decode_run_fp8kv(ctypes.byref(self.dims), q.data_ptr(), kv8.data_ptr(),
                                        kv_scale.data_ptr(), block_table.data_ptr(),
                                        seq_lens.data_ptr(), w_uk.data_ptr(), w_uv.data_ptr(),
@@ -205,8 +204,8 @@ class MlaDecode:
             "mla_decode_run_fp8kv")
 
     def attend_fp8kv(self, kv8, kv_scale, block_table, seq_lens, scale, lse):
-        stream = _checked_as(self._attend_spec, kv8, kv_scale, block_table, seq_lens, lse,
-                             self.workspace)
+        stream = _checked_as(self._attend_spec, self.workspace, kv8, kv_scale, block_table,
+                             seq_lens, lse)
         _ok(lib().mla_decode_attend_fp8kv(ctypes.byref(self.dims), kv8.data_ptr(),
                                           kv_scale.data_ptr(), block_table.data_ptr(),
                                           seq_lens.data_ptr(), float(scale), lse.data_ptr(),
@@ -306,18 +305,17 @@ def _checked(*tensors):
     return _raw_stream(device)
 
 
-def _checked_as(spec, *tensors):
-    """The same for (name, dtype, shape or number of elements), made once: 9 tensors
-    in the time that four take above."""
-    device = tensors[0].get_device() if tensors[0] is not None else -1
+def _checked_as(spec, workspace, *tensors):
+    """The same for (name, dtype, shape or number of elements), made once, on the
+    workspace's device: nine tensors in the time that four take above."""
+    device = workspace.get_device()
     for t, (name, dtype, shape) in zip(tensors, spec):
         if (t is None or t.dtype is not dtype
                 or (t.shape if type(shape) is tuple else t.numel()) != shape
                 or not t.is_contiguous() or t.get_device() != device):
             _refuse(name, t, dtype, shape)
     if device < 0 or device != _device():
-        name, dtype, shape = spec[0]
-        _refuse(name, tensors[0], dtype, shape)
+        _refuse(spec[0][0], tensors[0], *spec[0][1:])
     return _raw_stream(device)
 
 
