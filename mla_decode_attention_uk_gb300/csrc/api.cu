@@ -16,9 +16,10 @@
 
 namespace mla {
 cudaError_t launch_plan(const int32_t* seq_lens, int B, int T, int max_pages, int R,
-                        int piece_cost, int32_t* status, PlanHeader* header, int32_t* range_b, int32_t* range_p,
-                        int32_t* seq_first, int32_t* seq_nsplit, int32_t* seq_slot,
-                        int32_t* seq_len_eff, int32_t* prefix, cudaStream_t stream);
+                        int piece_cost, int32_t* status, PlanHeader* header, int32_t* range_b,
+                        int32_t* range_p, int32_t* seq_first, int32_t* seq_nsplit,
+                        int32_t* seq_slot, int32_t* seq_len_eff, int32_t* prefix,
+                        cudaStream_t stream);
 int bmm_token_tile(int BT, bool absorb);
 cudaError_t launch_absorb(const CUtensorMap& tm_wuk, const CUtensorMap& tm_q,
                           const CUtensorMap* tm_qlat, const CUtensorMap* tm_qlo, int BT, int H,
@@ -699,7 +700,8 @@ int mla_decode_attend_fp8kv(const mla_decode_dims* d, const uint8_t* kv_fp8,
   int rc = check_dims(d);
   if (rc) return rc;
   if (!softmax_scale_ok(scale) || !kv_fp8 || !kv_scale || !block_table || !seq_lens || !lse ||
-      !ws || !aligned16(kv_fp8) || !aligned16(ws) || !aligned4(kv_scale) || !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(lse))
+      !ws || !aligned16(kv_fp8) || !aligned16(ws) || !aligned4(kv_scale) ||
+      !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(lse))
     return MLA_DECODE_INVALID_ARG;
   WsLayout L;
   rc = layout_for(d, ws_bytes, &L);
@@ -719,11 +721,11 @@ int mla_decode_attend_fp8kv(const mla_decode_dims* d, const uint8_t* kv_fp8,
   rc = sm_count(&sms);
   if (rc) return rc;
   return cuda_rc(launch_decode_fp8kv(
-      tm_lat, tm_rope, tm_q, sms, block_table, kv_scale, at<int32_t>(ws, L.seq_len_eff), at<PlanHeader>(ws, L.header), ws,
-      at<int32_t>(ws, L.seq_first), at<int32_t>(ws, L.seq_nsplit), at<int32_t>(ws, L.seq_slot),
-      at<__nv_bfloat16>(ws, L.olat), lse, at<int32_t>(ws, L.status), d->batch, d->q_len,
-      d->num_heads, d->max_pages_per_seq, d->num_pages, scale,
-      static_cast<cudaStream_t>(stream)));
+      tm_lat, tm_rope, tm_q, sms, block_table, kv_scale, at<int32_t>(ws, L.seq_len_eff),
+      at<PlanHeader>(ws, L.header), ws, at<int32_t>(ws, L.seq_first),
+      at<int32_t>(ws, L.seq_nsplit), at<int32_t>(ws, L.seq_slot), at<__nv_bfloat16>(ws, L.olat),
+      lse, at<int32_t>(ws, L.status), d->batch, d->q_len, d->num_heads, d->max_pages_per_seq,
+      d->num_pages, scale, static_cast<cudaStream_t>(stream)));
 }
 
 int mla_decode_run_fp8kv(const mla_decode_dims* d, const void* q, const uint8_t* kv_fp8,

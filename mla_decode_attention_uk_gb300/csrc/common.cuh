@@ -65,6 +65,14 @@ constexpr int MLA_STATUS_TIMEOUT = 6;
 // Bounded waits give up after this long (ns).
 constexpr unsigned long long kWaitTimeoutNs = 2000000000ull;
 
+// How the attention steps spread over the SMs (decode.cu): CTA groups of tpg of a
+// sequence's 64-row tiles, in `sets` sets of tiles, and the default number of work
+// ranges that goes with them.
+struct DecodeShape {
+  int tiles, tpg, sets, groups, ranges;
+};
+DecodeShape decode_shape(int T, int H, int sm_count);
+
 // Plan written by the planner kernel into the workspace.
 //   ranges: num_ranges + 1 entries of (b, page) where range k starts;
 //           entry num_ranges is (B, 0).

@@ -741,9 +741,6 @@ int decode_smem_bytes(int T, int H) {
 // tpg = gcd(tiles, SMs) tiles instead, every SM gets a CTA, and the number of
 // ranges is the smallest that deals each group the same number of
 // (range, tile set) tasks.
-struct DecodeShape {
-  int tiles, tpg, sets, groups, ranges;
-};
 static int gcd_int(int a, int b) {
   while (b) {
     const int t = a % b;
@@ -752,7 +749,7 @@ static int gcd_int(int a, int b) {
   }
   return a;
 }
-static DecodeShape decode_shape(int T, int H, int sm_count) {
+DecodeShape decode_shape(int T, int H, int sm_count) {
   DecodeShape d;
   d.tiles = decode_tiles(T, H);
   const int sms = sm_count > 0 ? sm_count : 1;

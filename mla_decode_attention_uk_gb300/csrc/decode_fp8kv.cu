@@ -66,7 +66,6 @@
 
 namespace mla {
 
-int decode_tiles(int T, int H);
 int decode_q_box_rows(int T, int H);
 
 namespace {
@@ -689,6 +688,9 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
         } else {
           const float add = shift + kTopExp - m_used;
           float se[4] = {};
+          // What the rounding of this thread's 32 weights adds up to, in fp16: the
+          // terms are exact and at most 2^-7 of a weight, so 16 sums rounded by
+          // 2^-11 move the row's sum, which is fp32, by 2^-14 of it at most.
           __half2 err = __float2half2_rn(0.0f);
 #pragma unroll
           for (int t = 0; t < 8; ++t) {
@@ -829,25 +831,6 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
 
 }  // namespace
 
-// How the step spreads over the SMs: as decode.cu's, whose plan it runs on.  A
-// CTA group holds all tiles of a sequence, or gcd(tiles, SMs) of them where all
-// would leave 3 % or more of the SMs idle.
-struct Shape {
-  int tiles, tpg, sets, groups;
-};
-static Shape shape_for(int T, int H, int sm_count) {
-  Shape d;
-  d.tiles = decode_tiles(T, H);
-  const int sms = sm_count > 0 ? sm_count : 1;
-  const int idle = d.tiles <= sms ? sms % d.tiles : 0;
-  d.tpg = d.tiles;
-  if (100 * idle >= 3 * sms)
-    for (d.tpg = d.tiles; d.tiles % d.tpg || sms % d.tpg;) --d.tpg;
-  d.sets = d.tiles / d.tpg;
-  d.groups = sms / d.tpg > 0 ? sms / d.tpg : 1;
-  return d;
-}
-
 cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope,
                                 const CUtensorMap& tm_q, int sm_count,
                                 const int32_t* block_table, const float* kv_scale,
@@ -857,7 +840,7 @@ cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm
                                 int32_t* status, int B, int T, int H, int max_pages,
                                 int num_pages, float scale, cudaStream_t st) {
   Params P{};
-  const Shape shape = shape_for(T, H, sm_count);
+  const DecodeShape shape = decode_shape(T, H, sm_count);
   const cudaError_t e = cudaFuncSetAttribute(
       decode_fp8kv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
