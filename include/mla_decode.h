@@ -45,6 +45,11 @@
  *   kernels, written to the workspace status word and reported by
  *   mla_decode_check; the offending unit of work is skipped or computed on a
  *   substitute page, never trapped.
+ * - Kernels of this library may start before the kernel in front of them on the
+ *   stream has finished, and wait for it before they touch what it may use.  Only
+ *   the weights, and q in the absorb step, are read at once: a kernel of the
+ *   caller's that writes them and stands directly before the call must not itself
+ *   let its dependents launch early (ordinary kernels do not).
  * - Thread safety: concurrent calls are safe when each uses its own
  *   workspace.  A plan written into a workspace stays valid for every run with
  *   the same dims and seq_lens contents (one plan serves all layers of a
@@ -215,8 +220,9 @@ int mla_decode_up_project_fp8w(const mla_decode_dims* dims, const uint8_t* w_uv_
  * same block_table and seq_lens as in the bf16 cache.
  *
  * `status` of the calls in this part: device int32 or null; the first
- * device-side error (DEVICE_BOUNDS) is written there if it holds 0.  The
- * pages of a call that are in range are processed whatever the others are. */
+ * device-side error (DEVICE_BOUNDS, or TIMEOUT) is written there if it holds 0;
+ * without it such an error stays unseen.  The pages of a call that are in range
+ * are processed whatever the others are. */
 
 /* Appends new tokens: quantises rows of the bf16 cache's layout into the pages.
  *   rows        bf16 [B, max_new, 576]: row i < n_b of sequence b goes to
@@ -285,8 +291,10 @@ int mla_decode_attend_fp8kv(const mla_decode_dims* dims, const uint8_t* kv_fp8,
  *   plan, then attend or attend_fp8kv, combine and up_project, with dims {batch
  *     = B * T, q_len = 1, max_pages_per_seq = top_k}, sel_table and sel_lens (the
  *     plan leaves q_lat as it is; run or run_fp8kv would absorb once more)
- * (q [B, T, H, 192] is [B * T, 1, H, 192] as it stands.)  Not described by the
- * method's pages; for either kind of cache. */
+ * (q [B, T, H, 192] is [B * T, 1, H, 192] as it stands; B * T is at most 65535,
+ * as every batch.)  The plan clears the workspace's status word: in this order a
+ * TIMEOUT of the absorb shows only in a mla_decode_check between the two.  Not
+ * described by the method's pages; for either kind of cache. */
 
 /* Keys of the pages that hold any of each sequence's newest n_b tokens
  * (new_lens, max_new and seq_lens as for mla_decode_append_fp8kv):

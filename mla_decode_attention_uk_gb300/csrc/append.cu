@@ -430,7 +430,11 @@ page_keys_kernel(const uint8_t* __restrict__ cache, const float* __restrict__ kv
 }  // namespace
 
 // Up to so many new tokens a sequence, a CTA for each of the two pages that they
-// can touch; their rows fit the shared memory that needs no opt-in.
+// can touch; their rows fit the shared memory that needs no opt-in (42 rows).
+// Against the ring of pages, us in a graph, new tokens 1 / 8 / 24 / 32 / 40: one
+// sequence 2.1 / 2.3 / 2.6 / 2.8 / 2.9 and 3.6 / 3.6 / 3.8 / 3.8 / 4.0; 128 of them
+// 2.6 / 3.0 / 3.6 / 3.8 / 4.1 and 4.1 / 4.2 / 5.2 / 5.2 / 5.2; 512 of them 4.3 / 6.0 /
+// 9.9 / 11.6 / 12.9 and 6.9 / 7.7 / 10.4 / 11.5 / 13.0: where the large batches meet.
 constexpr int kFewTokens = 32;
 
 // Pages that max_new consecutive tokens can touch.

@@ -48,13 +48,16 @@
 //
 // What bounds it: with 64 rows the tensor pipe, whose 34 MMAs take 1,376 cycles of
 // the 1,500 that a page takes (PV 768, bound by shared-memory reads: 6 KB per
-// MMA of 4 KB worth); with 16 heads memory, 6.1 TB/s while pages stream.  Beside
-// the pages a piece costs 5 to 6 us (its query terms and its epilogue are not
-// hidden by each other's pages) and a launch 8 us.  Measured (one GB300, with the
-// query terms' tile, without absorb and merge): 64 sequences of 4,096 tokens x 16
-// heads 35 us; 128 of 1,000-10,000 (500k tokens) x 128 heads 113 us; 61 ragged
-// drafts of 4 queries x 128 heads (133k tokens) 100 us.  Prefetching pages into
-// L2 ahead of the ring only cost: 35 -> 39 us on the first, eight pages ahead.
+// MMA of 4 KB worth); with 16 heads memory, 6.1 TB/s while pages stream (both from
+// time stamps on one SM).  Beside the pages a piece costs 5 to 6 us (its query
+// terms and its epilogue are not hidden by each other's pages) and a launch 8 us:
+// over the whole launch the tensor pipe is active 51 % of the time on the second
+// case below and 42 % on the third, and DRAM at 51 % of its peak on the first.
+// Measured (one GB300, with the query terms' tile, without absorb and merge): 64
+// sequences of 4,096 tokens x 16 heads 36 us; 128 of 1,000-10,000 (500k tokens) x
+// 128 heads 113 us; 61 ragged drafts of 4 queries x 128 heads (133k tokens) 101 us.
+// Prefetching pages into L2 ahead of the ring only cost: 35 -> 39 us on the first,
+// eight pages ahead.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
