@@ -281,6 +281,109 @@ int mla_decode_attend_fp8kv(const mla_decode_dims* dims, const uint8_t* kv_fp8,
                             void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * The 4-bit latent cache, this library's own addition as well: 0.58 times the
+ * bytes of the 8-bit one.
+ *   kv_fp4      uint8 [num_pages, 64, 336], a token's row being
+ *                 256 bytes  c_kv as E2M1 codes (0 0.5 1 1.5 2 3 4 6 and a sign
+ *                            bit), value 2 i in the low half of byte i
+ *                  16 bytes  an exponent e of four bits for every 16 values
+ *                            (block 2 i in the low half of byte i); 15: NaN
+ *                  64 bytes  k_pe as E4M3 codes
+ *   kv_scale    fp32  [num_pages]  one scale per page, > 0
+ * A cached latent is code * 2^(e - 8) * scale, a RoPE value code * scale.  Each of
+ * them is an E4M3 code times the scale, so a page of this cache stands for exactly
+ * the values of a page of the 8-bit cache, and what holds there for scales, NaN
+ * codes, `status`, and rows past a sequence's length, holds here. */
+
+/* mla_decode_append_fp8kv into the 4-bit cache.  The scale of a page follows from
+ * its values as there (all 576 columns: |value| <= 448 s).  A block's e is the
+ * smallest from 0 to 14 with |value| <= 7 * 2^(e - 8) s for all its values, the
+ * codes are the nearest (ties to even; 6 beyond 6, infinities too).  A block with
+ * a NaN is NaN.  Where a page's scale grows, the rows that stay are quantised again
+ * from the values that they stand for.  One kernel. */
+int mla_decode_append_fp4kv(const mla_decode_dims* dims, const void* rows, int32_t max_new,
+                            const int32_t* new_lens, const int32_t* block_table,
+                            const int32_t* seq_lens, uint8_t* kv_fp4, float* kv_scale,
+                            int32_t* status, void* stream);
+
+/* mla_decode_run_fp8kv and its attention step over the 4-bit cache, after any plan
+ * (mla_decode_plan_fp8kv is balanced for this cache too).  The results are those over
+ * the 8-bit cache that holds the same values. */
+int mla_decode_run_fp4kv(const mla_decode_dims* dims, const void* q, const uint8_t* kv_fp4,
+                         const float* kv_scale, const int32_t* block_table,
+                         const int32_t* seq_lens, const void* w_uk, const void* w_uv,
+                         float softmax_scale, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
+int mla_decode_attend_fp4kv(const mla_decode_dims* dims, const uint8_t* kv_fp4,
+                            const float* kv_scale, const int32_t* block_table,
+                            const int32_t* seq_lens, float softmax_scale, float* lse,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * In front of the cache and back from it. */
+
+/* Norms and rotation of new tokens' queries and latents, in one pass over what the
+ * projections gave.  With the token at position p, c and s the cosines and sines of
+ * its 32 angles:
+ *   a query head of 192   x / sqrt(mean(x^2) + eps) * q_weight over its columns where
+ *                         q_weight is given; then the last 64 columns are rotated
+ *   a latent row of 576   the same over its first 512 columns, with kv_weight where
+ *                         that is given; its last 64 columns are rotated
+ * A pair (a, b) becomes (a c_i - b s_i, b c_i + a s_i) and keeps its places: columns
+ * 2 i and 2 i + 1 (interleaved = 1), or i and i + 32 (0).  All in fp32, rounded once.
+ *   q           bf16 [B, max_new, H, 192], q_stride elements from a token to the
+ *               next (>= H * 192, a multiple of 8); null for none
+ *   kv          bf16 [B, max_new, 576], kv_stride elements from a token to the next
+ *               (>= 576, a multiple of 8: columns of a wider projection); null for none
+ *   q_weight    bf16 [192], kv_weight bf16 [512]; either may be null: no norm
+ *   eps         finite and > 0
+ *   cos_sin     fp32 [max_position, 64]: a position's 32 cosines, then its 32 sines;
+ *               16-byte aligned
+ *   positions   int32 [B, max_new]; null: token i of sequence b is at its place in the
+ *               cache, seq_lens[b] - n_b + i
+ *   new_lens, max_new, seq_lens  as for mla_decode_append_fp8kv
+ *   q_out       bf16 [B, max_new, H, 192] (written); may be q where q_stride is H * 192
+ *   rows        bf16 [B, max_new, 576] (written), what the appends take; may be kv
+ *               where kv_stride is 576
+ *   kv_cache, block_table  the bf16 cache: tokens are written to their pages.  One of
+ *               rows and kv_cache must be given with kv, or both; block_table with
+ *               kv_cache
+ * Rows behind a sequence's n_b tokens are neither read nor written.  A position outside
+ * [0, max_position): DEVICE_BOUNDS, and nothing of the token is written; a block_table
+ * entry outside the pool: DEVICE_BOUNDS, and the page's tokens reach q_out and rows
+ * only; lengths as for the append.  The other arguments (q without q_out, outputs
+ * without their input, ...): INVALID_ARG.  Uses batch, num_heads, num_pages and
+ * max_pages_per_seq of dims.  One kernel. */
+int mla_decode_norm_rope(const mla_decode_dims* dims, const void* q, int64_t q_stride,
+                         const void* q_weight, const void* kv, int64_t kv_stride,
+                         const void* kv_weight, float eps, const float* cos_sin,
+                         int32_t max_position, int32_t interleaved, const int32_t* positions,
+                         int32_t max_new, const int32_t* new_lens, const int32_t* seq_lens,
+                         void* q_out, void* rows, void* kv_cache, const int32_t* block_table,
+                         int32_t* status, void* stream);
+
+/* Reading back, the appends' inverse: tokens of the cache as bf16 rows, for a chunk of
+ * a prompt that attends to them, or to move a sequence to another cache.
+ *   rows        bf16 [B, max_new, 576] (written): row i < n_b of sequence b is the
+ *               token at position seq_lens[b] - n_b + i (a range that ends before the
+ *               sequence: pass its end as the length); the rows behind stay as they are
+ * Values are rounded to bf16 once (they are exact where a page's scale is a power of
+ * two).  A page's scale outside [2^-32, 2^32] is taken as 1, with DEVICE_BOUNDS; a
+ * block_table entry outside the pool: DEVICE_BOUNDS, and its tokens' rows stay as they
+ * are.  One kernel. */
+int mla_decode_gather(const mla_decode_dims* dims, const void* kv_cache,
+                      const int32_t* block_table, const int32_t* seq_lens, int32_t max_new,
+                      const int32_t* new_lens, void* rows, int32_t* status, void* stream);
+int mla_decode_gather_fp8kv(const mla_decode_dims* dims, const uint8_t* kv_fp8,
+                            const float* kv_scale, const int32_t* block_table,
+                            const int32_t* seq_lens, int32_t max_new, const int32_t* new_lens,
+                            void* rows, int32_t* status, void* stream);
+int mla_decode_gather_fp4kv(const mla_decode_dims* dims, const uint8_t* kv_fp4,
+                            const float* kv_scale, const int32_t* block_table,
+                            const int32_t* seq_lens, int32_t max_new, const int32_t* new_lens,
+                            void* rows, int32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Block-sparse decode: each query token attends to top_k pages of its
  * sequence.  Every page has a key (the mean of its rows); a query's score for
  * a page is its largest head's product with the key; the pages selected form a
@@ -288,13 +391,13 @@ int mla_decode_attend_fp8kv(const mla_decode_dims* dims, const uint8_t* kv_fp8,
  * run as on any other:
  *   append or write tokens; page_keys          (per layer)
  *   absorb -> q_lat; score_pages(q_lat); select_pages -> sel_table, sel_lens
- *   plan, then attend or attend_fp8kv, combine and up_project, with dims {batch
+ *   plan, then attend, attend_fp8kv or _fp4kv, combine and up_project, with dims {batch
  *     = B * T, q_len = 1, max_pages_per_seq = top_k}, sel_table and sel_lens (the
  *     plan leaves q_lat as it is; run or run_fp8kv would absorb once more)
  * (q [B, T, H, 192] is [B * T, 1, H, 192] as it stands; B * T is at most 65535,
  * as every batch.)  The plan clears the workspace's status word: in this order a
  * TIMEOUT of the absorb shows only in a mla_decode_check between the two.  Not
- * described by the method's pages; for either kind of cache. */
+ * described by the method's pages; for every kind of cache. */
 
 /* Keys of the pages that hold any of each sequence's newest n_b tokens
  * (new_lens, max_new and seq_lens as for mla_decode_append_fp8kv):
@@ -308,6 +411,12 @@ int mla_decode_page_keys(const mla_decode_dims* dims, const void* kv_cache,
                          const int32_t* new_lens, void* page_keys, int32_t* status,
                          void* stream);
 int mla_decode_page_keys_fp8kv(const mla_decode_dims* dims, const uint8_t* kv_fp8,
+                               const float* kv_scale, const int32_t* block_table,
+                               const int32_t* seq_lens, int32_t max_new,
+                               const int32_t* new_lens, void* page_keys, int32_t* status,
+                               void* stream);
+
+int mla_decode_page_keys_fp4kv(const mla_decode_dims* dims, const uint8_t* kv_fp4,
                                const float* kv_scale, const int32_t* block_table,
                                const int32_t* seq_lens, int32_t max_new,
                                const int32_t* new_lens, void* page_keys, int32_t* status,

@@ -27,7 +27,10 @@ ENTRY_POINTS = (
     "mla_decode_run_fp8w", "mla_decode_absorb_fp8w", "mla_decode_up_project_fp8w",
     "mla_decode_append_fp8kv", "mla_decode_plan_fp8kv", "mla_decode_run_fp8kv",
     "mla_decode_attend_fp8kv", "mla_decode_page_keys", "mla_decode_page_keys_fp8kv",
-    "mla_decode_score_pages", "mla_decode_select_pages")
+    "mla_decode_score_pages", "mla_decode_select_pages", "mla_decode_append_fp4kv",
+    "mla_decode_run_fp4kv", "mla_decode_attend_fp4kv", "mla_decode_page_keys_fp4kv",
+    "mla_decode_norm_rope", "mla_decode_gather", "mla_decode_gather_fp8kv",
+    "mla_decode_gather_fp4kv")
 
 
 class Dims(ctypes.Structure):
@@ -83,6 +86,16 @@ def lib():
         L.mla_decode_page_keys_fp8kv.argtypes = [D, P, P, P, P, i32, P, P, P, P]
         L.mla_decode_score_pages.argtypes = [D, P, P, P, P, P, P, P]
         L.mla_decode_select_pages.argtypes = [D, P, P, P, i32, i32, i32, P, P, P, P, P]
+        L.mla_decode_append_fp4kv.argtypes = L.mla_decode_append_fp8kv.argtypes
+        L.mla_decode_run_fp4kv.argtypes = L.mla_decode_run_fp8kv.argtypes
+        L.mla_decode_attend_fp4kv.argtypes = L.mla_decode_attend_fp8kv.argtypes
+        L.mla_decode_page_keys_fp4kv.argtypes = L.mla_decode_page_keys_fp8kv.argtypes
+        L.mla_decode_gather.argtypes = L.mla_decode_page_keys.argtypes
+        L.mla_decode_gather_fp8kv.argtypes = L.mla_decode_page_keys_fp8kv.argtypes
+        L.mla_decode_gather_fp4kv.argtypes = L.mla_decode_page_keys_fp8kv.argtypes
+        i64 = ctypes.c_int64
+        L.mla_decode_norm_rope.argtypes = [D, P, i64, P, P, i64, P, ctypes.c_float, P, i32, i32, P,
+                                           i32, P, P, P, P, P, P, P, P]
         for n in ENTRY_POINTS:
             if n != "mla_decode_status_string":
                 getattr(L, n).restype = ctypes.c_int
@@ -144,9 +157,9 @@ def kernels_per_run(d: Dims, fp8_weights: bool = False) -> int:
 
 class MlaDecode:
     """Owns a device workspace for one set of dims; plan() once per decode step,
-    run() or run_fp8kv() once per layer.  All tensors must be CUDA, contiguous.
-    With fp8_kv plan() balances the work for the 8-bit cache (a plan of either
-    kind serves both)."""
+    run(), run_fp8kv() or run_fp4kv() once per layer.  All tensors must be CUDA,
+    contiguous.  With fp8_kv plan() balances the work for the 8-bit cache, and the
+    4-bit one (a plan of either kind serves all)."""
 
     def __init__(self, d: Dims, device=None, num_ranges: int = 0, fp8_kv: bool = False):
         self.dims = d
@@ -163,9 +176,12 @@ class MlaDecode:
             ("kv8", torch.uint8, (pages, 64, 576)), ("kv_scale", torch.float32, (pages,)),
             ("block_table", torch.int32, (B, d.max_pages_per_seq)),
             ("seq_lens", torch.int32, (B,)), ("lse", torch.float32, n))
-        self._run_spec = self._attend_spec + (
-            ("q", torch.bfloat16, n * 192), ("w_uk", torch.bfloat16, (H, 128, 512)),
-            ("w_uv", torch.bfloat16, (H, 512, 128)), ("out", torch.bfloat16, n * 128))
+        run = (("q", torch.bfloat16, n * 192), ("w_uk", torch.bfloat16, (H, 128, 512)),
+               ("w_uv", torch.bfloat16, (H, 512, 128)), ("out", torch.bfloat16, n * 128))
+        self._run_spec = self._attend_spec + run
+        # And over the 4-bit one.
+        self._attend_spec4 = (("kv4", torch.uint8, (pages, 64, 336)),) + self._attend_spec[1:]
+        self._run_spec4 = self._attend_spec4 + run
 
     def plan(self, seq_lens):
         if self.fp8_kv:
@@ -211,6 +227,25 @@ class MlaDecode:
                                           seq_lens.data_ptr(), float(scale), lse.data_ptr(),
                                           self.workspace.data_ptr(), self.ws_bytes, stream),
             "mla_decode_attend_fp8kv")
+
+    def run_fp4kv(self, q, kv4, kv_scale, block_table, seq_lens, w_uk, w_uv, scale, out, lse):
+        stream = _checked_as(self._run_spec4, self.workspace, kv4, kv_scale, block_table, seq_lens,
+                             lse, q, w_uk, w_uv, out)
+        _ok(lib().mla_decode_run_fp4kv(ctypes.byref(self.dims), q.data_ptr(), kv4.data_ptr(),
+                                       kv_scale.data_ptr(), block_table.data_ptr(),
+                                       seq_lens.data_ptr(), w_uk.data_ptr(), w_uv.data_ptr(),
+                                       float(scale), out.data_ptr(), lse.data_ptr(),
+                                       self.workspace.data_ptr(), self.ws_bytes, stream),
+            "mla_decode_run_fp4kv")
+
+    def attend_fp4kv(self, kv4, kv_scale, block_table, seq_lens, scale, lse):
+        stream = _checked_as(self._attend_spec4, self.workspace, kv4, kv_scale, block_table,
+                             seq_lens, lse)
+        _ok(lib().mla_decode_attend_fp4kv(ctypes.byref(self.dims), kv4.data_ptr(),
+                                          kv_scale.data_ptr(), block_table.data_ptr(),
+                                          seq_lens.data_ptr(), float(scale), lse.data_ptr(),
+                                          self.workspace.data_ptr(), self.ws_bytes, stream),
+            "mla_decode_attend_fp4kv")
 
     def absorb_fp8w(self, q, w_uk8, w_uk_scale):
         _ok(lib().mla_decode_absorb_fp8w(ctypes.byref(self.dims), _ptr(q), _ptr(w_uk8),
@@ -330,6 +365,20 @@ def _lines(d, block_table, seq_lens, new_lens=None, status=None):
     return lines
 
 
+def _append(name, d, rows, kv, kv_scale, block_table, seq_lens, new_lens, status):
+    fp4 = name == "mla_decode_append_fp4kv"
+    B, pages = d.batch, d.num_pages
+    max_new = rows.shape[1] if rows is not None and rows.dim() == 3 else 0
+    stream = _checked(("rows", rows, torch.bfloat16, (B, max_new, 576)),
+                      ("kv4" if fp4 else "kv8", kv, torch.uint8, (pages, 64, 336 if fp4 else 576)),
+                      ("kv_scale", kv_scale, torch.float32, (pages,)),
+                      *_lines(d, block_table, seq_lens, new_lens, status))
+    _ok(getattr(lib(), name)(ctypes.byref(d), rows.data_ptr(), max_new, _ptr(new_lens),
+                             block_table.data_ptr(), seq_lens.data_ptr(), kv.data_ptr(),
+                             kv_scale.data_ptr(), _ptr(status), stream),
+        name)
+
+
 def append_fp8kv(d: Dims, rows, kv8, kv_scale, block_table, seq_lens, new_lens=None,
                  status=None):
     """Quantise new rows (bf16 [B, max_new, 576]) into the 8-bit cache, in place.
@@ -337,16 +386,15 @@ def append_fp8kv(d: Dims, rows, kv8, kv_scale, block_table, seq_lens, new_lens=N
     Row i < new_lens[b] (default: every row) goes to position
     seq_lens[b] - new_lens[b] + i.  status: optional int32 [1] on the device
     that receives the first error found there."""
-    B, pages = d.batch, d.num_pages
-    max_new = rows.shape[1] if rows is not None and rows.dim() == 3 else 0
-    stream = _checked(("rows", rows, torch.bfloat16, (B, max_new, 576)),
-                      ("kv8", kv8, torch.uint8, (pages, 64, 576)),
-                      ("kv_scale", kv_scale, torch.float32, (pages,)),
-                      *_lines(d, block_table, seq_lens, new_lens, status))
-    _ok(lib().mla_decode_append_fp8kv(ctypes.byref(d), rows.data_ptr(), max_new, _ptr(new_lens),
-                                      block_table.data_ptr(), seq_lens.data_ptr(), kv8.data_ptr(),
-                                      kv_scale.data_ptr(), _ptr(status), stream),
-        "mla_decode_append_fp8kv")
+    _append("mla_decode_append_fp8kv", d, rows, kv8, kv_scale, block_table, seq_lens, new_lens,
+            status)
+
+
+def append_fp4kv(d: Dims, rows, kv4, kv_scale, block_table, seq_lens, new_lens=None,
+                 status=None):
+    """append_fp8kv() into the 4-bit cache (uint8 [num_pages, 64, 336])."""
+    _append("mla_decode_append_fp4kv", d, rows, kv4, kv_scale, block_table, seq_lens, new_lens,
+            status)
 
 
 def page_keys(d: Dims, cache, block_table, seq_lens, max_new, keys, new_lens=None, status=None):
@@ -375,6 +423,20 @@ def page_keys_fp8kv(d: Dims, kv8, kv_scale, block_table, seq_lens, max_new, keys
                                          block_table.data_ptr(), seq_lens.data_ptr(), max_new,
                                          _ptr(new_lens), keys.data_ptr(), _ptr(status), stream),
         "mla_decode_page_keys_fp8kv")
+
+
+def page_keys_fp4kv(d: Dims, kv4, kv_scale, block_table, seq_lens, max_new, keys, new_lens=None,
+                    status=None):
+    """page_keys() from the 4-bit cache."""
+    pages = d.num_pages
+    stream = _checked(("kv4", kv4, torch.uint8, (pages, 64, 336)),
+                      ("kv_scale", kv_scale, torch.float32, (pages,)),
+                      ("keys", keys, torch.bfloat16, (pages, 576)),
+                      *_lines(d, block_table, seq_lens, new_lens, status))
+    _ok(lib().mla_decode_page_keys_fp4kv(ctypes.byref(d), kv4.data_ptr(), kv_scale.data_ptr(),
+                                         block_table.data_ptr(), seq_lens.data_ptr(), max_new,
+                                         _ptr(new_lens), keys.data_ptr(), _ptr(status), stream),
+        "mla_decode_page_keys_fp4kv")
 
 
 def score_pages(d: Dims, query, keys, block_table, seq_lens, scores, status=None):
@@ -407,3 +469,111 @@ def select_pages(d: Dims, scores, block_table, seq_lens, top_k, keep_first, keep
                                       sel_table.data_ptr(), _ptr(sel_pages), sel_lens.data_ptr(),
                                       _ptr(status), stream),
         "mla_decode_select_pages")
+
+
+# ---------------------------------------------------------------- in front of the cache and back
+def _rows_of(rows):
+    return rows.shape[1] if rows is not None and rows.dim() == 3 else 0
+
+
+def gather(d: Dims, cache, block_table, seq_lens, rows, new_lens=None, status=None):
+    """Tokens of the bf16 cache as rows (bf16 [B, max_new, 576], in place): row i <
+    new_lens[b] (default: every row) is the token at position seq_lens[b] -
+    new_lens[b] + i."""
+    max_new = _rows_of(rows)
+    stream = _checked(("cache", cache, torch.bfloat16, (d.num_pages, 64, 576)),
+                      ("rows", rows, torch.bfloat16, (d.batch, max_new, 576)),
+                      *_lines(d, block_table, seq_lens, new_lens, status))
+    _ok(lib().mla_decode_gather(ctypes.byref(d), cache.data_ptr(), block_table.data_ptr(),
+                                seq_lens.data_ptr(), max_new, _ptr(new_lens), rows.data_ptr(),
+                                _ptr(status), stream),
+        "mla_decode_gather")
+
+
+def _gather(name, d, kv, kv_scale, block_table, seq_lens, rows, new_lens, status):
+    fp4 = name == "mla_decode_gather_fp4kv"
+    max_new, pages = _rows_of(rows), d.num_pages
+    stream = _checked(("kv4" if fp4 else "kv8", kv, torch.uint8, (pages, 64, 336 if fp4 else 576)),
+                      ("kv_scale", kv_scale, torch.float32, (pages,)),
+                      ("rows", rows, torch.bfloat16, (d.batch, max_new, 576)),
+                      *_lines(d, block_table, seq_lens, new_lens, status))
+    _ok(getattr(lib(), name)(ctypes.byref(d), kv.data_ptr(), kv_scale.data_ptr(),
+                             block_table.data_ptr(), seq_lens.data_ptr(), max_new, _ptr(new_lens),
+                             rows.data_ptr(), _ptr(status), stream),
+        name)
+
+
+def gather_fp8kv(d: Dims, kv8, kv_scale, block_table, seq_lens, rows, new_lens=None, status=None):
+    """gather() from the 8-bit cache: what append_fp8kv() stored, as bf16 rows."""
+    _gather("mla_decode_gather_fp8kv", d, kv8, kv_scale, block_table, seq_lens, rows, new_lens,
+            status)
+
+
+def gather_fp4kv(d: Dims, kv4, kv_scale, block_table, seq_lens, rows, new_lens=None, status=None):
+    """gather() from the 4-bit cache: what append_fp4kv() stored, as bf16 rows."""
+    _gather("mla_decode_gather_fp4kv", d, kv4, kv_scale, block_table, seq_lens, rows, new_lens,
+            status)
+
+
+def _token_stride(t, batch, tokens, width):
+    """Elements from a token to the next of a [batch, tokens, ...] tensor whose tokens
+    are contiguous and evenly spaced; None for another."""
+    if batch > 1 and tokens > 1 and t.stride(0) != tokens * t.stride(1):
+        return None
+    n = t.stride(1) if tokens > 1 else t.stride(0) if batch > 1 else width
+    if t.stride(-1) != 1 or (t.dim() == 4 and t.stride(2) != t.shape[3]) or n < width or n % 8:
+        return None
+    return n
+
+
+def norm_rope(d: Dims, seq_lens, cos_sin, q=None, q_out=None, q_weight=None, kv=None,
+              kv_weight=None, rows=None, cache=None, block_table=None, eps=1e-6,
+              interleaved=True, positions=None, new_lens=None, status=None):
+    """Norms and rotation of new tokens, one kernel: q (bf16 [B, max_new, H, 192]) to
+    q_out, latents kv (bf16 [B, max_new, 576]) to rows of the same shape, to the bf16
+    cache's pages (with block_table), or to both.
+
+    q_weight [192] and kv_weight [512]: RMS norms of each query head and of the
+    latent, none without them.  cos_sin: fp32 [positions, 64], 32 cosines and 32 sines
+    a line.  interleaved: columns 2 i and 2 i + 1 are a pair, else i and i + 32.  q and
+    kv may have gaps between tokens (columns of a wider projection); q_out may be q,
+    and rows kv, where they have none.  positions: int32 [B, max_new], by default a
+    token's place in the cache, seq_lens[b] - new_lens[b] + i."""
+    bf, B, H = torch.bfloat16, d.batch, d.num_heads
+    given = q if q is not None else kv
+    max_new = given.shape[1] if given is not None and given.dim() >= 3 else 0
+    most = cos_sin.shape[0] if cos_sin is not None and cos_sin.dim() == 2 else 0
+    tensors = [("cos_sin", cos_sin, torch.float32, (most, 64)),
+               ("seq_lens", seq_lens, torch.int32, (B,))]
+    strides = [0, 0]
+    for i, (name, t, shape, width) in enumerate((("q", q, (B, max_new, H, 192), H * 192),
+                                                 ("kv", kv, (B, max_new, 576), 576))):
+        if t is None:
+            continue
+        stride = _token_stride(t, B, max_new, width) if t.shape == shape else None
+        if stride is None or t.dtype is not bf or t.get_device() != seq_lens.get_device():
+            raise ValueError(
+                "%s: expected a %s tensor of shape %s on the current CUDA device, with contiguous, "
+                "evenly spaced tokens (a multiple of 8 elements apart), got %s" %
+                (name, bf, shape, (t.dtype, tuple(t.shape), t.stride(), str(t.device))))
+        strides[i] = stride
+    if q is not None or q_out is not None:
+        tensors.append(("q_out", q_out, bf, (B, max_new, H, 192)))
+    for name, t, dtype, shape in (("q_weight", q_weight, bf, (192,)),
+                                  ("kv_weight", kv_weight, bf, (512,)),
+                                  ("rows", rows, bf, (B, max_new, 576)),
+                                  ("cache", cache, bf, (d.num_pages, 64, 576)),
+                                  ("block_table", block_table, torch.int32,
+                                   (B, d.max_pages_per_seq)),
+                                  ("positions", positions, torch.int32, (B, max_new)),
+                                  ("new_lens", new_lens, torch.int32, (B,)),
+                                  ("status", status, torch.int32, (1,))):
+        if t is not None:
+            tensors.append((name, t, dtype, shape))
+    stream = _checked(*tensors)
+    _ok(lib().mla_decode_norm_rope(ctypes.byref(d), _ptr(q), strides[0], _ptr(q_weight), _ptr(kv),
+                                   strides[1], _ptr(kv_weight), float(eps), cos_sin.data_ptr(),
+                                   most, int(bool(interleaved)), _ptr(positions), max_new,
+                                   _ptr(new_lens), seq_lens.data_ptr(), _ptr(q_out), _ptr(rows),
+                                   _ptr(cache), _ptr(block_table), _ptr(status), stream),
+        "mla_decode_norm_rope")

@@ -12,6 +12,7 @@
 #include "../../include/mla_decode.h"
 #include "common.cuh"
 #include "host_checks.h"
+#include "prep.h"
 #include "ptx.cuh"
 
 namespace mla {
@@ -57,7 +58,7 @@ cudaError_t launch_combine_up(const CUtensorMap& tm_wuv, int B, int T, int H, co
                               __nv_bfloat16* out, int32_t* status, int splits_per_seq,
                               const float* wuv_scale, cudaStream_t st);
 cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope,
-                                const CUtensorMap& tm_q, int sm_count,
+                                const CUtensorMap& tm_q, const uint8_t* kv4, int sm_count,
                                 const int32_t* block_table, const float* kv_scale,
                                 const int32_t* seq_len_eff, const PlanHeader* header, void* ws,
                                 const int32_t* seq_first, const int32_t* seq_nsplit,
@@ -66,12 +67,17 @@ cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm
                                 int num_pages, float scale, cudaStream_t st);
 cudaError_t launch_append(const void* rows, int max_new, const int32_t* new_lens,
                           const int32_t* block_table, const int32_t* seq_lens, int B,
-                          int num_pages, int max_pages, uint8_t* kv8, float* kv_scale,
+                          int num_pages, int max_pages, uint8_t* kv, bool fp4, float* kv_scale,
                           int32_t* status, int sm_count, cudaStream_t st);
-cudaError_t launch_page_keys(const void* cache, const float* kv_scale,
+cudaError_t launch_page_keys(Kind kind, const void* cache, const float* kv_scale,
                              const int32_t* block_table, const int32_t* seq_lens, int max_new,
                              const int32_t* new_lens, int B, int num_pages, int max_pages,
                              __nv_bfloat16* keys, int32_t* status, cudaStream_t st);
+cudaError_t launch_gather(Kind kind, const void* cache, const float* kv_scale,
+                          const int32_t* block_table, const int32_t* seq_lens, int max_new,
+                          const int32_t* new_lens, int B, int num_pages, int max_pages,
+                          void* rows, int32_t* status, cudaStream_t st);
+cudaError_t launch_prep(const PrepParams& P, bool interleaved, int sm_count, cudaStream_t st);
 cudaError_t launch_score(const CUtensorMap& tm_q, const void* page_keys,
                          const int32_t* block_table, const int32_t* seq_lens, int B, int T, int H,
                          int num_pages, int max_pages, float* scores, int32_t* status,
@@ -693,39 +699,67 @@ int mla_decode_run_fp8w(const mla_decode_dims* d, const void* q, const void* kv_
   return finish_run(d, nullptr, w_uv_fp8, w_uv_scale, scale, out, lse, ws, ws_bytes, stream);
 }
 
-int mla_decode_attend_fp8kv(const mla_decode_dims* d, const uint8_t* kv_fp8,
+// The attention step over the 8-bit cache (fp4: the 4-bit one).
+static int attend_quantised(const mla_decode_dims* d, bool fp4, const uint8_t* kv,
                             const float* kv_scale, const int32_t* block_table,
                             const int32_t* seq_lens, float scale, float* lse, void* ws,
                             size_t ws_bytes, void* stream) {
   int rc = check_dims(d);
   if (rc) return rc;
-  if (!softmax_scale_ok(scale) || !kv_fp8 || !kv_scale || !block_table || !seq_lens || !lse ||
-      !ws || !aligned16(kv_fp8) || !aligned16(ws) || !aligned4(kv_scale) ||
+  if (!softmax_scale_ok(scale) || !kv || !kv_scale || !block_table || !seq_lens || !lse ||
+      !ws || !aligned16(kv) || !aligned16(ws) || !aligned4(kv_scale) ||
       !aligned4(block_table) || !aligned4(seq_lens) || !aligned4(lse))
     return MLA_DECODE_INVALID_ARG;
   WsLayout L;
   rc = layout_for(d, ws_bytes, &L);
   if (rc) return rc;
-  // A page is one copy of its latent columns, as four 128-column boxes one after
-  // the other, and one of its RoPE columns: a box of 128 whose second half lies
-  // past the row and is filled with zeros.
-  CUtensorMap tm_lat, tm_rope, tm_q;
+  // A page of the 8-bit cache is one copy of its latent columns, as four 128-column
+  // boxes one after the other, and one of its RoPE columns: a box of 128 whose second
+  // half lies past the row and is filled with zeros.  (One of the 4-bit cache is a
+  // copy without a map.)
+  CUtensorMap tm_lat{}, tm_rope{}, tm_q;
   if (!make_map(&tm_q, at<void>(ws, L.qlat),
                 static_cast<uint64_t>(d->batch) * d->q_len * d->num_heads, kDqk, kDqk, kBoxCols,
                 decode_q_box_rows(d->q_len, d->num_heads), false) ||
-      !make_map_chunks(&tm_lat, kv_fp8, static_cast<uint64_t>(d->num_pages) * kPage) ||
-      !make_map(&tm_rope, kv_fp8, static_cast<uint64_t>(d->num_pages) * kPage, kDqk, kDqk, 128,
-                kPage, true, 1))
+      (!fp4 && (!make_map_chunks(&tm_lat, kv, static_cast<uint64_t>(d->num_pages) * kPage) ||
+                !make_map(&tm_rope, kv, static_cast<uint64_t>(d->num_pages) * kPage, kDqk, kDqk,
+                          128, kPage, true, 1))))
     return MLA_DECODE_CUDA_ERROR;
   int sms = 0;
   rc = sm_count(&sms);
   if (rc) return rc;
   return cuda_rc(launch_decode_fp8kv(
-      tm_lat, tm_rope, tm_q, sms, block_table, kv_scale, at<int32_t>(ws, L.seq_len_eff),
-      at<PlanHeader>(ws, L.header), ws, at<int32_t>(ws, L.seq_first),
-      at<int32_t>(ws, L.seq_nsplit), at<int32_t>(ws, L.seq_slot), at<__nv_bfloat16>(ws, L.olat),
-      lse, at<int32_t>(ws, L.status), d->batch, d->q_len, d->num_heads, d->max_pages_per_seq,
-      d->num_pages, scale, static_cast<cudaStream_t>(stream)));
+      tm_lat, tm_rope, tm_q, fp4 ? kv : nullptr, sms, block_table, kv_scale,
+      at<int32_t>(ws, L.seq_len_eff), at<PlanHeader>(ws, L.header), ws,
+      at<int32_t>(ws, L.seq_first), at<int32_t>(ws, L.seq_nsplit), at<int32_t>(ws, L.seq_slot),
+      at<__nv_bfloat16>(ws, L.olat), lse, at<int32_t>(ws, L.status), d->batch, d->q_len,
+      d->num_heads, d->max_pages_per_seq, d->num_pages, scale,
+      static_cast<cudaStream_t>(stream)));
+}
+
+static int run_quantised(const mla_decode_dims* d, bool fp4, const void* q, const uint8_t* kv,
+                         const float* kv_scale, const int32_t* block_table,
+                         const int32_t* seq_lens, const void* w_uk, const void* w_uv,
+                         float scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                         void* stream) {
+  int rc = check_run(d, q, kv, block_table, seq_lens, w_uk, w_uv, false, nullptr, nullptr,
+                     scale, out, lse, ws, ws_bytes);
+  if (rc) return rc;
+  if (!kv_scale || !aligned4(kv_scale)) return MLA_DECODE_INVALID_ARG;
+  rc = mla_decode_absorb(d, q, w_uk, ws, ws_bytes, stream);
+  if (rc) return rc;
+  rc = attend_quantised(d, fp4, kv, kv_scale, block_table, seq_lens, scale, lse, ws, ws_bytes,
+                        stream);
+  if (rc) return rc;
+  return finish_run(d, w_uv, nullptr, nullptr, scale, out, lse, ws, ws_bytes, stream);
+}
+
+int mla_decode_attend_fp8kv(const mla_decode_dims* d, const uint8_t* kv_fp8,
+                            const float* kv_scale, const int32_t* block_table,
+                            const int32_t* seq_lens, float scale, float* lse, void* ws,
+                            size_t ws_bytes, void* stream) {
+  return attend_quantised(d, false, kv_fp8, kv_scale, block_table, seq_lens, scale, lse, ws,
+                          ws_bytes, stream);
 }
 
 int mla_decode_run_fp8kv(const mla_decode_dims* d, const void* q, const uint8_t* kv_fp8,
@@ -733,72 +767,184 @@ int mla_decode_run_fp8kv(const mla_decode_dims* d, const void* q, const uint8_t*
                          const int32_t* seq_lens, const void* w_uk, const void* w_uv,
                          float scale, void* out, float* lse, void* ws, size_t ws_bytes,
                          void* stream) {
-  int rc = check_run(d, q, kv_fp8, block_table, seq_lens, w_uk, w_uv, false, nullptr, nullptr,
-                     scale, out, lse, ws, ws_bytes);
-  if (rc) return rc;
-  if (!kv_scale || !aligned4(kv_scale)) return MLA_DECODE_INVALID_ARG;
-  rc = mla_decode_absorb(d, q, w_uk, ws, ws_bytes, stream);
-  if (rc) return rc;
-  rc = mla_decode_attend_fp8kv(d, kv_fp8, kv_scale, block_table, seq_lens, scale, lse, ws,
-                               ws_bytes, stream);
-  if (rc) return rc;
-  return finish_run(d, w_uv, nullptr, nullptr, scale, out, lse, ws, ws_bytes, stream);
+  return run_quantised(d, false, q, kv_fp8, kv_scale, block_table, seq_lens, w_uk, w_uv, scale,
+                       out, lse, ws, ws_bytes, stream);
 }
 
-int mla_decode_append_fp8kv(const mla_decode_dims* d, const void* rows, int32_t max_new,
-                            const int32_t* new_lens, const int32_t* block_table,
-                            const int32_t* seq_lens, uint8_t* kv_fp8, float* kv_scale,
-                            int32_t* status, void* stream) {
+int mla_decode_attend_fp4kv(const mla_decode_dims* d, const uint8_t* kv_fp4,
+                            const float* kv_scale, const int32_t* block_table,
+                            const int32_t* seq_lens, float scale, float* lse, void* ws,
+                            size_t ws_bytes, void* stream) {
+  return attend_quantised(d, true, kv_fp4, kv_scale, block_table, seq_lens, scale, lse, ws,
+                          ws_bytes, stream);
+}
+
+int mla_decode_run_fp4kv(const mla_decode_dims* d, const void* q, const uint8_t* kv_fp4,
+                         const float* kv_scale, const int32_t* block_table,
+                         const int32_t* seq_lens, const void* w_uk, const void* w_uv,
+                         float scale, void* out, float* lse, void* ws, size_t ws_bytes,
+                         void* stream) {
+  return run_quantised(d, true, q, kv_fp4, kv_scale, block_table, seq_lens, w_uk, w_uv, scale,
+                       out, lse, ws, ws_bytes, stream);
+}
+
+static int append_impl(const mla_decode_dims* d, bool fp4, const void* rows, int32_t max_new,
+                       const int32_t* new_lens, const int32_t* block_table,
+                       const int32_t* seq_lens, uint8_t* kv, float* kv_scale, int32_t* status,
+                       void* stream) {
   int rc = check_dims(d);
   if (rc) return rc;
   if (!rows || !aligned16(rows) || max_new < 1 || !aligned4(new_lens) || !block_table ||
-      !aligned4(block_table) || !seq_lens || !aligned4(seq_lens) || !kv_fp8 ||
-      !aligned16(kv_fp8) || !kv_scale || !aligned4(kv_scale) || !aligned4(status))
+      !aligned4(block_table) || !seq_lens || !aligned4(seq_lens) || !kv ||
+      !aligned16(kv) || !kv_scale || !aligned4(kv_scale) || !aligned4(status))
     return MLA_DECODE_INVALID_ARG;
   if (max_new > INT32_MAX - kPage) return MLA_DECODE_INVALID_ARG;
   int sms = 0;
   rc = sm_count(&sms);
   if (rc) return rc;
   return cuda_rc(launch_append(rows, max_new, new_lens, block_table, seq_lens, d->batch,
-                               d->num_pages, d->max_pages_per_seq, kv_fp8, kv_scale, status, sms,
+                               d->num_pages, d->max_pages_per_seq, kv, fp4, kv_scale, status, sms,
                                static_cast<cudaStream_t>(stream)));
 }
 
-static int page_keys_impl(const mla_decode_dims* d, const void* cache, const float* kv_scale,
-                          const int32_t* block_table, const int32_t* seq_lens, int32_t max_new,
-                          const int32_t* new_lens, void* page_keys, int32_t* status,
-                          void* stream) {
+int mla_decode_append_fp8kv(const mla_decode_dims* d, const void* rows, int32_t max_new,
+                            const int32_t* new_lens, const int32_t* block_table,
+                            const int32_t* seq_lens, uint8_t* kv_fp8, float* kv_scale,
+                            int32_t* status, void* stream) {
+  return append_impl(d, false, rows, max_new, new_lens, block_table, seq_lens, kv_fp8, kv_scale,
+                     status, stream);
+}
+
+int mla_decode_append_fp4kv(const mla_decode_dims* d, const void* rows, int32_t max_new,
+                            const int32_t* new_lens, const int32_t* block_table,
+                            const int32_t* seq_lens, uint8_t* kv_fp4, float* kv_scale,
+                            int32_t* status, void* stream) {
+  return append_impl(d, true, rows, max_new, new_lens, block_table, seq_lens, kv_fp4, kv_scale,
+                     status, stream);
+}
+
+// Page keys and reading back: the same arguments but for what they write.
+static int newest_impl(const mla_decode_dims* d, Kind kind, bool keys, const void* cache,
+                       const float* kv_scale, const int32_t* block_table,
+                       const int32_t* seq_lens, int32_t max_new, const int32_t* new_lens,
+                       void* dst, int32_t* status, void* stream) {
   const int rc = check_dims(d);
   if (rc) return rc;
-  if (!cache || !aligned16(cache) || !aligned4(kv_scale) || !block_table ||
-      !aligned4(block_table) || !seq_lens || !aligned4(seq_lens) || max_new < 1 ||
-      max_new > INT32_MAX - kPage || !aligned4(new_lens) || !page_keys ||
-      !aligned16(page_keys) || !aligned4(status))
+  if (!cache || !aligned16(cache) || (kind != Kind::kBf16 && !kv_scale) || !aligned4(kv_scale) ||
+      !block_table || !aligned4(block_table) || !seq_lens || !aligned4(seq_lens) || max_new < 1 ||
+      max_new > INT32_MAX - kPage || !aligned4(new_lens) || !dst || !aligned16(dst) ||
+      !aligned4(status))
     return MLA_DECODE_INVALID_ARG;
-  return cuda_rc(launch_page_keys(cache, kv_scale, block_table, seq_lens, max_new, new_lens,
-                                  d->batch, d->num_pages, d->max_pages_per_seq,
-                                  static_cast<__nv_bfloat16*>(page_keys), status,
-                                  static_cast<cudaStream_t>(stream)));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (keys)
+    return cuda_rc(launch_page_keys(kind, cache, kv_scale, block_table, seq_lens, max_new,
+                                    new_lens, d->batch, d->num_pages, d->max_pages_per_seq,
+                                    static_cast<__nv_bfloat16*>(dst), status, st));
+  return cuda_rc(launch_gather(kind, cache, kv_scale, block_table, seq_lens, max_new, new_lens,
+                               d->batch, d->num_pages, d->max_pages_per_seq, dst, status, st));
 }
 
 int mla_decode_page_keys(const mla_decode_dims* d, const void* kv_cache,
                          const int32_t* block_table, const int32_t* seq_lens, int32_t max_new,
                          const int32_t* new_lens, void* page_keys, int32_t* status,
                          void* stream) {
-  return page_keys_impl(d, kv_cache, nullptr, block_table, seq_lens, max_new, new_lens,
-                        page_keys, status, stream);
+  return newest_impl(d, Kind::kBf16, true, kv_cache, nullptr, block_table, seq_lens, max_new,
+                     new_lens, page_keys, status, stream);
 }
 
 int mla_decode_page_keys_fp8kv(const mla_decode_dims* d, const uint8_t* kv_fp8,
                                const float* kv_scale, const int32_t* block_table,
-                               const int32_t* seq_lens, int32_t max_new,
-                               const int32_t* new_lens, void* page_keys, int32_t* status,
-                               void* stream) {
-  const int rc = check_dims(d);
+                               const int32_t* seq_lens, int32_t max_new, const int32_t* new_lens,
+                               void* page_keys, int32_t* status, void* stream) {
+  return newest_impl(d, Kind::kFp8, true, kv_fp8, kv_scale, block_table, seq_lens, max_new,
+                     new_lens, page_keys, status, stream);
+}
+
+int mla_decode_page_keys_fp4kv(const mla_decode_dims* d, const uint8_t* kv_fp4,
+                               const float* kv_scale, const int32_t* block_table,
+                               const int32_t* seq_lens, int32_t max_new, const int32_t* new_lens,
+                               void* page_keys, int32_t* status, void* stream) {
+  return newest_impl(d, Kind::kFp4, true, kv_fp4, kv_scale, block_table, seq_lens, max_new,
+                     new_lens, page_keys, status, stream);
+}
+
+int mla_decode_gather(const mla_decode_dims* d, const void* kv_cache, const int32_t* block_table,
+                      const int32_t* seq_lens, int32_t max_new, const int32_t* new_lens,
+                      void* rows, int32_t* status, void* stream) {
+  return newest_impl(d, Kind::kBf16, false, kv_cache, nullptr, block_table, seq_lens, max_new,
+                     new_lens, rows, status, stream);
+}
+
+int mla_decode_gather_fp8kv(const mla_decode_dims* d, const uint8_t* kv_fp8,
+                            const float* kv_scale, const int32_t* block_table,
+                            const int32_t* seq_lens, int32_t max_new, const int32_t* new_lens,
+                            void* rows, int32_t* status, void* stream) {
+  return newest_impl(d, Kind::kFp8, false, kv_fp8, kv_scale, block_table, seq_lens, max_new,
+                     new_lens, rows, status, stream);
+}
+
+int mla_decode_gather_fp4kv(const mla_decode_dims* d, const uint8_t* kv_fp4,
+                            const float* kv_scale, const int32_t* block_table,
+                            const int32_t* seq_lens, int32_t max_new, const int32_t* new_lens,
+                            void* rows, int32_t* status, void* stream) {
+  return newest_impl(d, Kind::kFp4, false, kv_fp4, kv_scale, block_table, seq_lens, max_new,
+                     new_lens, rows, status, stream);
+}
+
+int mla_decode_norm_rope(const mla_decode_dims* d, const void* q, int64_t q_stride,
+                         const void* q_weight, const void* kv, int64_t kv_stride,
+                         const void* kv_weight, float eps, const float* cos_sin,
+                         int32_t max_position, int32_t interleaved, const int32_t* positions,
+                         int32_t max_new, const int32_t* new_lens, const int32_t* seq_lens,
+                         void* q_out, void* rows, void* kv_cache, const int32_t* block_table,
+                         int32_t* status, void* stream) {
+  int rc = check_dims(d);
   if (rc) return rc;
-  if (!kv_scale) return MLA_DECODE_INVALID_ARG;
-  return page_keys_impl(d, kv_fp8, kv_scale, block_table, seq_lens, max_new, new_lens, page_keys,
-                        status, stream);
+  if (!(q || kv) || !cos_sin || !aligned16(cos_sin) || max_position < 1 || max_new < 1 ||
+      interleaved < 0 || interleaved > 1 || !aligned4(positions) || !aligned4(new_lens) ||
+      !seq_lens || !aligned4(seq_lens) || !aligned4(status) || !std::isfinite(eps) || eps <= 0.0f)
+    return MLA_DECODE_INVALID_ARG;
+  // A row in 16-byte parts: strides are multiples of eight elements.
+  if (q ? (!aligned16(q) || !q_out || !aligned16(q_out) || !aligned16(q_weight) ||
+           q_stride < static_cast<int64_t>(d->num_heads) * kDq || q_stride % 8 != 0)
+        : (q_out || q_weight))
+    return MLA_DECODE_INVALID_ARG;
+  if (kv ? (!aligned16(kv) || !aligned16(kv_weight) || kv_stride < kDqk || kv_stride % 8 != 0 ||
+            !(rows || kv_cache) || !aligned16(rows) || !aligned16(kv_cache) ||
+            (kv_cache && (!block_table || !aligned4(block_table))))
+         : (rows || kv_cache || kv_weight))
+    return MLA_DECODE_INVALID_ARG;
+  // Warps count their tasks (four heads or a latent row) in 32 bits.
+  if (static_cast<int64_t>(d->batch) * max_new > INT32_MAX / 2 / (d->num_heads / 4 + 1))
+    return MLA_DECODE_INVALID_ARG;
+  int sms = 0;
+  rc = sm_count(&sms);
+  if (rc) return rc;
+  PrepParams P{};
+  P.q = static_cast<const __nv_bfloat16*>(q);
+  P.kv = static_cast<const __nv_bfloat16*>(kv);
+  P.q_stride = q_stride;
+  P.kv_stride = kv_stride;
+  P.q_weight = static_cast<const __nv_bfloat16*>(q_weight);
+  P.kv_weight = static_cast<const __nv_bfloat16*>(kv_weight);
+  P.cos_sin = cos_sin;
+  P.positions = positions;
+  P.new_lens = new_lens;
+  P.seq_lens = seq_lens;
+  P.block_table = block_table;
+  P.q_out = static_cast<__nv_bfloat16*>(q_out);
+  P.rows = static_cast<uint4*>(rows);
+  P.cache = static_cast<uint4*>(kv_cache);
+  P.status = status;
+  P.eps = eps;
+  P.B = d->batch;
+  P.H = d->num_heads;
+  P.max_new = max_new;
+  P.max_position = max_position;
+  P.num_pages = d->num_pages;
+  P.max_pages = d->max_pages_per_seq;
+  P.max_len = d->max_pages_per_seq * kPage;
+  return cuda_rc(launch_prep(P, interleaved != 0, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int mla_decode_score_pages(const mla_decode_dims* d, const void* query, const void* page_keys,

@@ -1,39 +1,19 @@
-// append.cu -- new tokens into the 8-bit latent cache, and the pages' mean keys.
+// append.cu -- new tokens into the 8-bit and the 4-bit latent cache, and the pages'
+// mean keys.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "fp4kv.cuh"
 #include "fp8kv.cuh"
 #include "ptx.cuh"
+#include "tokens.cuh"
 
 namespace mla {
 
 namespace {
 
 constexpr int kAppThreads = 384;  // that convert a page
-constexpr int kChunks = kDqk / 8;  // 16-byte chunks of a bf16 row: 72 (8-byte chunks of codes)
-
-// The new tokens of one sequence: positions [first, len).  False (and an error
-// on record, if `report`) if its lengths are out of range: the sequence is then
-// left alone.
-struct NewTokens {
-  int first, len;
-  __device__ bool load(const int32_t* seq_lens, const int32_t* new_lens, int max_new, int cap,
-                       int b, bool report, int32_t* status) {
-    len = seq_lens[b];
-    const int n = new_lens ? new_lens[b] : max_new;
-    first = len - n;
-    if (len < 0 || len > cap || n < 0 || n > max_new || first < 0) {
-      if (report) record_status(status, MLA_STATUS_BOUNDS);
-      return false;
-    }
-    return n > 0;
-  }
-  __device__ int pages() const { return (len - 1) / kPage - first / kPage + 1; }
-};
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 // Largest |x| of 8 packed bf16 values and `top`, NaN ignored.
 __device__ __forceinline__ __nv_bfloat162 absmax8(__nv_bfloat162 top, const uint4& v) {
@@ -71,6 +51,34 @@ __device__ __forceinline__ float mul_odd(float x, float y) {
   return __int_as_float(even ? ((rest > 0.0f) == (p > 0.0f) ? u + 1 : u - 1) : u);
 }
 
+// The block of 16 latent values that a thread's eight are half of: lanes l and l ^ 1
+// hold its halves.  Its exponent field under the page's scale 2^se (se = 0: values in
+// units of it), and the codes of this thread's eight.
+struct Block4 {
+  int e;
+  uint32_t codes;
+};
+__device__ __forceinline__ Block4 block4(const float (&v)[8], int se) {
+  float top = 0.0f;
+  bool nan = false;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    top = fmaxf(top, fabsf(v[k]));
+    nan = nan || v[k] != v[k];
+  }
+  top = nan ? __uint_as_float(0x7fffffffu) : top;
+  const float other = __shfl_xor_sync(0xffffffffu, top, 1);
+  top = top == top && other == other ? fmaxf(top, other) : __uint_as_float(0x7fffffffu);
+  Block4 b;
+  b.e = block_exp4(top, se);
+  b.codes = b.e == kExpNan4 ? 0u : e2m1x8(v, exp2_int(kExpBias4 - b.e - se));
+  return b;
+}
+// Four lanes' two exponents as a byte, for the first of them.
+__device__ __forceinline__ uint8_t exps_byte(int e) {
+  return static_cast<uint8_t>(e | (__shfl_xor_sync(0xffffffffu, e, 2) << 4));
+}
+
 struct AppendParams {
   const uint4* rows;
   int max_new;
@@ -78,7 +86,7 @@ struct AppendParams {
   const int32_t* block_table;
   const int32_t* seq_lens;
   int B, num_pages, max_pages;
-  uint8_t* kv8;
+  uint8_t* kv;  // 8 or 4 bits
   float* kv_scale;
   int32_t* status;
 };
@@ -147,17 +155,78 @@ struct Target {
   }
 };
 
+constexpr int kHeld = kPage * kChunks / kAppThreads;
+static_assert(kHeld * kAppThreads == kPage * kChunks, "a page is whole passes");
+
+// The part of fill_page behind the page's scale, for the 4-bit cache: x is what the
+// threads hold of the new rows (a block's halves in neighbouring lanes: kChunks and
+// kAppThreads are multiples of four).
+template <bool kFew>
+__device__ __forceinline__ void store_page4(const AppendParams& P, const Group& grp,
+                                            const Place& at, const Target& to,
+                                            const uint4 (&x)[kHeld], float scale) {
+  const int r0 = at.r0(), r1 = at.r1(), n = (r1 - r0) * kChunks;
+  const int se = static_cast<int>(__float_as_uint(scale) >> 23) - 127;
+  const __nv_bfloat162 inv = __float2bfloat162_rn(1.0f / scale);
+  uint8_t* const dst = P.kv + static_cast<size_t>(to.page) * kPageBytes4;
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    if (kFew && k * kAppThreads >= n) break;
+    const int i = grp.tid + k * kAppThreads, c = i % kChunks;
+    uint8_t* const row = dst + (r0 + i / kChunks) * kRow4;
+    const float v[8] = {bf16_lo(x[k].x), bf16_hi(x[k].x), bf16_lo(x[k].y), bf16_hi(x[k].y),
+                        bf16_lo(x[k].z), bf16_hi(x[k].z), bf16_lo(x[k].w), bf16_hi(x[k].w)};
+    const Block4 b = block4(v, se);
+    const uint8_t exps = exps_byte(b.e);
+    if (i >= n) continue;
+    if (c < kLora / 8) {
+      *reinterpret_cast<uint32_t*>(row + 4 * c) = b.codes;
+      if ((c & 3) == 0) row[kRowExps4 + (c >> 2)] = exps;
+    } else {
+      *reinterpret_cast<uint2*>(row + kRowRope4 + 8 * (c - kLora / 8)) = codes8(x[k], inv);
+    }
+  }
+  if (grp.tid == 0) P.kv_scale[to.page] = scale;
+  if (r0 == 0) {  // a page that starts here: cleared behind the new rows
+    uint4* const all = reinterpret_cast<uint4*>(dst);
+    for (int i = r1 * (kRow4 / 16) + grp.tid; i < kPageBytes4 / 16; i += kAppThreads)
+      all[i] = make_uint4(0u, 0u, 0u, 0u);
+    return;
+  }
+  if (scale == to.old) return;
+  // The scale grew: rows that stay are quantised again from their values.
+  const float ratio = to.old / scale;
+#pragma unroll 1
+  for (int i = grp.tid; i < kPage * kChunks; i += kAppThreads) {
+    const int r = i / kChunks, c = i % kChunks;
+    const bool stays = r < r0 || r >= r1;
+    uint8_t* const row = dst + r * kRow4;
+    float v[8] = {};
+    if (stays) row_values4(row, c, v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = mul_odd(v[k], ratio);
+    const Block4 b = block4(v, 0);
+    const uint8_t exps = exps_byte(b.e);  // (behind all four lanes' reads of the byte)
+    if (!stays) continue;
+    if (c < kLora / 8) {
+      *reinterpret_cast<uint32_t*>(row + 4 * c) = b.codes;
+      if ((c & 3) == 0) row[kRowExps4 + (c >> 2)] = exps;
+    } else {
+      *reinterpret_cast<uint2*>(row + kRowRope4 + 8 * (c - kLora / 8)) =
+          make_uint2(e4m3x4(v[0], v[1], v[2], v[3]), e4m3x4(v[4], v[5], v[6], v[7]));
+    }
+  }
+}
+
 // Fills a page from its new rows, which a thread holds in registers between their
 // maximum and the codes; `taken` is called once all have theirs.  kFew skips what
 // a few rows do not fill, at a price for whole pages (14 -> 15.5 us).  (Every thread
 // has its Target before the first barrier here; one thread replaces the scale
 // behind it.)
-template <bool kFew, typename Taken>
+template <bool kFew, bool kFp4, typename Taken>
 __device__ __forceinline__ void fill_page(const AppendParams& P, const Group& grp,
                                           const Place& at, const Target& to,
                                           const uint4* rows_sh, const Taken& taken) {
-  constexpr int kHeld = kPage * kChunks / kAppThreads;
-  static_assert(kHeld * kAppThreads == kPage * kChunks, "a page is whole passes");
   const int r0 = at.r0(), r1 = at.r1(), n = (r1 - r0) * kChunks;
   uint4 x[kHeld];
   __nv_bfloat162 most = __float2bfloat162_rn(0.0f);
@@ -182,7 +251,11 @@ __device__ __forceinline__ void fill_page(const AppendParams& P, const Group& gr
   if (!to.in_pool) return;
   float scale = exp2_int(page_scale_exp(top));
   if (r0 > 0) scale = fmaxf(scale, next_power_of_two(to.old));
-  uint2* const dst = reinterpret_cast<uint2*>(P.kv8 + static_cast<size_t>(to.page) * kPageBytes8);
+  if constexpr (kFp4) {
+    store_page4<kFew>(P, grp, at, to, x, scale);
+    return;
+  }
+  uint2* const dst = reinterpret_cast<uint2*>(P.kv + static_cast<size_t>(to.page) * kPageBytes8);
   const __nv_bfloat162 inv = __float2bfloat162_rn(1.0f / scale);
 #pragma unroll
   for (int k = 0; k < kHeld; ++k) {
@@ -216,6 +289,7 @@ __device__ __forceinline__ void fill_page(const AppendParams& P, const Group& gr
 // A few new tokens per sequence: one CTA per sequence and page that they can
 // touch.  One token for each of 128 sequences: 2.6 us in a graph, a launch and a
 // chain of three reads (lengths, block table, scale) beside the row's.
+template <bool kFp4>
 __global__ void __launch_bounds__(kAppThreads)
 append_few_kernel(AppendParams P) {
   extern __shared__ __align__(128) uint4 rows_sh[];
@@ -241,7 +315,7 @@ append_few_kernel(AppendParams P) {
   const Group grp{1, static_cast<int>(threadIdx.x), warp_top};
   const Target to(P, at, threadIdx.x == 0);
   if (wait_rows(grp, &landed, 0, &abort_sh, &timeout_sh)) {
-    fill_page<true>(P, grp, at, to, rows_sh, [] {});
+    fill_page<true, kFp4>(P, grp, at, to, rows_sh, [] {});
   } else if (threadIdx.x == 0) {
     record_status(P.status, MLA_STATUS_TIMEOUT);
     mbar_wait_drain(smem_u32(&landed), 0, &timeout_sh);
@@ -274,6 +348,7 @@ struct AppendShared {
   long long upto[kPlanSeqs];  // pages up to and with the sequence's
 };
 
+template <bool kFp4>
 __global__ void __launch_bounds__(kPagesThreads, 1)
 append_pages_kernel(AppendParams P) {
   extern __shared__ __align__(128) uint4 ring_sh[];
@@ -344,7 +419,7 @@ append_pages_kernel(AppendParams P) {
       failed = !wait_rows(grp, &sh.landed[bar], ((k + i) / kBars) & 1, &sh.abort, &sh.timeout);
       if (failed) break;
       const Place at = sh.place[bar];  // (written before its load was issued)
-      fill_page<false>(P, grp, at, Target(P, at, grp.tid == 0), rows_of(k + i), [&] {
+      fill_page<false, kFp4>(P, grp, at, Target(P, at, grp.tid == 0), rows_of(k + i), [&] {
         if (grp.tid == kAppThreads - 32 && i + kRing < mine) issue(i + kRing);
       });
     }
@@ -370,7 +445,7 @@ constexpr int kKeyThreads = 288;
 // TB/s with the launch and the lengths' and the table's reads (eight rows in flight
 // 11.2, sixteen 14.9: registers and the ragged pages' remainders); the last pages of
 // 128 sequences 3.0 us, 8-bit.
-template <bool kFp8>
+template <Kind kKind>
 __global__ void __launch_bounds__(kKeyThreads)
 page_keys_kernel(const uint8_t* __restrict__ cache, const float* __restrict__ kv_scale,
                  const int32_t* __restrict__ block_table, const int32_t* __restrict__ seq_lens,
@@ -395,7 +470,12 @@ page_keys_kernel(const uint8_t* __restrict__ cache, const float* __restrict__ kv
   float s[8] = {};
 #pragma unroll 4
   for (int r = r0; r < filled; r += 4) {
-    if constexpr (kFp8) {
+    if constexpr (kKind == Kind::kFp4) {
+      float x[8];
+      row_values4(cache + static_cast<size_t>(page) * kPageBytes4 + r * kRow4, c, x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s[k] += x[k];
+    } else if constexpr (kKind == Kind::kFp8) {
       const uint2 v = *reinterpret_cast<const uint2*>(
           cache + static_cast<size_t>(page) * kPageBytes8 + r * kDqk + c * 8);
       const float2 x0 = e4m3x2_to_float2(v.x), x1 = e4m3x2_to_float2(v.x >> 16);
@@ -413,7 +493,7 @@ page_keys_kernel(const uint8_t* __restrict__ cache, const float* __restrict__ kv
   for (int k = 0; k < 8; ++k) part[r0][c * 8 + k] = s[k];
   __syncthreads();
   float scale = 1.0f;
-  if constexpr (kFp8) {
+  if constexpr (kKind != Kind::kBf16) {
     scale = kv_scale[page];
     if (!scale_in_range(scale)) {
       if (threadIdx.x == 0) record_status(status, MLA_STATUS_BOUNDS);
@@ -437,33 +517,30 @@ page_keys_kernel(const uint8_t* __restrict__ cache, const float* __restrict__ kv
 // 9.9 / 11.6 / 12.9 and 6.9 / 7.7 / 10.4 / 11.5 / 13.0: where the large batches meet.
 constexpr int kFewTokens = 32;
 
-// Pages that max_new consecutive tokens can touch.
-static int touched_pages(int max_new, int max_pages) {
-  const int most = (max_new + kPage - 2) / kPage + 1;
-  return most < max_pages ? most : max_pages;
-}
-
 cudaError_t launch_append(const void* rows, int max_new, const int32_t* new_lens,
                           const int32_t* block_table, const int32_t* seq_lens, int B,
-                          int num_pages, int max_pages, uint8_t* kv8, float* kv_scale,
+                          int num_pages, int max_pages, uint8_t* kv, bool fp4, float* kv_scale,
                           int32_t* status, int sm_count, cudaStream_t st) {
   const AppendParams P{static_cast<const uint4*>(rows), max_new, new_lens, block_table, seq_lens,
-                       B, num_pages, max_pages, kv8, kv_scale, status};
+                       B, num_pages, max_pages, kv, kv_scale, status};
   if (max_new <= kFewTokens)
-    return launch_pdl(append_few_kernel, dim3(touched_pages(max_new, max_pages), B),
+    return launch_pdl(fp4 ? append_few_kernel<true> : append_few_kernel<false>, dim3(touched_pages(max_new, max_pages), B),
                       dim3(kAppThreads), max_new * kDqk * 2, st, P);
   const int smem = kRing * kRowsBytes;
+  const auto kern = fp4 ? append_pages_kernel<true> : append_pages_kernel<false>;
   const cudaError_t e = cudaFuncSetAttribute(
-      append_pages_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(append_pages_kernel, dim3(sm_count), dim3(kPagesThreads), smem, st, P);
+  return launch_pdl(kern, dim3(sm_count), dim3(kPagesThreads), smem, st, P);
 }
 
-cudaError_t launch_page_keys(const void* cache, const float* kv_scale,
+cudaError_t launch_page_keys(Kind kind, const void* cache, const float* kv_scale,
                              const int32_t* block_table, const int32_t* seq_lens, int max_new,
                              const int32_t* new_lens, int B, int num_pages, int max_pages,
                              __nv_bfloat16* keys, int32_t* status, cudaStream_t st) {
-  auto kern = kv_scale ? page_keys_kernel<true> : page_keys_kernel<false>;
+  const auto kern = kind == Kind::kFp4   ? page_keys_kernel<Kind::kFp4>
+                    : kind == Kind::kFp8 ? page_keys_kernel<Kind::kFp8>
+                                         : page_keys_kernel<Kind::kBf16>;
   return launch_pdl(kern, dim3(touched_pages(max_new, max_pages), B), dim3(kKeyThreads), 0, st,
                     static_cast<const uint8_t*>(cache), kv_scale, block_table, seq_lens, max_new,
                     new_lens, num_pages, max_pages, keys, status);

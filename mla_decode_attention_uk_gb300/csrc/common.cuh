@@ -57,6 +57,9 @@ constexpr float kQloInvScale = 1.0f / 1024.0f;
 // Cost of starting a piece of work (loading Q, writing the result), in pages.
 constexpr int kPieceCost = 2;
 
+// What a page of the cache holds.
+enum class Kind { kBf16, kFp8, kFp4 };
+
 // Device status word values (same numbering as mla_decode_status).
 constexpr int MLA_STATUS_OK = 0;
 constexpr int MLA_STATUS_BOUNDS = 5;

@@ -64,6 +64,7 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "fp4kv.cuh"
 #include "fp8kv.cuh"
 #include "ptx.cuh"
 
@@ -76,10 +77,16 @@ namespace {
 constexpr int kThreads = 512;                     // 16 warps
 constexpr int kBox = kPage * 128;                 // 64 keys x 128 codes: 8 KB
 constexpr int kSlot = kBoxes8 * kBox;             // 40 KB (the last box half empty)
-constexpr int kSlots = 5;
+constexpr int kMaxSlots = 5;
+constexpr int kRaw = 2;                           // pages of the 4-bit cache as they come
 constexpr int kSBufs = 2;                         // S buffers of 64 columns
 constexpr int kRopeBox8 = kBoxes8 - 1;
-constexpr int kSmemBytes = 1024 + kQBox8 + kSlots * kSlot;
+// Slots of a page of E4M3 codes: over the 4-bit cache two pages as they come take the
+// place of one.
+constexpr int slots(bool fp4) { return fp4 ? 4 : kMaxSlots; }
+constexpr int smem_bytes(bool fp4) {
+  return 1024 + kQBox8 + slots(fp4) * kSlot + (fp4 ? kRaw * kPageBytes4 : 0);
+}
 constexpr uint32_t kTmemAll = 512;
 constexpr uint32_t kTmemQ = 128;                  // the query's latent terms: 128 columns
 constexpr uint32_t kTmemOut = 256;                // O^T blocks at 256 + 64 m
@@ -95,6 +102,7 @@ constexpr float kRoundedFrom = 1.0f / 512.0f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct Params {
+  const uint8_t* kv4;  // the 4-bit cache
   const int32_t* block_table;
   const float* kv_scale;
   const int32_t* seq_len_eff;
@@ -171,10 +179,29 @@ struct Pieces {
   }
 };
 
+// Four E2M1 codes (the low halves of a word's first two bytes and their high ones: 16
+// bits of `sel`, without signs) to E4M3 codes of their block, `signs` in the sign bits.
+__device__ __forceinline__ uint32_t e4m3_of(uint2 lut, uint32_t sel, uint32_t signs) {
+  return __byte_perm(lut.x, lut.y, sel) | (signs & 0x80808080u);
+}
+// The E4M3 codes of a block's eight sizes 0 0.5 1 1.5 2 3 4 6 times 2^(e - 8).  Where
+// half of the unit is a normal number of E4M3 (2^-6 and more) an exponent more adds 8
+// to each code but zero's.
+__device__ __forceinline__ uint2 e4m3_sizes(uint32_t e) {
+  if (e - 3 < 12)
+    return make_uint2(0x14100800u + (e - 3) * 0x08080800u, 0x24201c18u + (e - 3) * 0x08080808u);
+  if (e == 2) return make_uint2(0x0c080400u, 0x1c181410u);
+  if (e == 1) return make_uint2(0x06040200u, 0x14100c08u);
+  if (e == 0) return make_uint2(0x03020100u, 0x0c080604u);
+  return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+
+template <bool kFp4>
 __global__ void __launch_bounds__(kThreads, 1)
 decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
                     const __grid_constant__ CUtensorMap tm_rope,
                     const __grid_constant__ CUtensorMap tm_q, Params P) {
+  constexpr int kSlots = slots(kFp4);
   extern __shared__ uint8_t smem_raw[];
   // By slot: slot_full, a page has landed; slot_free, PV has read it and its P^T,
   // or the query terms are made of the tile that was there.
@@ -186,13 +213,15 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
   // next phase here takes PV of page g + kSlots, which follows that of page g +
   // 1, the group's own.  The phase before is over: page g + 1 is in a slot, so PV
   // has read every page up to g + 1 - kSlots.)
+  // Over the 4-bit cache a page lands in raw_full's buffer and warps 12-15 expand it
+  // into a slot: slot_full is theirs then.
   __shared__ __align__(8) uint64_t q_full, q_free, slot_full[kSlots], slot_free[kSlots],
       s_full[kSBufs], s_free[kSBufs], p_full[kSlots], pv_done[kSlots], q_raw, o_full, o_free,
-      m_final[2][4], sums_full, epi_done, drain_bar[3];
+      m_final[2][4], sums_full, epi_done, drain_bar[3], raw_full[kRaw], raw_free[kRaw];
   __shared__ PlanView view;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
-  __shared__ float page_scale_sh[kSlots], q_scale_sh[kTileRows];
+  __shared__ float page_scale_sh[kSlots], q_scale_sh[kTileRows], raw_scale_sh[kRaw];
   __shared__ float alpha_sh[2][kTileRows], m_sh[kTileRows];
   __shared__ __align__(16) float inv_sh[8][kTileRows];
   __shared__ float l_sh[2][kTileRows], l_r_sh[2][kTileRows], m_l_sh[2][kTileRows];
@@ -205,17 +234,24 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
   const int TH = P.T * P.H;
   const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sSlot0 = sQ + kQBox8;
+  const uint32_t sRaw0 = sSlot0 + kSlots * kSlot;
+  constexpr uint32_t kSlotWriters = kFp4 ? 4 : 1;
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&q_full), 12);
     mbar_init(smem_u32(&q_free), 1 + 8);  // QK^T, and the softmax warps (the rows' scales)
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(smem_u32(&slot_full[i]), 1);
+      mbar_init(smem_u32(&slot_full[i]), kSlotWriters);
       mbar_init(smem_u32(&slot_free[i]), 2);
       mbar_init(smem_u32(&p_full[i]), 4);
       mbar_init(smem_u32(&pv_done[i]), 2);
     }
     mbar_init(smem_u32(&q_raw), 1);
+    if constexpr (kFp4)
+      for (int i = 0; i < kRaw; ++i) {
+        mbar_init(smem_u32(&raw_full[i]), 1);
+        mbar_init(smem_u32(&raw_free[i]), 4);
+      }
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
       mbar_init(smem_u32(&s_free[i]), 4);
@@ -228,8 +264,10 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
     for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&drain_bar[i]), 1);
     abort_sh = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tm_lat);
-    tma_prefetch_desc(&tm_rope);
+    if constexpr (!kFp4) {
+      tma_prefetch_desc(&tm_lat);
+      tma_prefetch_desc(&tm_rope);
+    }
     tma_prefetch_desc(&tm_q);
   }
   griddep_wait();
@@ -260,7 +298,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
     // time, a block ahead, so that those dependent loads are off the path from
     // a free box to its copy (looked up page by page they bounded the kernel,
     // at 1,700 cycles a page, together with eight more copies and prefetches).
-    int ring = 0, n = 0;  // slots filled, pieces
+    int ring = 0, n = 0, raw = 0;  // slots filled, pieces, pages of the 4-bit cache
     bool ok = true;
     while (ok && walk.next(P, view, pc)) {
       const int nc = pc.pend - pc.pbeg;
@@ -291,8 +329,8 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
                                        &abort_sh, P.status);
         if (ok) {
           // (Every fill of a slot is a phase of its barrier.)
-          mbar_arrive(smem_u32(&slot_full[ring % kSlots]));
-          mbar_arrive(smem_u32(&slot_full[(ring + 1) % kSlots]));
+          mbar_arrive_n(smem_u32(&slot_full[ring % kSlots]), kSlotWriters);
+          mbar_arrive_n(smem_u32(&slot_full[(ring + 1) % kSlots]), kSlotWriters);
           mbar_expect_tx(smem_u32(&q_raw), kBoxes * P.q_box_rows * 128);
           for (int j = 0; j < kBoxes; ++j)
             tma_load_2d(sSlot0 + ((ring + j / kBoxes8) % kSlots) * kSlot + (j % kBoxes8) * kBox,
@@ -312,7 +350,19 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
         }
         const int page = __shfl_sync(0xffffffffu, pg, i & 31);
         const float scale = __shfl_sync(0xffffffffu, sc, i & 31);
-        if (lane == 0) {
+        if (kFp4 && lane == 0) {
+          const int s = raw % kRaw, u = raw / kRaw;
+          ok = u == 0 || mbar_wait(smem_u32(&raw_free[s]), (u - 1) & 1, &abort_sh, P.status);
+          if (ok) {
+            *static_cast<volatile float*>(&raw_scale_sh[s]) = scale;
+            const uint32_t fb = smem_u32(&raw_full[s]);
+            mbar_expect_tx(fb, kPageBytes4);
+            bulk_load(sRaw0 + s * kPageBytes4, P.kv4 + static_cast<size_t>(page) * kPageBytes4,
+                      kPageBytes4, fb);
+            ++raw;
+          }
+        }
+        if (!kFp4 && lane == 0) {
           const int s = ring % kSlots, u = ring / kSlots;
           ok = u == 0 || mbar_wait(smem_u32(&slot_free[s]), (u - 1) & 1, &abort_sh, P.status);
           if (ok) {
@@ -331,9 +381,16 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
     if (lane == 0) {
       // Every copy lands before the CTA exits, after an abort too.
       if (n > 0) mbar_wait_drain(smem_u32(&q_raw), (n - 1) & 1, P.status);
-      for (int s = 0; s < kSlots; ++s) {
-        const int k = (ring - s + kSlots - 1) / kSlots;  // fills of slot s
-        if (k > 0) mbar_wait_drain(smem_u32(&slot_full[s]), (k - 1) & 1, P.status);
+      if constexpr (kFp4) {
+        for (int s = 0; s < kRaw; ++s) {
+          const int k = (raw - s + kRaw - 1) / kRaw;
+          if (k > 0) mbar_wait_drain(smem_u32(&raw_full[s]), (k - 1) & 1, P.status);
+        }
+      } else {
+        for (int s = 0; s < kSlots; ++s) {
+          const int k = (ring - s + kSlots - 1) / kSlots;  // fills of slot s
+          if (k > 0) mbar_wait_drain(smem_u32(&slot_full[s]), (k - 1) & 1, P.status);
+        }
       }
     }
   } else if (warp < 4) {
@@ -552,6 +609,61 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
           if (threadIdx.x == 12 * 32) {
             mbar_arrive_n(smem_u32(&slot_free[(g + 2 * n) % kSlots]), 2);
             mbar_arrive_n(smem_u32(&slot_free[(g + 2 * n + 1) % kSlots]), 2);
+          }
+          if constexpr (kFp4) {
+            // The piece's pages, from E2M1 to E4M3 codes.  This thread has a row's
+            // columns 256 half .. + 255 and a half of its RoPE codes.  (Lanes are rows:
+            // 336 bytes are 21 x 16, so that loads and swizzled stores of 16 bytes meet
+            // no bank conflict.)
+            const int t = threadIdx.x - 12 * 32, row = t & 63, half = t >> 6;
+            bool ok = true;
+            for (int i = pc.pbeg; i < pc.pend; ++i) {
+              const int at = g + i - pc.pbeg, ring = at + 2 * (n + 1), s = ring % kSlots;
+              const int r = at % kRaw;
+              ok = mbar_wait(smem_u32(&raw_full[r]), (at / kRaw) & 1, &abort_sh, P.status) &&
+                   (ring < kSlots || mbar_wait(smem_u32(&slot_free[s]), (ring / kSlots - 1) & 1,
+                                               &abort_sh, P.status));
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              const uint32_t src = sRaw0 + r * kPageBytes4 + row * kRow4;
+              const uint32_t dst = sSlot0 + s * kSlot + row * 128;
+              const uint2 exps = ld_shared_v2(src + kRowExps4 + 8 * half);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {  // 32 columns
+                const uint4 w = ld_shared_v4(src + 128 * half + 16 * j);
+                const uint32_t e2 = (j < 4 ? exps.x : exps.y) >> (8 * (j & 3));
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {  // a block
+                  const uint2 lut = e4m3_sizes((e2 >> (4 * k)) & 15u);
+                  uint32_t o[4];
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    const uint32_t x = k ? (h ? w.w : w.z) : (h ? w.y : w.x);
+                    const uint32_t sel = x & 0x77777777u, low = x << 4;
+                    o[2 * h] = e4m3_of(lut, sel, __byte_perm(low, x, 0x5140));
+                    o[2 * h + 1] = e4m3_of(lut, sel >> 16, __byte_perm(low, x, 0x7362));
+                  }
+                  const int chunk = 2 * (j & 3) + k;
+                  st_shared_v4(dst + (2 * half + (j >> 2)) * kBox + ((chunk ^ (row & 7)) << 4),
+                               o[0], o[1], o[2], o[3]);
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint4 w = ld_shared_v4(src + kRowRope4 + 32 * half + 16 * k);
+                st_shared_v4(dst + kRopeBox8 * kBox + (((2 * half + k) ^ (row & 7)) << 4), w.x,
+                             w.y, w.z, w.w);
+              }
+              if (t == 0) *static_cast<volatile float*>(&page_scale_sh[s]) =
+                  *static_cast<volatile float*>(&raw_scale_sh[r]);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                mbar_arrive(smem_u32(&slot_full[s]));
+                mbar_arrive(smem_u32(&raw_free[r]));
+              }
+            }
+            if (!ok) break;
           }
           g += pc.pend - pc.pbeg;
           ++n;
@@ -835,7 +947,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
 }  // namespace
 
 cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm_rope,
-                                const CUtensorMap& tm_q, int sm_count,
+                                const CUtensorMap& tm_q, const uint8_t* kv4, int sm_count,
                                 const int32_t* block_table, const float* kv_scale,
                                 const int32_t* seq_len_eff, const PlanHeader* header, void* ws,
                                 const int32_t* seq_first, const int32_t* seq_nsplit,
@@ -844,9 +956,12 @@ cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm
                                 int num_pages, float scale, cudaStream_t st) {
   Params P{};
   const DecodeShape shape = decode_shape(T, H, sm_count);
+  const auto kern = kv4 ? decode_fp8kv_kernel<true> : decode_fp8kv_kernel<false>;
+  const int smem = smem_bytes(kv4 != nullptr);
   const cudaError_t e = cudaFuncSetAttribute(
-      decode_fp8kv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
+  P.kv4 = kv4;
   P.block_table = block_table;
   P.kv_scale = kv_scale;
   P.seq_len_eff = seq_len_eff;
@@ -867,8 +982,8 @@ cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm
   P.tpg = shape.tpg;
   P.sets = shape.sets;
   P.scale_log2 = scale * 1.4426950408889634f;
-  return launch_pdl(decode_fp8kv_kernel, dim3(shape.groups * shape.tpg), dim3(kThreads),
-                    kSmemBytes, st, tm_lat, tm_rope, tm_q, P);
+  return launch_pdl(kern, dim3(shape.groups * shape.tpg), dim3(kThreads), smem, st, tm_lat, tm_rope,
+                    tm_q, P);
 }
 
 }  // namespace mla
