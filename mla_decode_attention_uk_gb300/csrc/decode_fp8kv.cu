@@ -63,6 +63,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "fp4kv.cuh"
 #include "fp8kv.cuh"
@@ -74,7 +76,20 @@ int decode_q_box_rows(int T, int H);
 
 namespace {
 
-constexpr int kThreads = 512;                     // 16 warps
+// 16 warps; over the 4-bit cache 20, which share the registers out anew.
+constexpr int threads(bool fp4) { return fp4 ? 640 : 512; }
+// Registers a thread, by warp group (warps 0-3, 4-11, 12-19): 128 * (56 + 2 * 128 + 2 *
+// 80) of the 640 * 96 that the block is launched with.
+constexpr int kRegsIssue = 56, kRegsSoftmax = 128, kRegsExpand = 80;
+static_assert(kRegsIssue + 2 * kRegsSoftmax + 2 * kRegsExpand <= 5 * 96, "setmaxnreg would wait");
+template <int kRegs>
+__device__ __forceinline__ void fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
 constexpr int kBox = kPage * 128;                 // 64 keys x 128 codes: 8 KB
 constexpr int kSlot = kBoxes8 * kBox;             // 40 KB (the last box half empty)
 constexpr int kMaxSlots = 5;
@@ -179,25 +194,42 @@ struct Pieces {
   }
 };
 
-// Four E2M1 codes (the low halves of a word's first two bytes and their high ones: 16
-// bits of `sel`, without signs) to E4M3 codes of their block, `signs` in the sign bits.
-__device__ __forceinline__ uint32_t e4m3_of(uint2 lut, uint32_t sel, uint32_t signs) {
-  return __byte_perm(lut.x, lut.y, sel) | (signs & 0x80808080u);
-}
 // The E4M3 codes of a block's eight sizes 0 0.5 1 1.5 2 3 4 6 times 2^(e - 8).  Where
-// half of the unit is a normal number of E4M3 (2^-6 and more) an exponent more adds 8
-// to each code but zero's.
+// half of the unit is a normal number of E4M3 (2^-6 and more: e >= 3) an exponent more
+// adds 8 to each code but zero's.
 __device__ __forceinline__ uint2 e4m3_sizes(uint32_t e) {
-  if (e - 3 < 12)
-    return make_uint2(0x14100800u + (e - 3) * 0x08080800u, 0x24201c18u + (e - 3) * 0x08080808u);
+  return make_uint2(0x14100800u - 3u * 0x08080800u + e * 0x08080800u,
+                    0x24201c18u - 3u * 0x08080808u + e * 0x08080808u);
+}
+// Whether that holds for all eight exponents (and none is the NaN block's, 15).
+__device__ __forceinline__ bool usual_exps(uint32_t x) {
+  const uint32_t lo = x & 0x0f0f0f0fu, hi = (x >> 4) & 0x0f0f0f0fu;
+  return ((lo + 0x7d7d7d7du) & (hi + 0x7d7d7d7du) & ~(lo + 0x71717171u) & ~(hi + 0x71717171u) &
+          0x80808080u) == 0x80808080u;
+}
+__device__ __forceinline__ uint2 e4m3_sizes_any(uint32_t e) {
   if (e == 2) return make_uint2(0x0c080400u, 0x1c181410u);
   if (e == 1) return make_uint2(0x06040200u, 0x14100c08u);
   if (e == 0) return make_uint2(0x03020100u, 0x0c080604u);
-  return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+  if (e == kExpNan4) return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
+  return e4m3_sizes(e);
+}
+// A block's 16 E2M1 codes to E4M3 codes: byte selections by the sizes' bits, four at a
+// time, and the signs moved to their bytes (nine instructions for eight values; two
+// conversion instructions a pair, by way of fp16, are twelve).
+__device__ __forceinline__ uint4 e4m3_block(uint2 lut, uint32_t x, uint32_t y) {
+  auto four = [&](uint32_t sel, uint32_t signs) {
+    return __byte_perm(lut.x, lut.y, sel) | (signs & 0x80808080u);
+  };
+  const uint32_t sx = x & 0x77777777u, sy = y & 0x77777777u, lx = x << 4, ly = y << 4;
+  return make_uint4(four(sx, __byte_perm(lx, x, 0x5140)),
+                    four(sx >> 16, __byte_perm(lx, x, 0x7362)),
+                    four(sy, __byte_perm(ly, y, 0x5140)),
+                    four(sy >> 16, __byte_perm(ly, y, 0x7362)));
 }
 
 template <bool kFp4>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads(kFp4), 1)
 decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
                     const __grid_constant__ CUtensorMap tm_rope,
                     const __grid_constant__ CUtensorMap tm_q, Params P) {
@@ -235,7 +267,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
   const uint32_t sQ = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sSlot0 = sQ + kQBox8;
   const uint32_t sRaw0 = sSlot0 + kSlots * kSlot;
-  constexpr uint32_t kSlotWriters = kFp4 ? 4 : 1;
+  constexpr uint32_t kSlotWriters = kFp4 ? 8 : 1;
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&q_full), 12);
@@ -250,7 +282,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
     if constexpr (kFp4)
       for (int i = 0; i < kRaw; ++i) {
         mbar_init(smem_u32(&raw_full[i]), 1);
-        mbar_init(smem_u32(&raw_free[i]), 4);
+        mbar_init(smem_u32(&raw_free[i]), 8);
       }
     for (int i = 0; i < kSBufs; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
@@ -291,7 +323,21 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
   const uint32_t tmem = tmem_base_sh;
   Pieces walk(P, view, gi);
   Piece pc;
+  // One thread's copies of a piece's query tile into slots ring and ring + 1.  (Every
+  // fill of a slot is a phase of its barrier.)
+  auto load_query = [&](const Piece& piece, int ring) {
+    const int row = piece.b * TH + ((piece.task % sets) * tpg + ti) * kTileRows;
+    mbar_arrive_n(smem_u32(&slot_full[ring % kSlots]), kSlotWriters);
+    mbar_arrive_n(smem_u32(&slot_full[(ring + 1) % kSlots]), kSlotWriters);
+    mbar_expect_tx(smem_u32(&q_raw), kBoxes * P.q_box_rows * 128);
+    for (int j = 0; j < kBoxes; ++j)
+      tma_load_2d(sSlot0 + ((ring + j / kBoxes8) % kSlots) * kSlot + (j % kBoxes8) * kBox, &tm_q,
+                  j * kBoxCols, row, smem_u32(&q_raw));
+  };
 
+  if constexpr (kFp4) {
+    if (warp < 4) fewer_regs<kRegsIssue>();
+  }
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     // Lane 0 issues the copies.  The lanes look pages and scales up 32 at a
@@ -318,29 +364,22 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
           scale = 1.0f;
         }
       };
-      // The query tile comes first, through two slots.
-      if (lane == 0) {
-        const int row = pc.b * TH + ((pc.task % sets) * tpg + ti) * kTileRows;
-        // (One tile at a time: the last one's terms are made, so its barrier's
-        // phase is over and seen.)
-        ok = n == 0 || mbar_wait(smem_u32(&q_full), (n - 1) & 1, &abort_sh, P.status);
-        for (int r = ring; r < ring + 2 && ok; ++r)
-          ok = r < kSlots || mbar_wait(smem_u32(&slot_free[r % kSlots]), (r / kSlots - 1) & 1,
-                                       &abort_sh, P.status);
-        if (ok) {
-          // (Every fill of a slot is a phase of its barrier.)
-          mbar_arrive_n(smem_u32(&slot_full[ring % kSlots]), kSlotWriters);
-          mbar_arrive_n(smem_u32(&slot_full[(ring + 1) % kSlots]), kSlotWriters);
-          mbar_expect_tx(smem_u32(&q_raw), kBoxes * P.q_box_rows * 128);
-          for (int j = 0; j < kBoxes; ++j)
-            tma_load_2d(sSlot0 + ((ring + j / kBoxes8) % kSlots) * kSlot + (j % kBoxes8) * kBox,
-                        &tm_q, j * kBoxCols, row, smem_u32(&q_raw));
+      if constexpr (!kFp4) {
+        // The query tile comes first, through two slots.
+        if (lane == 0) {
+          // (One tile at a time: the last one's terms are made, so its barrier's
+          // phase is over and seen.)
+          ok = n == 0 || mbar_wait(smem_u32(&q_full), (n - 1) & 1, &abort_sh, P.status);
+          for (int r = ring; r < ring + 2 && ok; ++r)
+            ok = r < kSlots || mbar_wait(smem_u32(&slot_free[r % kSlots]), (r / kSlots - 1) & 1,
+                                         &abort_sh, P.status);
+          if (ok) load_query(pc, ring);
         }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        ring += 2;
+        ++n;
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      ring += 2;
-      ++n;
       look(lane, pg_next, sc_next);
       for (int i = 0; i < nc; ++i, ++ring) {
         if ((i & 31) == 0) {
@@ -380,7 +419,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
     }
     if (lane == 0) {
       // Every copy lands before the CTA exits, after an abort too.
-      if (n > 0) mbar_wait_drain(smem_u32(&q_raw), (n - 1) & 1, P.status);
+      if (!kFp4 && n > 0) mbar_wait_drain(smem_u32(&q_raw), (n - 1) & 1, P.status);
       if constexpr (kFp4) {
         for (int s = 0; s < kRaw; ++s) {
           const int k = (raw - s + kRaw - 1) / kRaw;
@@ -473,189 +512,212 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
       mbar_wait_drain(db, 0, P.status);
     }
   } else {
-    // ------------------------------------------------------------ query terms
-    // Warps 12-15 turn the query tile into its terms, warp 12 + w tile rows 16 w
-    // .. + 15, between the end of a piece's QK^T and that of its epilogue.  (A
-    // kernel of its own took 3 to 14 us; the softmax warps' help, between their
-    // last page and the epilogue, made the step slower: 138 -> 144 us on 128
-    // sequences x 128 heads; making the terms in place before QK^T's end and
-    // copying them after it too: 146.)  A CTA's first piece waits for its terms,
-    // so all twelve warps make them.
-    //
-    // Lane layout of TMEM loads and stores of 16 lanes x 64 bits: this thread has
-    // row rig of the quarter's 16, and the words (four codes) or keys of parity
-    // par.
-    const int wq = warp & 3;
-    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
-    const int rig = (lane >> 2) + 8 * (lane & 1);
-    const int par = (lane >> 1) & 1;
-    const int srow = 16 * wq + rig;
-    const bool softmax = warp < 12;
-    int g = 0, n = 0;
-    bool fail = false;
-    bool have = walk.next(P, view, pc);
-    while (!fail && have) {
-      if (n == 0 || !softmax) {
-        // Where columns 64 block + 8 j + 4 half .. + 3 of a row are: four bf16
-        // values, or in their place a word of hi codes and one of mid codes.
-        auto word = [&](int row, int block, int j, int half) {
-          const int ring = g + 2 * n + (block >= kBoxes8 ? 1 : 0);
-          return sSlot0 + (ring % kSlots) * kSlot + (block % kBoxes8) * kBox + row * 128 +
-                 ((j ^ (row & 7)) << 4) + 8 * half;
-        };
-        const int rows_here = min(kTileRows, TH - ((pc.task % sets) * tpg + ti) * kTileRows);
-        bool ok = mbar_wait(smem_u32(&q_raw), n & 1, &abort_sh, P.status);
-        int e = 0;
-        float amax = 0.0f;
-        if (n == 0) {
-          // All warps share the rows out, whatever TMEM lanes they belong to (16
-          // heads would leave three quarters of the SM idle else), and make the
-          // terms in place.
-          for (int row = warp - 4; row < rows_here; row += 12) {
-            uint2 x[5];  // words lane, lane + 32, ... of the row's 144
-            __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
-#pragma unroll
-            for (int i = 0; i < 5; ++i) {
-              const int w = lane + 32 * i;
-              x[i] = make_uint2(0u, 0u);
-              if (i < 4 || lane < 16) x[i] = ld_shared_v2(word(row, w >> 4, (w >> 1) & 7, w & 1));
-              top = max_abs(max_abs(top, x[i].x), x[i].y);
-            }
-            const float amax =
-                __uint_as_float(__reduce_max_sync(0xffffffffu, larger_half(top)));
-            const int er = term_exp(amax);
-            const __nv_bfloat162 down = term_factor(er);
-            if (er > kTermExpMax)
-#pragma unroll
-              for (int i = 0; i < 5; ++i) x[i] = lower_terms(x[i], er);
-            if (lane == 0) q_scale_sh[row] = row_scale(amax, er);
-#pragma unroll
-            for (int i = 0; i < 5; ++i) {
-              const int w = lane + 32 * i;
-              uint32_t hi, mid;
-              split_terms(x[i], down, hi, mid);
-              if (i < 4 || lane < 16) st_shared_v2(word(row, w >> 4, (w >> 1) & 7, w & 1), hi, mid);
-            }
+    // Warps 4-11, the softmax's, and the others behind them.
+    auto compute = [&](const auto softmax) {
+      using Role = std::decay_t<decltype(softmax)>;
+      if constexpr (std::is_same_v<Role, std::true_type>) more_regs<kRegsSoftmax>();
+      if constexpr (std::is_same_v<Role, std::false_type>) fewer_regs<kRegsExpand>();
+      // ------------------------------------------------------------ query terms
+      // Warps 12-15 turn the query tile into its terms, warp 12 + w tile rows 16 w
+      // .. + 15, between the end of a piece's QK^T and that of its epilogue.  (A
+      // kernel of its own took 3 to 14 us; the softmax warps' help, between their
+      // last page and the epilogue, made the step slower: 138 -> 144 us on 128
+      // sequences x 128 heads; making the terms in place before QK^T's end and
+      // copying them after it too: 146.)  A CTA's first piece waits for its terms,
+      // so all twelve warps make them.
+      //
+      // Lane layout of TMEM loads and stores of 16 lanes x 64 bits: this thread has
+      // row rig of the quarter's 16, and the words (four codes) or keys of parity
+      // par.
+      const int wq = warp & 3;
+      const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+      const int rig = (lane >> 2) + 8 * (lane & 1);
+      const int par = (lane >> 1) & 1;
+      const int srow = 16 * wq + rig;
+      int g = 0, n = 0;
+      bool fail = false;
+      int tiles = 0;  // that this thread has loaded
+      bool have = walk.next(P, view, pc);
+      while (!fail && have) {
+        if (kFp4 && !softmax) {
+          // Warp 12 loads the piece's query tile: a thread that fills slots sees every
+          // phase of theirs, or a wait for a phase may meet the one before the last.
+          // (So all of these warps wait here.)
+          bool ok = true;
+          for (int r = g + 2 * n; r < g + 2 * n + 2 && ok; ++r)
+            ok = r < kSlots || mbar_wait(smem_u32(&slot_free[r % kSlots]), (r / kSlots - 1) & 1,
+                                         &abort_sh, P.status);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          if (threadIdx.x == 12 * 32) {
+            load_query(pc, g + 2 * n);
+            ++tiles;
           }
-          // (Here and below warps that share a named barrier leave together, or the
-          // others would wait there for one that has given up.)
-          __syncwarp();
-          ok = !bar_any(3, 384, !ok);
-        } else {
-          __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
+        }
+        if ((n == 0 || !softmax) && warp < 16) {
+          // Where columns 64 block + 8 j + 4 half .. + 3 of a row are: four bf16
+          // values, or in their place a word of hi codes and one of mid codes.
+          auto word = [&](int row, int block, int j, int half) {
+            const int ring = g + 2 * n + (block >= kBoxes8 ? 1 : 0);
+            return sSlot0 + (ring % kSlots) * kSlot + (block % kBoxes8) * kBox + row * 128 +
+                   ((j ^ (row & 7)) << 4) + 8 * half;
+          };
+          const int rows_here = min(kTileRows, TH - ((pc.task % sets) * tpg + ti) * kTileRows);
+          bool ok = mbar_wait(smem_u32(&q_raw), n & 1, &abort_sh, P.status);
+          int e = 0;
+          float amax = 0.0f;
+          if (n == 0) {
+            // All warps share the rows out, whatever TMEM lanes they belong to (16
+            // heads would leave three quarters of the SM idle else), and make the
+            // terms in place.
+            for (int row = warp - 4; row < rows_here; row += 12) {
+              uint2 x[5];  // words lane, lane + 32, ... of the row's 144
+              __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
+#pragma unroll
+              for (int i = 0; i < 5; ++i) {
+                const int w = lane + 32 * i;
+                x[i] = make_uint2(0u, 0u);
+                if (i < 4 || lane < 16) x[i] = ld_shared_v2(word(row, w >> 4, (w >> 1) & 7, w & 1));
+                top = max_abs(max_abs(top, x[i].x), x[i].y);
+              }
+              const float amax =
+                  __uint_as_float(__reduce_max_sync(0xffffffffu, larger_half(top)));
+              const int er = term_exp(amax);
+              const __nv_bfloat162 down = term_factor(er);
+              if (er > kTermExpMax)
+#pragma unroll
+                for (int i = 0; i < 5; ++i) x[i] = lower_terms(x[i], er);
+              if (lane == 0) q_scale_sh[row] = row_scale(amax, er);
+#pragma unroll
+              for (int i = 0; i < 5; ++i) {
+                const int w = lane + 32 * i;
+                uint32_t hi, mid;
+                split_terms(x[i], down, hi, mid);
+                if (i < 4 || lane < 16) st_shared_v2(word(row, w >> 4, (w >> 1) & 7, w & 1), hi, mid);
+              }
+            }
+            // (Here and below warps that share a named barrier leave together, or the
+            // others would wait there for one that has given up.)
+            __syncwarp();
+            ok = !bar_any(3, 384, !ok);
+          } else {
+            __nv_bfloat162 top = __float2bfloat162_rn(0.0f);
 #pragma unroll 1
-          for (int block = 0; block < kBoxes; ++block)
+            for (int block = 0; block < kBoxes; ++block)
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const uint2 x = ld_shared_v2(word(srow, block, j, par));
+                top = max_abs(max_abs(top, x.x), x.y);
+              }
+            const uint32_t t = larger_half(top);
+            amax = __uint_as_float(max(t, __shfl_xor_sync(0xffffffffu, t, 2)));
+            e = term_exp(amax);
+            // A loop of its own, as it is rare (rows past the last hold anything).
+            const bool lower = srow < rows_here && e > kTermExpMax;
+            if (__any_sync(0xffffffffu, lower))
+#pragma unroll 1
+              for (int w = 0; w < 8 * kBoxes; ++w) {
+                const uint32_t at = word(srow, w >> 3, w & 7, par);
+                if (lower) {
+                  const uint2 x = lower_terms(ld_shared_v2(at), e);
+                  st_shared_v2(at, x.x, x.y);
+                }
+              }
+            ok = ok && mbar_wait(smem_u32(&q_free), (n - 1) & 1, &abort_sh, P.status);
+          }
+          const __nv_bfloat162 down = term_factor(e);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc_fence_after();
+          if (par == 0 && n > 0) q_scale_sh[srow] = row_scale(amax, e);
+          const int b0 = n == 0 ? 3 * ((warp - 4) >> 2) : 0, b1 = n == 0 ? b0 + 3 : kBoxes;
+#pragma unroll 1
+          for (int block = b0; block < b1; ++block) {
+            uint32_t hi[8], mid[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               const uint2 x = ld_shared_v2(word(srow, block, j, par));
-              top = max_abs(max_abs(top, x.x), x.y);
+              hi[j] = x.x;
+              mid[j] = x.y;
             }
-          const uint32_t t = larger_half(top);
-          amax = __uint_as_float(max(t, __shfl_xor_sync(0xffffffffu, t, 2)));
-          e = term_exp(amax);
-          // A loop of its own, as it is rare (rows past the last hold anything).
-          const bool lower = srow < rows_here && e > kTermExpMax;
-          if (__any_sync(0xffffffffu, lower))
-#pragma unroll 1
-            for (int w = 0; w < 8 * kBoxes; ++w) {
-              const uint32_t at = word(srow, w >> 3, w & 7, par);
-              if (lower) {
-                const uint2 x = lower_terms(ld_shared_v2(at), e);
-                st_shared_v2(at, x.x, x.y);
+            if (n > 0)
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                split_terms(make_uint2(hi[j], mid[j]), down, hi[j], mid[j]);
+            if (block < kLatBoxes) {
+              const uint32_t ta = tmem + lane_off + kTmemQ + 16 * block;
+              tmem_st_16x64b_x8(ta, hi);
+              tmem_st_16x64b_x8(ta + (16u << 16), mid);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {  // word 2 j + par (row + 16: the same swizzle)
+                const uint32_t a = sQ + (32 * wq + rig) * 128 +
+                                   (((j >> 1) ^ (rig & 7)) << 4) + 8 * (j & 1) + 4 * par;
+                st_shared_b32(a, hi[j]);
+                st_shared_b32(a + 16 * 128, mid[j]);
               }
             }
-          ok = ok && mbar_wait(smem_u32(&q_free), (n - 1) & 1, &abort_sh, P.status);
-        }
-        const __nv_bfloat162 down = term_factor(e);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc_fence_after();
-        if (par == 0 && n > 0) q_scale_sh[srow] = row_scale(amax, e);
-        const int b0 = n == 0 ? 3 * ((warp - 4) >> 2) : 0, b1 = n == 0 ? b0 + 3 : kBoxes;
-#pragma unroll 1
-        for (int block = b0; block < b1; ++block) {
-          uint32_t hi[8], mid[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint2 x = ld_shared_v2(word(srow, block, j, par));
-            hi[j] = x.x;
-            mid[j] = x.y;
           }
-          if (n > 0)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              split_terms(make_uint2(hi[j], mid[j]), down, hi[j], mid[j]);
-          if (block < kLatBoxes) {
-            const uint32_t ta = tmem + lane_off + kTmemQ + 16 * block;
-            tmem_st_16x64b_x8(ta, hi);
-            tmem_st_16x64b_x8(ta + (16u << 16), mid);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {  // word 2 j + par (row + 16: the same swizzle)
-              const uint32_t a = sQ + (32 * wq + rig) * 128 +
-                                 (((j >> 1) ^ (rig & 7)) << 4) + 8 * (j & 1) + 4 * par;
-              st_shared_b32(a, hi[j]);
-              st_shared_b32(a + 16 * 128, mid[j]);
+          tmem_wait_st();
+          tc_fence_before();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_n(smem_u32(&q_full), n == 0 ? 1 : 3);
+          if (!softmax) {
+            // Everyone is done with the tile: its slots are free.
+            if (warp == 12 && !mbar_wait(smem_u32(&q_full), n & 1, &abort_sh, P.status)) break;
+            if (threadIdx.x == 12 * 32) {
+              mbar_arrive_n(smem_u32(&slot_free[(g + 2 * n) % kSlots]), 2);
+              mbar_arrive_n(smem_u32(&slot_free[(g + 2 * n + 1) % kSlots]), 2);
             }
           }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_n(smem_u32(&q_full), n == 0 ? 1 : 3);
         if (!softmax) {
-          // Everyone is done with the tile: its slots are free.
-          if (warp == 12 && !mbar_wait(smem_u32(&q_full), n & 1, &abort_sh, P.status)) break;
-          if (threadIdx.x == 12 * 32) {
-            mbar_arrive_n(smem_u32(&slot_free[(g + 2 * n) % kSlots]), 2);
-            mbar_arrive_n(smem_u32(&slot_free[(g + 2 * n + 1) % kSlots]), 2);
-          }
           if constexpr (kFp4) {
-            // The piece's pages, from E2M1 to E4M3 codes.  This thread has a row's
-            // columns 256 half .. + 255 and a half of its RoPE codes.  (Lanes are rows:
-            // 336 bytes are 21 x 16, so that loads and swizzled stores of 16 bytes meet
-            // no bank conflict.)
-            const int t = threadIdx.x - 12 * 32, row = t & 63, half = t >> 6;
+            // The piece's pages, from E2M1 to E4M3 codes.  This thread has a box of a row
+            // (128 columns) and a quarter of its RoPE codes.  (Lanes are rows: 336 bytes
+            // are 21 x 16, so that loads and swizzled stores of 16 bytes meet no bank
+            // conflict.)
+            const int t = threadIdx.x - 12 * 32, row = t & 63, box = t >> 6;
+            const uint32_t swizzle = (row & 7) << 4;
+            uint8_t* const slot_pages = smem_raw + (sSlot0 - smem_u32(smem_raw)) + row * 128;
+            const uint8_t* const raw_pages = smem_raw + (sRaw0 - smem_u32(smem_raw)) + row * kRow4;
             bool ok = true;
+#pragma unroll 1
             for (int i = pc.pbeg; i < pc.pend; ++i) {
               const int at = g + i - pc.pbeg, ring = at + 2 * (n + 1), s = ring % kSlots;
               const int r = at % kRaw;
-              ok = mbar_wait(smem_u32(&raw_full[r]), (at / kRaw) & 1, &abort_sh, P.status) &&
-                   (ring < kSlots || mbar_wait(smem_u32(&slot_free[s]), (ring / kSlots - 1) & 1,
-                                               &abort_sh, P.status));
-              ok = __all_sync(0xffffffffu, ok);
+              ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&raw_full[r]), (at / kRaw) & 1,
+                                                     &abort_sh, P.status));
               if (!ok) break;
-              const uint32_t src = sRaw0 + r * kPageBytes4 + row * kRow4;
-              const uint32_t dst = sSlot0 + s * kSlot + row * 128;
-              const uint2 exps = ld_shared_v2(src + kRowExps4 + 8 * half);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {  // 32 columns
-                const uint4 w = ld_shared_v4(src + 128 * half + 16 * j);
-                const uint32_t e2 = (j < 4 ? exps.x : exps.y) >> (8 * (j & 3));
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {  // a block
-                  const uint2 lut = e4m3_sizes((e2 >> (4 * k)) & 15u);
-                  uint32_t o[4];
-#pragma unroll
-                  for (int h = 0; h < 2; ++h) {
-                    const uint32_t x = k ? (h ? w.w : w.z) : (h ? w.y : w.x);
-                    const uint32_t sel = x & 0x77777777u, low = x << 4;
-                    o[2 * h] = e4m3_of(lut, sel, __byte_perm(low, x, 0x5140));
-                    o[2 * h + 1] = e4m3_of(lut, sel >> 16, __byte_perm(low, x, 0x7362));
-                  }
-                  const int chunk = 2 * (j & 3) + k;
-                  st_shared_v4(dst + (2 * half + (j >> 2)) * kBox + ((chunk ^ (row & 7)) << 4),
-                               o[0], o[1], o[2], o[3]);
+              ok = __all_sync(0xffffffffu,
+                              ring < kSlots ||
+                                  mbar_wait(smem_u32(&slot_free[s]), (ring / kSlots - 1) & 1,
+                                            &abort_sh, P.status));
+              if (!ok) break;
+              const uint8_t* const src = raw_pages + r * kPageBytes4;
+              uint8_t* const dst = slot_pages + s * kSlot;
+              uint32_t exps = *reinterpret_cast<const uint32_t*>(src + kRowExps4 + 4 * box);
+              const uint4 rope = *reinterpret_cast<const uint4*>(src + kRowRope4 + 16 * box);
+              const bool usual = usual_exps(exps);
+              // (Not unrolled: instructions that run once a page take longer to fetch
+              // than to execute: 63 us instead of 49 on 64 x 4,096 tokens x 16 heads.)
+#pragma unroll 1
+              for (int j = 0; j < 4; ++j) {  // 32 columns, two blocks
+                const uint4 x = *reinterpret_cast<const uint4*>(src + 64 * box + 16 * j);
+                uint2 l0 = e4m3_sizes(exps & 15u), l1 = e4m3_sizes((exps >> 4) & 15u);
+                if (!usual) {
+                  l0 = e4m3_sizes_any(exps & 15u);
+                  l1 = e4m3_sizes_any((exps >> 4) & 15u);
                 }
+                exps >>= 8;
+                uint8_t* const to = dst + box * kBox;
+                const uint32_t chunk = (j << 5) ^ swizzle;
+                *reinterpret_cast<uint4*>(to + chunk) = e4m3_block(l0, x.x, x.y);
+                *reinterpret_cast<uint4*>(to + (chunk ^ 16u)) = e4m3_block(l1, x.z, x.w);
               }
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint4 w = ld_shared_v4(src + kRowRope4 + 32 * half + 16 * k);
-                st_shared_v4(dst + kRopeBox8 * kBox + (((2 * half + k) ^ (row & 7)) << 4), w.x,
-                             w.y, w.z, w.w);
-              }
-              if (t == 0) *static_cast<volatile float*>(&page_scale_sh[s]) =
-                  *static_cast<volatile float*>(&raw_scale_sh[r]);
+              *reinterpret_cast<uint4*>(dst + kRopeBox8 * kBox + ((box << 4) ^ swizzle)) = rope;
+              if (t == 0)
+                *static_cast<volatile float*>(&page_scale_sh[s]) =
+                    *static_cast<volatile float*>(&raw_scale_sh[r]);
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
@@ -670,270 +732,278 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
           have = walk.next(P, view, pc);
           continue;
         }
-      }
-      // ---------------------------------------------------------- softmax + epilogue
-      // Two groups of four warps take turns: group q has the pages g with g mod 2
-      // = q, and S buffer q.  A warp has the rows of its TMEM lane quarter; this
-      // thread row srow of the tile (its hi term in lane rig of the quarter, its
-      // mid term in lane 16 + rig) and keys of parity par.
-      const int q = (warp - 4) >> 2;
-      const bool owner = par == 0;
-      const int row0 = ((pc.task % sets) * tpg + ti) * kTileRows;  // of the sequence's T * H
-      const int rows_here = min(kTileRows, TH - row0);
-      // Where the rows' results go: row of o_lat, or ~row of the partial results.
-      const int dest = P.seq_nsplit[pc.b] > 1
-                           ? ~((P.seq_slot[pc.b] + pc.task / sets - P.seq_first[pc.b]) * TH + row0)
-                           : pc.b * TH + row0;
-      const int n_row = srow < rows_here ? pc.len - P.T + (row0 + srow) / P.H + 1 : 0;
-      // The running maximum of a row is m_sh (one group raises it, the other
-      // finds it raised); m_mine is the one that this thread's sums are in.
-      float m_mine = -INFINITY;
-      // The last piece's epilogue has read m_sh and the sums; the query is there.
-      bool bad = (n > 0 && !mbar_wait(smem_u32(&epi_done), (n - 1) & 1, &abort_sh, P.status)) ||
-                 !mbar_wait(smem_u32(&q_full), n & 1, &abort_sh, P.status);
-      const float q_scale = q_scale_sh[srow] * P.scale_log2;
-      // This thread's shares of the row's sums: exact, as rounded.  NaN from the
-      // start where the query is not finite, whatever its codes give.
-      float l = 0.0f * q_scale, l_r = l;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&q_free));
-      for (int i = pc.pbeg; i < pc.pend; ++i, ++g) {
-        if ((g & 1) != q) continue;
-        const int ring = g + 2 * (n + 1), s = ring % kSlots;
-        // (The page has landed, QK^T has read it; its barrier orders the
-        // producer's page_scale_sh.)
-        bad = bad || !mbar_wait(smem_u32(&s_full[q]), (g >> 1) & 1, &abort_sh, P.status) ||
-              !mbar_wait(smem_u32(&slot_full[s]), (ring / kSlots) & 1, &abort_sh, P.status);
-        bad = __any_sync(0xffffffffu, bad);
-        const float page_scale = *static_cast<volatile float*>(&page_scale_sh[s]);
-        uint32_t v[32];  // v[j]: key kb + 2 j
-        if (!bad) {
-          tc_fence_after();
-          tmem_ld_16x64b_x32(tmem + lane_off + 64 * q, v);
+        // ---------------------------------------------------------- softmax + epilogue
+        // Two groups of four warps take turns: group q has the pages g with g mod 2
+        // = q, and S buffer q.  A warp has the rows of its TMEM lane quarter; this
+        // thread row srow of the tile (its hi term in lane rig of the quarter, its
+        // mid term in lane 16 + rig) and keys of parity par.
+        const int q = (warp - 4) >> 2;
+        const bool owner = par == 0;
+        const int row0 = ((pc.task % sets) * tpg + ti) * kTileRows;  // of the sequence's T * H
+        const int rows_here = min(kTileRows, TH - row0);
+        // Where the rows' results go: row of o_lat, or ~row of the partial results.
+        const int dest = P.seq_nsplit[pc.b] > 1
+                             ? ~((P.seq_slot[pc.b] + pc.task / sets - P.seq_first[pc.b]) * TH + row0)
+                             : pc.b * TH + row0;
+        const int n_row = srow < rows_here ? pc.len - P.T + (row0 + srow) / P.H + 1 : 0;
+        // The running maximum of a row is m_sh (one group raises it, the other
+        // finds it raised); m_mine is the one that this thread's sums are in.
+        float m_mine = -INFINITY;
+        // The last piece's epilogue has read m_sh and the sums; the query is there.
+        bool bad = (n > 0 && !mbar_wait(smem_u32(&epi_done), (n - 1) & 1, &abort_sh, P.status)) ||
+                   !mbar_wait(smem_u32(&q_full), n & 1, &abort_sh, P.status);
+        const float q_scale = q_scale_sh[srow] * P.scale_log2;
+        // This thread's shares of the row's sums: exact, as rounded.  NaN from the
+        // start where the query is not finite, whatever its codes give.
+        float l = 0.0f * q_scale, l_r = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&q_free));
+        for (int i = pc.pbeg; i < pc.pend; ++i, ++g) {
+          if ((g & 1) != q) continue;
+          const int ring = g + 2 * (n + 1), s = ring % kSlots;
+          // (The page has landed, QK^T has read it; its barrier orders the
+          // producer's page_scale_sh.)
+          bad = bad || !mbar_wait(smem_u32(&s_full[q]), (g >> 1) & 1, &abort_sh, P.status) ||
+                !mbar_wait(smem_u32(&slot_full[s]), (ring / kSlots) & 1, &abort_sh, P.status);
+          bad = __any_sync(0xffffffffu, bad);
+          const float page_scale = *static_cast<volatile float*>(&page_scale_sh[s]);
+          uint32_t v[32];  // v[j]: key kb + 2 j
+          if (!bad) {
+            tc_fence_after();
+            tmem_ld_16x64b_x32(tmem + lane_off + 64 * q, v);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // (in halves for the registers)
-            uint32_t v2[16];
-            tmem_ld_16x64b_x16(tmem + lane_off + (16u << 16) + 64 * q + 32 * h, v2);
-            tmem_wait_ld();
+            for (int h = 0; h < 2; ++h) {  // (in halves for the registers)
+              uint32_t v2[16];
+              tmem_ld_16x64b_x16(tmem + lane_off + (16u << 16) + 64 * q + 32 * h, v2);
+              tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              v[16 * h + j] = __float_as_uint(fmaf(__uint_as_float(v2[j]), 1.0f / kQMidScale,
-                                                   __uint_as_float(v[16 * h + j])));
+              for (int j = 0; j < 16; ++j)
+                v[16 * h + j] = __float_as_uint(fmaf(__uint_as_float(v2[j]), 1.0f / kQMidScale,
+                                                     __uint_as_float(v[16 * h + j])));
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&s_free[q]));
+          const int kb = i * kPage + par;
+          if (kb + 62 >= n_row) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (kb + 2 * j >= n_row) v[j] = __float_as_uint(-INFINITY);
+          }
+          float a3[11];
+#pragma unroll
+          for (int t = 0; t < 10; ++t)
+            a3[t] = max3(__uint_as_float(v[3 * t]), __uint_as_float(v[3 * t + 1]),
+                         __uint_as_float(v[3 * t + 2]));
+          a3[10] = fmaxf(__uint_as_float(v[30]), __uint_as_float(v[31]));
+          float vmax = fmaxf(max3(max3(a3[0], a3[1], a3[2]), max3(a3[3], a3[4], a3[5]),
+                                  max3(a3[6], a3[7], a3[8])),
+                             fmaxf(a3[9], a3[10]));
+          vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+          // Not zero, so that a hidden key's -inf times it stays -inf (a
+          // product below 2^-100 is 0 to the exponent either way).
+          const float mul = fmaxf(q_scale * page_scale, 7.9e-31f);
+          const float shift = __log2f(page_scale);
+          const float pmax = fmaf(vmax, mul, shift);
+          // The page before, the other group's, is through with the maximum.
+          if (g > 0)
+            bad = !mbar_wait(smem_u32(&m_final[q ^ 1][wq]), ((g - 1) >> 1) & 1, &abort_sh,
+                             P.status) || bad;
+          const bool first = i == pc.pbeg;
+          const float m_old = first ? -INFINITY : m_sh[srow];
+          const bool raise = pmax > m_old + kRaise;
+          const float m_used = raise ? pmax : m_old;
+          __syncwarp();
+          if (owner && (raise || first)) m_sh[srow] = m_used;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&m_final[q][wq]));
+          if (m_used != m_mine) {
+            const float f = ex2_approx(m_mine - m_used);
+            l *= f;
+            l_r *= f;
+            m_mine = m_used;
+          }
+          // One barrier of the group per page: a raised maximum (the group then
+          // rescales O^T, rows are its columns), or a wait that gave up.
+          if (bar_any(1 + q, 128, bad || (raise && !first))) {
+            bool f = *static_cast<volatile int*>(&abort_sh) != 0;
+            if (owner) alpha_sh[q][srow] = raise ? ex2_approx(m_old - pmax) : 1.0f;
+            if (!f && !first &&
+                !mbar_wait(smem_u32(&pv_done[(g - 1) % kSlots]), ((g - 1) / kSlots) & 1, &abort_sh,
+                           P.status))
+              f = true;
+            if (bar_any(1 + q, 128, f)) { fail = true; break; }
+            if (!first) {
+              tc_fence_after();
+#pragma unroll 1
+              for (int m = 0; m < 4; ++m) {
+#pragma unroll 1
+                for (int h2 = 0; 16 * h2 < rows_here; ++h2) {
+                  uint32_t vv[16];
+                  const uint32_t ta = tmem + lane_off + kTmemOut + 64 * m + 16 * h2;
+                  tmem_ld_x16(ta, vv);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int j = 0; j < 16; ++j)
+                    vv[j] = __float_as_uint(__uint_as_float(vv[j]) * alpha_sh[q][16 * h2 + j]);
+                  tmem_st_x16(ta, vv);
+                }
+              }
+              tmem_wait_st();
+              tc_fence_before();
+            }
+          }
+          // Codes are the upper bytes of fp16 pairs, four to a word.
+          uint32_t hw[8], mw[8];
+          if (m_used == -INFINITY) {
+#pragma unroll
+            for (int t = 0; t < 8; ++t) hw[t] = mw[t] = 0u;
+            // No key yet, or NaN alone, which a maximum passes over.
+            if (kb < n_row) l = l_r = __uint_as_float(0x7fffffffu);
+          } else {
+            const float add = shift + kTopExp - m_used;
+            float se[4] = {};
+            // What the rounding of this thread's 32 weights adds up to, in fp16: the
+            // terms are exact and at most 2^-7 of a weight, so 16 sums rounded by
+            // 2^-11 move the row's sum, which is fp32, by 2^-14 of it at most.
+            __half2 err = __float2half2_rn(0.0f);
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+              uint32_t hb[2], mb[2];
+#pragma unroll
+              for (int j = 2 * t; j < 2 * t + 2; ++j) {
+                const float p0 = ex2_approx(fmaf(__uint_as_float(v[2 * j]), mul, add));
+                const float p1 = ex2_approx(fmaf(__uint_as_float(v[2 * j + 1]), mul, add));
+                se[(2 * j) & 3] += p0;
+                se[(2 * j + 1) & 3] += p1;
+                const __half2 h = __floats2half2_rn(p0, p1);
+                const __half2 hi = e5m2_in_half2(h);
+                const __half2 mid = e5m2_in_half2(__hsub2(h, hi));
+                err = __hfma2(__hsub2(__hadd2(hi, mid), h),
+                              __hge2(h, __float2half2_rn(kRoundedFrom)), err);
+                hb[j & 1] = bits(hi);
+                mb[j & 1] = bits(mid);
+              }
+              hw[t] = __byte_perm(hb[0], hb[1], 0x7531);
+              mw[t] = __byte_perm(mb[0], mb[1], 0x7531);
+            }
+            const float sum = (se[0] + se[1]) + (se[2] + se[3]);
+            const float2 e = __half22float2(err);
+            const float inv_scale = __frcp_rn(page_scale);
+            l = fmaf(sum, inv_scale, l);
+            l_r = fmaf(sum + (e.x + e.y), inv_scale, l_r);
+          }
+          // The even-key thread writes keys 0-31, the odd-key thread keys 32-63:
+          // half of each thread's codes cross to its partner.
+          uint32_t ph[8], pm[8];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const uint32_t keep_h = par ? hw[4 + t] : hw[t], keep_m = par ? mw[4 + t] : mw[t];
+            const uint32_t got_h = __shfl_xor_sync(0xffffffffu, par ? hw[t] : hw[4 + t], 2);
+            const uint32_t got_m = __shfl_xor_sync(0xffffffffu, par ? mw[t] : mw[4 + t], 2);
+            const uint32_t eh = par ? got_h : keep_h, oh = par ? keep_h : got_h;
+            const uint32_t em = par ? got_m : keep_m, om = par ? keep_m : got_m;
+            ph[2 * t] = __byte_perm(eh, oh, 0x5140);
+            ph[2 * t + 1] = __byte_perm(eh, oh, 0x7362);
+            pm[2 * t] = __byte_perm(em, om, 0x5140);
+            pm[2 * t + 1] = __byte_perm(em, om, 0x7362);
+          }
+          // P^T row: 64 bytes of hi codes (chunks 0-3), 64 of mid codes (4-7),
+          // into the page's RoPE box, which QK^T is done with.  Rows r and r + 8
+          // of a quarter-warp's store share their swizzle, so the latter's
+          // threads write mid before hi: eight distinct positions.
+          const uint32_t rowaddr = sSlot0 + s * kSlot + kRopeBox8 * kBox + srow * 128;
+          const bool late = (srow >> 3) & 1;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            const int h4 = 4 * (t & 1);
+            const bool is_mid = (t >= 2) != late;
+            const int chunk = (is_mid ? 4 : 0) + 2 * par + (t & 1);
+            st_shared_v4(rowaddr + ((chunk ^ (srow & 7)) << 4), is_mid ? pm[h4] : ph[h4],
+                         is_mid ? pm[h4 + 1] : ph[h4 + 1], is_mid ? pm[h4 + 2] : ph[h4 + 2],
+                         is_mid ? pm[h4 + 3] : ph[h4 + 3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&p_full[g % kSlots]));
+        }
+        if (fail) break;
+        have = walk.next(P, view, pc);
+
+        // ---------------- epilogue of this piece, a half of the columns each
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        l_r += __shfl_xor_sync(0xffffffffu, l_r, 2);
+        if (owner) {
+          l_sh[q][srow] = l;
+          l_r_sh[q][srow] = l_r;
+          m_l_sh[q][srow] = m_mine;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sums_full));
+        bad = bad || !mbar_wait(smem_u32(&sums_full), n & 1, &abort_sh, P.status) ||
+              !mbar_wait(smem_u32(&o_full), n & 1, &abort_sh, P.status);
+        __syncwarp();
+        if (bar_any(1 + q, 128, bad)) break;
+        tc_fence_after();
+        const size_t row_base = dest < 0 ? ~dest : dest;
+        __nv_bfloat16* const out = (dest < 0 ? view.opart : P.olat) + row_base * kLora;
+#pragma unroll 1
+        for (int row = lane; row < rows_here; row += 32) {
+          // The row's sums, in its last maximum.
+          const float m = m_sh[row];
+          const float w0 = m_l_sh[0][row] == -INFINITY ? 0.0f : ex2_approx(m_l_sh[0][row] - m);
+          const float w1 = m_l_sh[1][row] == -INFINITY ? 0.0f : ex2_approx(m_l_sh[1][row] - m);
+          const float total_r = fmaf(l_r_sh[0][row], w0, l_r_sh[1][row] * w1);
+          inv_sh[warp - 4][row] = total_r == 0.0f ? 0.0f : 1.0f / total_r;  // (NaN stays NaN)
+          if (q == 0 && wq == 0) {
+            const float total = fmaf(l_sh[0][row], w0, l_sh[1][row] * w1);
+            const float lse2 = total == 0.0f ? -INFINITY : m - kTopExp + __log2f(total);
+            (dest < 0 ? view.lpart : P.lse)[row_base + row] = lse2 * kLn2;
+          }
+        }
+        __syncwarp();
+#pragma unroll 1
+        for (int h = 0; 16 * h < rows_here; ++h) {
+          uint32_t v[2][16];
+          const uint32_t ta = tmem + lane_off + kTmemOut + 128 * q + 16 * h;
+          tmem_ld_x16(ta, v[0]);
+          tmem_ld_x16(ta + 64, v[1]);
+          tmem_wait_ld();
+          // Lane = latent column, v[.][j] = row j.  Of two rows the even lane
+          // stores one and the odd lane the other, two columns each.
+          uint32_t* const dst = reinterpret_cast<uint32_t*>(
+              out + (16 * h + (lane & 1)) * kLora + 256 * q + 32 * wq + (lane & ~1));
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            const float2 il = *reinterpret_cast<const float2*>(&inv_sh[warp - 4][16 * h + j]);
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const float x = __uint_as_float(v[m][j]) * il.x;
+              const float y = __uint_as_float(v[m][j + 1]) * il.y;
+              const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? x : y, 1);
+              dst[j * (kLora / 2) + 64 * m] =
+                  lane & 1 ? pack_bf16x2(got, y) : pack_bf16x2(x, got);
+            }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&s_free[q]));
-        const int kb = i * kPage + par;
-        if (kb + 62 >= n_row) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (kb + 2 * j >= n_row) v[j] = __float_as_uint(-INFINITY);
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&o_free));
+          mbar_arrive(smem_u32(&epi_done));
         }
-        float a3[11];
-#pragma unroll
-        for (int t = 0; t < 10; ++t)
-          a3[t] = max3(__uint_as_float(v[3 * t]), __uint_as_float(v[3 * t + 1]),
-                       __uint_as_float(v[3 * t + 2]));
-        a3[10] = fmaxf(__uint_as_float(v[30]), __uint_as_float(v[31]));
-        float vmax = fmaxf(max3(max3(a3[0], a3[1], a3[2]), max3(a3[3], a3[4], a3[5]),
-                                max3(a3[6], a3[7], a3[8])),
-                           fmaxf(a3[9], a3[10]));
-        vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
-        // Not zero, so that a hidden key's -inf times it stays -inf (a
-        // product below 2^-100 is 0 to the exponent either way).
-        const float mul = fmaxf(q_scale * page_scale, 7.9e-31f);
-        const float shift = __log2f(page_scale);
-        const float pmax = fmaf(vmax, mul, shift);
-        // The page before, the other group's, is through with the maximum.
-        if (g > 0)
-          bad = !mbar_wait(smem_u32(&m_final[q ^ 1][wq]), ((g - 1) >> 1) & 1, &abort_sh,
-                           P.status) || bad;
-        const bool first = i == pc.pbeg;
-        const float m_old = first ? -INFINITY : m_sh[srow];
-        const bool raise = pmax > m_old + kRaise;
-        const float m_used = raise ? pmax : m_old;
-        __syncwarp();
-        if (owner && (raise || first)) m_sh[srow] = m_used;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&m_final[q][wq]));
-        if (m_used != m_mine) {
-          const float f = ex2_approx(m_mine - m_used);
-          l *= f;
-          l_r *= f;
-          m_mine = m_used;
-        }
-        // One barrier of the group per page: a raised maximum (the group then
-        // rescales O^T, rows are its columns), or a wait that gave up.
-        if (bar_any(1 + q, 128, bad || (raise && !first))) {
-          bool f = *static_cast<volatile int*>(&abort_sh) != 0;
-          if (owner) alpha_sh[q][srow] = raise ? ex2_approx(m_old - pmax) : 1.0f;
-          if (!f && !first &&
-              !mbar_wait(smem_u32(&pv_done[(g - 1) % kSlots]), ((g - 1) / kSlots) & 1, &abort_sh,
-                         P.status))
-            f = true;
-          if (bar_any(1 + q, 128, f)) { fail = true; break; }
-          if (!first) {
-            tc_fence_after();
-#pragma unroll 1
-            for (int m = 0; m < 4; ++m) {
-#pragma unroll 1
-              for (int h2 = 0; 16 * h2 < rows_here; ++h2) {
-                uint32_t vv[16];
-                const uint32_t ta = tmem + lane_off + kTmemOut + 64 * m + 16 * h2;
-                tmem_ld_x16(ta, vv);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  vv[j] = __float_as_uint(__uint_as_float(vv[j]) * alpha_sh[q][16 * h2 + j]);
-                tmem_st_x16(ta, vv);
-              }
-            }
-            tmem_wait_st();
-            tc_fence_before();
-          }
-        }
-        // Codes are the upper bytes of fp16 pairs, four to a word.
-        uint32_t hw[8], mw[8];
-        if (m_used == -INFINITY) {
-#pragma unroll
-          for (int t = 0; t < 8; ++t) hw[t] = mw[t] = 0u;
-          // No key yet, or NaN alone, which a maximum passes over.
-          if (kb < n_row) l = l_r = __uint_as_float(0x7fffffffu);
-        } else {
-          const float add = shift + kTopExp - m_used;
-          float se[4] = {};
-          // What the rounding of this thread's 32 weights adds up to, in fp16: the
-          // terms are exact and at most 2^-7 of a weight, so 16 sums rounded by
-          // 2^-11 move the row's sum, which is fp32, by 2^-14 of it at most.
-          __half2 err = __float2half2_rn(0.0f);
-#pragma unroll
-          for (int t = 0; t < 8; ++t) {
-            uint32_t hb[2], mb[2];
-#pragma unroll
-            for (int j = 2 * t; j < 2 * t + 2; ++j) {
-              const float p0 = ex2_approx(fmaf(__uint_as_float(v[2 * j]), mul, add));
-              const float p1 = ex2_approx(fmaf(__uint_as_float(v[2 * j + 1]), mul, add));
-              se[(2 * j) & 3] += p0;
-              se[(2 * j + 1) & 3] += p1;
-              const __half2 h = __floats2half2_rn(p0, p1);
-              const __half2 hi = e5m2_in_half2(h);
-              const __half2 mid = e5m2_in_half2(__hsub2(h, hi));
-              err = __hfma2(__hsub2(__hadd2(hi, mid), h),
-                            __hge2(h, __float2half2_rn(kRoundedFrom)), err);
-              hb[j & 1] = bits(hi);
-              mb[j & 1] = bits(mid);
-            }
-            hw[t] = __byte_perm(hb[0], hb[1], 0x7531);
-            mw[t] = __byte_perm(mb[0], mb[1], 0x7531);
-          }
-          const float sum = (se[0] + se[1]) + (se[2] + se[3]);
-          const float2 e = __half22float2(err);
-          const float inv_scale = __frcp_rn(page_scale);
-          l = fmaf(sum, inv_scale, l);
-          l_r = fmaf(sum + (e.x + e.y), inv_scale, l_r);
-        }
-        // The even-key thread writes keys 0-31, the odd-key thread keys 32-63:
-        // half of each thread's codes cross to its partner.
-        uint32_t ph[8], pm[8];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const uint32_t keep_h = par ? hw[4 + t] : hw[t], keep_m = par ? mw[4 + t] : mw[t];
-          const uint32_t got_h = __shfl_xor_sync(0xffffffffu, par ? hw[t] : hw[4 + t], 2);
-          const uint32_t got_m = __shfl_xor_sync(0xffffffffu, par ? mw[t] : mw[4 + t], 2);
-          const uint32_t eh = par ? got_h : keep_h, oh = par ? keep_h : got_h;
-          const uint32_t em = par ? got_m : keep_m, om = par ? keep_m : got_m;
-          ph[2 * t] = __byte_perm(eh, oh, 0x5140);
-          ph[2 * t + 1] = __byte_perm(eh, oh, 0x7362);
-          pm[2 * t] = __byte_perm(em, om, 0x5140);
-          pm[2 * t + 1] = __byte_perm(em, om, 0x7362);
-        }
-        // P^T row: 64 bytes of hi codes (chunks 0-3), 64 of mid codes (4-7),
-        // into the page's RoPE box, which QK^T is done with.  Rows r and r + 8
-        // of a quarter-warp's store share their swizzle, so the latter's
-        // threads write mid before hi: eight distinct positions.
-        const uint32_t rowaddr = sSlot0 + s * kSlot + kRopeBox8 * kBox + srow * 128;
-        const bool late = (srow >> 3) & 1;
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int h4 = 4 * (t & 1);
-          const bool is_mid = (t >= 2) != late;
-          const int chunk = (is_mid ? 4 : 0) + 2 * par + (t & 1);
-          st_shared_v4(rowaddr + ((chunk ^ (srow & 7)) << 4), is_mid ? pm[h4] : ph[h4],
-                       is_mid ? pm[h4 + 1] : ph[h4 + 1], is_mid ? pm[h4 + 2] : ph[h4 + 2],
-                       is_mid ? pm[h4 + 3] : ph[h4 + 3]);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&p_full[g % kSlots]));
+        ++n;
       }
-      if (fail) break;
-      have = walk.next(P, view, pc);
-
-      // ---------------- epilogue of this piece, a half of the columns each
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      l_r += __shfl_xor_sync(0xffffffffu, l_r, 2);
-      if (owner) {
-        l_sh[q][srow] = l;
-        l_r_sh[q][srow] = l_r;
-        m_l_sh[q][srow] = m_mine;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sums_full));
-      bad = bad || !mbar_wait(smem_u32(&sums_full), n & 1, &abort_sh, P.status) ||
-            !mbar_wait(smem_u32(&o_full), n & 1, &abort_sh, P.status);
-      __syncwarp();
-      if (bar_any(1 + q, 128, bad)) break;
-      tc_fence_after();
-      const size_t row_base = dest < 0 ? ~dest : dest;
-      __nv_bfloat16* const out = (dest < 0 ? view.opart : P.olat) + row_base * kLora;
-#pragma unroll 1
-      for (int row = lane; row < rows_here; row += 32) {
-        // The row's sums, in its last maximum.
-        const float m = m_sh[row];
-        const float w0 = m_l_sh[0][row] == -INFINITY ? 0.0f : ex2_approx(m_l_sh[0][row] - m);
-        const float w1 = m_l_sh[1][row] == -INFINITY ? 0.0f : ex2_approx(m_l_sh[1][row] - m);
-        const float total_r = fmaf(l_r_sh[0][row], w0, l_r_sh[1][row] * w1);
-        inv_sh[warp - 4][row] = total_r == 0.0f ? 0.0f : 1.0f / total_r;  // (NaN stays NaN)
-        if (q == 0 && wq == 0) {
-          const float total = fmaf(l_sh[0][row], w0, l_sh[1][row] * w1);
-          const float lse2 = total == 0.0f ? -INFINITY : m - kTopExp + __log2f(total);
-          (dest < 0 ? view.lpart : P.lse)[row_base + row] = lse2 * kLn2;
-        }
-      }
-      __syncwarp();
-#pragma unroll 1
-      for (int h = 0; 16 * h < rows_here; ++h) {
-        uint32_t v[2][16];
-        const uint32_t ta = tmem + lane_off + kTmemOut + 128 * q + 16 * h;
-        tmem_ld_x16(ta, v[0]);
-        tmem_ld_x16(ta + 64, v[1]);
-        tmem_wait_ld();
-        // Lane = latent column, v[.][j] = row j.  Of two rows the even lane
-        // stores one and the odd lane the other, two columns each.
-        uint32_t* const dst = reinterpret_cast<uint32_t*>(
-            out + (16 * h + (lane & 1)) * kLora + 256 * q + 32 * wq + (lane & ~1));
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-          const float2 il = *reinterpret_cast<const float2*>(&inv_sh[warp - 4][16 * h + j]);
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const float x = __uint_as_float(v[m][j]) * il.x;
-            const float y = __uint_as_float(v[m][j + 1]) * il.y;
-            const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? x : y, 1);
-            dst[j * (kLora / 2) + 64 * m] =
-                lane & 1 ? pack_bf16x2(got, y) : pack_bf16x2(x, got);
-          }
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&o_free));
-        mbar_arrive(smem_u32(&epi_done));
-      }
-      ++n;
-    }
+      if (tiles > 0) mbar_wait_drain(smem_u32(&q_raw), (tiles - 1) & 1, P.status);
+    };
+    // (Known when compiled where the roles' registers differ.)
+    if constexpr (!kFp4)
+      compute(warp < 12);
+    else if (warp < 12)
+      compute(std::true_type{});
+    else
+      compute(std::false_type{});
   }
 
   tc_fence_before();
@@ -982,8 +1052,8 @@ cudaError_t launch_decode_fp8kv(const CUtensorMap& tm_lat, const CUtensorMap& tm
   P.tpg = shape.tpg;
   P.sets = shape.sets;
   P.scale_log2 = scale * 1.4426950408889634f;
-  return launch_pdl(kern, dim3(shape.groups * shape.tpg), dim3(kThreads), smem, st, tm_lat, tm_rope,
-                    tm_q, P);
+  return launch_pdl(kern, dim3(shape.groups * shape.tpg), dim3(threads(kv4 != nullptr)), smem, st,
+                    tm_lat, tm_rope, tm_q, P);
 }
 
 }  // namespace mla
