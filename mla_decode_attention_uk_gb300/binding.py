@@ -515,14 +515,21 @@ def gather_fp4kv(d: Dims, kv4, kv_scale, block_table, seq_lens, rows, new_lens=N
             status)
 
 
-def _token_stride(t, batch, tokens, width):
+def _gapped(name, t, shape, width, other):
     """Elements from a token to the next of a [batch, tokens, ...] tensor whose tokens
-    are contiguous and evenly spaced; None for another."""
-    if batch > 1 and tokens > 1 and t.stride(0) != tokens * t.stride(1):
-        return None
-    n = t.stride(1) if tokens > 1 else t.stride(0) if batch > 1 else width
-    if t.stride(-1) != 1 or (t.dim() == 4 and t.stride(2) != t.shape[3]) or n < width or n % 8:
-        return None
+    are contiguous and evenly spaced (columns of a wider one)."""
+    n = None
+    if t.shape == shape and t.dtype is torch.bfloat16 and t.get_device() == other.get_device():
+        batch, tokens = shape[:2]
+        n = t.stride(1) if tokens > 1 else t.stride(0)
+        if (t.stride(-1) != 1 or (len(shape) == 4 and t.stride(2) != shape[3]) or n < width or n % 8
+                or (batch > 1 and t.stride(0) != tokens * n)):
+            n = None
+    if n is None:
+        raise ValueError(
+            "%s: expected a bfloat16 tensor of shape %s on the current CUDA device, with "
+            "contiguous, evenly spaced tokens (a multiple of 8 elements apart), got %s" %
+            (name, shape, (t.dtype, tuple(t.shape), t.stride(), str(t.device))))
     return n
 
 
@@ -545,35 +552,39 @@ def norm_rope(d: Dims, seq_lens, cos_sin, q=None, q_out=None, q_weight=None, kv=
     most = cos_sin.shape[0] if cos_sin is not None and cos_sin.dim() == 2 else 0
     tensors = [("cos_sin", cos_sin, torch.float32, (most, 64)),
                ("seq_lens", seq_lens, torch.int32, (B,))]
-    strides = [0, 0]
-    for i, (name, t, shape, width) in enumerate((("q", q, (B, max_new, H, 192), H * 192),
-                                                 ("kv", kv, (B, max_new, 576), 576))):
-        if t is None:
-            continue
-        stride = _token_stride(t, B, max_new, width) if t.shape == shape else None
-        if stride is None or t.dtype is not bf or t.get_device() != seq_lens.get_device():
-            raise ValueError(
-                "%s: expected a %s tensor of shape %s on the current CUDA device, with contiguous, "
-                "evenly spaced tokens (a multiple of 8 elements apart), got %s" %
-                (name, bf, shape, (t.dtype, tuple(t.shape), t.stride(), str(t.device))))
-        strides[i] = stride
-    if q is not None or q_out is not None:
-        tensors.append(("q_out", q_out, bf, (B, max_new, H, 192)))
-    for name, t, dtype, shape in (("q_weight", q_weight, bf, (192,)),
-                                  ("kv_weight", kv_weight, bf, (512,)),
-                                  ("rows", rows, bf, (B, max_new, 576)),
-                                  ("cache", cache, bf, (d.num_pages, 64, 576)),
-                                  ("block_table", block_table, torch.int32,
-                                   (B, d.max_pages_per_seq)),
-                                  ("positions", positions, torch.int32, (B, max_new)),
-                                  ("new_lens", new_lens, torch.int32, (B,)),
-                                  ("status", status, torch.int32, (1,))):
-        if t is not None:
-            tensors.append((name, t, dtype, shape))
+    add = tensors.append
+    q_stride, kv_stride = H * 192, 576
+    if q is not None:
+        if q.is_contiguous():
+            add(("q", q, bf, (B, max_new, H, 192)))
+        else:
+            q_stride = _gapped("q", q, (B, max_new, H, 192), q_stride, seq_lens)
+        add(("q_out", q_out, bf, (B, max_new, H, 192)))
+    if kv is not None:
+        if kv.is_contiguous():
+            add(("kv", kv, bf, (B, max_new, 576)))
+        else:
+            kv_stride = _gapped("kv", kv, (B, max_new, 576), 576, seq_lens)
+    if q_weight is not None:
+        add(("q_weight", q_weight, bf, (192,)))
+    if kv_weight is not None:
+        add(("kv_weight", kv_weight, bf, (512,)))
+    if rows is not None:
+        add(("rows", rows, bf, (B, max_new, 576)))
+    if cache is not None:
+        add(("cache", cache, bf, (d.num_pages, 64, 576)))
+    if block_table is not None:
+        add(("block_table", block_table, torch.int32, (B, d.max_pages_per_seq)))
+    if positions is not None:
+        add(("positions", positions, torch.int32, (B, max_new)))
+    if new_lens is not None:
+        add(("new_lens", new_lens, torch.int32, (B,)))
+    if status is not None:
+        add(("status", status, torch.int32, (1,)))
     stream = _checked(*tensors)
-    _ok(lib().mla_decode_norm_rope(ctypes.byref(d), _ptr(q), strides[0], _ptr(q_weight), _ptr(kv),
-                                   strides[1], _ptr(kv_weight), float(eps), cos_sin.data_ptr(),
-                                   most, int(bool(interleaved)), _ptr(positions), max_new,
+    _ok(lib().mla_decode_norm_rope(ctypes.byref(d), _ptr(q), q_stride, _ptr(q_weight), _ptr(kv),
+                                   kv_stride, _ptr(kv_weight), float(eps), cos_sin.data_ptr(),
+                                   most, 1 if interleaved else 0, _ptr(positions), max_new,
                                    _ptr(new_lens), seq_lens.data_ptr(), _ptr(q_out), _ptr(rows),
                                    _ptr(cache), _ptr(block_table), _ptr(status), stream),
         "mla_decode_norm_rope")

@@ -72,11 +72,12 @@ cudaError_t launch_append(const void* rows, int max_new, const int32_t* new_lens
 cudaError_t launch_page_keys(Kind kind, const void* cache, const float* kv_scale,
                              const int32_t* block_table, const int32_t* seq_lens, int max_new,
                              const int32_t* new_lens, int B, int num_pages, int max_pages,
-                             __nv_bfloat16* keys, int32_t* status, cudaStream_t st);
+                             __nv_bfloat16* keys, int32_t* status, int sm_count,
+                             cudaStream_t st);
 cudaError_t launch_gather(Kind kind, const void* cache, const float* kv_scale,
                           const int32_t* block_table, const int32_t* seq_lens, int max_new,
                           const int32_t* new_lens, int B, int num_pages, int max_pages,
-                          void* rows, int32_t* status, cudaStream_t st);
+                          void* rows, int32_t* status, int sm_count, cudaStream_t st);
 cudaError_t launch_prep(const PrepParams& P, bool interleaved, int sm_count, cudaStream_t st);
 cudaError_t launch_score(const CUtensorMap& tm_q, const void* page_keys,
                          const int32_t* block_table, const int32_t* seq_lens, int B, int T, int H,
@@ -828,20 +829,23 @@ static int newest_impl(const mla_decode_dims* d, Kind kind, bool keys, const voi
                        const float* kv_scale, const int32_t* block_table,
                        const int32_t* seq_lens, int32_t max_new, const int32_t* new_lens,
                        void* dst, int32_t* status, void* stream) {
-  const int rc = check_dims(d);
+  int rc = check_dims(d);
   if (rc) return rc;
   if (!cache || !aligned16(cache) || (kind != Kind::kBf16 && !kv_scale) || !aligned4(kv_scale) ||
       !block_table || !aligned4(block_table) || !seq_lens || !aligned4(seq_lens) || max_new < 1 ||
       max_new > INT32_MAX - kPage || !aligned4(new_lens) || !dst || !aligned16(dst) ||
       !aligned4(status))
     return MLA_DECODE_INVALID_ARG;
+  int sms = 0;
+  rc = sm_count(&sms);
+  if (rc) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (keys)
     return cuda_rc(launch_page_keys(kind, cache, kv_scale, block_table, seq_lens, max_new,
                                     new_lens, d->batch, d->num_pages, d->max_pages_per_seq,
-                                    static_cast<__nv_bfloat16*>(dst), status, st));
+                                    static_cast<__nv_bfloat16*>(dst), status, sms, st));
   return cuda_rc(launch_gather(kind, cache, kv_scale, block_table, seq_lens, max_new, new_lens,
-                               d->batch, d->num_pages, d->max_pages_per_seq, dst, status, st));
+                               d->batch, d->num_pages, d->max_pages_per_seq, dst, status, sms, st));
 }
 
 int mla_decode_page_keys(const mla_decode_dims* d, const void* kv_cache,

@@ -74,6 +74,28 @@ __device__ __forceinline__ Block4 block4(const float (&v)[8], int se) {
   b.codes = b.e == kExpNan4 ? 0u : e2m1x8(v, exp2_int(kExpBias4 - b.e - se));
   return b;
 }
+// A whole block of bf16 values, two at a time (their maximum is exact, and so are the
+// products with a power of two but for what vanishes): e, and the codes of a and of b.
+__device__ __forceinline__ uint32_t e2m1x8(const uint4& x, __nv_bfloat162 mul) {
+  const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+  uint32_t w = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    w |= static_cast<uint32_t>(__nv_cvt_float2_to_fp4x2(
+             __bfloat1622float2(__hmul2(as_bf162(in[k]), mul)), __NV_E2M1, cudaRoundNearest))
+         << (8 * k);
+  return w;
+}
+__device__ __forceinline__ int block4(const uint4& a, const uint4& b, int se, uint32_t& codes_a,
+                                      uint32_t& codes_b) {
+  __nv_bfloat162 m = max_abs(max_abs(max_abs(__habs2(as_bf162(a.x)), a.y), a.z), a.w);
+  m = max_abs(max_abs(max_abs(max_abs(m, b.x), b.y), b.z), b.w);
+  const int e = block_exp4(__uint_as_float(larger_half(m)), se);
+  const __nv_bfloat162 mul = __float2bfloat162_rn(exp2_int(kExpBias4 - e - se));
+  codes_a = e == kExpNan4 ? 0u : e2m1x8(a, mul);
+  codes_b = e == kExpNan4 ? 0u : e2m1x8(b, mul);
+  return e;
+}
 // Four lanes' two exponents as a byte, for the first of them.
 __device__ __forceinline__ uint8_t exps_byte(int e) {
   return static_cast<uint8_t>(e | (__shfl_xor_sync(0xffffffffu, e, 2) << 4));
@@ -158,34 +180,52 @@ struct Target {
 constexpr int kHeld = kPage * kChunks / kAppThreads;
 static_assert(kHeld * kAppThreads == kPage * kChunks, "a page is whole passes");
 
-// The part of fill_page behind the page's scale, for the 4-bit cache: x is what the
-// threads hold of the new rows (a block's halves in neighbouring lanes: kChunks and
-// kAppThreads are multiples of four).
-template <bool kFew>
+// The 4-bit cache's threads hold blocks of 16 values, two chunks of 16 bytes: every
+// other lane takes its second one first, so that eight lanes' loads of 16 bytes meet
+// all banks.
+constexpr int kBlocks = kDqk / kBlock4;  // of a row, the RoPE columns' four among them
+__device__ __forceinline__ bool swapped_halves(int tid) { return (tid ^ (tid >> 2)) & 1; }
+
+// The part of fill_page behind the page's scale, for the 4-bit cache.  The threads read
+// the new rows a second time (held in registers they were spilled, 36 us; eight values
+// to a thread and a shuffle for the block's maximum 28 us: 13 prompts of 512 to 8190
+// tokens).
+template <typename Taken>
 __device__ __forceinline__ void store_page4(const AppendParams& P, const Group& grp,
                                             const Place& at, const Target& to,
-                                            const uint4 (&x)[kHeld], float scale) {
-  const int r0 = at.r0(), r1 = at.r1(), n = (r1 - r0) * kChunks;
+                                            const uint4* rows_sh, float scale,
+                                            const Taken& taken) {
+  const int r0 = at.r0(), r1 = at.r1();
+  const int n = (r1 - r0) * kBlocks, whole_warps = (n + 31) & ~31;
   const int se = static_cast<int>(__float_as_uint(scale) >> 23) - 127;
   const __nv_bfloat162 inv = __float2bfloat162_rn(1.0f / scale);
   uint8_t* const dst = P.kv + static_cast<size_t>(to.page) * kPageBytes4;
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k) {
-    if (kFew && k * kAppThreads >= n) break;
-    const int i = grp.tid + k * kAppThreads, c = i % kChunks;
-    uint8_t* const row = dst + (r0 + i / kChunks) * kRow4;
-    const float v[8] = {bf16_lo(x[k].x), bf16_hi(x[k].x), bf16_lo(x[k].y), bf16_hi(x[k].y),
-                        bf16_lo(x[k].z), bf16_hi(x[k].z), bf16_lo(x[k].w), bf16_hi(x[k].w)};
-    const Block4 b = block4(v, se);
-    const uint8_t exps = exps_byte(b.e);
-    if (i >= n) continue;
-    if (c < kLora / 8) {
-      *reinterpret_cast<uint32_t*>(row + 4 * c) = b.codes;
-      if ((c & 3) == 0) row[kRowExps4 + (c >> 2)] = exps;
+  const bool swapped = swapped_halves(grp.tid);
+#pragma unroll 2
+  for (int i = grp.tid; i < whole_warps; i += kAppThreads) {
+    const int c = i % kBlocks;
+    uint4 xa = make_uint4(0u, 0u, 0u, 0u), xb = xa;
+    if (i < n) {
+      xa = rows_sh[2 * i + swapped];
+      xb = rows_sh[2 * i + !swapped];
+    }
+    uint8_t* const row = dst + (r0 + i / kBlocks) * kRow4;
+    uint32_t wa, wb;
+    const int e = block4(xa, xb, se, wa, wb);
+    const int next = __shfl_xor_sync(0xffffffffu, e, 1);
+    if (i >= n || !to.in_pool) continue;
+    if (c < kLora / kBlock4) {
+      *reinterpret_cast<uint2*>(row + 8 * c) = swapped ? make_uint2(wb, wa) : make_uint2(wa, wb);
+      if ((c & 1) == 0) row[kRowExps4 + (c >> 1)] = static_cast<uint8_t>(e | (next << 4));
     } else {
-      *reinterpret_cast<uint2*>(row + kRowRope4 + 8 * (c - kLora / 8)) = codes8(x[k], inv);
+      const uint2 ca = codes8(xa, inv), cb = codes8(xb, inv);
+      *reinterpret_cast<uint4*>(row + kRowRope4 + 16 * (c - kLora / kBlock4)) =
+          swapped ? make_uint4(cb.x, cb.y, ca.x, ca.y) : make_uint4(ca.x, ca.y, cb.x, cb.y);
     }
   }
+  grp.sync();
+  taken();
+  if (!to.in_pool) return;
   if (grp.tid == 0) P.kv_scale[to.page] = scale;
   if (r0 == 0) {  // a page that starts here: cleared behind the new rows
     uint4* const all = reinterpret_cast<uint4*>(dst);
@@ -202,7 +242,7 @@ __device__ __forceinline__ void store_page4(const AppendParams& P, const Group& 
     const bool stays = r < r0 || r >= r1;
     uint8_t* const row = dst + r * kRow4;
     float v[8] = {};
-    if (stays) row_values4(row, c, v);
+    if (stays) values4(load_raw4(row, c), c, v);
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = mul_odd(v[k], ratio);
     const Block4 b = block4(v, 0);
@@ -239,7 +279,7 @@ __device__ __forceinline__ void fill_page(const AppendParams& P, const Group& gr
     most = absmax8(most, x[k]);
   }
   float top = grp.max_of(fmaxf(__low2float(most), __high2float(most)));
-  taken();
+  if constexpr (!kFp4) taken();
   if (top == INFINITY) {  // rare: once more, without the infinities
     grp.sync();
     top = 0.0f;
@@ -248,11 +288,11 @@ __device__ __forceinline__ void fill_page(const AppendParams& P, const Group& gr
       if (!kFew || k * kAppThreads < n) top = finite_absmax8(top, x[k]);
     top = grp.max_of(top);
   }
-  if (!to.in_pool) return;
+  if (!kFp4 && !to.in_pool) return;
   float scale = exp2_int(page_scale_exp(top));
   if (r0 > 0) scale = fmaxf(scale, next_power_of_two(to.old));
   if constexpr (kFp4) {
-    store_page4<kFew>(P, grp, at, to, x, scale);
+    store_page4(P, grp, at, to, rows_sh, scale, taken);
     return;
   }
   uint2* const dst = reinterpret_cast<uint2*>(P.kv + static_cast<size_t>(to.page) * kPageBytes8);
@@ -438,55 +478,70 @@ append_pages_kernel(AppendParams P) {
 }
 
 constexpr int kKeyThreads = 288;
+constexpr int kKeyCtas = 4;  // on an SM, of a list
 
-// One CTA per (sequence, page that holds new tokens): the mean of its filled
-// rows.  Thread t sums columns 8 (t mod 72) .. + 7 over rows t / 72, + 4, ...
-// Four rows in flight: 13 prompts of 512 to 8190 tokens 10.6 us from a bf16 cache, 4.1
-// TB/s with the launch and the lengths' and the table's reads (eight rows in flight
-// 11.2, sixteen 14.9: registers and the ragged pages' remainders); the last pages of
-// 128 sequences 3.0 us, 8-bit.
+struct KeyParams {
+  const uint8_t* cache;
+  const float* kv_scale;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  __nv_bfloat16* keys;
+  int32_t* status;
+  int B, max_new, num_pages, max_pages;
+};
+
+// The mean of a page's filled rows.  Thread t sums columns 8 (t mod 72) .. + 7 over rows
+// t / 72, + 4, ...  Four rows in flight from a bf16 cache: 13 prompts of 512 to 8190
+// tokens, in a grid of all their pages, 10.6 us (eight 11.2, sixteen 14.9: registers and
+// the ragged pages' remainders); the last pages of 128 sequences 3.0 us, 8-bit.
 template <Kind kKind>
-__global__ void __launch_bounds__(kKeyThreads)
-page_keys_kernel(const uint8_t* __restrict__ cache, const float* __restrict__ kv_scale,
-                 const int32_t* __restrict__ block_table, const int32_t* __restrict__ seq_lens,
-                 int max_new, const int32_t* __restrict__ new_lens, int num_pages, int max_pages,
-                 __nv_bfloat16* __restrict__ keys, int32_t* __restrict__ status) {
-  __shared__ float part[4][kDqk];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int b = blockIdx.y;
-  NewTokens nt;
-  if (!nt.load(seq_lens, new_lens, max_new, max_pages * kPage, b, threadIdx.x == 0, status))
-    return;
-  const int logical = nt.first / kPage + blockIdx.x;
-  if (logical * kPage >= nt.len) return;
+__device__ __forceinline__ void page_mean(const KeyParams& P, int b, int len, int logical,
+                                          float (&part)[4][kDqk]) {
+  const auto [cache, kv_scale, block_table, seq_lens, new_lens, keys, status, B, max_new,
+              num_pages, max_pages] = P;
   const int page = block_table[static_cast<size_t>(b) * max_pages + logical];
   if (page < 0 || page >= num_pages) {
     if (threadIdx.x == 0) record_status(status, MLA_STATUS_BOUNDS);
     return;
   }
-  const int filled = min(nt.len - logical * kPage, kPage);
+  const int filled = min(len - logical * kPage, kPage);
   const int c = threadIdx.x % kChunks, r0 = threadIdx.x / kChunks;
   float s[8] = {};
-#pragma unroll 4
-  for (int r = r0; r < filled; r += 4) {
-    if constexpr (kKind == Kind::kFp4) {
-      float x[8];
-      row_values4(cache + static_cast<size_t>(page) * kPageBytes4 + r * kRow4, c, x);
+  auto add = [&](const float (&x)[8]) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s[k] += x[k];
-    } else if constexpr (kKind == Kind::kFp8) {
-      const uint2 v = *reinterpret_cast<const uint2*>(
-          cache + static_cast<size_t>(page) * kPageBytes8 + r * kDqk + c * 8);
-      const float2 x0 = e4m3x2_to_float2(v.x), x1 = e4m3x2_to_float2(v.x >> 16);
-      const float2 x2 = e4m3x2_to_float2(v.y), x3 = e4m3x2_to_float2(v.y >> 16);
-      s[0] += x0.x; s[1] += x0.y; s[2] += x1.x; s[3] += x1.y;
-      s[4] += x2.x; s[5] += x2.y; s[6] += x3.x; s[7] += x3.y;
-    } else {
-      const uint4 v = *reinterpret_cast<const uint4*>(
-          cache + (static_cast<size_t>(page) * kPage + r) * (kDqk * 2) + c * 16);
-      s[0] += bf16_lo(v.x); s[1] += bf16_hi(v.x); s[2] += bf16_lo(v.y); s[3] += bf16_hi(v.y);
-      s[4] += bf16_lo(v.z); s[5] += bf16_hi(v.z); s[6] += bf16_lo(v.w); s[7] += bf16_hi(v.w);
+    for (int k = 0; k < 8; ++k) s[k] += x[k];
+  };
+  if constexpr (kKind == Kind::kFp4) {
+    const uint8_t* const base = cache + static_cast<size_t>(page) * kPageBytes4;
+    constexpr int kDeep = 8;  // rows' loads in flight
+    for (int r = r0; r < filled; r += 4 * kDeep) {
+      Raw4 raw[kDeep];
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k)
+        raw[k] = load_raw4(base + min(r + 4 * k, filled - 1) * kRow4, c);
+#pragma unroll
+      for (int k = 0; k < kDeep; ++k) {
+        if (r + 4 * k >= filled) break;
+        float x[8];
+        values4(raw[k], c, x);
+        add(x);
+      }
+    }
+  } else {
+#pragma unroll 4
+    for (int r = r0; r < filled; r += 4) {
+      float x[8];
+      if constexpr (kKind == Kind::kFp8) {
+        values8x8(*reinterpret_cast<const uint2*>(
+                      cache + static_cast<size_t>(page) * kPageBytes8 + r * kDqk + c * 8), x);
+      } else {
+        const uint4 v = *reinterpret_cast<const uint4*>(
+            cache + (static_cast<size_t>(page) * kPage + r) * (kDqk * 2) + c * 16);
+        x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
+        x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z); x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
+      }
+      add(x);
     }
   }
 #pragma unroll
@@ -505,6 +560,33 @@ page_keys_kernel(const uint8_t* __restrict__ cache, const float* __restrict__ kv
   const float x = ((part[0][k] + part[1][k]) + (part[2][k] + part[3][k])) * mul;
   const float y = ((part[0][k + 1] + part[1][k + 1]) + (part[2][k + 1] + part[3][k + 1])) * mul;
   *reinterpret_cast<uint32_t*>(keys + static_cast<size_t>(page) * kDqk + k) = pack_bf16x2(x, y);
+}
+
+// One CTA per (sequence, page that it can touch), or a list of the pages.
+template <Kind kKind, bool kList>
+__global__ void __launch_bounds__(kKeyThreads, kKeyCtas)
+page_keys_kernel(const __grid_constant__ KeyParams P) {
+  __shared__ float part[4][kDqk];
+  griddep_wait();
+  griddep_launch_dependents();
+  if constexpr (kList) {
+    __shared__ UnitList list;
+    const long long pages = list.make(P.seq_lens, P.new_lens, P.max_new, P.max_pages * kPage, P.B,
+                                      P.status, [](const NewTokens& nt) { return nt.pages(); });
+    for (long long f = blockIdx.x; f < pages; f += gridDim.x) {
+      const int b = list.find(f), len = list.len[b];
+      page_mean<kKind>(P, b, len, (len - 1) / kPage - static_cast<int>(list.upto[b] - 1 - f),
+                       part);
+      __syncthreads();  // `part` has been read
+    }
+  } else {
+    const int b = blockIdx.y;
+    NewTokens nt;
+    if (nt.load(P.seq_lens, P.new_lens, P.max_new, P.max_pages * kPage, b, threadIdx.x == 0,
+                P.status) &&
+        blockIdx.x < nt.pages())
+      page_mean<kKind>(P, b, nt.len, nt.first / kPage + static_cast<int>(blockIdx.x), part);
+  }
 }
 
 }  // namespace
@@ -534,16 +616,28 @@ cudaError_t launch_append(const void* rows, int max_new, const int32_t* new_lens
   return launch_pdl(kern, dim3(sm_count), dim3(kPagesThreads), smem, st, P);
 }
 
+template <Kind kKind>
+static cudaError_t launch_keys(const KeyParams& P, int sm_count, cudaStream_t st) {
+  const int touched = touched_pages(P.max_new, P.max_pages);
+  if (use_list(P.max_new, P.B)) {
+    const int64_t most = static_cast<int64_t>(touched) * P.B;
+    const int ctas = most < sm_count * kKeyCtas ? static_cast<int>(most) : sm_count * kKeyCtas;
+    return launch_pdl(page_keys_kernel<kKind, true>, dim3(ctas), dim3(kKeyThreads), 0, st, P);
+  }
+  return launch_pdl(page_keys_kernel<kKind, false>, dim3(touched, P.B), dim3(kKeyThreads), 0, st,
+                    P);
+}
+
 cudaError_t launch_page_keys(Kind kind, const void* cache, const float* kv_scale,
                              const int32_t* block_table, const int32_t* seq_lens, int max_new,
                              const int32_t* new_lens, int B, int num_pages, int max_pages,
-                             __nv_bfloat16* keys, int32_t* status, cudaStream_t st) {
-  const auto kern = kind == Kind::kFp4   ? page_keys_kernel<Kind::kFp4>
-                    : kind == Kind::kFp8 ? page_keys_kernel<Kind::kFp8>
-                                         : page_keys_kernel<Kind::kBf16>;
-  return launch_pdl(kern, dim3(touched_pages(max_new, max_pages), B), dim3(kKeyThreads), 0, st,
-                    static_cast<const uint8_t*>(cache), kv_scale, block_table, seq_lens, max_new,
-                    new_lens, num_pages, max_pages, keys, status);
+                             __nv_bfloat16* keys, int32_t* status, int sm_count,
+                             cudaStream_t st) {
+  const KeyParams P{static_cast<const uint8_t*>(cache), kv_scale, block_table, seq_lens, new_lens,
+                    keys, status, B, max_new, num_pages, max_pages};
+  return kind == Kind::kFp4   ? launch_keys<Kind::kFp4>(P, sm_count, st)
+         : kind == Kind::kFp8 ? launch_keys<Kind::kFp8>(P, sm_count, st)
+                              : launch_keys<Kind::kBf16>(P, sm_count, st);
 }
 
 }  // namespace mla

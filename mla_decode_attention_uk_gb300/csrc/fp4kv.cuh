@@ -76,15 +76,25 @@ __device__ __forceinline__ void values8x8(uint2 c, float (&v)[8]) {
   v[4] = x2.x; v[5] = x2.y; v[6] = x3.x; v[7] = x3.y;
 }
 
-// Columns 8 c .. 8 c + 7 of a row of the 4-bit cache, in units of the page's scale.
-__device__ __forceinline__ void row_values4(const uint8_t* row, int c, float (&v)[8]) {
-  if (c < kLora / 8) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(row + 4 * c);
-    const uint32_t e = row[kRowExps4 + (c >> 2)];
-    values4x8(w, (e >> (2 * (c & 2))) & 15u, v);
-  } else {
-    values8x8(*reinterpret_cast<const uint2*>(row + kRowRope4 + 8 * (c - kLora / 8)), v);
-  }
+// Columns 8 c .. 8 c + 7 of a row of the 4-bit cache, as two words: the codes of latent
+// columns and the word that holds their block's exponent, or eight RoPE codes.  (Two
+// loads for either, so that lanes with either kind load together.)
+struct Raw4 {
+  uint32_t a, b;
+};
+__device__ __forceinline__ Raw4 load_raw4(const uint8_t* row, int c) {
+  const bool latent = c < kLora / 8;
+  const int at = latent ? 4 * c : kRowRope4 + 8 * (c - kLora / 8);
+  return Raw4{*reinterpret_cast<const uint32_t*>(row + at),
+              *reinterpret_cast<const uint32_t*>(row + (latent ? kRowExps4 + 4 * (c >> 4)
+                                                               : at + 4))};
+}
+// Their values in units of the page's scale.
+__device__ __forceinline__ void values4(const Raw4& x, int c, float (&v)[8]) {
+  if (c < kLora / 8)
+    values4x8(x.a, (x.b >> (4 * ((c >> 1) & 7))) & 15u, v);
+  else
+    values8x8(make_uint2(x.a, x.b), v);
 }
 
 }  // namespace mla

@@ -25,6 +25,7 @@ namespace mla {
 namespace {
 
 constexpr int kPrepThreads = 256;
+constexpr int kPrepCtas = 4;  // on an SM
 constexpr int kHeadsPerWarp = 4;
 constexpr int kHalf = kRope / 2;
 
@@ -77,96 +78,170 @@ __device__ __forceinline__ void rotate8(float (&v)[8], const float* __restrict__
   }
 }
 
+// A warp's task: four heads of a token, or its latent row.
+struct Task {
+  int b, first, i, part;  // token i of sequence b's new ones, which start at `first`
+};
+
+// What a lane has of it: 48 bytes of a head (RoPE columns last), or of the latent row
+// (the last eight values, which lanes c, c + 8, ... share, RoPE columns).
+__device__ __forceinline__ void load_task(const PrepParams& P, const Task& t, int q_tasks,
+                                          uint4 (&x)[3]) {
+  const int lane = threadIdx.x & 31, c = lane & 7;
+  const int64_t token = static_cast<int64_t>(t.b) * P.max_new + t.i;
+  const bool q = t.part < q_tasks;
+  const uint4* const src = reinterpret_cast<const uint4*>(
+      q ? P.q + token * P.q_stride + (t.part * kHeadsPerWarp + (lane >> 3)) * kDq
+        : P.kv + token * P.kv_stride);
+  x[0] = src[q ? c : lane];
+  x[1] = src[q ? c + 8 : lane + 32];
+  x[2] = src[q ? c + 16 : 64 + c];
+}
+
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kPrepThreads)
-prep_kernel(const PrepParams P) {
+__device__ __forceinline__ void do_task(const PrepParams& P, const Task& t, int q_tasks,
+                                        const uint4 (&x)[3]) {
+  const int lane = threadIdx.x & 31, c = lane & 7;
+  const int64_t token = static_cast<int64_t>(t.b) * P.max_new + t.i;
+  const int pos = P.positions ? P.positions[token] : t.first + t.i;
+  if (pos < 0 || pos >= P.max_position) {
+    if (t.part == 0 && lane == 0) record_status(P.status, MLA_STATUS_BOUNDS);
+    return;
+  }
+  const float* const cos_sin = P.cos_sin + static_cast<size_t>(pos) * kRope;
+  const bool q = t.part < q_tasks;
+  const __nv_bfloat16* const weight = q ? P.q_weight : P.kv_weight;
+  float v[3][8];
+#pragma unroll
+  for (int k = 0; k < 3; ++k) unpack8(x[k], v[k]);
+  if (weight) {
+    // Over eight lanes and all their columns, or all lanes and the first two parts.
+    float sum = squares8(v[1], squares8(v[0], 0.0f));
+    if (q) sum = squares8(v[2], sum);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (!q)
+#pragma unroll
+      for (int o = 8; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float by = rsqrtf(sum * (q ? 1.0f / kDq : 1.0f / kLora) + P.eps);
+    const uint4* const w = reinterpret_cast<const uint4*>(weight) + (q ? c : lane);
+    scale8(v[0], by, w[0]);
+    scale8(v[1], by, w[q ? 8 : 32]);
+    if (q) scale8(v[2], by, w[16]);
+  }
+  rotate8<kInterleaved>(v[2], cos_sin, c);
+  const uint4 y0 = pack8(v[0]), y1 = pack8(v[1]), y2 = pack8(v[2]);
+  if (q) {
+    uint4* const dst = reinterpret_cast<uint4*>(
+        P.q_out + (token * P.H + t.part * kHeadsPerWarp + (lane >> 3)) * kDq);
+    dst[c] = y0;
+    dst[c + 8] = y1;
+    dst[c + 16] = y2;
+    return;
+  }
+  auto store = [&](uint4* dst) {
+    dst[lane] = y0;
+    dst[32 + lane] = y1;
+    if (lane < 8) dst[64 + lane] = y2;
+  };
+  if (P.rows) store(P.rows + token * kChunks);
+  if (P.cache) {
+    const int at = t.first + t.i;
+    const int page = P.block_table[static_cast<size_t>(t.b) * P.max_pages + at / kPage];
+    if (page >= 0 && page < P.num_pages)
+      store(P.cache + (static_cast<size_t>(page) * kPage + at % kPage) * kChunks);
+    else if (lane == 0)
+      record_status(P.status, MLA_STATUS_BOUNDS);
+  }
+}
+
+// A list of the tokens: a warp takes tasks that follow each other, and has the next
+// one's loads in flight.
+template <bool kInterleaved>
+__global__ void __launch_bounds__(kPrepThreads, kPrepCtas)
+prep_list_kernel(const __grid_constant__ PrepParams P) {
+  __shared__ UnitList list;
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
+  const int q_tasks = P.q ? P.H / kHeadsPerWarp : 0;
+  const int per_token = q_tasks + (P.kv ? 1 : 0);
+  const long long tasks =
+      per_token * list.make(P.seq_lens, P.new_lens, P.max_new, P.max_len, P.B, P.status,
+                            [](const NewTokens& nt) { return nt.len - nt.first; });
+  const int warps = gridDim.x * (kPrepThreads / 32);
+  const int w = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5);
+  long long at = tasks * w / warps;
+  const long long end = tasks * (w + 1) / warps;
+  if (at >= end) return;
+  Task t;
+  {
+    const long long token = at / per_token;
+    t.part = static_cast<int>(at - token * per_token);
+    t.b = list.find(token);
+    t.first = list.first[t.b];
+    t.i = static_cast<int>(token - (list.upto[t.b] - (list.len[t.b] - t.first)));
+  }
+  uint4 x[3];
+  load_task(P, t, q_tasks, x);
+#pragma unroll 1
+  while (true) {
+    const Task now = t;
+    uint4 y[3] = {x[0], x[1], x[2]};
+    const bool more = ++at < end;
+    if (more) {
+      if (++t.part == per_token) {
+        t.part = 0;
+        if (++t.i == list.len[t.b] - t.first) {
+          t.b = list.find(list.upto[t.b]);  // (the next one with tokens)
+          t.first = list.first[t.b];
+          t.i = 0;
+        }
+      }
+      load_task(P, t, q_tasks, x);
+    }
+    do_task<kInterleaved>(P, now, q_tasks, y);
+    if (!more) break;
+  }
+}
+
+// Every token that there may be, for single tokens and large batches of a few.
+template <bool kInterleaved>
+__global__ void __launch_bounds__(kPrepThreads, kPrepCtas)
+prep_kernel(const __grid_constant__ PrepParams P) {
+  griddep_wait();
+  griddep_launch_dependents();
   const int q_tasks = P.q ? P.H / kHeadsPerWarp : 0;
   const int per_token = q_tasks + (P.kv ? 1 : 0);
   const int tasks = P.B * P.max_new * per_token;
   const int warps = gridDim.x * (kPrepThreads / 32);
-  for (int task = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5); task < tasks;
-       task += warps) {
-    const int token = task / per_token, part = task - token * per_token;
-    const int b = token / P.max_new, i = token - b * P.max_new;
+  for (int at = blockIdx.x * (kPrepThreads / 32) + (threadIdx.x >> 5); at < tasks; at += warps) {
+    const int token = at / per_token;
+    Task t;
+    t.part = at - token * per_token;
+    t.b = token / P.max_new;
+    t.i = token - t.b * P.max_new;
     NewTokens nt;
-    const bool first = i == 0 && part == 0 && lane == 0;
-    if (!nt.load(P.seq_lens, P.new_lens, P.max_new, P.max_len, b, first, P.status) ||
-        i >= nt.len - nt.first)
+    const bool report = t.i == 0 && t.part == 0 && (threadIdx.x & 31) == 0;
+    if (!nt.load(P.seq_lens, P.new_lens, P.max_new, P.max_len, t.b, report, P.status) ||
+        t.i >= nt.len - nt.first)
       continue;
-    const int pos = P.positions ? P.positions[token] : nt.first + i;
-    if (pos < 0 || pos >= P.max_position) {
-      if (part == 0 && lane == 0) record_status(P.status, MLA_STATUS_BOUNDS);
-      continue;
-    }
-    const float* const cos_sin = P.cos_sin + static_cast<size_t>(pos) * kRope;
-    if (part < q_tasks) {
-      const int c = lane & 7;
-      const int head = part * kHeadsPerWarp + (lane >> 3);
-      const uint4* const src =
-          reinterpret_cast<const uint4*>(P.q + token * P.q_stride + head * kDq) + c;
-      float v[3][8];
-#pragma unroll
-      for (int k = 0; k < 3; ++k) unpack8(src[8 * k], v[k]);
-      if (P.q_weight) {
-        float sum = squares8(v[2], squares8(v[1], squares8(v[0], 0.0f)));
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float by = rsqrtf(sum * (1.0f / kDq) + P.eps);
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-          scale8(v[k], by, reinterpret_cast<const uint4*>(P.q_weight)[8 * k + c]);
-      }
-      rotate8<kInterleaved>(v[2], cos_sin, c);
-      uint4* const dst =
-          reinterpret_cast<uint4*>(P.q_out + (static_cast<int64_t>(token) * P.H + head) * kDq) + c;
-#pragma unroll
-      for (int k = 0; k < 3; ++k) dst[8 * k] = pack8(v[k]);
-    } else {
-      const uint4* const src = reinterpret_cast<const uint4*>(P.kv + token * P.kv_stride);
-      const int c = lane & 7;
-      float v[2][8], rope[8];
-      unpack8(src[lane], v[0]);
-      unpack8(src[32 + lane], v[1]);
-      unpack8(src[64 + c], rope);
-      if (P.kv_weight) {
-        float sum = squares8(v[1], squares8(v[0], 0.0f));
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const float by = rsqrtf(sum * (1.0f / kLora) + P.eps);
-        scale8(v[0], by, reinterpret_cast<const uint4*>(P.kv_weight)[lane]);
-        scale8(v[1], by, reinterpret_cast<const uint4*>(P.kv_weight)[32 + lane]);
-      }
-      rotate8<kInterleaved>(rope, cos_sin, c);
-      const uint4 x0 = pack8(v[0]), x1 = pack8(v[1]), x2 = pack8(rope);
-      auto store = [&](uint4* dst) {
-        dst[lane] = x0;
-        dst[32 + lane] = x1;
-        if (lane < 8) dst[64 + lane] = x2;
-      };
-      if (P.rows) store(P.rows + static_cast<size_t>(token) * kChunks);
-      if (P.cache) {
-        const int at = nt.first + i;
-        const int page = P.block_table[static_cast<size_t>(b) * P.max_pages + at / kPage];
-        if (page >= 0 && page < P.num_pages)
-          store(P.cache + (static_cast<size_t>(page) * kPage + at % kPage) * kChunks);
-        else if (lane == 0)
-          record_status(P.status, MLA_STATUS_BOUNDS);
-      }
-    }
+    t.first = nt.first;
+    uint4 x[3];
+    load_task(P, t, q_tasks, x);
+    do_task<kInterleaved>(P, t, q_tasks, x);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_prep(const PrepParams& P, bool interleaved, int sm_count, cudaStream_t st) {
-  const auto kern = interleaved ? prep_kernel<true> : prep_kernel<false>;
+  const bool list = use_list(P.max_new, P.B);
+  const auto kern = list ? (interleaved ? prep_list_kernel<true> : prep_list_kernel<false>)
+                         : (interleaved ? prep_kernel<true> : prep_kernel<false>);
   const int64_t tasks = static_cast<int64_t>(P.B) * P.max_new *
                         ((P.q ? P.H / kHeadsPerWarp : 0) + (P.kv ? 1 : 0));
   const int64_t ctas = (tasks + kPrepThreads / 32 - 1) / (kPrepThreads / 32);
-  const int most = sm_count * 6;
+  const int most = sm_count * kPrepCtas;
   return launch_pdl(kern, dim3(ctas < most ? static_cast<int>(ctas) : most), dim3(kPrepThreads),
                     0, st, P);
 }

@@ -29,6 +29,54 @@ struct NewTokens {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
+// The units (pages, tokens) of up to kListed sequences, one sequence's after the other's,
+// as every CTA of a grid works them out for itself: prompts of different lengths fill a
+// padded grid by a third, and its empty CTAs took longer than the work.  (At least
+// kListed threads; `count`: a sequence's units.)
+constexpr int kListed = 256;
+struct UnitList {
+  long long warp_sum[kListed / 32];
+  long long upto[kListed];  // units up to and with the sequence's
+  int first[kListed], len[kListed];
+
+  template <typename Count>
+  __device__ long long make(const int32_t* seq_lens, const int32_t* new_lens, int max_new,
+                            int cap, int B, int32_t* status, const Count& count) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    long long n = 0;
+    if (tid < kListed) {
+      NewTokens nt{0, 0};
+      if (tid < B &&
+          nt.load(seq_lens, new_lens, max_new, cap, tid, blockIdx.x == 0, status))
+        n = count(nt);
+      first[tid] = nt.first;
+      len[tid] = nt.len;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, n, o);
+        if (lane >= o) n += v;
+      }
+      if (lane == 31) warp_sum[warp] = n;
+    }
+    __syncthreads();
+    if (tid < kListed) {
+      for (int w = 0; w < warp; ++w) n += warp_sum[w];
+      upto[tid] = n;
+    }
+    __syncthreads();
+    return upto[kListed - 1];
+  }
+  // The sequence of a unit below the total.
+  __device__ int find(long long unit) const {
+    int b = 0;
+    for (int step = kListed / 2; step; step >>= 1)
+      if (upto[b + step - 1] <= unit) b += step;
+    return b;
+  }
+};
+// From so many new tokens a sequence on.
+constexpr int kListFrom = 64;
+inline bool use_list(int max_new, int B) { return max_new > kListFrom && B <= kListed; }
+
 // Pages that max_new consecutive tokens can touch.
 inline int touched_pages(int max_new, int max_pages) {
   const int most = (max_new + kPage - 2) / kPage + 1;
