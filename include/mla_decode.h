@@ -351,16 +351,33 @@ int mla_decode_attend_fp4kv(const mla_decode_dims* dims, const uint8_t* kv_fp4,
  * Rows behind a sequence's n_b tokens are neither read nor written.  A position outside
  * [0, max_position): DEVICE_BOUNDS, and nothing of the token is written; a block_table
  * entry outside the pool: DEVICE_BOUNDS, and the page's tokens reach q_out and rows
- * only; lengths as for the append.  The other arguments (q without q_out, outputs
- * without their input, ...): INVALID_ARG.  Uses batch, num_heads, num_pages and
+ * only; lengths as for the append.  Anything else (q without q_out, outputs without
+ * their input, ...): INVALID_ARG.  Uses batch, num_heads, num_pages and
  * max_pages_per_seq of dims.  One kernel. */
-int mla_decode_norm_rope(const mla_decode_dims* dims, const void* q, int64_t q_stride,
-                         const void* q_weight, const void* kv, int64_t kv_stride,
-                         const void* kv_weight, float eps, const float* cos_sin,
-                         int32_t max_position, int32_t interleaved, const int32_t* positions,
-                         int32_t max_new, const int32_t* new_lens, const int32_t* seq_lens,
-                         void* q_out, void* rows, void* kv_cache, const int32_t* block_table,
-                         int32_t* status, void* stream);
+typedef struct {
+  const void* q;
+  int64_t q_stride;
+  const void* q_weight;
+  const void* kv;
+  int64_t kv_stride;
+  const void* kv_weight;
+  const float* cos_sin;
+  const int32_t* positions;
+  const int32_t* new_lens;
+  const int32_t* seq_lens;
+  void* q_out;
+  void* rows;
+  void* kv_cache;
+  const int32_t* block_table;
+  int32_t* status;
+  float eps;
+  int32_t max_position;
+  int32_t interleaved;
+  int32_t max_new;
+} mla_decode_norm_rope_args;
+
+int mla_decode_norm_rope(const mla_decode_dims* dims, const mla_decode_norm_rope_args* args,
+                         void* stream);
 
 /* Reading back, the appends' inverse: tokens of the cache as bf16 rows, for a chunk of
  * a prompt that attends to them, or to move a sequence to another cache.

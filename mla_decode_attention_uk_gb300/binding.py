@@ -7,6 +7,7 @@ raises.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -93,9 +94,7 @@ def lib():
         L.mla_decode_gather.argtypes = L.mla_decode_page_keys.argtypes
         L.mla_decode_gather_fp8kv.argtypes = L.mla_decode_page_keys_fp8kv.argtypes
         L.mla_decode_gather_fp4kv.argtypes = L.mla_decode_page_keys_fp8kv.argtypes
-        i64 = ctypes.c_int64
-        L.mla_decode_norm_rope.argtypes = [D, P, i64, P, P, i64, P, ctypes.c_float, P, i32, i32, P,
-                                           i32, P, P, P, P, P, P, P, P]
+        L.mla_decode_norm_rope.argtypes = [D, P, P]
         for n in ENTRY_POINTS:
             if n != "mla_decode_status_string":
                 getattr(L, n).restype = ctypes.c_int
@@ -533,6 +532,11 @@ def _gapped(name, t, shape, width, other):
     return n
 
 
+# mla_decode_norm_rope_args as bytes (a call's arguments one by one through ctypes take
+# 2 us longer).
+_NORM_ROPE = struct.Struct("=QqQQqQQQQQQQQQQfiii").pack
+
+
 def norm_rope(d: Dims, seq_lens, cos_sin, q=None, q_out=None, q_weight=None, kv=None,
               kv_weight=None, rows=None, cache=None, block_table=None, eps=1e-6,
               interleaved=True, positions=None, new_lens=None, status=None):
@@ -582,9 +586,15 @@ def norm_rope(d: Dims, seq_lens, cos_sin, q=None, q_out=None, q_weight=None, kv=
     if status is not None:
         add(("status", status, torch.int32, (1,)))
     stream = _checked(*tensors)
-    _ok(lib().mla_decode_norm_rope(ctypes.byref(d), _ptr(q), q_stride, _ptr(q_weight), _ptr(kv),
-                                   kv_stride, _ptr(kv_weight), float(eps), cos_sin.data_ptr(),
-                                   most, 1 if interleaved else 0, _ptr(positions), max_new,
-                                   _ptr(new_lens), seq_lens.data_ptr(), _ptr(q_out), _ptr(rows),
-                                   _ptr(cache), _ptr(block_table), _ptr(status), stream),
-        "mla_decode_norm_rope")
+    args = _NORM_ROPE(
+        q.data_ptr() if q is not None else 0, q_stride,
+        q_weight.data_ptr() if q_weight is not None else 0,
+        kv.data_ptr() if kv is not None else 0, kv_stride,
+        kv_weight.data_ptr() if kv_weight is not None else 0, cos_sin.data_ptr(),
+        positions.data_ptr() if positions is not None else 0,
+        new_lens.data_ptr() if new_lens is not None else 0, seq_lens.data_ptr(),
+        q_out.data_ptr() if q_out is not None else 0, rows.data_ptr() if rows is not None else 0,
+        cache.data_ptr() if cache is not None else 0,
+        block_table.data_ptr() if block_table is not None else 0,
+        status.data_ptr() if status is not None else 0, eps, most, 1 if interleaved else 0, max_new)
+    _ok(lib().mla_decode_norm_rope(ctypes.byref(d), args, stream), "mla_decode_norm_rope")

@@ -12,7 +12,6 @@
 #include "../../include/mla_decode.h"
 #include "common.cuh"
 #include "host_checks.h"
-#include "prep.h"
 #include "ptx.cuh"
 
 namespace mla {
@@ -78,7 +77,8 @@ cudaError_t launch_gather(Kind kind, const void* cache, const float* kv_scale,
                           const int32_t* block_table, const int32_t* seq_lens, int max_new,
                           const int32_t* new_lens, int B, int num_pages, int max_pages,
                           void* rows, int32_t* status, int sm_count, cudaStream_t st);
-cudaError_t launch_prep(const PrepParams& P, bool interleaved, int sm_count, cudaStream_t st);
+cudaError_t launch_prep(const mla_decode_norm_rope_args& a, const mla_decode_dims& d, int sm_count,
+                        cudaStream_t st);
 cudaError_t launch_score(const CUtensorMap& tm_q, const void* page_keys,
                          const int32_t* block_table, const int32_t* seq_lens, int B, int T, int H,
                          int num_pages, int max_pages, float* scores, int32_t* status,
@@ -895,60 +895,33 @@ int mla_decode_gather_fp4kv(const mla_decode_dims* d, const uint8_t* kv_fp4,
                      new_lens, rows, status, stream);
 }
 
-int mla_decode_norm_rope(const mla_decode_dims* d, const void* q, int64_t q_stride,
-                         const void* q_weight, const void* kv, int64_t kv_stride,
-                         const void* kv_weight, float eps, const float* cos_sin,
-                         int32_t max_position, int32_t interleaved, const int32_t* positions,
-                         int32_t max_new, const int32_t* new_lens, const int32_t* seq_lens,
-                         void* q_out, void* rows, void* kv_cache, const int32_t* block_table,
-                         int32_t* status, void* stream) {
+int mla_decode_norm_rope(const mla_decode_dims* d, const mla_decode_norm_rope_args* a,
+                         void* stream) {
   int rc = check_dims(d);
   if (rc) return rc;
-  if (!(q || kv) || !cos_sin || !aligned16(cos_sin) || max_position < 1 || max_new < 1 ||
-      interleaved < 0 || interleaved > 1 || !aligned4(positions) || !aligned4(new_lens) ||
-      !seq_lens || !aligned4(seq_lens) || !aligned4(status) || !std::isfinite(eps) || eps <= 0.0f)
+  if (!a || !(a->q || a->kv) || !a->cos_sin || !aligned16(a->cos_sin) || a->max_position < 1 ||
+      a->max_new < 1 || a->interleaved < 0 || a->interleaved > 1 || !aligned4(a->positions) ||
+      !aligned4(a->new_lens) || !a->seq_lens || !aligned4(a->seq_lens) || !aligned4(a->status) ||
+      !std::isfinite(a->eps) || a->eps <= 0.0f)
     return MLA_DECODE_INVALID_ARG;
   // A row in 16-byte parts: strides are multiples of eight elements.
-  if (q ? (!aligned16(q) || !q_out || !aligned16(q_out) || !aligned16(q_weight) ||
-           q_stride < static_cast<int64_t>(d->num_heads) * kDq || q_stride % 8 != 0)
-        : (q_out || q_weight))
+  if (a->q ? (!aligned16(a->q) || !a->q_out || !aligned16(a->q_out) || !aligned16(a->q_weight) ||
+              a->q_stride < static_cast<int64_t>(d->num_heads) * kDq || a->q_stride % 8 != 0)
+           : (a->q_out || a->q_weight))
     return MLA_DECODE_INVALID_ARG;
-  if (kv ? (!aligned16(kv) || !aligned16(kv_weight) || kv_stride < kDqk || kv_stride % 8 != 0 ||
-            !(rows || kv_cache) || !aligned16(rows) || !aligned16(kv_cache) ||
-            (kv_cache && (!block_table || !aligned4(block_table))))
-         : (rows || kv_cache || kv_weight))
+  if (a->kv ? (!aligned16(a->kv) || !aligned16(a->kv_weight) || a->kv_stride < kDqk ||
+               a->kv_stride % 8 != 0 || !(a->rows || a->kv_cache) || !aligned16(a->rows) ||
+               !aligned16(a->kv_cache) ||
+               (a->kv_cache && (!a->block_table || !aligned4(a->block_table))))
+            : (a->rows || a->kv_cache || a->kv_weight))
     return MLA_DECODE_INVALID_ARG;
   // Warps count their tasks (four heads or a latent row) in 32 bits.
-  if (static_cast<int64_t>(d->batch) * max_new > INT32_MAX / 2 / (d->num_heads / 4 + 1))
+  if (static_cast<int64_t>(d->batch) * a->max_new > INT32_MAX / 2 / (d->num_heads / 4 + 1))
     return MLA_DECODE_INVALID_ARG;
   int sms = 0;
   rc = sm_count(&sms);
   if (rc) return rc;
-  PrepParams P{};
-  P.q = static_cast<const __nv_bfloat16*>(q);
-  P.kv = static_cast<const __nv_bfloat16*>(kv);
-  P.q_stride = q_stride;
-  P.kv_stride = kv_stride;
-  P.q_weight = static_cast<const __nv_bfloat16*>(q_weight);
-  P.kv_weight = static_cast<const __nv_bfloat16*>(kv_weight);
-  P.cos_sin = cos_sin;
-  P.positions = positions;
-  P.new_lens = new_lens;
-  P.seq_lens = seq_lens;
-  P.block_table = block_table;
-  P.q_out = static_cast<__nv_bfloat16*>(q_out);
-  P.rows = static_cast<uint4*>(rows);
-  P.cache = static_cast<uint4*>(kv_cache);
-  P.status = status;
-  P.eps = eps;
-  P.B = d->batch;
-  P.H = d->num_heads;
-  P.max_new = max_new;
-  P.max_position = max_position;
-  P.num_pages = d->num_pages;
-  P.max_pages = d->max_pages_per_seq;
-  P.max_len = d->max_pages_per_seq * kPage;
-  return cuda_rc(launch_prep(P, interleaved != 0, sms, static_cast<cudaStream_t>(stream)));
+  return cuda_rc(launch_prep(*a, *d, sms, static_cast<cudaStream_t>(stream)));
 }
 
 int mla_decode_score_pages(const mla_decode_dims* d, const void* query, const void* page_keys,

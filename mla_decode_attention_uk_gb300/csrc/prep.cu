@@ -14,15 +14,37 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "../../include/mla_decode.h"
 #include "common.cuh"
 #include "fp8kv.cuh"
-#include "prep.h"
 #include "ptx.cuh"
 #include "tokens.cuh"
 
 namespace mla {
 
 namespace {
+
+// The call's arguments, typed (q, kv, q_weight, kv_weight, positions, new_lens, rows and
+// cache may be null).
+struct PrepParams {
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* kv;
+  int64_t q_stride, kv_stride;
+  const __nv_bfloat16* q_weight;
+  const __nv_bfloat16* kv_weight;
+  const float* cos_sin;
+  const int32_t* positions;
+  const int32_t* new_lens;
+  const int32_t* seq_lens;
+  const int32_t* block_table;
+  __nv_bfloat16* q_out;
+  uint4* rows;
+  uint4* cache;
+  int32_t* status;
+  float eps;
+  int B, H, max_new, max_position, num_pages, max_pages;
+  int max_len;  // that a sequence may have
+};
 
 constexpr int kPrepThreads = 256;
 constexpr int kPrepCtas = 4;  // on an SM
@@ -234,10 +256,35 @@ prep_kernel(const __grid_constant__ PrepParams P) {
 
 }  // namespace
 
-cudaError_t launch_prep(const PrepParams& P, bool interleaved, int sm_count, cudaStream_t st) {
+cudaError_t launch_prep(const mla_decode_norm_rope_args& a, const mla_decode_dims& d, int sm_count,
+                        cudaStream_t st) {
+  PrepParams P{};
+  P.q = static_cast<const __nv_bfloat16*>(a.q);
+  P.kv = static_cast<const __nv_bfloat16*>(a.kv);
+  P.q_stride = a.q_stride;
+  P.kv_stride = a.kv_stride;
+  P.q_weight = static_cast<const __nv_bfloat16*>(a.q_weight);
+  P.kv_weight = static_cast<const __nv_bfloat16*>(a.kv_weight);
+  P.cos_sin = a.cos_sin;
+  P.positions = a.positions;
+  P.new_lens = a.new_lens;
+  P.seq_lens = a.seq_lens;
+  P.block_table = a.block_table;
+  P.q_out = static_cast<__nv_bfloat16*>(a.q_out);
+  P.rows = static_cast<uint4*>(a.rows);
+  P.cache = static_cast<uint4*>(a.kv_cache);
+  P.status = a.status;
+  P.eps = a.eps;
+  P.B = d.batch;
+  P.H = d.num_heads;
+  P.max_new = a.max_new;
+  P.max_position = a.max_position;
+  P.num_pages = d.num_pages;
+  P.max_pages = d.max_pages_per_seq;
+  P.max_len = d.max_pages_per_seq * kPage;
   const bool list = use_list(P.max_new, P.B);
-  const auto kern = list ? (interleaved ? prep_list_kernel<true> : prep_list_kernel<false>)
-                         : (interleaved ? prep_kernel<true> : prep_kernel<false>);
+  const auto kern = list ? (a.interleaved ? prep_list_kernel<true> : prep_list_kernel<false>)
+                         : (a.interleaved ? prep_kernel<true> : prep_kernel<false>);
   const int64_t tasks = static_cast<int64_t>(P.B) * P.max_new *
                         ((P.q ? P.H / kHeadsPerWarp : 0) + (P.kv ? 1 : 0));
   const int64_t ctas = (tasks + kPrepThreads / 32 - 1) / (kPrepThreads / 32);

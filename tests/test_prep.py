@@ -16,26 +16,42 @@ EPS = 1e-6
 
 
 # ---------------------------------------------------------------- refusals (no GPU)
+class Args(ctypes.Structure):
+    P, I64 = ctypes.c_void_p, ctypes.c_int64
+    _fields_ = [("q", P), ("q_stride", I64), ("q_weight", P), ("kv", P), ("kv_stride", I64),
+                ("kv_weight", P), ("cos_sin", P), ("positions", P), ("new_lens", P),
+                ("seq_lens", P), ("q_out", P), ("rows", P), ("kv_cache", P), ("block_table", P),
+                ("status", P), ("eps", ctypes.c_float), ("max_position", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("max_new", ctypes.c_int32)]
+
+
 def test_refuses_bad_arguments():
-    eps = ctypes.c_float(EPS)
-    #      0  1        2   3   4    5   6    7   8  9 10  11 12  13  14  15  16  17  18  19
-    #      q  stride   qw  kv  str  kvw eps  cs mp il pos mn new len qo rows kvc tab st  stream
-    args = [OK, 16 * 192, OK, OK, 576, OK, eps, OK, 9, 1, OK, 1, OK, OK, OK, OK, OK, OK, OK, None]
-    for change in ({0: ODD8}, {1: 16 * 192 - 8}, {1: 16 * 192 + 4}, {1: -(16 * 192)}, {2: ODD8},
-                   {3: ODD8}, {4: 568}, {4: 580}, {5: ODD8}, {6: ctypes.c_float(0.0)},
-                   {6: ctypes.c_float(-1.0)}, {6: ctypes.c_float(math.nan)},
-                   {6: ctypes.c_float(math.inf)}, {7: None}, {7: ODD8}, {8: 0}, {8: -1}, {9: 2},
-                   {9: -1}, {10: ODD2}, {11: 0}, {11: -1}, {12: ODD2}, {13: None}, {13: ODD2},
-                   {14: None}, {14: ODD8}, {15: ODD8}, {16: ODD8}, {17: None}, {17: ODD2},
-                   {18: ODD2},
-                   {0: None},                       # outputs and a weight without their input
-                   {3: None}, {0: None, 14: None}, {3: None, 5: None}, {0: None, 2: None},
-                   {15: None, 16: None},            # nowhere to write the latents
-                   {0: None, 2: None, 14: None, 3: None, 5: None, 15: None, 16: None},
-                   {11: 2 ** 30}):                  # more than 2^30 tasks
-        assert call("mla_decode_norm_rope", args, change) == 1, change
-    assert call("mla_decode_norm_rope", args, d=good_dims(qk_rope=32)) == 2
-    assert binding.lib().mla_decode_norm_rope(None, *args) == 1
+    good = {name: OK for name, kind in Args._fields_ if kind is ctypes.c_void_p}
+    good.update(q_stride=16 * 192, kv_stride=576, eps=EPS, max_position=9, interleaved=1, max_new=1)
+
+    def code(d=None, **change):
+        return call("mla_decode_norm_rope", [ctypes.byref(Args(**dict(good, **change))), None], d=d)
+
+    pointers = ("q", "kv", "q_weight", "kv_weight", "cos_sin", "q_out", "rows", "kv_cache")
+    bad = [{name: ODD8} for name in pointers]
+    bad += [{name: ODD2} for name in ("positions", "new_lens", "seq_lens", "block_table", "status")]
+    bad += [{name: None} for name in ("cos_sin", "seq_lens", "q_out", "block_table")]
+    bad += [{"q_stride": n} for n in (16 * 192 - 8, 16 * 192 + 4, -16 * 192)]
+    bad += [{"kv_stride": n} for n in (568, 580, -576)]
+    bad += [{"eps": x} for x in (0.0, -1.0, math.nan, math.inf)]
+    bad += [{"max_position": 0}, {"max_position": -1}, {"interleaved": 2}, {"interleaved": -1},
+            {"max_new": 0}, {"max_new": -1}, {"max_new": 2 ** 30}]  # (more than 2^30 tasks)
+    no_q, no_kv = dict(q=None, q_out=None, q_weight=None), dict(kv=None, kv_weight=None, rows=None,
+                                                               kv_cache=None)
+    # Outputs and weights without their input, and nowhere to write the latents.
+    bad += [dict(no_q, q_out=OK), dict(no_q, q_weight=OK), dict(no_kv, kv_weight=OK),
+            dict(no_kv, rows=OK), dict(no_kv, kv_cache=OK), {"rows": None, "kv_cache": None},
+            {**no_q, **no_kv}]
+    for change in bad:
+        assert code(**change) == 1, change
+    assert call("mla_decode_norm_rope", [None, None]) == 1
+    assert code(d=good_dims(qk_rope=32)) == 2
+    assert binding.lib().mla_decode_norm_rope(None, ctypes.byref(Args(**good)), None) == 1
 
 
 def test_python_call_checks_types_and_shapes():
