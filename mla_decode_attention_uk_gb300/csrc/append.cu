@@ -74,8 +74,7 @@ __device__ __forceinline__ Block4 block4(const float (&v)[8], int se) {
   b.codes = b.e == kExpNan4 ? 0u : e2m1x8(v, exp2_int(kExpBias4 - b.e - se));
   return b;
 }
-// A whole block of bf16 values, two at a time (their maximum is exact, and so are the
-// products with a power of two but for what vanishes): e, and the codes of a and of b.
+// Eight bf16 values times a power of two (exact but for what vanishes) to codes.
 __device__ __forceinline__ uint32_t e2m1x8(const uint4& x, __nv_bfloat162 mul) {
   const uint32_t in[4] = {x.x, x.y, x.z, x.w};
   uint32_t w = 0;
@@ -86,15 +85,10 @@ __device__ __forceinline__ uint32_t e2m1x8(const uint4& x, __nv_bfloat162 mul) {
          << (8 * k);
   return w;
 }
-__device__ __forceinline__ int block4(const uint4& a, const uint4& b, int se, uint32_t& codes_a,
-                                      uint32_t& codes_b) {
+// The largest size in a block, as its fp32 bits (NaN above all).
+__device__ __forceinline__ uint32_t block_top(const uint4& a, const uint4& b) {
   __nv_bfloat162 m = max_abs(max_abs(max_abs(__habs2(as_bf162(a.x)), a.y), a.z), a.w);
-  m = max_abs(max_abs(max_abs(max_abs(m, b.x), b.y), b.z), b.w);
-  const int e = block_exp4(__uint_as_float(larger_half(m)), se);
-  const __nv_bfloat162 mul = __float2bfloat162_rn(exp2_int(kExpBias4 - e - se));
-  codes_a = e == kExpNan4 ? 0u : e2m1x8(a, mul);
-  codes_b = e == kExpNan4 ? 0u : e2m1x8(b, mul);
-  return e;
+  return larger_half(max_abs(max_abs(max_abs(max_abs(m, b.x), b.y), b.z), b.w));
 }
 // Four lanes' two exponents as a byte, for the first of them.
 __device__ __forceinline__ uint8_t exps_byte(int e) {
@@ -133,6 +127,14 @@ struct Group {
     if ((tid & 31) == 0) warp_top[tid >> 5] = top;
     sync();
     for (int w = 0; w < kAppThreads / 32; ++w) top = fmaxf(top, warp_top[w]);
+    return top;
+  }
+  // The same of fp32 bits, NaN above all.
+  __device__ uint32_t max_of_bits(uint32_t top) const {
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((tid & 31) == 0) warp_top[tid >> 5] = __uint_as_float(top);
+    sync();
+    for (int w = 0; w < kAppThreads / 32; ++w) top = max(top, __float_as_uint(warp_top[w]));
     return top;
   }
 };
@@ -180,51 +182,151 @@ struct Target {
 constexpr int kHeld = kPage * kChunks / kAppThreads;
 static_assert(kHeld * kAppThreads == kPage * kChunks, "a page is whole passes");
 
-// The 4-bit cache's threads hold blocks of 16 values, two chunks of 16 bytes: every
-// other lane takes its second one first, so that eight lanes' loads of 16 bytes meet
-// all banks.
-constexpr int kBlocks = kDqk / kBlock4;  // of a row, the RoPE columns' four among them
-__device__ __forceinline__ bool swapped_halves(int tid) { return (tid ^ (tid >> 2)) & 1; }
-
-// The part of fill_page behind the page's scale, for the 4-bit cache.  The threads read
-// the new rows a second time (held in registers they were spilled, 36 us; eight values
-// to a thread and a shuffle for the block's maximum 28 us: 13 prompts of 512 to 8190
-// tokens).
-template <typename Taken>
-__device__ __forceinline__ void store_page4(const AppendParams& P, const Group& grp,
-                                            const Place& at, const Target& to,
-                                            const uint4* rows_sh, float scale,
-                                            const Taken& taken) {
-  const int r0 = at.r0(), r1 = at.r1();
-  const int n = (r1 - r0) * kBlocks, whole_warps = (n + 31) & ~31;
-  const int se = static_cast<int>(__float_as_uint(scale) >> 23) - 127;
+// Fills a page from its new rows, which a thread holds in registers between their
+// maximum and the codes; `taken` is called once all have theirs.  kFew skips what
+// a few rows do not fill, at a price for whole pages (14 -> 15.5 us).  (Every thread
+// has its Target before the first barrier here; one thread replaces the scale
+// behind it.)
+template <bool kFew, typename Taken>
+__device__ __forceinline__ void fill_page8(const AppendParams& P, const Group& grp,
+                                          const Place& at, const Target& to,
+                                          const uint4* rows_sh, const Taken& taken) {
+  const int r0 = at.r0(), r1 = at.r1(), n = (r1 - r0) * kChunks;
+  uint4 x[kHeld];
+  __nv_bfloat162 most = __float2bfloat162_rn(0.0f);
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int i = grp.tid + k * kAppThreads;
+    if (kFew && k * kAppThreads >= n) break;
+    x[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (i < n) x[k] = rows_sh[i];
+    most = absmax8(most, x[k]);
+  }
+  float top = grp.max_of(fmaxf(__low2float(most), __high2float(most)));
+  taken();
+  if (top == INFINITY) {  // rare: once more, without the infinities
+    grp.sync();
+    top = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      if (!kFew || k * kAppThreads < n) top = finite_absmax8(top, x[k]);
+    top = grp.max_of(top);
+  }
+  if (!to.in_pool) return;
+  float scale = exp2_int(page_scale_exp(top));
+  if (r0 > 0) scale = fmaxf(scale, next_power_of_two(to.old));
+  uint2* const dst = reinterpret_cast<uint2*>(P.kv + static_cast<size_t>(to.page) * kPageBytes8);
   const __nv_bfloat162 inv = __float2bfloat162_rn(1.0f / scale);
-  uint8_t* const dst = P.kv + static_cast<size_t>(to.page) * kPageBytes4;
-  const bool swapped = swapped_halves(grp.tid);
-#pragma unroll 2
-  for (int i = grp.tid; i < whole_warps; i += kAppThreads) {
-    const int c = i % kBlocks;
-    uint4 xa = make_uint4(0u, 0u, 0u, 0u), xb = xa;
-    if (i < n) {
-      xa = rows_sh[2 * i + swapped];
-      xb = rows_sh[2 * i + !swapped];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int i = grp.tid + k * kAppThreads;
+    if (kFew && k * kAppThreads >= n) break;
+    if (i < n) dst[r0 * kChunks + i] = codes8(x[k], inv);
+  }
+  if (grp.tid == 0) P.kv_scale[to.page] = scale;
+  // Rows that stay: cleared in a page that starts here, re-coded if the scale
+  // grew.
+  if (r0 > 0 && scale == to.old) return;
+  const float ratio = to.old / scale;
+  for (int i = grp.tid; i < kPage * kChunks; i += kAppThreads) {
+    if (i >= r0 * kChunks && i < r1 * kChunks) continue;
+    uint2 c = make_uint2(0u, 0u);
+    if (r0 > 0) {
+      c = dst[i];
+      uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float2 p = e4m3x2_to_float2(w[k]), q = e4m3x2_to_float2(w[k] >> 16);
+        w[k] = e4m3x4(mul_odd(p.x, ratio), mul_odd(p.y, ratio), mul_odd(q.x, ratio),
+                      mul_odd(q.y, ratio));
+      }
+      c = make_uint2(w[0], w[1]);
     }
-    uint8_t* const row = dst + (r0 + i / kBlocks) * kRow4;
-    uint32_t wa, wb;
-    const int e = block4(xa, xb, se, wa, wb);
-    const int next = __shfl_xor_sync(0xffffffffu, e, 1);
-    if (i >= n || !to.in_pool) continue;
-    if (c < kLora / kBlock4) {
-      *reinterpret_cast<uint2*>(row + 8 * c) = swapped ? make_uint2(wb, wa) : make_uint2(wa, wb);
-      if ((c & 1) == 0) row[kRowExps4 + (c >> 1)] = static_cast<uint8_t>(e | (next << 4));
-    } else {
-      const uint2 ca = codes8(xa, inv), cb = codes8(xb, inv);
-      *reinterpret_cast<uint4*>(row + kRowRope4 + 16 * (c - kLora / kBlock4)) =
-          swapped ? make_uint4(cb.x, cb.y, ca.x, ca.y) : make_uint4(ca.x, ca.y, cb.x, cb.y);
+    dst[i] = c;
+  }
+}
+
+// The same into the 4-bit cache: a thread has blocks of 16 values, two chunks of 16 bytes,
+// first the rows' latent ones, then their RoPE columns (a warp's are of one kind).  Every
+// other lane takes its second chunk first, so that eight lanes' loads meet all banks.
+// The blocks' maxima stay in registers; the rows are read a second time for the codes
+// (held, they were spilled).  13 prompts of 512 to 8190 tokens: 36 us with the rows held,
+// 28 with eight values to a thread and a shuffle for the block's maximum, 19 with latent
+// and RoPE blocks in one warp and the maxima found twice.
+constexpr int kLatBlocks = kLora / kBlock4, kRopeBlocks = kRope / kBlock4;
+constexpr int kBlocks = kLatBlocks + kRopeBlocks;  // of a row: 36
+constexpr int kPasses = kPage * kBlocks / kAppThreads;
+static_assert(kPasses * kAppThreads == kPage * kBlocks && kLatBlocks == 32, "whole passes");
+
+template <bool kFew, typename Taken>
+__device__ __forceinline__ void fill_page4(const AppendParams& P, const Group& grp,
+                                           const Place& at, const Target& to,
+                                           const uint4* rows_sh, const Taken& taken) {
+  const int r0 = at.r0(), r1 = at.r1(), rows = r1 - r0, n = rows * kBlocks;
+  const int swapped = (grp.tid ^ (grp.tid >> 2)) & 1;
+  // Block i's first chunk.
+  auto chunk_of = [&](int i) {
+    const int u = i - rows * kLatBlocks;
+    return u < 0 ? (i / kLatBlocks) * kChunks + 2 * (i % kLatBlocks)
+                 : (u / kRopeBlocks) * kChunks + 2 * kLatBlocks + 2 * (u % kRopeBlocks);
+  };
+  uint32_t tops[kPasses], top = 0;
+#pragma unroll
+  for (int k = 0; k < kPasses; ++k) {
+    const int i = grp.tid + k * kAppThreads;
+    tops[k] = 0;
+    if (kFew && k * kAppThreads >= n) break;
+    if (i < n) {
+      const uint4* const x = rows_sh + chunk_of(i);
+      tops[k] = block_top(x[swapped], x[swapped ^ 1]);
+    }
+    top = max(top, tops[k]);
+  }
+  top = grp.max_of_bits(top);
+  float largest = __uint_as_float(top);
+  if (top >= 0x7f800000u) {  // rare: once more, without infinities and NaN
+    grp.sync();
+    largest = 0.0f;
+    for (int i = grp.tid; i < rows * kChunks; i += kAppThreads)
+      largest = finite_absmax8(largest, rows_sh[i]);
+    largest = grp.max_of(largest);
+  }
+  float scale = exp2_int(page_scale_exp(largest));
+  if (r0 > 0) scale = fmaxf(scale, next_power_of_two(to.old));
+  const int se = static_cast<int>(__float_as_uint(scale) >> 23) - 127;
+  uint8_t* const dst = P.kv + static_cast<size_t>(to.page) * kPageBytes4;
+  if (to.in_pool) {
+#pragma unroll
+    for (int k = 0; k < kPasses; ++k) {
+      if (kFew && k * kAppThreads >= n) break;
+      const int i = grp.tid + k * kAppThreads, u = i - rows * kLatBlocks;
+      const int e = block_exp4(__uint_as_float(tops[k]), se);
+      const int next = __shfl_xor_sync(0xffffffffu, e, 1);
+      if (i >= n) continue;
+      const uint4* const x = rows_sh + chunk_of(i);
+      const uint4 xa = x[swapped], xb = x[swapped ^ 1];
+      if (u < 0) {
+        uint8_t* const row = dst + (r0 + i / kLatBlocks) * kRow4;
+        const int c = i % kLatBlocks;
+        const __nv_bfloat162 mul = __float2bfloat162_rn(exp2_int(kExpBias4 - e - se));
+        uint32_t wa = e2m1x8(xa, mul), wb = e2m1x8(xb, mul);
+        if (e == kExpNan4) wa = wb = 0u;
+        *reinterpret_cast<uint2*>(row + 8 * c) =
+            swapped ? make_uint2(wb, wa) : make_uint2(wa, wb);
+        if ((c & 1) == 0) row[kRowExps4 + (c >> 1)] = static_cast<uint8_t>(e | (next << 4));
+      } else {
+        const __nv_bfloat162 inv = __float2bfloat162_rn(1.0f / scale);
+        const uint2 ca = codes8(xa, inv), cb = codes8(xb, inv);
+        *reinterpret_cast<uint4*>(dst + (r0 + u / kRopeBlocks) * kRow4 + kRowRope4 +
+                                  16 * (u % kRopeBlocks)) =
+            swapped ? make_uint4(cb.x, cb.y, ca.x, ca.y) : make_uint4(ca.x, ca.y, cb.x, cb.y);
+      }
     }
   }
-  grp.sync();
-  taken();
+  if (!kFew) {
+    grp.sync();
+    taken();
+  }
   if (!to.in_pool) return;
   if (grp.tid == 0) P.kv_scale[to.page] = scale;
   if (r0 == 0) {  // a page that starts here: cleared behind the new rows
@@ -258,72 +360,14 @@ __device__ __forceinline__ void store_page4(const AppendParams& P, const Group& 
   }
 }
 
-// Fills a page from its new rows, which a thread holds in registers between their
-// maximum and the codes; `taken` is called once all have theirs.  kFew skips what
-// a few rows do not fill, at a price for whole pages (14 -> 15.5 us).  (Every thread
-// has its Target before the first barrier here; one thread replaces the scale
-// behind it.)
 template <bool kFew, bool kFp4, typename Taken>
 __device__ __forceinline__ void fill_page(const AppendParams& P, const Group& grp,
                                           const Place& at, const Target& to,
                                           const uint4* rows_sh, const Taken& taken) {
-  const int r0 = at.r0(), r1 = at.r1(), n = (r1 - r0) * kChunks;
-  uint4 x[kHeld];
-  __nv_bfloat162 most = __float2bfloat162_rn(0.0f);
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k) {
-    const int i = grp.tid + k * kAppThreads;
-    if (kFew && k * kAppThreads >= n) break;
-    x[k] = make_uint4(0u, 0u, 0u, 0u);
-    if (i < n) x[k] = rows_sh[i];
-    most = absmax8(most, x[k]);
-  }
-  float top = grp.max_of(fmaxf(__low2float(most), __high2float(most)));
-  if constexpr (!kFp4) taken();
-  if (top == INFINITY) {  // rare: once more, without the infinities
-    grp.sync();
-    top = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k)
-      if (!kFew || k * kAppThreads < n) top = finite_absmax8(top, x[k]);
-    top = grp.max_of(top);
-  }
-  if (!kFp4 && !to.in_pool) return;
-  float scale = exp2_int(page_scale_exp(top));
-  if (r0 > 0) scale = fmaxf(scale, next_power_of_two(to.old));
-  if constexpr (kFp4) {
-    store_page4(P, grp, at, to, rows_sh, scale, taken);
-    return;
-  }
-  uint2* const dst = reinterpret_cast<uint2*>(P.kv + static_cast<size_t>(to.page) * kPageBytes8);
-  const __nv_bfloat162 inv = __float2bfloat162_rn(1.0f / scale);
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k) {
-    const int i = grp.tid + k * kAppThreads;
-    if (kFew && k * kAppThreads >= n) break;
-    if (i < n) dst[r0 * kChunks + i] = codes8(x[k], inv);
-  }
-  if (grp.tid == 0) P.kv_scale[to.page] = scale;
-  // Rows that stay: cleared in a page that starts here, re-coded if the scale
-  // grew.
-  if (r0 > 0 && scale == to.old) return;
-  const float ratio = to.old / scale;
-  for (int i = grp.tid; i < kPage * kChunks; i += kAppThreads) {
-    if (i >= r0 * kChunks && i < r1 * kChunks) continue;
-    uint2 c = make_uint2(0u, 0u);
-    if (r0 > 0) {
-      c = dst[i];
-      uint32_t w[2] = {c.x, c.y};
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const float2 p = e4m3x2_to_float2(w[k]), q = e4m3x2_to_float2(w[k] >> 16);
-        w[k] = e4m3x4(mul_odd(p.x, ratio), mul_odd(p.y, ratio), mul_odd(q.x, ratio),
-                      mul_odd(q.y, ratio));
-      }
-      c = make_uint2(w[0], w[1]);
-    }
-    dst[i] = c;
-  }
+  if constexpr (kFp4)
+    fill_page4<kFew>(P, grp, at, to, rows_sh, taken);
+  else
+    fill_page8<kFew>(P, grp, at, to, rows_sh, taken);
 }
 
 // A few new tokens per sequence: one CTA per sequence and page that they can
