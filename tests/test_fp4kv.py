@@ -571,3 +571,231 @@ def test_a_cache_beyond_two_gigabytes():
     binding.gather_fp4kv(d, kv4, kvs, t.cuda(), cuda_ints([256]), rows[:, :64].contiguous())
     assert torch.equal(ref.decode(kv4[at[3]].cpu()) * float(kvs[at[3]]),
                        inp.cache[order[3]].double())
+
+
+@gpu
+def test_one_plan_serves_every_cache_and_the_steps_equal_the_run():
+    inp, kv4, kvs = fp4_inputs(make_inputs(4, [700, 64, 65, 300], 2, 32, seed=33))
+    g = inp.to(torch.device("cuda"))
+    k, s = kv4.cuda(), kvs.cuda()
+    for fp8_kv in (True, False):  # a plan of either balance
+        m = binding.MlaDecode(binding.dims_for(g.q, g.cache, g.block_table), fp8_kv=fp8_kv)
+        (o1, l1), (o2, l2), (o3, l3) = [(torch.empty(4, 2, 32, 128, dtype=BF, device="cuda"),
+                                         torch.empty(4, 2, 32, device="cuda")) for _ in range(3)]
+        m.plan(g.seq_lens)
+        m.run(g.q, g.cache, g.block_table, g.seq_lens, g.w_uk, g.w_uv, g.scale, o1, l1)
+        m.run_fp4kv(g.q, k, s, g.block_table, g.seq_lens, g.w_uk, g.w_uv, g.scale, o2, l2)
+        m.absorb(g.q, g.w_uk)
+        m.attend_fp4kv(k, s, g.block_table, g.seq_lens, g.scale, l3)
+        m.combine(g.scale, l3)
+        m.up_project(g.w_uv, o3)
+        assert m.check() == 0
+        assert torch.equal(o2, o3) and torch.equal(l2, l3)
+        # The bf16 cache holds the same values: the two parity bounds together.
+        assert float((o1.float() - o2.float()).abs().max()) <= 2e-2 + ref8.OUT_MAX
+        assert float((l1 - l2).abs().max()) <= 2e-3
+
+
+@gpu
+@pytest.mark.parametrize("B,H,ranges", [(24, 16, 1), (24, 128, 1), (160, 16, 2), (40, 64, 0)])
+def test_runs_of_other_queries_back_to_back_on_one_plan(B, H, ranges):
+    inp, kv4, kvs = fp4_inputs(make_inputs(B, [500 + 37 * i % 300 for i in range(B)], 1, H, seed=80))
+    g = inp.to(torch.device("cuda"))
+    k, s = kv4.cuda(), kvs.cuda()
+    m = binding.MlaDecode(binding.dims_for(g.q, g.cache, g.block_table), num_ranges=ranges,
+                          fp8_kv=True)
+    gen = torch.Generator().manual_seed(81)
+    queries = [torch.randn(B, 1, H, 192, generator=gen).to(BF).cuda() for _ in range(4)]
+    alone, together = [[(torch.zeros(B, 1, H, 128, dtype=BF, device="cuda"),
+                         torch.zeros(B, 1, H, device="cuda")) for _ in queries] for _ in range(2)]
+
+    def run(q, out, lse):
+        m.run_fp4kv(q, k, s, g.block_table, g.seq_lens, g.w_uk, g.w_uv, g.scale, out, lse)
+
+    m.plan(g.seq_lens)
+    for q, (out, lse) in zip(queries, alone):
+        run(q, out, lse)
+        torch.cuda.synchronize()
+    for _ in range(5):
+        for q, (out, lse) in zip(queries, together):
+            run(q, out, lse)
+    assert m.check() == 0
+    for (o1, l1), (o2, l2) in zip(alone, together):
+        assert torch.equal(o1, o2) and torch.equal(l1, l2)
+
+
+@gpu
+@pytest.mark.parametrize("H,T,ranges", [(16, 1, 1), (16, 1, 3), (128, 1, 1), (80, 1, 2)])
+def test_a_maximum_that_rises_with_every_page_of_many_pieces(H, T, ranges):
+    # Scores that grow by more than the lazy maximum's slack from page to page: every
+    # page but a piece's first rescales the output, while the next pieces' pages are
+    # expanded and their query tiles take the slots that become free.
+    lens = [64 * (3 + i % 4) - i % 7 for i in range(48)]
+    inp = make_inputs(len(lens), lens, T, H, seed=82)
+    inp.q[..., :128] = 0.0
+    inp.q[..., 128:] = 1.0
+    inp.cache[..., 512:] = 0.0
+    for b, n in enumerate(lens):
+        for j in range((n + 63) // 64):
+            # 64 products of 2 j, times 1 / sqrt(192): 9.2 a page, 8 ln 2 = 5.5.
+            inp.cache[int(inp.block_table[b, j]), :, 512:] = 2.0 * j
+    inp, kv4, kvs = fp4_inputs(inp)
+    out, lse = run_fp4(inp, kv4, kvs, num_ranges=ranges)
+    assert_parity(compare(inp, out, lse), "ranges %d" % ranges)
+    for _ in range(20):
+        out2, lse2 = run_fp4(inp, kv4, kvs, num_ranges=ranges)
+        assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+@gpu
+@pytest.mark.parametrize("low,high", [(-12, 2), (-30, 0)])
+def test_pages_of_very_different_scales(low, high):
+    inp = make_inputs(3, [1000, 130, 640], 1, 32, seed=27)
+    g = torch.Generator().manual_seed(28)
+    e = torch.randint(low, high + 1, (inp.cache.shape[0],), generator=g)
+    inp.cache = (inp.cache.float() * torch.exp2(e.float())[:, None, None]).to(BF)
+    inp.scale = inp.scale / 2.0 ** max(0, high)
+    inp, kv4, kvs = fp4_inputs(inp)
+    out, lse = run_fp4(inp, kv4, kvs)
+    s = compare(inp, out, lse)
+    # Values up to 2^high: the outputs' bounds grow with them.
+    assert s["out_max"] <= ref8.OUT_MAX * 2.0 ** max(0, high) and s["lse_max"] <= 1e-3, s
+
+
+@gpu
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_a_query_that_is_not_finite_gives_nan(value):
+    for H, num_ranges, lens in ((16, 0, [2, 130, 90]), (128, 2, [700, 900, 64])):
+        inp, kv4, kvs = fp4_inputs(make_inputs(3, lens, 2, H, seed=48))
+        out0, lse0 = run_fp4(inp, kv4, kvs, num_ranges=num_ranges)
+        inp.q[:, 1, 3, 5] = value
+        inp.q[:, 0, H - 1, 140] = value
+        out, lse = run_fp4(inp, kv4, kvs, num_ranges=num_ranges)
+        changed = torch.zeros_like(lse, dtype=torch.bool)
+        changed[:, 1, 3] = changed[:, 0, H - 1] = True
+        assert out[changed].isnan().all() and lse[changed].isnan().all()
+        assert torch.equal(out[~changed], out0[~changed])
+        assert torch.equal(lse[~changed], lse0[~changed])
+
+
+@gpu
+def test_lengths_out_of_range_are_clamped_and_reported():
+    inp, kv4, kvs = fp4_inputs(make_inputs(2, [100, 64], 1, 16, seed=32))
+    out0, lse0 = run_fp4(inp, kv4, kvs)
+    inp.seq_lens = torch.tensor([100, 0], dtype=torch.int32)
+    out, lse = run_fp4(inp, kv4, kvs, expect=5)
+    assert torch.equal(out[0], out0[0]) and torch.equal(lse[0], lse0[0])
+
+
+@gpu
+def test_two_calls_at_once_on_two_streams():
+    # Attention on one stream, appends, keys and reading back of other caches on others.
+    cases = []
+    for seed in (38, 39):
+        inp, kv4, kvs = fp4_inputs(make_inputs(6, [900, 64, 65, 300, 1, 511], 1, 64, seed=seed))
+        cases.append((inp, kv4, kvs, *run_fp4(inp, kv4, kvs)))
+    dev = torch.device("cuda")
+    live = []
+    for inp, kv4, kvs, _, _ in cases:
+        g = inp.to(dev)
+        m = binding.MlaDecode(binding.dims_for(g.q, g.cache, g.block_table), fp8_kv=True)
+        live.append((g, kv4.cuda(), kvs.cuda(), m, torch.empty(6, 1, 64, 128, dtype=BF, device=dev),
+                     torch.empty(6, 1, 64, device=dev), torch.cuda.Stream(),
+                     torch.zeros(6, 900, 576, dtype=BF, device=dev),
+                     torch.zeros(kv4.shape[0], 576, dtype=BF, device=dev)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, k, s, m, out, lse, st, rows, keys in live:
+            with torch.cuda.stream(st):
+                binding.gather_fp4kv(m.dims, k, s, g.block_table, g.seq_lens, rows, g.seq_lens)
+                binding.append_fp4kv(m.dims, rows, k, s, g.block_table, g.seq_lens, g.seq_lens)
+                binding.page_keys_fp4kv(m.dims, k, s, g.block_table, g.seq_lens, 900, keys,
+                                        g.seq_lens)
+                m.plan(g.seq_lens)
+                m.run_fp4kv(g.q, k, s, g.block_table, g.seq_lens, g.w_uk, g.w_uv, g.scale, out,
+                            lse)
+    torch.cuda.synchronize()
+    for (inp, kv4, kvs, out0, lse0), (_, k, s, m, out, lse, _, _, _) in zip(cases, live):
+        assert m.check() == 0
+        # What is read back and appended again keeps its values, whatever the page's scale
+        # becomes (it may shrink with the largest value's rounding).
+        v = ref.decode(k.cpu()) * s.cpu().double()[:, None, None]
+        w = ref.decode(kv4) * kvs.double()[:, None, None]
+        for b, n in enumerate(inp.seq_lens.tolist()):
+            pages = inp.block_table[b, :(n + 63) // 64].long()
+            assert torch.equal(v[pages].reshape(-1, 576)[:n], w[pages].reshape(-1, 576)[:n])
+        s2 = compare(inp, out.cpu(), lse.cpu())
+        assert_parity(s2, "two streams")
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp4", "fp8", "bf16"])
+@pytest.mark.parametrize("B", [255, 256, 257])
+@pytest.mark.parametrize("max_new", [64, 65])
+def test_gather_and_keys_with_and_without_a_list(kind, B, max_new):
+    # Up to 256 sequences of more than 64 tokens go by a list of their pages.
+    lens = [(37 * i) % (max_new + 30) for i in range(B)]
+    new = [min(n, max_new) - (i % 3 == 0 and n > 0) for i, n in enumerate(lens)]
+    table, used = tables(lens, 67)
+    tensors, values = any_cache(kind, used + 1, 68)
+    if kind != "bf16":  # finite ones, for the means
+        if kind == "fp8":
+            tensors[0] %= 0x70
+            values = ref8.values(tensors[0]) * tensors[1].double()[:, None, None]
+        else:
+            tensors[0][..., 256:272] &= 0x77
+            tensors[0][..., 272:] %= 0x70
+            values = ref.decode(tensors[0]) * tensors[1].double()[:, None, None]
+    rows, st = run_gather(kind, tensors, table, lens, new, max_new)
+    assert st == 0
+    want = torch.full((B, max_new, 576), 7.0, dtype=BF)
+    keys, size = torch.full((2, used + 1, 576), 7.0, dtype=torch.float64)
+    for b, n in enumerate(new):
+        if n == 0:
+            continue
+        pages = table[b, :(lens[b] + 63) // 64].long()
+        want[b, :n] = values[pages].reshape(-1, 576)[lens[b] - n:lens[b]].float().to(BF)
+        for j in range((lens[b] - n) // 64, len(pages)):
+            filled = values[pages[j], :lens[b] - 64 * j]
+            keys[pages[j]], size[pages[j]] = filled.mean(dim=0), filled.abs().mean(dim=0)
+    assert torch.equal(rows, want)
+    d = good_dims(batch=B, num_pages=used + 1, max_pages_per_seq=table.shape[1])
+    f = dict(bf16=binding.page_keys, fp8=binding.page_keys_fp8kv, fp4=binding.page_keys_fp4kv)[kind]
+    got = torch.full((used + 1, 576), 7.0, dtype=BF, device="cuda")
+    f(d, *[t.cuda() for t in tensors], table.cuda(), cuda_ints(lens), max_new, got, cuda_ints(new))
+    # As in test_page_keys_are_the_means_of_the_filled_rows.
+    bound = keys.abs() * 2.0 ** -8 + size * 66 * 2.0 ** -24
+    assert bool(((got.cpu().double() - keys).abs() <= bound).all())
+
+
+def test_run_and_attend_check_every_tensor(monkeypatch):
+    # (In host memory: a call whose tensors are right is refused for that alone.)
+    monkeypatch.setattr(binding, "workspace_size", lambda d, ranges=0: 4096)
+    B, T, H = 2, 2, 16
+    m = binding.MlaDecode(good_dims(q_len=T), device=torch.device("cpu"))
+    good = dict(q=torch.zeros(B, T, H, 192, dtype=BF),
+                kv4=torch.zeros(4, 64, 336, dtype=torch.uint8), kv_scale=torch.ones(4),
+                block_table=torch.zeros(B, 2, dtype=torch.int32),
+                seq_lens=torch.ones(B, dtype=torch.int32),
+                w_uk=torch.zeros(H, 128, 512, dtype=BF), w_uv=torch.zeros(H, 512, 128, dtype=BF),
+                out=torch.zeros(B, T, H, 128, dtype=BF), lse=torch.zeros(B, T, H))
+    attend = ("kv4", "kv_scale", "block_table", "seq_lens", "lse")
+
+    def refused(name, **change):
+        a = dict(good, **change)
+        with pytest.raises(ValueError, match="^%s: " % name):
+            m.run_fp4kv(scale=0.07, **a)
+        if name in attend:
+            with pytest.raises(ValueError, match="^%s: " % name):
+                m.attend_fp4kv(scale=0.07, **{k: a[k] for k in attend})
+
+    for name, t in good.items():
+        refused(name, **{name: None})
+        refused(name, **{name: t.double()})                          # another type
+        refused(name, **{name: t[:-1]})                              # too short
+        refused(name, **{name: torch.cat([t, t])[::2]})              # strided
+    refused("kv4", kv4=torch.zeros(4, 64, 576, dtype=torch.uint8))   # the 8-bit cache
+    with pytest.raises(ValueError, match="^kv4: .*CUDA device"):
+        m.run_fp4kv(scale=0.07, **good)
+    with pytest.raises(ValueError, match="^kv4: .*CUDA device"):
+        m.attend_fp4kv(scale=0.07, **{k: good[k] for k in attend})

@@ -219,6 +219,43 @@ def test_columns_of_wider_projections(wide_q, wide_kv):
 
 
 @gpu
+@pytest.mark.parametrize("wide_q,wide_kv", [(0, 8), (8, 0), (576, 1024)])
+@pytest.mark.parametrize("B,max_new", [(1, 1), (1, 5), (4, 1), (4, 3), (4, 64), (3, 65)])
+def test_columns_of_wider_projections_of_few_tokens(wide_q, wide_kv, B, max_new):
+    lens = [max_new + 3 * i for i in range(B)]
+    check(B=B, lens=lens, new=[max_new - (i == 1) for i in range(B)], max_new=max_new,
+          wide_q=wide_q, wide_kv=wide_kv, seed=9)
+
+
+@gpu
+@pytest.mark.parametrize("B", [255, 256, 257])
+@pytest.mark.parametrize("max_new", [64, 65])
+def test_with_and_without_a_list(B, max_new):
+    # Up to 256 sequences of more than 64 tokens go by a list of their tokens, which many
+    # of them do not have.
+    lens = [(37 * i) % (max_new + 30) for i in range(B)]
+    check(B=B, lens=lens, new=[min(n, max_new) if i % 4 else 0 for i, n in enumerate(lens)],
+          max_new=max_new, to="both", seed=10)
+
+
+@gpu
+@pytest.mark.parametrize("max_new", [1, 70])
+def test_queries_alone_and_latents_alone(max_new):
+    g = torch.Generator().manual_seed(11)
+    d = good_dims(batch=2, num_heads=32, num_pages=4, max_pages_per_seq=2)
+    q = torch.randn(2, max_new, 32, 192, generator=g).to(BF).cuda()
+    kv = torch.randn(2, max_new, 576, generator=g).to(BF).cuda()
+    lens = torch.tensor([max_new, max_new + 20], dtype=torch.int32).cuda()
+    cs, w = cos_sin_table(128).cuda(), torch.randn(512, generator=g).to(BF).cuda()
+    both = torch.empty_like(q), torch.empty_like(kv)
+    binding.norm_rope(d, lens, cs, q=q, q_out=both[0], kv=kv, kv_weight=w, rows=both[1])
+    alone = torch.empty_like(q), torch.empty_like(kv)
+    binding.norm_rope(d, lens, cs, q=q, q_out=alone[0])
+    binding.norm_rope(d, lens, cs, kv=kv, kv_weight=w, rows=alone[1])
+    assert torch.equal(both[0], alone[0]) and torch.equal(both[1], alone[1])
+
+
+@gpu
 @pytest.mark.parametrize("interleaved", [True, False])
 def test_given_positions_and_in_place(interleaved):
     check(positions="random", interleaved=interleaved, seed=4)
