@@ -458,7 +458,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
             }
             tc_fence_after();
             const uint64_t bd = dslot0 + static_cast<uint64_t>((s * kSlot) >> 4);
-#pragma unroll
+#pragma unroll 4
             for (int kk = 0; kk < kLora / 32; ++kk)  // four steps to a box
               umma_f8_ta(tmem + 64 * sb, tmem + kTmemQ + 8 * kk,
                          bd + (((kk >> 2) * kBox) >> 4) + (kk & 3) * 2, idesc, kk != 0);
@@ -854,22 +854,29 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
               tc_fence_before();
             }
           }
-          // Codes are the upper bytes of fp16 pairs, four to a word.
-          uint32_t hw[8], mw[8];
-          if (m_used == -INFINITY) {
+          // No key yet, or NaN alone, which a maximum passes over.
+          const bool none = m_used == -INFINITY;
+          if (none && kb < n_row) l = l_r = __uint_as_float(0x7fffffffu);
+          const float add = none ? 0.0f : shift + kTopExp - m_used;
+          float se[4] = {};
+          // What the rounding of this thread's 32 weights adds up to, in fp16: the
+          // terms are exact and at most 2^-7 of a weight, so 16 sums rounded by
+          // 2^-11 move the row's sum, which is fp32, by 2^-14 of it at most.
+          __half2 err = __float2half2_rn(0.0f);
+          // P^T row: 64 bytes of hi codes (chunks 0-3), 64 of mid codes (4-7), into the
+          // page's RoPE box, which QK^T is done with.  Of a half page's the even-key thread
+          // writes the hi codes and the odd-key thread the mid codes, which cross to it.
+          // (Rows r and r + 8 of a quarter-warp's store share their swizzle, so the latter's
+          // threads write their second chunk first.)
+          const uint32_t rowaddr = sSlot0 + s * kSlot + kRopeBox8 * kBox + srow * 128;
+          const int late = (srow >> 3) & 1;
+          const uint32_t even = par ? 0x1504 : 0x5140, odd = par ? 0x3726 : 0x7362;
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            // Codes are the upper bytes of fp16 pairs, four to a word.
+            uint32_t hw[4], mw[4];
 #pragma unroll
-            for (int t = 0; t < 8; ++t) hw[t] = mw[t] = 0u;
-            // No key yet, or NaN alone, which a maximum passes over.
-            if (kb < n_row) l = l_r = __uint_as_float(0x7fffffffu);
-          } else {
-            const float add = shift + kTopExp - m_used;
-            float se[4] = {};
-            // What the rounding of this thread's 32 weights adds up to, in fp16: the
-            // terms are exact and at most 2^-7 of a weight, so 16 sums rounded by
-            // 2^-11 move the row's sum, which is fp32, by 2^-14 of it at most.
-            __half2 err = __float2half2_rn(0.0f);
-#pragma unroll
-            for (int t = 0; t < 8; ++t) {
+            for (int t = 0; t < 4; ++t) {
               uint32_t hb[2], mb[2];
 #pragma unroll
               for (int j = 2 * t; j < 2 * t + 2; ++j) {
@@ -877,52 +884,41 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
                 const float p1 = ex2_approx(fmaf(__uint_as_float(v[2 * j + 1]), mul, add));
                 se[(2 * j) & 3] += p0;
                 se[(2 * j + 1) & 3] += p1;
-                const __half2 h = __floats2half2_rn(p0, p1);
-                const __half2 hi = e5m2_in_half2(h);
-                const __half2 mid = e5m2_in_half2(__hsub2(h, hi));
-                err = __hfma2(__hsub2(__hadd2(hi, mid), h),
-                              __hge2(h, __float2half2_rn(kRoundedFrom)), err);
+                const __half2 h2 = __floats2half2_rn(p0, p1);
+                const __half2 hi = e5m2_in_half2(h2);
+                const __half2 mid = e5m2_in_half2(__hsub2(h2, hi));
+                err = __hfma2(__hsub2(__hadd2(hi, mid), h2),
+                              __hge2(h2, __float2half2_rn(kRoundedFrom)), err);
                 hb[j & 1] = bits(hi);
                 mb[j & 1] = bits(mid);
               }
               hw[t] = __byte_perm(hb[0], hb[1], 0x7531);
               mw[t] = __byte_perm(mb[0], mb[1], 0x7531);
             }
+            uint32_t out[8];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const uint32_t keep = par ? mw[t] : hw[t];
+              const uint32_t got = __shfl_xor_sync(0xffffffffu, par ? hw[t] : mw[t], 2);
+              out[2 * t] = __byte_perm(keep, got, even);
+              out[2 * t + 1] = __byte_perm(keep, got, odd);
+            }
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const int chunk = 4 * par + 2 * h + (t ^ late);
+              st_shared_v4(rowaddr + ((chunk ^ (srow & 7)) << 4), late != t ? out[4] : out[0],
+                           late != t ? out[5] : out[1], late != t ? out[6] : out[2],
+                           late != t ? out[7] : out[3]);
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = v[16 + j];
+          }
+          if (!none) {
             const float sum = (se[0] + se[1]) + (se[2] + se[3]);
             const float2 e = __half22float2(err);
             const float inv_scale = __frcp_rn(page_scale);
             l = fmaf(sum, inv_scale, l);
             l_r = fmaf(sum + (e.x + e.y), inv_scale, l_r);
-          }
-          // The even-key thread writes keys 0-31, the odd-key thread keys 32-63:
-          // half of each thread's codes cross to its partner.
-          uint32_t ph[8], pm[8];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const uint32_t keep_h = par ? hw[4 + t] : hw[t], keep_m = par ? mw[4 + t] : mw[t];
-            const uint32_t got_h = __shfl_xor_sync(0xffffffffu, par ? hw[t] : hw[4 + t], 2);
-            const uint32_t got_m = __shfl_xor_sync(0xffffffffu, par ? mw[t] : mw[4 + t], 2);
-            const uint32_t eh = par ? got_h : keep_h, oh = par ? keep_h : got_h;
-            const uint32_t em = par ? got_m : keep_m, om = par ? keep_m : got_m;
-            ph[2 * t] = __byte_perm(eh, oh, 0x5140);
-            ph[2 * t + 1] = __byte_perm(eh, oh, 0x7362);
-            pm[2 * t] = __byte_perm(em, om, 0x5140);
-            pm[2 * t + 1] = __byte_perm(em, om, 0x7362);
-          }
-          // P^T row: 64 bytes of hi codes (chunks 0-3), 64 of mid codes (4-7),
-          // into the page's RoPE box, which QK^T is done with.  Rows r and r + 8
-          // of a quarter-warp's store share their swizzle, so the latter's
-          // threads write mid before hi: eight distinct positions.
-          const uint32_t rowaddr = sSlot0 + s * kSlot + kRopeBox8 * kBox + srow * 128;
-          const bool late = (srow >> 3) & 1;
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const int h4 = 4 * (t & 1);
-            const bool is_mid = (t >= 2) != late;
-            const int chunk = (is_mid ? 4 : 0) + 2 * par + (t & 1);
-            st_shared_v4(rowaddr + ((chunk ^ (srow & 7)) << 4), is_mid ? pm[h4] : ph[h4],
-                         is_mid ? pm[h4 + 1] : ph[h4 + 1], is_mid ? pm[h4 + 2] : ph[h4 + 2],
-                         is_mid ? pm[h4 + 3] : ph[h4 + 3]);
           }
           fence_proxy_async_smem();
           __syncwarp();
