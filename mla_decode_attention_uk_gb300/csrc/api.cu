@@ -76,7 +76,7 @@ cudaError_t launch_page_keys(Kind kind, const void* cache, const float* kv_scale
 cudaError_t launch_gather(Kind kind, const void* cache, const float* kv_scale,
                           const int32_t* block_table, const int32_t* seq_lens, int max_new,
                           const int32_t* new_lens, int B, int num_pages, int max_pages,
-                          void* rows, int32_t* status, int sm_count, cudaStream_t st);
+                          void* rows, int32_t* status, cudaStream_t st);
 cudaError_t launch_prep(const mla_decode_norm_rope_args& a, const mla_decode_dims& d, int sm_count,
                         cudaStream_t st);
 cudaError_t launch_score(const CUtensorMap& tm_q, const void* page_keys,
@@ -845,7 +845,7 @@ static int newest_impl(const mla_decode_dims* d, Kind kind, bool keys, const voi
                                     new_lens, d->batch, d->num_pages, d->max_pages_per_seq,
                                     static_cast<__nv_bfloat16*>(dst), status, sms, st));
   return cuda_rc(launch_gather(kind, cache, kv_scale, block_table, seq_lens, max_new, new_lens,
-                               d->batch, d->num_pages, d->max_pages_per_seq, dst, status, sms, st));
+                               d->batch, d->num_pages, d->max_pages_per_seq, dst, status, st));
 }
 
 int mla_decode_page_keys(const mla_decode_dims* d, const void* kv_cache,

@@ -538,7 +538,9 @@ struct KeyParams {
 // The mean of a page's filled rows.  Thread t sums columns 8 (t mod 72) .. + 7 over rows
 // t / 72, + 4, ...  Four rows in flight from a bf16 cache: 13 prompts of 512 to 8190
 // tokens, in a grid of all their pages, 10.6 us (eight 11.2, sixteen 14.9: registers and
-// the ragged pages' remainders); the last pages of 128 sequences 3.0 us, 8-bit.
+// the ragged pages' remainders); 9.9 by a list of the pages, 8 bits 6.9, 4 bits 9.0 (its
+// codes' conversion: two thirds of that on the ALUs).  The last pages of 128 sequences
+// 3.0 us from 8 bits, 4.2 from 4.
 template <Kind kKind>
 __device__ __forceinline__ void page_mean(const KeyParams& P, int b, int len, int logical,
                                           float (&part)[4][kDqk]) {
@@ -558,7 +560,7 @@ __device__ __forceinline__ void page_mean(const KeyParams& P, int b, int len, in
   };
   if constexpr (kKind == Kind::kFp4) {
     const uint8_t* const base = cache + static_cast<size_t>(page) * kPageBytes4;
-    constexpr int kDeep = 8;  // rows' loads in flight
+    constexpr int kDeep = 8;  // rows' loads in flight (128 last pages: four 4.3 us, two 4.8)
     for (int r = r0; r < filled; r += 4 * kDeep) {
       Raw4 raw[kDeep];
 #pragma unroll
@@ -663,11 +665,9 @@ cudaError_t launch_append(const void* rows, int max_new, const int32_t* new_lens
 template <Kind kKind>
 static cudaError_t launch_keys(const KeyParams& P, int sm_count, cudaStream_t st) {
   const int touched = touched_pages(P.max_new, P.max_pages);
-  if (use_list(P.max_new, P.B)) {
-    const int64_t most = static_cast<int64_t>(touched) * P.B;
-    const int ctas = most < sm_count * kKeyCtas ? static_cast<int>(most) : sm_count * kKeyCtas;
-    return launch_pdl(page_keys_kernel<kKind, true>, dim3(ctas), dim3(kKeyThreads), 0, st, P);
-  }
+  if (use_list(static_cast<int64_t>(touched) * P.B, 6 * sm_count, P.B, P.new_lens))
+    return launch_pdl(page_keys_kernel<kKind, true>, dim3(sm_count * kKeyCtas), dim3(kKeyThreads),
+                      0, st, P);
   return launch_pdl(page_keys_kernel<kKind, false>, dim3(touched, P.B), dim3(kKeyThreads), 0, st,
                     P);
 }

@@ -14,7 +14,7 @@ namespace {
 
 constexpr int kGatherThreads = 288;  // four rows of 72 chunks
 
-constexpr int kGatherCtas = 4;  // on an SM, of a list
+constexpr int kGatherCtas = 4;  // on an SM
 
 struct GatherParams {
   const uint8_t* cache;
@@ -98,42 +98,21 @@ __device__ __forceinline__ void copy_page(const GatherParams& P, int b, int firs
   }
 }
 
-// One CTA per (sequence, page that it can touch), or a list of the pages.
-template <Kind kKind, bool kList>
+// One CTA per (sequence, page that it can touch).  13 prompts of 512 to 8190 tokens: 13.0
+// us from 4 bits, 4.3 TB/s (three to start: lengths, table and scale one after the other;
+// with a list of the pages 12.7, and 0.8 more for small calls; codes looked up instead of
+// converted 13.8), 13.5 from 8 bits, 16.2 from bf16 (5.4 TB/s).
+template <Kind kKind>
 __global__ void __launch_bounds__(kGatherThreads, kGatherCtas)
 gather_kernel(const __grid_constant__ GatherParams P) {
   griddep_wait();
   griddep_launch_dependents();
-  if constexpr (kList) {
-    __shared__ UnitList list;
-    const long long pages = list.make(P.seq_lens, P.new_lens, P.max_new, P.max_pages * kPage, P.B,
-                                      P.status, [](const NewTokens& nt) { return nt.pages(); });
-    for (long long f = blockIdx.x; f < pages; f += gridDim.x) {
-      const int b = list.find(f), len = list.len[b];
-      copy_page<kKind>(P, b, list.first[b], len,
-                       (len - 1) / kPage - static_cast<int>(list.upto[b] - 1 - f));
-    }
-  } else {
-    const int b = blockIdx.y;
-    NewTokens nt;
-    if (nt.load(P.seq_lens, P.new_lens, P.max_new, P.max_pages * kPage, b, threadIdx.x == 0,
-                P.status) &&
-        blockIdx.x < nt.pages())
-      copy_page<kKind>(P, b, nt.first, nt.len, nt.first / kPage + static_cast<int>(blockIdx.x));
-  }
-}
-
-template <Kind kKind>
-cudaError_t launch(const GatherParams& P, int sm_count, cudaStream_t st) {
-  const int touched = touched_pages(P.max_new, P.max_pages);
-  if (use_list(P.max_new, P.B)) {
-    const int64_t most = static_cast<int64_t>(touched) * P.B;
-    const int ctas =
-        most < sm_count * kGatherCtas ? static_cast<int>(most) : sm_count * kGatherCtas;
-    return launch_pdl(gather_kernel<kKind, true>, dim3(ctas), dim3(kGatherThreads), 0, st, P);
-  }
-  return launch_pdl(gather_kernel<kKind, false>, dim3(touched, P.B), dim3(kGatherThreads), 0, st,
-                    P);
+  const int b = blockIdx.y;
+  NewTokens nt;
+  if (nt.load(P.seq_lens, P.new_lens, P.max_new, P.max_pages * kPage, b, threadIdx.x == 0,
+              P.status) &&
+      blockIdx.x < nt.pages())
+    copy_page<kKind>(P, b, nt.first, nt.len, nt.first / kPage + static_cast<int>(blockIdx.x));
 }
 
 }  // namespace
@@ -141,13 +120,15 @@ cudaError_t launch(const GatherParams& P, int sm_count, cudaStream_t st) {
 cudaError_t launch_gather(Kind kind, const void* cache, const float* kv_scale,
                           const int32_t* block_table, const int32_t* seq_lens, int max_new,
                           const int32_t* new_lens, int B, int num_pages, int max_pages,
-                          void* rows, int32_t* status, int sm_count, cudaStream_t st) {
+                          void* rows, int32_t* status, cudaStream_t st) {
   const GatherParams P{static_cast<const uint8_t*>(cache), kv_scale, block_table, seq_lens,
                        new_lens, static_cast<uint4*>(rows), status, B, max_new, num_pages,
                        max_pages};
-  return kind == Kind::kFp4   ? launch<Kind::kFp4>(P, sm_count, st)
-         : kind == Kind::kFp8 ? launch<Kind::kFp8>(P, sm_count, st)
-                              : launch<Kind::kBf16>(P, sm_count, st);
+  const auto kern = kind == Kind::kFp4   ? gather_kernel<Kind::kFp4>
+                    : kind == Kind::kFp8 ? gather_kernel<Kind::kFp8>
+                                         : gather_kernel<Kind::kBf16>;
+  return launch_pdl(kern, dim3(touched_pages(max_new, max_pages), B), dim3(kGatherThreads), 0, st,
+                    P);
 }
 
 }  // namespace mla

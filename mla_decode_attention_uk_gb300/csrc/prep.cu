@@ -48,6 +48,7 @@ struct PrepParams {
 
 constexpr int kPrepThreads = 256;
 constexpr int kPrepCtas = 4;  // on an SM
+constexpr int kListFrom = 16384;  // tokens
 constexpr int kHeadsPerWarp = 4;
 constexpr int kHalf = kRope / 2;
 
@@ -282,7 +283,7 @@ cudaError_t launch_prep(const mla_decode_norm_rope_args& a, const mla_decode_dim
   P.num_pages = d.num_pages;
   P.max_pages = d.max_pages_per_seq;
   P.max_len = d.max_pages_per_seq * kPage;
-  const bool list = use_list(P.max_new, P.B);
+  const bool list = use_list(static_cast<int64_t>(P.B) * P.max_new, kListFrom, P.B, P.new_lens);
   const auto kern = list ? (a.interleaved ? prep_list_kernel<true> : prep_list_kernel<false>)
                          : (a.interleaved ? prep_kernel<true> : prep_kernel<false>);
   const int64_t tasks = static_cast<int64_t>(P.B) * P.max_new *

@@ -730,10 +730,9 @@ def test_two_calls_at_once_on_two_streams():
 
 @gpu
 @pytest.mark.parametrize("kind", ["fp4", "fp8", "bf16"])
-@pytest.mark.parametrize("B", [255, 256, 257])
-@pytest.mark.parametrize("max_new", [64, 65])
+@pytest.mark.parametrize("B,max_new", [(256, 65), (3, 200), (256, 300), (257, 300), (255, 200)])
 def test_gather_and_keys_with_and_without_a_list(kind, B, max_new):
-    # Up to 256 sequences of more than 64 tokens go by a list of their pages.
+    # The page keys of up to 256 sequences with many pages go by a list of them.
     lens = [(37 * i) % (max_new + 30) for i in range(B)]
     new = [min(n, max_new) - (i % 3 == 0 and n > 0) for i, n in enumerate(lens)]
     table, used = tables(lens, 67)

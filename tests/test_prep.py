@@ -231,8 +231,8 @@ def test_columns_of_wider_projections_of_few_tokens(wide_q, wide_kv, B, max_new)
 @pytest.mark.parametrize("B", [255, 256, 257])
 @pytest.mark.parametrize("max_new", [64, 65])
 def test_with_and_without_a_list(B, max_new):
-    # Up to 256 sequences of more than 64 tokens go by a list of their tokens, which many
-    # of them do not have.
+    # Up to 256 sequences go by a list of their tokens from 16,384 on, which many of them
+    # do not have.
     lens = [(37 * i) % (max_new + 30) for i in range(B)]
     check(B=B, lens=lens, new=[min(n, max_new) if i % 4 else 0 for i, n in enumerate(lens)],
           max_new=max_new, to="both", seed=10)
