@@ -252,7 +252,8 @@ __device__ __forceinline__ void fill_page8(const AppendParams& P, const Group& g
 // The blocks' maxima stay in registers; the rows are read a second time for the codes
 // (held, they were spilled).  13 prompts of 512 to 8190 tokens: 36 us with the rows held,
 // 28 with eight values to a thread and a shuffle for the block's maximum, 19 with latent
-// and RoPE blocks in one warp and the maxima found twice.
+// and RoPE blocks in one warp and the maxima found twice, 16 so; its ALU pipes are then busy
+// for 40 % of it, and a page's barriers come next.
 constexpr int kLatBlocks = kLora / kBlock4, kRopeBlocks = kRope / kBlock4;
 constexpr int kBlocks = kLatBlocks + kRopeBlocks;  // of a row: 36
 constexpr int kPasses = kPage * kBlocks / kAppThreads;
@@ -411,8 +412,8 @@ append_few_kernel(AppendParams P) {
 // a third of the time).  The CTA's pages pass through a ring of three buffers, and
 // two groups of threads take turns at filling them, so that loads and conversions
 // overlap: 13 prompts of 512 to 8190 tokens 14.5 us, 4.5 TB/s; three CTAs of one
-// buffer took 16.2, and two passes over shared memory in place of registers 16.
-// What is left is mostly the start (lengths, sums, first loads: 2 us with nothing in
+// buffer took 16.2, and two passes over shared memory in place of registers 16.  (Into
+// the 4-bit cache 16.)  What is left is mostly the start (lengths, sums, first loads: 2 us with nothing in
 // flight) and the last pages' conversion.
 constexpr int kRing = 3;
 constexpr int kGroups = 2;
@@ -652,8 +653,8 @@ cudaError_t launch_append(const void* rows, int max_new, const int32_t* new_lens
   const AppendParams P{static_cast<const uint4*>(rows), max_new, new_lens, block_table, seq_lens,
                        B, num_pages, max_pages, kv, kv_scale, status};
   if (max_new <= kFewTokens)
-    return launch_pdl(fp4 ? append_few_kernel<true> : append_few_kernel<false>, dim3(touched_pages(max_new, max_pages), B),
-                      dim3(kAppThreads), max_new * kDqk * 2, st, P);
+    return launch_pdl(fp4 ? append_few_kernel<true> : append_few_kernel<false>,
+                      dim3(touched_pages(max_new, max_pages), B), dim3(kAppThreads), max_new * kDqk * 2, st, P);
   const int smem = kRing * kRowsBytes;
   const auto kern = fp4 ? append_pages_kernel<true> : append_pages_kernel<false>;
   const cudaError_t e = cudaFuncSetAttribute(

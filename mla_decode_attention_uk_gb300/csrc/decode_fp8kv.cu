@@ -1,4 +1,4 @@
-// decode_fp8kv.cu -- the attention step over the 8-bit latent cache.
+// decode_fp8kv.cu -- the attention step over the 8-bit and the 4-bit latent cache.
 //
 // The cache holds E4M3 codes and one scale s per page (fp8kv.cuh).  With the
 // absorbed query q and codes c_j of a page:
@@ -36,7 +36,8 @@
 // however the scales of a sequence's pages differ.
 //
 // Warp roles: 0 TMA producer, 1 QK^T issuer, 2 and 3 PV issuers (latent halves;
-// warp 2 also owns TMEM), 4-7 and 8-11 softmax and epilogue, 12-15 query terms.
+// warp 2 also owns TMEM), 4-7 and 8-11 softmax and epilogue, 12-15 query terms (and,
+// with 16-19, the expansion of 4-bit pages).
 // The two softmax groups take turns, page by page: a page's chain of waits,
 // exponentials and stores is about 1,700 cycles long however many warps share
 // it (measured with four and with eight), while the tensor core is done in
@@ -46,9 +47,9 @@
 // (QK^T has one issuer: two that took turns would each see only some phases of a
 // slot's barriers.)
 //
-// What bounds it: with 64 rows the tensor pipe, whose 34 MMAs take 1,376 cycles of
-// the 1,500 that a page takes (PV 768, bound by shared-memory reads: 6 KB per
-// MMA of 4 KB worth); with 16 heads memory, 6.1 TB/s while pages stream (both from
+// What bounds it over the 8-bit cache: with 64 rows the tensor pipe, whose 34 MMAs take
+// 1,376 cycles of the 1,500 that a page takes (PV 768, bound by shared-memory reads: 6 KB
+// per MMA of 4 KB worth); with 16 heads memory, 6.1 TB/s while pages stream (both from
 // time stamps on one SM).  Beside the pages a piece costs 5 to 6 us (its query
 // terms and its epilogue are not hidden by each other's pages) and a launch 8 us:
 // over the whole launch the tensor pipe is active 51 % of the time on the second
@@ -57,7 +58,29 @@
 // sequences of 4,096 tokens x 16 heads 36 us; 128 of 1,000-10,000 (500k tokens) x
 // 128 heads 113 us; 61 ragged drafts of 4 queries x 128 heads (133k tokens) 101 us.
 // Prefetching pages into L2 ahead of the ring only cost: 35 -> 39 us on the first,
-// eight pages ahead.
+// eight pages ahead.  The weights go in a loop of half pages, and QK^T in one of boxes:
+// whole ones are more code than stays in the instruction cache next to the other roles'
+// (104.9 -> 102 us on the third, the same bits).
+//
+// Over the 4-bit cache (fp4kv.cuh) a page stands for the same codes: it comes as it is,
+// 21 KB in one copy into one of two buffers, and eight warps more, 12-19, expand it into a
+// slot; everything behind is as above.  (E2M1 operands would not do: PV wants a page with
+// its keys along the other axis, which exists for 8-bit types only, and the block
+// exponents differ along it.)  Four slots and 20 warps, which share the registers out
+// anew.  Warp 12 loads the query's tile there, as the warps that fill slots see each phase
+// of their barriers.
+// What bounds that: the expansion, whose eight warps take 1,500 of the 2,000 cycles that a
+// page takes (980 with the SM to themselves) next to the softmax's 1,550 on the same
+// schedulers; byte selections issue at half the rate of logic instructions, and the ALU
+// pipes are half busy over the launch.  Tried and no better, us on the first two cases
+// below: four warps in place of eight (52 and 165), sixteen (58, 172), four for every other
+// page each (52, 152), a half page at a time through buffers of
+// that size (58, 180), three slots and four buffers, L2 prefetch (51), loops unrolled
+// (57, 166), P^T's terms as rows of their own, which reads a page for PV once instead of
+// twice (51, 159).
+// Measured: 64 sequences of 4,096 tokens x 16 heads 48 us; 61 ragged drafts of 4 queries x
+// 128 heads 143 us; 128 of 1,000-10,000 x 128 heads 158 us: slower than the 8-bit cache,
+// for 0.58 times its bytes.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -592,7 +615,8 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
                 const int w = lane + 32 * i;
                 uint32_t hi, mid;
                 split_terms(x[i], down, hi, mid);
-                if (i < 4 || lane < 16) st_shared_v2(word(row, w >> 4, (w >> 1) & 7, w & 1), hi, mid);
+                if (i < 4 || lane < 16)
+                  st_shared_v2(word(row, w >> 4, (w >> 1) & 7, w & 1), hi, mid);
               }
             }
             // (Here and below warps that share a named barrier leave together, or the
@@ -698,8 +722,8 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
               uint32_t exps = *reinterpret_cast<const uint32_t*>(src + kRowExps4 + 4 * box);
               const uint4 rope = *reinterpret_cast<const uint4*>(src + kRowRope4 + 16 * box);
               const bool usual = usual_exps(exps);
-              // (Not unrolled: instructions that run once a page take longer to fetch
-              // than to execute: 63 us instead of 49 on 64 x 4,096 tokens x 16 heads.)
+              // (Not unrolled, to stay small in the instruction cache: 57 us instead of 48
+              // on 64 x 4,096 tokens x 16 heads.)
 #pragma unroll 1
               for (int j = 0; j < 4; ++j) {  // 32 columns, two blocks
                 const uint4 x = *reinterpret_cast<const uint4*>(src + 64 * box + 16 * j);
@@ -743,7 +767,8 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
         const int rows_here = min(kTileRows, TH - row0);
         // Where the rows' results go: row of o_lat, or ~row of the partial results.
         const int dest = P.seq_nsplit[pc.b] > 1
-                             ? ~((P.seq_slot[pc.b] + pc.task / sets - P.seq_first[pc.b]) * TH + row0)
+                             ? ~((P.seq_slot[pc.b] + pc.task / sets - P.seq_first[pc.b]) * TH +
+                                 row0)
                              : pc.b * TH + row0;
         const int n_row = srow < rows_here ? pc.len - P.T + (row0 + srow) / P.H + 1 : 0;
         // The running maximum of a row is m_sh (one group raises it, the other

@@ -13,8 +13,11 @@
 // smallest.  So every value of the cache is an E4M3 code times the page's scale: a
 // page expands exactly to one of the 8-bit cache, and the attention step (tensor
 // cores, query terms, weights, the page's scale) is the same from there on.
-// 16 values to a block: a latent row has a few large channels, and a block of 32
-// loses twice as many small values next to one; 336 bytes a token instead of 328.
+// 16 values to a block: a latent row has a few large channels, which take the small
+// values of their blocks with them.  Root mean square error of standard normal rows, and
+// of rows in which every 97th channel is six times as large, relative: blocks of 16 0.110
+// and 0.122, of 32 0.112 and 0.136, one scale a row 0.122 and 0.271; a row is 336 bytes,
+// 328 and 321.
 #pragma once
 #include <cuda_fp4.h>
 

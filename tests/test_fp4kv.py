@@ -599,7 +599,8 @@ def test_one_plan_serves_every_cache_and_the_steps_equal_the_run():
 @gpu
 @pytest.mark.parametrize("B,H,ranges", [(24, 16, 1), (24, 128, 1), (160, 16, 2), (40, 64, 0)])
 def test_runs_of_other_queries_back_to_back_on_one_plan(B, H, ranges):
-    inp, kv4, kvs = fp4_inputs(make_inputs(B, [500 + 37 * i % 300 for i in range(B)], 1, H, seed=80))
+    lens = [500 + 37 * i % 300 for i in range(B)]
+    inp, kv4, kvs = fp4_inputs(make_inputs(B, lens, 1, H, seed=80))
     g = inp.to(torch.device("cuda"))
     k, s = kv4.cuda(), kvs.cuda()
     m = binding.MlaDecode(binding.dims_for(g.q, g.cache, g.block_table), num_ranges=ranges,
