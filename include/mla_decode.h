@@ -348,7 +348,9 @@ int mla_decode_attend_fp4kv(const mla_decode_dims* dims, const uint8_t* kv_fp4,
  *   kv_cache, block_table  the bf16 cache: tokens are written to their pages.  One of
  *               rows and kv_cache must be given with kv, or both; block_table with
  *               kv_cache
- * Rows behind a sequence's n_b tokens are neither read nor written.  A position outside
+ * (A row whose sum of squares passes fp32's range becomes zeros.)  No two tokens of a
+ * call may have one place in the cache.  Rows behind a sequence's n_b tokens are neither
+ * read nor written.  A position outside
  * [0, max_position): DEVICE_BOUNDS, and nothing of the token is written; a block_table
  * entry outside the pool: DEVICE_BOUNDS, and the page's tokens reach q_out and rows
  * only; lengths as for the append.  Anything else (q without q_out, outputs without

@@ -364,18 +364,22 @@ def _lines(d, block_table, seq_lens, new_lens=None, status=None):
     return lines
 
 
-def _append(name, d, rows, kv, kv_scale, block_table, seq_lens, new_lens, status):
-    fp4 = name == "mla_decode_append_fp4kv"
+def _rows_of(rows):
+    return rows.shape[1] if rows is not None and rows.dim() == 3 else 0
+
+
+def _append(fp4, d, rows, kv, kv_scale, block_table, seq_lens, new_lens, status):
     B, pages = d.batch, d.num_pages
-    max_new = rows.shape[1] if rows is not None and rows.dim() == 3 else 0
+    max_new = _rows_of(rows)
     stream = _checked(("rows", rows, torch.bfloat16, (B, max_new, 576)),
-                      ("kv4" if fp4 else "kv8", kv, torch.uint8, (pages, 64, 336 if fp4 else 576)),
+                      ("kv4", kv, torch.uint8, (pages, 64, 336)) if fp4 else
+                      ("kv8", kv, torch.uint8, (pages, 64, 576)),
                       ("kv_scale", kv_scale, torch.float32, (pages,)),
                       *_lines(d, block_table, seq_lens, new_lens, status))
-    _ok(getattr(lib(), name)(ctypes.byref(d), rows.data_ptr(), max_new, _ptr(new_lens),
-                             block_table.data_ptr(), seq_lens.data_ptr(), kv.data_ptr(),
-                             kv_scale.data_ptr(), _ptr(status), stream),
-        name)
+    f = lib().mla_decode_append_fp4kv if fp4 else lib().mla_decode_append_fp8kv
+    _ok(f(ctypes.byref(d), rows.data_ptr(), max_new, _ptr(new_lens), block_table.data_ptr(),
+          seq_lens.data_ptr(), kv.data_ptr(), kv_scale.data_ptr(), _ptr(status), stream),
+        f.__name__)
 
 
 def append_fp8kv(d: Dims, rows, kv8, kv_scale, block_table, seq_lens, new_lens=None,
@@ -385,15 +389,13 @@ def append_fp8kv(d: Dims, rows, kv8, kv_scale, block_table, seq_lens, new_lens=N
     Row i < new_lens[b] (default: every row) goes to position
     seq_lens[b] - new_lens[b] + i.  status: optional int32 [1] on the device
     that receives the first error found there."""
-    _append("mla_decode_append_fp8kv", d, rows, kv8, kv_scale, block_table, seq_lens, new_lens,
-            status)
+    _append(False, d, rows, kv8, kv_scale, block_table, seq_lens, new_lens, status)
 
 
 def append_fp4kv(d: Dims, rows, kv4, kv_scale, block_table, seq_lens, new_lens=None,
                  status=None):
     """append_fp8kv() into the 4-bit cache (uint8 [num_pages, 64, 336])."""
-    _append("mla_decode_append_fp4kv", d, rows, kv4, kv_scale, block_table, seq_lens, new_lens,
-            status)
+    _append(True, d, rows, kv4, kv_scale, block_table, seq_lens, new_lens, status)
 
 
 def page_keys(d: Dims, cache, block_table, seq_lens, max_new, keys, new_lens=None, status=None):
@@ -471,10 +473,6 @@ def select_pages(d: Dims, scores, block_table, seq_lens, top_k, keep_first, keep
 
 
 # ---------------------------------------------------------------- in front of the cache and back
-def _rows_of(rows):
-    return rows.shape[1] if rows is not None and rows.dim() == 3 else 0
-
-
 def gather(d: Dims, cache, block_table, seq_lens, rows, new_lens=None, status=None):
     """Tokens of the bf16 cache as rows (bf16 [B, max_new, 576], in place): row i <
     new_lens[b] (default: every row) is the token at position seq_lens[b] -
@@ -489,29 +487,27 @@ def gather(d: Dims, cache, block_table, seq_lens, rows, new_lens=None, status=No
         "mla_decode_gather")
 
 
-def _gather(name, d, kv, kv_scale, block_table, seq_lens, rows, new_lens, status):
-    fp4 = name == "mla_decode_gather_fp4kv"
+def _gather(fp4, d, kv, kv_scale, block_table, seq_lens, rows, new_lens, status):
     max_new, pages = _rows_of(rows), d.num_pages
-    stream = _checked(("kv4" if fp4 else "kv8", kv, torch.uint8, (pages, 64, 336 if fp4 else 576)),
+    stream = _checked(("kv4", kv, torch.uint8, (pages, 64, 336)) if fp4 else
+                      ("kv8", kv, torch.uint8, (pages, 64, 576)),
                       ("kv_scale", kv_scale, torch.float32, (pages,)),
                       ("rows", rows, torch.bfloat16, (d.batch, max_new, 576)),
                       *_lines(d, block_table, seq_lens, new_lens, status))
-    _ok(getattr(lib(), name)(ctypes.byref(d), kv.data_ptr(), kv_scale.data_ptr(),
-                             block_table.data_ptr(), seq_lens.data_ptr(), max_new, _ptr(new_lens),
-                             rows.data_ptr(), _ptr(status), stream),
-        name)
+    f = lib().mla_decode_gather_fp4kv if fp4 else lib().mla_decode_gather_fp8kv
+    _ok(f(ctypes.byref(d), kv.data_ptr(), kv_scale.data_ptr(), block_table.data_ptr(),
+          seq_lens.data_ptr(), max_new, _ptr(new_lens), rows.data_ptr(), _ptr(status), stream),
+        f.__name__)
 
 
 def gather_fp8kv(d: Dims, kv8, kv_scale, block_table, seq_lens, rows, new_lens=None, status=None):
     """gather() from the 8-bit cache: what append_fp8kv() stored, as bf16 rows."""
-    _gather("mla_decode_gather_fp8kv", d, kv8, kv_scale, block_table, seq_lens, rows, new_lens,
-            status)
+    _gather(False, d, kv8, kv_scale, block_table, seq_lens, rows, new_lens, status)
 
 
 def gather_fp4kv(d: Dims, kv4, kv_scale, block_table, seq_lens, rows, new_lens=None, status=None):
     """gather() from the 4-bit cache: what append_fp4kv() stored, as bf16 rows."""
-    _gather("mla_decode_gather_fp4kv", d, kv4, kv_scale, block_table, seq_lens, rows, new_lens,
-            status)
+    _gather(True, d, kv4, kv_scale, block_table, seq_lens, rows, new_lens, status)
 
 
 def _gapped(name, t, shape, width, other):

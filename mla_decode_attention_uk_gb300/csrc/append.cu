@@ -552,6 +552,10 @@ __device__ __forceinline__ void page_mean(const KeyParams& P, int b, int len, in
     if (threadIdx.x == 0) record_status(status, MLA_STATUS_BOUNDS);
     return;
   }
+  // (Looked at behind the rows' loads: a trip to memory next to theirs, not before.)
+  const float given = kKind != Kind::kBf16 ? kv_scale[page] : 1.0f;
+  const bool in_range = scale_in_range(given);
+  const float scale = in_range ? given : 1.0f;
   const int filled = min(len - logical * kPage, kPage);
   const int c = threadIdx.x % kChunks, r0 = threadIdx.x / kChunks;
   float s[8] = {};
@@ -594,19 +598,12 @@ __device__ __forceinline__ void page_mean(const KeyParams& P, int b, int len, in
 #pragma unroll
   for (int k = 0; k < 8; ++k) part[r0][c * 8 + k] = s[k];
   __syncthreads();
-  float scale = 1.0f;
-  if constexpr (kKind != Kind::kBf16) {
-    scale = kv_scale[page];
-    if (!scale_in_range(scale)) {
-      if (threadIdx.x == 0) record_status(status, MLA_STATUS_BOUNDS);
-      scale = 1.0f;
-    }
-  }
   const float mul = scale / static_cast<float>(filled);
   const int k = threadIdx.x * 2;
   const float x = ((part[0][k] + part[1][k]) + (part[2][k] + part[3][k])) * mul;
   const float y = ((part[0][k + 1] + part[1][k + 1]) + (part[2][k + 1] + part[3][k + 1])) * mul;
   *reinterpret_cast<uint32_t*>(keys + static_cast<size_t>(page) * kDqk + k) = pack_bf16x2(x, y);
+  if (!in_range && threadIdx.x == 0) record_status(status, MLA_STATUS_BOUNDS);
 }
 
 // One CTA per (sequence, page that it can touch), or a list of the pages.

@@ -38,14 +38,10 @@ __device__ __forceinline__ void copy_page(const GatherParams& P, int b, int firs
     if (threadIdx.x == 0) record_status(status, MLA_STATUS_BOUNDS);
     return;
   }
-  float scale = 1.0f;
-  if constexpr (kKind != Kind::kBf16) {
-    scale = kv_scale[page];
-    if (!scale_in_range(scale)) {
-      if (threadIdx.x == 0) record_status(status, MLA_STATUS_BOUNDS);
-      scale = 1.0f;
-    }
-  }
+  // (Looked at behind the rows' loads: a trip to memory next to theirs, not before.)
+  const float given = kKind != Kind::kBf16 ? kv_scale[page] : 1.0f;
+  const bool in_range = scale_in_range(given);
+  const float scale = in_range ? given : 1.0f;
   const int c = threadIdx.x % kChunks;
   const int r0 = max(first - logical * kPage, 0), r1 = min(len - logical * kPage, kPage);
   uint4* const dst = rows + (static_cast<ptrdiff_t>(b) * max_new + logical * kPage - first) *
@@ -96,6 +92,7 @@ __device__ __forceinline__ void copy_page(const GatherParams& P, int b, int firs
       }
     }
   }
+  if (!in_range && threadIdx.x == 0) record_status(status, MLA_STATUS_BOUNDS);
 }
 
 // One CTA per (sequence, page that it can touch).  13 prompts of 512 to 8190 tokens: 13.0
