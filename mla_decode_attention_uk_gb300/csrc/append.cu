@@ -522,8 +522,12 @@ append_pages_kernel(AppendParams P) {
   }
 }
 
-constexpr int kKeyThreads = 288;
-constexpr int kKeyCtas = 4;  // on an SM, of a list
+// Rows that a CTA sums side by side, 72 threads to each.  Eight of the 4-bit cache where
+// there are few pages to an SM, as its codes' conversion is what takes long: the last pages
+// of 128 sequences 3.5 us instead of 4.2, but 13 prompts by a list 9.7 instead of 8.6.
+constexpr int key_groups(Kind kind, bool list) { return kind == Kind::kFp4 && !list ? 8 : 4; }
+constexpr int key_threads(Kind kind, bool list) { return kChunks * key_groups(kind, list); }
+constexpr int key_ctas(Kind kind, bool list) { return 16 / key_groups(kind, list); }  // an SM
 
 struct KeyParams {
   const uint8_t* cache;
@@ -539,12 +543,12 @@ struct KeyParams {
 // The mean of a page's filled rows.  Thread t sums columns 8 (t mod 72) .. + 7 over rows
 // t / 72, + 4, ...  Four rows in flight from a bf16 cache: 13 prompts of 512 to 8190
 // tokens, in a grid of all their pages, 10.6 us (eight 11.2, sixteen 14.9: registers and
-// the ragged pages' remainders); 9.9 by a list of the pages, 8 bits 6.9, 4 bits 9.0 (its
+// the ragged pages' remainders); 9.8 by a list of the pages, 8 bits 6.6, 4 bits 8.6 (its
 // codes' conversion: two thirds of that on the ALUs).  The last pages of 128 sequences
-// 3.0 us from 8 bits, 4.2 from 4.
-template <Kind kKind>
+// 3.2 us from 8 bits.
+template <Kind kKind, int kSide>
 __device__ __forceinline__ void page_mean(const KeyParams& P, int b, int len, int logical,
-                                          float (&part)[4][kDqk]) {
+                                          float (&part)[kSide][kDqk]) {
   const auto [cache, kv_scale, block_table, seq_lens, new_lens, keys, status, B, max_new,
               num_pages, max_pages] = P;
   const int page = block_table[static_cast<size_t>(b) * max_pages + logical];
@@ -565,15 +569,15 @@ __device__ __forceinline__ void page_mean(const KeyParams& P, int b, int len, in
   };
   if constexpr (kKind == Kind::kFp4) {
     const uint8_t* const base = cache + static_cast<size_t>(page) * kPageBytes4;
-    constexpr int kDeep = 8;  // rows' loads in flight (128 last pages: four 4.3 us, two 4.8)
-    for (int r = r0; r < filled; r += 4 * kDeep) {
+    constexpr int kDeep = 8, kStep = kSide;  // its rows' loads in flight
+    for (int r = r0; r < filled; r += kStep * kDeep) {
       Raw4 raw[kDeep];
 #pragma unroll
       for (int k = 0; k < kDeep; ++k)
-        raw[k] = load_raw4(base + min(r + 4 * k, filled - 1) * kRow4, c);
+        raw[k] = load_raw4(base + min(r + kStep * k, filled - 1) * kRow4, c);
 #pragma unroll
       for (int k = 0; k < kDeep; ++k) {
-        if (r + 4 * k >= filled) break;
+        if (r + kStep * k >= filled) break;
         float x[8];
         values4(raw[k], c, x);
         add(x);
@@ -600,17 +604,24 @@ __device__ __forceinline__ void page_mean(const KeyParams& P, int b, int len, in
   __syncthreads();
   const float mul = scale / static_cast<float>(filled);
   const int k = threadIdx.x * 2;
-  const float x = ((part[0][k] + part[1][k]) + (part[2][k] + part[3][k])) * mul;
-  const float y = ((part[0][k + 1] + part[1][k + 1]) + (part[2][k + 1] + part[3][k + 1])) * mul;
-  *reinterpret_cast<uint32_t*>(keys + static_cast<size_t>(page) * kDqk + k) = pack_bf16x2(x, y);
+  if (k < kDqk) {
+    float x = (part[0][k] + part[1][k]) + (part[2][k] + part[3][k]);
+    float y = (part[0][k + 1] + part[1][k + 1]) + (part[2][k + 1] + part[3][k + 1]);
+    if constexpr (kSide == 8) {
+      x += (part[4][k] + part[5][k]) + (part[6][k] + part[7][k]);
+      y += (part[4][k + 1] + part[5][k + 1]) + (part[6][k + 1] + part[7][k + 1]);
+    }
+    *reinterpret_cast<uint32_t*>(keys + static_cast<size_t>(page) * kDqk + k) =
+        pack_bf16x2(x * mul, y * mul);
+  }
   if (!in_range && threadIdx.x == 0) record_status(status, MLA_STATUS_BOUNDS);
 }
 
 // One CTA per (sequence, page that it can touch), or a list of the pages.
 template <Kind kKind, bool kList>
-__global__ void __launch_bounds__(kKeyThreads, kKeyCtas)
+__global__ void __launch_bounds__(key_threads(kKind, kList), key_ctas(kKind, kList))
 page_keys_kernel(const __grid_constant__ KeyParams P) {
-  __shared__ float part[4][kDqk];
+  __shared__ float part[key_groups(kKind, kList)][kDqk];
   griddep_wait();
   griddep_launch_dependents();
   if constexpr (kList) {
@@ -619,8 +630,8 @@ page_keys_kernel(const __grid_constant__ KeyParams P) {
                                       P.status, [](const NewTokens& nt) { return nt.pages(); });
     for (long long f = blockIdx.x; f < pages; f += gridDim.x) {
       const int b = list.find(f), len = list.len[b];
-      page_mean<kKind>(P, b, len, (len - 1) / kPage - static_cast<int>(list.upto[b] - 1 - f),
-                       part);
+      const int logical = (len - 1) / kPage - static_cast<int>(list.upto[b] - 1 - f);
+      page_mean<kKind, key_groups(kKind, kList)>(P, b, len, logical, part);
       __syncthreads();  // `part` has been read
     }
   } else {
@@ -629,7 +640,8 @@ page_keys_kernel(const __grid_constant__ KeyParams P) {
     if (nt.load(P.seq_lens, P.new_lens, P.max_new, P.max_pages * kPage, b, threadIdx.x == 0,
                 P.status) &&
         blockIdx.x < nt.pages())
-      page_mean<kKind>(P, b, nt.len, nt.first / kPage + static_cast<int>(blockIdx.x), part);
+      page_mean<kKind, key_groups(kKind, kList)>(
+          P, b, nt.len, nt.first / kPage + static_cast<int>(blockIdx.x), part);
   }
 }
 
@@ -664,10 +676,10 @@ template <Kind kKind>
 static cudaError_t launch_keys(const KeyParams& P, int sm_count, cudaStream_t st) {
   const int touched = touched_pages(P.max_new, P.max_pages);
   if (use_list(static_cast<int64_t>(touched) * P.B, 6 * sm_count, P.B, P.new_lens))
-    return launch_pdl(page_keys_kernel<kKind, true>, dim3(sm_count * kKeyCtas), dim3(kKeyThreads),
-                      0, st, P);
-  return launch_pdl(page_keys_kernel<kKind, false>, dim3(touched, P.B), dim3(kKeyThreads), 0, st,
-                    P);
+    return launch_pdl(page_keys_kernel<kKind, true>, dim3(sm_count * key_ctas(kKind, true)),
+                      dim3(key_threads(kKind, true)), 0, st, P);
+  return launch_pdl(page_keys_kernel<kKind, false>, dim3(touched, P.B),
+                    dim3(key_threads(kKind, false)), 0, st, P);
 }
 
 cudaError_t launch_page_keys(Kind kind, const void* cache, const float* kv_scale,
