@@ -413,8 +413,8 @@ append_few_kernel(AppendParams P) {
 // two groups of threads take turns at filling them, so that loads and conversions
 // overlap: 13 prompts of 512 to 8190 tokens 14.5 us, 4.5 TB/s; three CTAs of one
 // buffer took 16.2, and two passes over shared memory in place of registers 16.  (Into
-// the 4-bit cache 16.)  What is left is mostly the start (lengths, sums, first loads: 2 us with nothing in
-// flight) and the last pages' conversion.
+// the 4-bit cache 16.)  What is left is mostly the start (lengths, sums, first loads: 2 us
+// with nothing in flight) and the last pages' conversion.
 constexpr int kRing = 3;
 constexpr int kGroups = 2;
 constexpr int kBars = kRing * kGroups;  // a barrier is always the same group's, whose
@@ -663,7 +663,8 @@ cudaError_t launch_append(const void* rows, int max_new, const int32_t* new_lens
                        B, num_pages, max_pages, kv, kv_scale, status};
   if (max_new <= kFewTokens)
     return launch_pdl(fp4 ? append_few_kernel<true> : append_few_kernel<false>,
-                      dim3(touched_pages(max_new, max_pages), B), dim3(kAppThreads), max_new * kDqk * 2, st, P);
+                      dim3(touched_pages(max_new, max_pages), B), dim3(kAppThreads),
+                      max_new * kDqk * 2, st, P);
   const int smem = kRing * kRowsBytes;
   const auto kern = fp4 ? append_pages_kernel<true> : append_pages_kernel<false>;
   const cudaError_t e = cudaFuncSetAttribute(
