@@ -512,9 +512,11 @@ def gather_fp4kv(d: Dims, kv4, kv_scale, block_table, seq_lens, rows, new_lens=N
 
 def _gapped(name, t, shape, width, other):
     """Elements from a token to the next of a [batch, tokens, ...] tensor whose tokens
-    are contiguous and evenly spaced (columns of a wider one)."""
+    are contiguous and evenly spaced (columns of a wider one), on the device of `other`
+    (which is checked later)."""
     n = None
-    if t.shape == shape and t.dtype is torch.bfloat16 and t.get_device() == other.get_device():
+    if (t.shape == shape and t.dtype is torch.bfloat16
+            and (other is None or t.get_device() == other.get_device())):
         batch, tokens = shape[:2]
         n = t.stride(1) if tokens > 1 else t.stride(0)
         if (t.stride(-1) != 1 or (len(shape) == 4 and t.stride(2) != shape[3]) or n < width or n % 8

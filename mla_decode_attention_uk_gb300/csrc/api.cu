@@ -915,6 +915,11 @@ int mla_decode_norm_rope(const mla_decode_dims* d, const mla_decode_norm_rope_ar
                (a->kv_cache && (!a->block_table || !aligned4(a->block_table))))
             : (a->rows || a->kv_cache || a->kv_weight))
     return MLA_DECODE_INVALID_ARG;
+  // In place only where both sides have no gaps: a token would else be written over another
+  // that has not been read.
+  if ((a->q && a->q_out == a->q && a->q_stride != static_cast<int64_t>(d->num_heads) * kDq) ||
+      (a->kv && a->rows == a->kv && a->kv_stride != kDqk))
+    return MLA_DECODE_INVALID_ARG;
   // Warps count their tasks (four heads or a latent row) in 32 bits.
   if (static_cast<int64_t>(d->batch) * a->max_new > INT32_MAX / 2 / (d->num_heads / 4 + 1))
     return MLA_DECODE_INVALID_ARG;

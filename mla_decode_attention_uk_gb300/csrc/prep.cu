@@ -15,8 +15,8 @@
 // (0.79 of a copy; without the next task's loads in flight 68; three CTAs an SM 57, five
 // or six, which spill registers, 92 and more; cosines and sines loaded ahead as well 59, in
 // two CTAs; two to five tasks ahead by asynchronous copies into shared memory 57 to 61: the
-// rest is not for want of loads in flight); one token of 128 sequences x 128 heads 3.7 us, 3.4 TB/s; of two x 16 heads
-// 2.1, a launch.
+// rest is not for want of loads in flight); one token of 128 sequences x 128 heads 3.7 us,
+// 3.4 TB/s; of two x 16 heads 2.1, a launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

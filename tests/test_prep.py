@@ -38,6 +38,8 @@ def test_refuses_bad_arguments():
     bad += [{name: None} for name in ("cos_sin", "seq_lens", "q_out", "block_table")]
     bad += [{"q_stride": n} for n in (16 * 192 - 8, 16 * 192 + 4, -16 * 192)]
     bad += [{"kv_stride": n} for n in (568, 580, -576)]
+    # In place, but with gaps on one side only.
+    bad += [{"q_stride": 16 * 192 + 8}, {"kv_stride": 584}]
     bad += [{"eps": x} for x in (0.0, -1.0, math.nan, math.inf)]
     bad += [{"max_position": 0}, {"max_position": -1}, {"interleaved": 2}, {"interleaved": -1},
             {"max_new": 0}, {"max_new": -1}, {"max_new": 2 ** 30}]  # (more than 2^30 tasks)
@@ -75,12 +77,16 @@ def test_python_call_checks_types_and_shapes():
                  ("cos_sin", torch.zeros(9, 64, dtype=torch.float64)),
                  ("cache", good["cache"][:3]), ("block_table", good["block_table"].long()),
                  ("positions", good["positions"][:1]), ("new_lens", good["new_lens"].long()),
-                 ("status", torch.zeros(2, dtype=torch.int32)),
+                 ("status", torch.zeros(2, dtype=torch.int32)), ("seq_lens", None),
                  ("seq_lens", good["seq_lens"][:1])):
         with pytest.raises(ValueError):
             binding.norm_rope(d, **dict(good, **{k: v}))
     with pytest.raises(ValueError, match="CUDA device"):
         binding.norm_rope(d, **good)  # right shapes, but in host memory
+    for k in ("seq_lens", "cos_sin"):
+        with pytest.raises(ValueError, match=k):
+            binding.norm_rope(d, **dict(good, kv=torch.zeros(2, 3, 704, dtype=BF)[..., :576],
+                                        **{k: None}))
 
 
 # ---------------------------------------------------------------- the formulas
@@ -288,6 +294,40 @@ def test_a_row_of_zeros_and_rows_that_are_not_finite():
     assert not rows[0, 3, :512].isnan().any() and not rows[0, 3, 512:].isfinite().all()
     assert rows[0, 4, 0].isnan() and not rows[0, 4, 1:512].any() and rows[0, 4, 512:].any()
     assert rows[0, 5].isfinite().all()
+
+
+@gpu
+@pytest.mark.parametrize("new", [None, [5]])
+def test_tokens_and_pages_beyond_two_gigabytes(new):
+    # Tokens 2^29 elements (2^30 bytes) apart, and pages on both sides of byte 2^31 and 2^32.
+    gap, pages = 1 << 29, (1 << 32) // (64 * 576 * 2) + 3
+    at = [(1 << 31) // (64 * 576 * 2), (1 << 32) // (64 * 576 * 2), pages - 1]
+    d = good_dims(batch=1, num_heads=16, num_pages=pages, max_pages_per_seq=3)
+    g = torch.Generator().manual_seed(5)
+    q = torch.randn(1, 5, 16, 192, generator=g).to(BF)
+    kv = torch.randn(1, 5, 576, generator=g).to(BF)
+    far_q = torch.empty(4 * gap + 16 * 192, dtype=BF, device="cuda")
+    far_kv = torch.empty(4 * gap + 576, dtype=BF, device="cuda")
+    far_q = far_q.as_strided((1, 5, 16, 192), (5 * gap, gap, 192, 1))
+    far_kv = far_kv.as_strided((1, 5, 576), (5 * gap, gap, 1))
+    far_q.copy_(q)
+    far_kv.copy_(kv)
+    cache = torch.zeros(pages, 64, 576, dtype=BF, device="cuda")
+    table = torch.tensor([at], dtype=torch.int32, device="cuda")
+    ints = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+    cs = cos_sin_table(140).cuda()
+    for first in (62, 126):  # (the third token is in the next page)
+        want_q, want_rows = torch.empty_like(q).cuda(), torch.empty_like(kv).cuda()
+        got_q, got_rows = torch.zeros_like(want_q), torch.zeros_like(want_rows)
+        binding.norm_rope(d, ints([first + 5]), cs, q=q.cuda(), q_out=want_q, kv=kv.cuda(),
+                          rows=want_rows)
+        binding.norm_rope(d, ints([first + 5]), cs, q=far_q, q_out=got_q, kv=far_kv, cache=cache,
+                          block_table=table, new_lens=None if new is None else ints(new))
+        binding.gather(d, cache, table, ints([first + 5]), got_rows)
+        assert torch.equal(got_q, want_q) and torch.equal(got_rows, want_rows)
+        for i in range(5):
+            p = first + i
+            assert torch.equal(cache[at[p // 64], p % 64], want_rows[0, i])
 
 
 @gpu
