@@ -293,7 +293,7 @@ int mla_decode_attend_fp8kv(const mla_decode_dims* dims, const uint8_t* kv_fp8,
  * A cached latent is code * 2^(e - 8) * scale, a RoPE value code * scale.  Each of
  * them is an E4M3 code times the scale, so a page of this cache stands for exactly
  * the values of a page of the 8-bit cache, and what holds there for scales, NaN
- * codes, `status`, and rows past a sequence's length, holds here. */
+ * codes and `status` holds here; but rows past a sequence's length may hold anything. */
 
 /* mla_decode_append_fp8kv into the 4-bit cache.  The scale of a page follows from
  * its values as there (all 576 columns: |value| <= 448 s).  A block's e is the

@@ -721,6 +721,9 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
               uint8_t* const dst = slot_pages + s * kSlot;
               uint32_t exps = *reinterpret_cast<const uint32_t*>(src + kRowExps4 + 4 * box);
               const uint4 rope = *reinterpret_cast<const uint4*>(src + kRowRope4 + 16 * box);
+              // Rows past the length may hold anything: no NaN of theirs meets a weight of 0.
+              // (Their RoPE columns reach only the scores, which are masked.)
+              if (i * kPage + row >= pc.len) exps = 0x88888888u;
               const bool usual = usual_exps(exps);
               // (Not unrolled, to stay small in the instruction cache: 57 us instead of 48
               // on 64 x 4,096 tokens x 16 heads.)

@@ -506,6 +506,20 @@ def test_unused_pages_and_tail_rows_do_not_matter():
 
 
 @gpu
+@pytest.mark.parametrize("H,T", [(16, 1), (128, 1), (64, 3)])
+def test_nan_past_the_length_does_not_matter(H, T):
+    lens = [T, 70, 5, 200, 127, 64]
+    inp, kv4, kvs = fp4_inputs(make_inputs(len(lens), lens, T, H, seed=25))
+    out, lse = run_fp4(inp, kv4, kvs)
+    poisoned = kv4.clone()
+    for b, n in enumerate(lens):
+        if n % 64:
+            poisoned[int(inp.block_table[b, n // 64]), n % 64:] = 0xFF
+    out2, lse2 = run_fp4(inp, poisoned, kvs)
+    assert torch.equal(out, out2) and torch.equal(lse, lse2)
+
+
+@gpu
 @pytest.mark.parametrize("where", ["block", "rope"])
 def test_nan_in_a_visible_token_reaches_its_sequence_only(where):
     inp, kv4, kvs = fp4_inputs(make_inputs(3, [200, 70, 130], 1, 16, seed=47))
