@@ -268,7 +268,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
   // next phase here takes PV of page g + kSlots, which follows that of page g +
   // 1, the group's own.  The phase before is over: page g + 1 is in a slot, so PV
   // has read every page up to g + 1 - kSlots.)
-  // Over the 4-bit cache a page lands in raw_full's buffer and warps 12-15 expand it
+  // Over the 4-bit cache a page lands in raw_full's buffer and warps 12-19 expand it
   // into a slot: slot_full is theirs then.
   __shared__ __align__(8) uint64_t q_full, q_free, slot_full[kSlots], slot_free[kSlots],
       s_full[kSBufs], s_free[kSBufs], p_full[kSlots], pv_done[kSlots], q_raw, o_full, o_free,
