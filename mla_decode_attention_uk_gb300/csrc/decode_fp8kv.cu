@@ -75,11 +75,11 @@
 // pipes are half busy over the launch.  Tried and no better, us on the first two cases
 // below: four warps in place of eight (52 and 165), sixteen (58, 172), four for every other
 // page each (52, 152), a half page at a time through buffers of
-// that size (58, 180), three slots and four buffers, L2 prefetch (51), loops unrolled
-// (57, 166), P^T's terms as rows of their own, which reads a page for PV once instead of
-// twice (51, 159).
+// that size (58, 180), L2 prefetch (51), loops unrolled (57, 166), P^T's terms as rows of
+// their own, which reads a page for PV once instead of twice (51, 159), softmax warps
+// without rows that skip theirs and parts of a page taken as warps come free (50, 156).
 // Measured: 64 sequences of 4,096 tokens x 16 heads 48 us; 61 ragged drafts of 4 queries x
-// 128 heads 143 us; 128 of 1,000-10,000 x 128 heads 158 us: slower than the 8-bit cache,
+// 128 heads 142 us; 128 of 1,000-10,000 x 128 heads 158 us: slower than the 8-bit cache,
 // for 0.58 times its bytes.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -239,12 +239,17 @@ __device__ __forceinline__ uint2 e4m3_sizes_any(uint32_t e) {
 }
 // A block's 16 E2M1 codes to E4M3 codes: byte selections by the sizes' bits, four at a
 // time, and the signs moved to their bytes (nine instructions for eight values; two
-// conversion instructions a pair, by way of fp16, are twelve).
-__device__ __forceinline__ uint4 e4m3_block(uint2 lut, uint32_t x, uint32_t y) {
+// conversion instructions a pair, by way of fp16, are twelve).  `sixteen`: a value that the
+// compiler does not know, so that the shift by four is a multiplication, away from the ALU
+// pipe that the rest waits for (61 drafts 144.4 -> 142.4 us, 64 x 4,096 48.8 -> 48.1; the
+// right shifts as high halves of products too: 151, 50.5).
+__device__ __forceinline__ uint4 e4m3_block(uint2 lut, uint32_t x, uint32_t y,
+                                            uint32_t sixteen) {
   auto four = [&](uint32_t sel, uint32_t signs) {
     return __byte_perm(lut.x, lut.y, sel) | (signs & 0x80808080u);
   };
-  const uint32_t sx = x & 0x77777777u, sy = y & 0x77777777u, lx = x << 4, ly = y << 4;
+  const uint32_t sx = x & 0x77777777u, sy = y & 0x77777777u, lx = x * sixteen,
+                 ly = y * sixteen;
   return make_uint4(four(sx, __byte_perm(lx, x, 0x5140)),
                     four(sx >> 16, __byte_perm(lx, x, 0x7362)),
                     four(sy, __byte_perm(ly, y, 0x5140)),
@@ -725,8 +730,9 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
               // (Their RoPE columns reach only the scores, which are masked.)
               if (i * kPage + row >= pc.len) exps = 0x88888888u;
               const bool usual = usual_exps(exps);
+              const uint32_t sixteen = P.kv4 ? 16u : 0u;
               // (Not unrolled, to stay small in the instruction cache: 57 us instead of 48
-              // on 64 x 4,096 tokens x 16 heads.)
+              // on 64 x 4,096 tokens x 16 heads, 50.5 unrolled by two; a block at a time 52.)
 #pragma unroll 1
               for (int j = 0; j < 4; ++j) {  // 32 columns, two blocks
                 const uint4 x = *reinterpret_cast<const uint4*>(src + 64 * box + 16 * j);
@@ -738,8 +744,8 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
                 exps >>= 8;
                 uint8_t* const to = dst + box * kBox;
                 const uint32_t chunk = (j << 5) ^ swizzle;
-                *reinterpret_cast<uint4*>(to + chunk) = e4m3_block(l0, x.x, x.y);
-                *reinterpret_cast<uint4*>(to + (chunk ^ 16u)) = e4m3_block(l1, x.z, x.w);
+                *reinterpret_cast<uint4*>(to + chunk) = e4m3_block(l0, x.x, x.y, sixteen);
+                *reinterpret_cast<uint4*>(to + (chunk ^ 16u)) = e4m3_block(l1, x.z, x.w, sixteen);
               }
               *reinterpret_cast<uint4*>(dst + kRopeBox8 * kBox + ((box << 4) ^ swizzle)) = rope;
               if (t == 0)
