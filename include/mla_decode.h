@@ -354,7 +354,8 @@ int mla_decode_attend_fp4kv(const mla_decode_dims* dims, const uint8_t* kv_fp4,
  * [0, max_position): DEVICE_BOUNDS, and nothing of the token is written; a block_table
  * entry outside the pool: DEVICE_BOUNDS, and the page's tokens reach q_out and rows
  * only; lengths as for the append.  Anything else (q without q_out, outputs without
- * their input, ...): INVALID_ARG.  Uses batch, num_heads, num_pages and
+ * their input, in place with gaps on one side, batch * max_new * (H / 4 + 1) beyond
+ * 2^30, ...): INVALID_ARG.  Uses batch, num_heads, num_pages and
  * max_pages_per_seq of dims.  One kernel. */
 typedef struct {
   const void* q;
