@@ -49,7 +49,8 @@
  *   stream has finished, and wait for it before they touch what it may use.  Only
  *   the weights, and q in the absorb step, are read at once: a kernel of the
  *   caller's that writes them and stands directly before the call must not itself
- *   let its dependents launch early (ordinary kernels do not).
+ *   let its dependents launch early (ordinary kernels do not, nor does
+ *   mla_decode_norm_rope where it writes queries).
  * - Thread safety: concurrent calls are safe when each uses its own
  *   workspace.  A plan written into a workspace stays valid for every run with
  *   the same dims and seq_lens contents (one plan serves all layers of a

@@ -58,6 +58,13 @@ constexpr int kListFrom = 16384;  // tokens
 constexpr int kHeadsPerWarp = 4;
 constexpr int kHalf = kRope / 2;
 
+// The absorb step reads q without a wait, as what stands in front of it has finished when
+// it starts, unless that let it start early: so only a call without queries does.
+__device__ __forceinline__ void wait_and_let_go(const PrepParams& P) {
+  griddep_wait();
+  if (!P.q) griddep_launch_dependents();
+}
+
 __device__ __forceinline__ void unpack8(const uint4& x, float (&v)[8]) {
   v[0] = bf16_lo(x.x); v[1] = bf16_hi(x.x); v[2] = bf16_lo(x.y); v[3] = bf16_hi(x.y);
   v[4] = bf16_lo(x.z); v[5] = bf16_hi(x.z); v[6] = bf16_lo(x.w); v[7] = bf16_hi(x.w);
@@ -190,8 +197,7 @@ template <bool kInterleaved>
 __global__ void __launch_bounds__(kPrepThreads, kPrepCtas)
 prep_list_kernel(const __grid_constant__ PrepParams P) {
   __shared__ UnitList list;
-  griddep_wait();
-  griddep_launch_dependents();
+  wait_and_let_go(P);
   const int q_tasks = P.q ? P.H / kHeadsPerWarp : 0;
   const int per_token = q_tasks + (P.kv ? 1 : 0);
   const long long tasks =
@@ -237,8 +243,7 @@ prep_list_kernel(const __grid_constant__ PrepParams P) {
 template <bool kInterleaved>
 __global__ void __launch_bounds__(kPrepThreads, kPrepCtas)
 prep_kernel(const __grid_constant__ PrepParams P) {
-  griddep_wait();
-  griddep_launch_dependents();
+  wait_and_let_go(P);
   const int q_tasks = P.q ? P.H / kHeadsPerWarp : 0;
   const int per_token = q_tasks + (P.kv ? 1 : 0);
   const int tasks = P.B * P.max_new * per_token;

@@ -456,6 +456,94 @@ def test_a_decode_step_eager_captured_and_on_another_stream(B, T, H):
 
 
 @gpu
+@pytest.mark.parametrize("B,T,H", [(2, 1, 16), (3, 2, 128), (128, 1, 128), (300, 4, 64),
+                                   (512, 8, 128)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_queries_are_rotated_before_the_absorb_step_reads_them(B, T, H, in_place):
+    # The absorb step reads q without waiting for the kernel in front of it.  Layers of
+    # their own queries go through one q_out, nothing between its writer and the step.
+    layers, lens = 4, [T + (29 * i) % 150 for i in range(B)]
+    d, x = chain_inputs(B, T, H, lens, 83)
+    cache = torch.zeros(d.num_pages, 64, 576, dtype=BF, device="cuda")
+    prompt = torch.tensor(lens, dtype=torch.int32).cuda()
+    binding.norm_rope(d, prompt, x["cos_sin"], kv=x["prompt"], cache=cache,
+                      block_table=x["table"], new_lens=prompt)
+    queries = [x["q"].roll(7 * i, -1) for i in range(layers)]
+    latents = [x["kv"].roll(7 * i, -1) for i in range(layers)]
+    q_buf = torch.empty_like(x["q"])
+    m = binding.MlaDecode(d)
+    outs = [[(torch.empty(B, T, H, 128, dtype=BF, device="cuda"),
+              torch.empty(B, T, H, device="cuda"),
+              torch.empty(B * T * H, 576, dtype=BF, device="cuda")) for _ in range(layers)]
+            for _ in range(3)]
+
+    def steps(results, between=lambda: None):
+        m.plan(x["lens"])
+        between()
+        for q, kv, (out, lse, lat) in zip(queries, latents, results):
+            # In place: on a buffer that the queries were copied to just before.
+            src = q_buf.copy_(q) if in_place else q
+            binding.norm_rope(d, x["lens"], x["cos_sin"], q=src, q_out=q_buf, kv=kv,
+                              kv_weight=x["kvw"], cache=cache, block_table=x["table"])
+            between()
+            m.run(q_buf, cache, x["table"], x["lens"], x["w_uk"], x["w_uv"], 192 ** -0.5, out, lse)
+            between()
+            src = q_buf.copy_(-q) if in_place else -q
+            binding.norm_rope(d, x["lens"], x["cos_sin"], q=src, q_out=q_buf)
+            between()
+            m.absorb(q_buf, x["w_uk"])
+            between()
+            lat.copy_(m.q_lat())
+
+    steps(outs[0], torch.cuda.synchronize)
+    assert m.check() == 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        steps(outs[2])
+    for _ in range(3):
+        for results in outs[1:]:
+            for t in (t for r in results for t in r):
+                t.fill_(7)
+        steps(outs[1])
+        graph.replay()
+        assert m.check() == 0
+        for results in outs[1:]:
+            for got, want in zip(results, outs[0]):
+                assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@gpu
+@pytest.mark.parametrize("H", [16, 128])
+def test_queries_of_prompts_are_rotated_before_the_absorb_step_reads_them(H):
+    # Enough tokens for a list of them; the absorb step takes them eight at a time.
+    B, n, layers = 4, 4096, 3
+    d = good_dims(batch=B, num_heads=H, num_pages=1, max_pages_per_seq=64)
+    m = binding.MlaDecode(good_dims(batch=B * n // 8, q_len=8, num_heads=H))
+    g = torch.Generator(device="cuda").manual_seed(84)
+    queries = [torch.randn(B, n, H, 192, generator=g, device="cuda").to(BF) for _ in range(layers)]
+    w_uk = (torch.randn(H, 128, 512, generator=g, device="cuda") / 11).to(BF)
+    q_buf, cs = torch.empty_like(queries[0]), cos_sin_table(n).cuda()
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+
+    def steps(between=lambda: None):
+        got = []
+        for q in queries:
+            binding.norm_rope(d, lens, cs, q=q, q_out=q_buf, new_lens=lens)
+            between()
+            m.absorb(q_buf.view(-1, 8, H, 192), w_uk)
+            between()
+            got.append(m.q_lat().clone())
+            between()
+        return got
+
+    m.plan(torch.full((B * n // 8,), 8, dtype=torch.int32, device="cuda"))
+    want = steps(torch.cuda.synchronize)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(steps(), want))
+    assert m.check() == 0
+
+
+@gpu
 def test_block_sparse_decode_over_the_4_bit_cache():
     # Keys, scores, selection and attention over what an append wrote; with as many
     # pages as there are the sparse step is the dense one.
