@@ -541,11 +541,11 @@ struct KeyParams {
 };
 
 // The mean of a page's filled rows.  Thread t sums columns 8 (t mod 72) .. + 7 over rows
-// t / 72, + 4, ...  Four rows in flight from a bf16 cache: 13 prompts of 512 to 8190
-// tokens, in a grid of all their pages, 10.6 us (eight 11.2, sixteen 14.9: registers and
-// the ragged pages' remainders); 9.8 by a list of the pages, 8 bits 6.6, 4 bits 8.6 (its
-// codes' conversion: two thirds of that on the ALUs).  The last pages of 128 sequences
-// 3.2 us from 8 bits.
+// t / 72, + 4, ...  Caches that are not in L2, 13 prompts of 512 to 8190 tokens (63k): 13.9 us
+// from bf16, 8.3 from 8 bits, 16.9 from 4 (its codes' conversion: two thirds of it on the
+// ALUs); four rows in flight from the first two (bf16 with eight or sixteen: slower, for
+// registers and the ragged pages' remainders).  The last pages of 128 sequences 2.8 us from
+// 8 bits.
 template <Kind kKind, int kSide>
 __device__ __forceinline__ void page_mean(const KeyParams& P, int b, int len, int logical,
                                           float (&part)[kSide][kDqk]) {
@@ -556,10 +556,10 @@ __device__ __forceinline__ void page_mean(const KeyParams& P, int b, int len, in
     if (threadIdx.x == 0) record_status(status, MLA_STATUS_BOUNDS);
     return;
   }
-  // (Looked at behind the rows' loads: a trip to memory next to theirs, not before.)
-  const float given = kKind != Kind::kBf16 ? kv_scale[page] : 1.0f;
-  const bool in_range = scale_in_range(given);
-  const float scale = in_range ? given : 1.0f;
+  // (Looked at behind the rows' loads: a trip to memory next to theirs, not before.  From
+  // 8 bits it is loaded there, and all by way of the read-only path: 2.81 us on the last
+  // pages of 128 sequences, 2.94 else.)
+  float given = kKind == Kind::kFp4 ? kv_scale[page] : 1.0f;
   const int filled = min(len - logical * kPage, kPage);
   const int c = threadIdx.x % kChunks, r0 = threadIdx.x / kChunks;
   float s[8] = {};
@@ -588,11 +588,11 @@ __device__ __forceinline__ void page_mean(const KeyParams& P, int b, int len, in
     for (int r = r0; r < filled; r += 4) {
       float x[8];
       if constexpr (kKind == Kind::kFp8) {
-        values8x8(*reinterpret_cast<const uint2*>(
-                      cache + static_cast<size_t>(page) * kPageBytes8 + r * kDqk + c * 8), x);
+        values8x8(__ldg(reinterpret_cast<const uint2*>(
+                      cache + static_cast<size_t>(page) * kPageBytes8 + r * kDqk + c * 8)), x);
       } else {
-        const uint4 v = *reinterpret_cast<const uint4*>(
-            cache + (static_cast<size_t>(page) * kPage + r) * (kDqk * 2) + c * 16);
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(
+            cache + (static_cast<size_t>(page) * kPage + r) * (kDqk * 2) + c * 16));
         x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
         x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z); x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
       }
@@ -602,7 +602,9 @@ __device__ __forceinline__ void page_mean(const KeyParams& P, int b, int len, in
 #pragma unroll
   for (int k = 0; k < 8; ++k) part[r0][c * 8 + k] = s[k];
   __syncthreads();
-  const float mul = scale / static_cast<float>(filled);
+  if constexpr (kKind == Kind::kFp8) given = __ldg(kv_scale + page);
+  const bool in_range = scale_in_range(given);
+  const float mul = (in_range ? given : 1.0f) / static_cast<float>(filled);
   const int k = threadIdx.x * 2;
   if (k < kDqk) {
     float x = (part[0][k] + part[1][k]) + (part[2][k] + part[3][k]);
@@ -617,7 +619,7 @@ __device__ __forceinline__ void page_mean(const KeyParams& P, int b, int len, in
   if (!in_range && threadIdx.x == 0) record_status(status, MLA_STATUS_BOUNDS);
 }
 
-// One CTA per (sequence, page that it can touch), or a list of the pages.
+// One CTA per (sequence, page that it can touch), or a list of the pages (launch_keys).
 template <Kind kKind, bool kList>
 __global__ void __launch_bounds__(key_threads(kKind, kList), key_ctas(kKind, kList))
 page_keys_kernel(const __grid_constant__ KeyParams P) {
@@ -676,9 +678,15 @@ cudaError_t launch_append(const void* rows, int max_new, const int32_t* new_lens
 template <Kind kKind>
 static cudaError_t launch_keys(const KeyParams& P, int sm_count, cudaStream_t st) {
   const int touched = touched_pages(P.max_new, P.max_pages);
-  if (use_list(static_cast<int64_t>(touched) * P.B, 6 * sm_count, P.B, P.new_lens))
-    return launch_pdl(page_keys_kernel<kKind, true>, dim3(sm_count * key_ctas(kKind, true)),
-                      dim3(key_threads(kKind, true)), 0, st, P);
+  // Caches that are not in L2, us with a list and without: from 4 bits 100 prompts of 100 to
+  // 2000 tokens 23.9 and 30.3, the 13 of 512 to 8190 16.9 and 17.4, 8 of 8000 (nothing to
+  // skip) 16.9 and 16.2.  The others have more to load than to convert and want the padded
+  // grid's CTAs: from 8 bits 17.3 and 13.9, 12.3 and 8.4, 12.4 and 8.6; from bf16 23.7 and
+  // 23.5, 14.6 and 13.9, 15.3 and 14.7.
+  if constexpr (kKind == Kind::kFp4)
+    if (use_list(static_cast<int64_t>(touched) * P.B, 6 * sm_count, P.B, P.new_lens))
+      return launch_pdl(page_keys_kernel<kKind, true>, dim3(sm_count * key_ctas(kKind, true)),
+                        dim3(key_threads(kKind, true)), 0, st, P);
   return launch_pdl(page_keys_kernel<kKind, false>, dim3(touched, P.B),
                     dim3(key_threads(kKind, false)), 0, st, P);
 }

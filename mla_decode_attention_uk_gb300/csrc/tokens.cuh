@@ -32,10 +32,9 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // The units (pages, tokens) of up to kListed sequences, one sequence's after the other's,
 // as every CTA of a grid works them out for itself (at least kListed threads; `count`: a
 // sequence's units).  Prompts of different lengths leave most of a padded grid empty; the
-// list takes 1 us to make.  us with a list and without: page keys (four rows side by side)
-// of 13 prompts of 512 to 8190 tokens 9.0 and 11.4, of 8 of 4096 9.0 and 7.9; norms and
-// rotation (16 heads) of the 13 prompts 92 and 107, of 30 of 100 to 1000 32.0 and 35.8, of
-// 8 of 4096 80.7 and 76.3, of 65 tokens of each 4.3 and 3.0.
+// list takes 1 us to make.  us with a list and without: norms and rotation (16 heads) of 13
+// prompts of 512 to 8190 tokens 92 and 107, of 30 of 100 to 1000 32.0 and 35.8, of 8 of 4096
+// 80.7 and 76.3, of 65 tokens of each 4.3 and 3.0; page keys: see launch_keys.
 constexpr int kListed = 256;
 struct UnitList {
   long long warp_sum[kListed / 32];
