@@ -298,7 +298,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
   constexpr uint32_t kSlotWriters = kFp4 ? 8 : 1;
 
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&q_full), 12);
+    mbar_init(smem_u32(&q_full), kFp4 ? 16 : 12);
     mbar_init(smem_u32(&q_free), 1 + 8);  // QK^T, and the softmax warps (the rows' scales)
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(smem_u32(&slot_full[i]), kSlotWriters);
@@ -570,7 +570,9 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
         if (kFp4 && !softmax) {
           // Warp 12 loads the piece's query tile: a thread that fills slots sees every
           // phase of theirs, or a wait for a phase may meet the one before the last.
-          // (So all of these warps wait here.)
+          // So all of these warps wait here, and the tile's slots do not move on to their
+          // next phase (behind q_full, below) before each has: 12-15 arrive there with the
+          // terms, 16-19 at once.
           bool ok = true;
           for (int r = g + 2 * n; r < g + 2 * n + 2 && ok; ++r)
             ok = r < kSlots || mbar_wait(smem_u32(&slot_free[r % kSlots]), (r / kSlots - 1) & 1,
@@ -580,6 +582,7 @@ decode_fp8kv_kernel(const __grid_constant__ CUtensorMap tm_lat,
             load_query(pc, g + 2 * n);
             ++tiles;
           }
+          if (warp >= 16 && lane == 0) mbar_arrive(smem_u32(&q_full));
         }
         if ((n == 0 || !softmax) && warp < 16) {
           // Where columns 64 block + 8 j + 4 half .. + 3 of a row are: four bf16

@@ -471,6 +471,29 @@ def test_attention_equals_the_8_bit_cache_of_the_same_values(H, T, ranges):
 
 
 @gpu
+@pytest.mark.parametrize("H,T,ranges", [(16, 1, 1), (16, 1, 0), (32, 1, 2), (128, 1, 1),
+                                        (80, 2, 5), (128, 8, 1)])
+def test_attention_pieces_that_end_as_the_next_query_is_due(H, T, ranges):
+    # Hundreds of pieces of one page (and a few more) to a CTA: each time the warps that
+    # expand pages have done their last one, the slots of the next query's tile become free.
+    lens = [max(T, 64 * (1 + (i % 11 == 3) * (i % 4)) - 5 * i % 63) for i in range(300)]
+    inp, kv4, kvs = fp4_inputs(make_inputs(len(lens), lens, T, H, seed=49))
+    out, lse = run_fp4(inp, kv4, kvs, num_ranges=ranges)
+    out8, lse8 = run_fp8(inp, ref.expand(kv4), kvs, num_ranges=ranges)
+    assert torch.equal(out, out8) and torch.equal(lse, lse8)
+    g = inp.to(torch.device("cuda"))
+    k, s = kv4.cuda(), kvs.cuda()
+    m = binding.MlaDecode(binding.dims_for(g.q, g.cache, g.block_table), num_ranges=ranges,
+                          fp8_kv=True)
+    m.plan(g.seq_lens)
+    for _ in range(50):
+        got, got_lse = torch.zeros_like(g.q[..., :128]), torch.zeros(lse.shape, device="cuda")
+        m.run_fp4kv(g.q, k, s, g.block_table, g.seq_lens, g.w_uk, g.w_uv, g.scale, got, got_lse)
+        assert m.check() == 0
+        assert torch.equal(got.cpu(), out) and torch.equal(got_lse.cpu(), lse)
+
+
+@gpu
 def test_attention_repeated_runs_give_the_same_bits_while_memory_is_busy():
     inp, kv4, kvs = fp4_inputs(make_inputs(64, [4096 - 7 * i for i in range(64)], 1, 16, seed=44))
     g = inp.to(torch.device("cuda"))
