@@ -41,16 +41,6 @@ __device__ __forceinline__ uint2 codes8(const uint4& v, __nv_bfloat162 inv) {
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
-// x * y rounded to odd: the nearest fp32 value with the last bit set where the
-// product is between two, so that rounding it on to a code rounds the product
-// itself (a product next to a tie of E4M3 would be rounded to the tie first).
-__device__ __forceinline__ float mul_odd(float x, float y) {
-  const float p = x * y, rest = fmaf(x, y, -p);
-  const int u = __float_as_int(p);
-  const bool even = rest != 0.0f && !(u & 1);
-  return __int_as_float(even ? ((rest > 0.0f) == (p > 0.0f) ? u + 1 : u - 1) : u);
-}
-
 // The block of 16 latent values that a thread's eight are half of: lanes l and l ^ 1
 // hold its halves.  Its exponent field under the page's scale 2^se (se = 0: values in
 // units of it), and the codes of this thread's eight.

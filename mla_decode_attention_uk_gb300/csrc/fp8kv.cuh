@@ -60,6 +60,16 @@ __device__ __forceinline__ float next_power_of_two(float s) {
   return __uint_as_float((__float_as_uint(s) + 0x7fffffu) & 0x7f800000u);
 }
 
+// x * y rounded to odd: the nearest fp32 value with the last bit set where the
+// product is between two, so that rounding it on to a code or to bf16 rounds the
+// product itself (a product next to a tie of theirs would be rounded to the tie first).
+__device__ __forceinline__ float mul_odd(float x, float y) {
+  const float p = x * y, rest = fmaf(x, y, -p);
+  const int u = __float_as_int(p);
+  const bool even = rest != 0.0f && !(u & 1);
+  return __int_as_float(even ? ((rest > 0.0f) == (p > 0.0f) ? u + 1 : u - 1) : u);
+}
+
 // Four values to four E4M3 codes, round to nearest even, finite values beyond
 // 448 (infinities too) saturated; NaN keeps NaN's code.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {

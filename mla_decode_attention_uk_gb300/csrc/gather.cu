@@ -2,6 +2,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "fp4kv.cuh"
 #include "fp8kv.cuh"
@@ -46,52 +48,66 @@ __device__ __forceinline__ void copy_page(const GatherParams& P, int b, int firs
   const int r0 = max(first - logical * kPage, 0), r1 = min(len - logical * kPage, kPage);
   uint4* const dst = rows + (static_cast<ptrdiff_t>(b) * max_new + logical * kPage - first) *
                                 kChunks + c;
-  auto put = [&](int r, const float (&v)[8]) {
+  // Values are rounded once: products by a power of two, as every scale of the appends is,
+  // are exact; others may need 28 bits.
+  auto put = [&](int r, const float (&v)[8], const auto exact) {
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = exact ? v[k] * scale : mul_odd(v[k], scale);
     dst[static_cast<ptrdiff_t>(r) * kChunks] =
-        make_uint4(pack_bf16x2(v[0] * scale, v[1] * scale), pack_bf16x2(v[2] * scale, v[3] * scale),
-                   pack_bf16x2(v[4] * scale, v[5] * scale),
-                   pack_bf16x2(v[6] * scale, v[7] * scale));
+        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                   pack_bf16x2(x[6], x[7]));
   };
   // kDeep rows' loads in flight.
-  constexpr int kStep = kGatherThreads / kChunks, kDeep = 8;
-  for (int r = r0 + threadIdx.x / kChunks; r < r1; r += kStep * kDeep) {
-    if constexpr (kKind == Kind::kBf16) {
-      uint4 x[kDeep];
+  auto copy = [&](const auto deep, const auto exact) {
+    constexpr int kStep = kGatherThreads / kChunks, kDeep = deep;
+#pragma unroll 1
+    for (int r = r0 + threadIdx.x / kChunks; r < r1; r += kStep * kDeep) {
+      if constexpr (kKind == Kind::kBf16) {
+        uint4 x[kDeep];
 #pragma unroll
-      for (int k = 0; k < kDeep; ++k)
-        x[k] = *reinterpret_cast<const uint4*>(
-            cache + (static_cast<size_t>(page) * kPage + min(r + kStep * k, r1 - 1)) * (kDqk * 2) +
-            c * 16);
+        for (int k = 0; k < kDeep; ++k)
+          x[k] = *reinterpret_cast<const uint4*>(
+              cache + c * 16 +
+              (static_cast<size_t>(page) * kPage + min(r + kStep * k, r1 - 1)) * (kDqk * 2));
 #pragma unroll
-      for (int k = 0; k < kDeep; ++k)
-        if (r + kStep * k < r1) dst[static_cast<ptrdiff_t>(r + kStep * k) * kChunks] = x[k];
-    } else if constexpr (kKind == Kind::kFp8) {
-      uint2 x[kDeep];
+        for (int k = 0; k < kDeep; ++k)
+          if (r + kStep * k < r1) dst[static_cast<ptrdiff_t>(r + kStep * k) * kChunks] = x[k];
+      } else if constexpr (kKind == Kind::kFp8) {
+        uint2 x[kDeep];
 #pragma unroll
-      for (int k = 0; k < kDeep; ++k)
-        x[k] = *reinterpret_cast<const uint2*>(cache + static_cast<size_t>(page) * kPageBytes8 +
-                                               min(r + kStep * k, r1 - 1) * kDqk + c * 8);
+        for (int k = 0; k < kDeep; ++k)
+          x[k] = *reinterpret_cast<const uint2*>(cache + static_cast<size_t>(page) * kPageBytes8 +
+                                                 min(r + kStep * k, r1 - 1) * kDqk + c * 8);
 #pragma unroll
-      for (int k = 0; k < kDeep; ++k) {
-        float v[8];
-        values8x8(x[k], v);
-        if (r + kStep * k < r1) put(r + kStep * k, v);
-      }
-    } else {
-      Raw4 x[kDeep];
+        for (int k = 0; k < kDeep; ++k) {
+          float v[8];
+          values8x8(x[k], v);
+          if (r + kStep * k < r1) put(r + kStep * k, v, exact);
+        }
+      } else {
+        Raw4 x[kDeep];
 #pragma unroll
-      for (int k = 0; k < kDeep; ++k)
-        x[k] = load_raw4(cache + static_cast<size_t>(page) * kPageBytes4 +
-                             min(r + kStep * k, r1 - 1) * kRow4,
-                         c);
+        for (int k = 0; k < kDeep; ++k)
+          x[k] = load_raw4(cache + static_cast<size_t>(page) * kPageBytes4 +
+                               min(r + kStep * k, r1 - 1) * kRow4,
+                           c);
 #pragma unroll
-      for (int k = 0; k < kDeep; ++k) {
-        float v[8];
-        values4(x[k], c, v);
-        if (r + kStep * k < r1) put(r + kStep * k, v);
+        for (int k = 0; k < kDeep; ++k) {
+          float v[8];
+          values4(x[k], c, v);
+          if (r + kStep * k < r1) put(r + kStep * k, v, exact);
+        }
       }
     }
-  }
+  };
+  using std::integral_constant;
+  copy(integral_constant<int, 8>{}, std::true_type{});
+  // (Rare pages: a second time.  A branch in the loop above cost all pages 4 to 7 %, one in
+  // front of it would wait for the scale.)
+  if constexpr (kKind != Kind::kBf16)
+    if ((__float_as_uint(scale) & 0x7fffffu) != 0)
+      copy(integral_constant<int, 2>{}, std::false_type{});
   if (!in_range && threadIdx.x == 0) record_status(status, MLA_STATUS_BOUNDS);
 }
 

@@ -334,6 +334,49 @@ def test_gather_equals_the_cache(kind, lens, new, max_new):
     assert torch.equal(rows.nan_to_num(0.0), want.nan_to_num(0.0))
 
 
+def bf16_once(x):
+    """fp64 values (normal numbers of bf16, or zero) to bf16, ties to even, in one step
+    (torch goes by way of fp32)."""
+    step = torch.exp2(torch.floor(torch.log2(x.abs().clamp(min=2.0 ** -120))) - 7)
+    return (torch.round(x / step) * step).to(BF)
+
+
+def scales_next_to_ties(mantissa, count):
+    """Scales in [1, 2) whose product with mantissa / 8 fp32 rounds onto a tie of bf16 and,
+    rounded on from there, to another value than its own nearest."""
+    s = torch.arange(2 ** 23, 2 ** 24)
+    p = s * mantissa
+    s = s[(p.float().long() != p) & (p.float().view(torch.int32) % 2 ** 16 == 2 ** 15)].double()
+    s = s * 2.0 ** -23
+    x = s * (mantissa / 8)
+    s = s[x.float().to(BF) != bf16_once(x)]
+    assert len(s) >= count
+    return s[:count].float()
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["fp8", "fp4"])
+def test_gather_rounds_once(kind):
+    # Codes of every mantissa under scales for which one of their products is next to a tie.
+    s = torch.cat([scales_next_to_ties(m, 8) for m in (range(9, 16) if kind == "fp8" else [12])])
+    s = torch.cat([s, s * 2.0 ** -9, s * 2.0 ** 14])
+    pages, g = len(s), torch.Generator().manual_seed(69)
+    kv = torch.randint(0, 256, (pages, 64, 576 if kind == "fp8" else 336), generator=g,
+                       dtype=torch.uint8)
+    if kind == "fp4":
+        kv[..., 256:272] &= 0x77  # no NaN blocks
+        kv[..., 272:] &= 0xF7
+    kv[(kv == 0x7F) | (kv == 0xFF)] = 0x3F
+    values = ref8.values(kv) if kind == "fp8" else ref.decode(kv)
+    exact = values * s.double()[:, None, None]
+    table, lens = torch.arange(pages, dtype=torch.int32)[None], [64 * pages]
+    rows, st = run_gather(kind, [kv, s], table, lens, None, lens[0])
+    assert st == 0
+    want = bf16_once(exact).reshape(1, -1, 576)
+    assert bool((exact.float().to(BF).reshape(1, -1, 576) != want).any())
+    assert torch.equal(rows, want)
+
+
 @gpu
 @pytest.mark.parametrize("kind", ["bf16", "fp8", "fp4"])
 def test_gather_reports_bad_lines_and_leaves_their_rows(kind):
