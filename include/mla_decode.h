@@ -350,14 +350,16 @@ int mla_decode_attend_fp4kv(const mla_decode_dims* dims, const uint8_t* kv_fp4,
  *               rows and kv_cache must be given with kv, or both; block_table with
  *               kv_cache
  * (A row whose sum of squares passes fp32's range becomes zeros.)  No two tokens of a
- * call may have one place in the cache.  Rows behind a sequence's n_b tokens are neither
- * read nor written.  A position outside
- * [0, max_position): DEVICE_BOUNDS, and nothing of the token is written; a block_table
- * entry outside the pool: DEVICE_BOUNDS, and the page's tokens reach q_out and rows
- * only; lengths as for the append.  Anything else (q without q_out, outputs without
- * their input, in place with gaps on one side, batch * max_new * (H / 4 + 1) beyond
- * 2^30, ...): INVALID_ARG.  Uses batch, num_heads, num_pages and
- * max_pages_per_seq of dims.  One kernel. */
+ * call may have one place in the cache; the pages that are written hold nothing else that
+ * the call reads, and their rows past a sequence's length stay as they were (mla_decode_run
+ * wants them finite).  Rows behind a sequence's n_b tokens are neither read nor written.
+ * A position outside [0, max_position): DEVICE_BOUNDS, and nothing of the token is
+ * written; a block_table entry outside the pool: DEVICE_BOUNDS, and the page's tokens
+ * reach q_out and rows only; lengths as for the append.  Anything else (q without q_out,
+ * outputs without their input, q_out or rows that overlap each other, q or kv in another
+ * way than in place, with the rows behind n_b counted, batch * max_new * (H / 4 + 1)
+ * beyond 2^30, ...): INVALID_ARG.  Uses batch, num_heads, num_pages and max_pages_per_seq
+ * of dims.  One kernel. */
 typedef struct {
   const void* q;
   int64_t q_stride;

@@ -546,8 +546,8 @@ def norm_rope(d: Dims, seq_lens, cos_sin, q=None, q_out=None, q_weight=None, kv=
     latent, none without them.  cos_sin: fp32 [positions, 64], 32 cosines and 32 sines
     a line.  interleaved: columns 2 i and 2 i + 1 are a pair, else i and i + 32.  q and
     kv may have gaps between tokens (columns of a wider projection); q_out may be q,
-    and rows kv, where they have none.  positions: int32 [B, max_new], by default a
-    token's place in the cache, seq_lens[b] - new_lens[b] + i."""
+    and rows kv, where they have none; they overlap in no other way.  positions: int32
+    [B, max_new], by default a token's place in the cache, seq_lens[b] - new_lens[b] + i."""
     bf, B, H = torch.bfloat16, d.batch, d.num_heads
     given = q if q is not None else kv
     max_new = given.shape[1] if given is not None and given.dim() >= 3 else 0

@@ -895,6 +895,26 @@ int mla_decode_gather_fp4kv(const mla_decode_dims* d, const uint8_t* kv_fp4,
                      new_lens, rows, status, stream);
 }
 
+// Rows of bf16 values: where the first is, from one to the next, and how long.
+struct Rows {
+  const void* at;
+  int64_t stride, length;
+};
+static bool same_rows(const Rows& x, const Rows& y) {
+  return x.at == y.at && x.stride == y.stride;
+}
+// Whether n rows without gaps meet any of n rows that may have gaps.
+static bool overlap(const Rows& packed, const Rows& gapped, int64_t n) {
+  if (!packed.at || !gapped.at) return false;
+  using Wide = __int128;  // (strides are the caller's)
+  const Wide b0 = reinterpret_cast<uintptr_t>(packed.at), b1 = b0 + Wide(2) * n * packed.length;
+  const Wide g0 = reinterpret_cast<uintptr_t>(gapped.at), step = Wide(2) * gapped.stride,
+             size = Wide(2) * gapped.length;
+  // The first of them that ends behind b0, and whether it is there and starts before b1.
+  const Wide i = g0 + size > b0 ? 0 : (b0 - g0 - size) / step + 1;
+  return i < n && g0 + i * step < b1;
+}
+
 int mla_decode_norm_rope(const mla_decode_dims* d, const mla_decode_norm_rope_args* a,
                          void* stream) {
   int rc = check_dims(d);
@@ -915,13 +935,17 @@ int mla_decode_norm_rope(const mla_decode_dims* d, const mla_decode_norm_rope_ar
                (a->kv_cache && (!a->block_table || !aligned4(a->block_table))))
             : (a->rows || a->kv_cache || a->kv_weight))
     return MLA_DECODE_INVALID_ARG;
-  // In place only where both sides have no gaps: a token would else be written over another
-  // that has not been read.
-  if ((a->q && a->q_out == a->q && a->q_stride != static_cast<int64_t>(d->num_heads) * kDq) ||
-      (a->kv && a->rows == a->kv && a->kv_stride != kDqk))
-    return MLA_DECODE_INVALID_ARG;
   // Warps count their tasks (four heads or a latent row) in 32 bits.
-  if (static_cast<int64_t>(d->batch) * a->max_new > INT32_MAX / 2 / (d->num_heads / 4 + 1))
+  const int64_t tokens = static_cast<int64_t>(d->batch) * a->max_new;
+  if (tokens > INT32_MAX / 2 / (d->num_heads / 4 + 1)) return MLA_DECODE_INVALID_ARG;
+  // In place a token is written where it was read (no gaps on either side); anywhere else
+  // over an input, another token would be overwritten that has not been read.
+  const int64_t q_row = static_cast<int64_t>(d->num_heads) * kDq;
+  const Rows q{a->q, a->q_stride, q_row}, kv{a->kv, a->kv_stride, kDqk};
+  const Rows q_out{a->q_out, q_row, q_row}, rows{a->rows, kDqk, kDqk};
+  if ((!same_rows(q_out, q) && overlap(q_out, q, tokens)) ||
+      (!same_rows(rows, kv) && overlap(rows, kv, tokens)) || overlap(q_out, kv, tokens) ||
+      overlap(rows, q, tokens) || overlap(q_out, rows, tokens))
     return MLA_DECODE_INVALID_ARG;
   int sms = 0;
   rc = sm_count(&sms);

@@ -2,6 +2,7 @@
 the whole chain over the 4-bit cache."""
 import ctypes
 import math
+import random
 
 import pytest
 import torch
@@ -54,6 +55,49 @@ def test_refuses_bad_arguments():
     assert call("mla_decode_norm_rope", [None, None]) == 1
     assert code(d=good_dims(qk_rope=32)) == 2
     assert binding.lib().mla_decode_norm_rope(None, ctypes.byref(Args(**good)), None) == 1
+
+
+def test_refuses_outputs_over_other_tokens_or_each_other():
+    # Against every token's bytes, with the four tensors at places near each other.  (Without
+    # a device a call whose arguments are right ends there, with 4.)
+    if torch.cuda.is_available():
+        pytest.skip("addresses that are not memory")
+    rng = random.Random(5)
+    H, row, lat = 16, 16 * 192, 576
+
+    def tokens(at, stride, length, n):
+        return [(at + 2 * stride * i, at + 2 * (stride * i + length)) for i in range(n)]
+
+    def meet(x, y):
+        return any(a < d and c < b for a, b in x for c, d in y)
+
+    refused = 0
+    for _ in range(4000):
+        B, T = rng.randint(1, 2), rng.randint(1, 3)
+        n = B * T
+        span = rng.choice((400, 4000, 40000))
+        place = lambda: 1 << 20 | 16 * rng.randint(0, span)  # noqa: E731
+        x = dict(q=place(), kv=place(), q_out=place(), rows=place(),
+                 q_stride=row + 8 * rng.choice((0, 0, 8, 144, 1000, 5000)),
+                 kv_stride=lat + 8 * rng.choice((0, 0, 8, 400, 5000)))
+        if rng.random() < 0.4:
+            x["q_out"] = x["q"]
+        if rng.random() < 0.4:
+            x["rows"] = x["kv"]
+        q, kv = tokens(x["q"], x["q_stride"], row, n), tokens(x["kv"], x["kv_stride"], lat, n)
+        q_out, rows = tokens(x["q_out"], row, row, n), tokens(x["rows"], lat, lat, n)
+        bad = (q_out != q and meet(q_out, q)) or (rows != kv and meet(rows, kv))
+        bad = bad or meet(q_out, kv) or meet(rows, q) or meet(q_out, rows)
+        # (One token is in place whatever the stride, but the strides have to say so.)
+        bad = bad or (x["q_out"] == x["q"] and x["q_stride"] != row)
+        bad = bad or (x["rows"] == x["kv"] and x["kv_stride"] != lat)
+        args = Args(q_weight=OK, kv_weight=OK, cos_sin=OK, seq_lens=OK, eps=EPS, max_position=9,
+                    interleaved=1, max_new=T, **x)
+        got = call("mla_decode_norm_rope", [ctypes.byref(args), None],
+                   d=good_dims(batch=B, num_heads=H))
+        assert got == (1 if bad else 4), x
+        refused += bad
+    assert 1000 < refused < 3800
 
 
 def test_python_call_checks_types_and_shapes():
@@ -267,6 +311,26 @@ def test_given_positions_and_in_place(interleaved):
     check(positions="random", interleaved=interleaved, seed=4)
     check(in_place=True, interleaved=interleaved, seed=5)
     check(in_place=True, q_norm=False, kv_norm=False, to="rows", interleaved=interleaved, seed=6)
+
+
+@gpu
+def test_outputs_over_a_wider_projection_are_refused_and_leave_it():
+    B, T, H = 2, 3, 16
+    g = torch.Generator().manual_seed(12)
+    wide = torch.randn(B, T, H * 192 + 576, generator=g).to(BF).cuda()
+    q, kv = wide[..., :H * 192].unflatten(-1, (H, 192)), wide[..., H * 192:]
+    flat, before = wide.view(-1), wide.clone()
+    q_out = flat[:B * T * H * 192].view(B, T, H, 192)
+    rows = flat[-B * T * 576:].view(B, T, 576)
+    d = good_dims(batch=B, num_heads=H)
+    lens, cs = torch.full((B,), T, dtype=torch.int32).cuda(), cos_sin_table(9).cuda()
+    over_q = flat[:B * T * 576].view(B, T, 576)
+    for change in (dict(q_out=q_out), dict(rows=rows), dict(rows=over_q)):
+        a = dict(dict(q=q, kv=kv, q_out=torch.empty_like(q_out), rows=torch.empty_like(rows)),
+                 **change)
+        with pytest.raises(binding.MlaDecodeError, match="INVALID_ARG"):
+            binding.norm_rope(d, lens, cs, **a)
+    assert torch.equal(wide, before)
 
 
 @gpu
