@@ -47,6 +47,18 @@ def test_the_reference_rounds_to_the_nearest_value():
     assert bool((err <= torch.exp2(j)[..., None]).all() | (top > 448).any())
 
 
+def test_quantising_what_was_quantised_keeps_its_values_and_settles():
+    # A block's exponent may fall the first time (its largest value was rounded down to where
+    # a smaller unit holds it), the values do not move, and the second time nothing does.
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(200, 576, generator=g, dtype=torch.float64)
+    x *= torch.exp2(torch.randint(-12, 8, (200, 576), generator=g).double())
+    once = ref.encode(x)
+    twice = ref.encode(ref.decode(once))
+    assert torch.equal(ref.decode(twice), ref.decode(once))
+    assert torch.equal(ref.encode(ref.decode(twice)), twice)
+
+
 # ---------------------------------------------------------------- refusals (no GPU)
 def test_append_refuses_bad_arguments():
     #       rows max_new new_lens table lens kv4 scale status stream
@@ -651,6 +663,35 @@ def test_a_cache_beyond_two_gigabytes():
     binding.gather_fp4kv(d, kv4, kvs, t.cuda(), cuda_ints([256]), rows[:, :64].contiguous())
     assert torch.equal(ref.decode(kv4[at[3]].cpu()) * float(kvs[at[3]]),
                        inp.cache[order[3]].double())
+
+
+@gpu
+def test_append_to_pages_beyond_two_gigabytes_equals_the_definition():
+    # Pages on both sides of byte offset 2^31 and 2^32 of the pool; 70 new tokens in the last
+    # two of them: six rows behind 58 that stay, and a page that starts afresh.
+    pages = (1 << 32) // (64 * 336) + 4
+    at = [0, (1 << 31) // (64 * 336), (1 << 32) // (64 * 336), pages - 1]
+    kv4, kvs = pool(4, 17)
+    rows = (torch.randn(1, 70, 576, generator=torch.Generator().manual_seed(18)) * 64).to(BF)
+    far, far_s = torch.zeros(pages, 64, 336, dtype=torch.uint8, device="cuda"), torch.ones(pages)
+    where = torch.tensor(at)
+    far[where], far_s[where] = kv4.cuda(), kvs
+    far_s = far_s.cuda()
+    d = good_dims(batch=1, num_pages=pages, max_pages_per_seq=4)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    table = torch.tensor([at], dtype=torch.int32).cuda()
+    binding.append_fp4kv(d, rows.cuda(), far, far_s, table, cuda_ints([256]), status=status)
+    near = torch.arange(4, dtype=torch.int32)[None]
+    rk, rs = ref.append(rows, [70], near, [256], kv4, kvs)
+    assert int(status.item()) == 0
+    assert torch.equal(far[where].cpu(), rk) and torch.equal(far_s[where].cpu(), rs)
+    # Nothing else was written, and what was is read back.
+    assert int(far.any(dim=2).any(dim=1).sum()) == 4
+    assert int((far_s != 1).sum()) == int((rs != 1).sum())
+    got = torch.full((1, 256, 576), 7.0, dtype=BF, device="cuda")
+    binding.gather_fp4kv(d, far, far_s, table, cuda_ints([256]), got)
+    want = (ref.decode(rk) * rs.double()[:, None, None]).to(BF)
+    assert torch.equal(got.cpu().view(4, 64, 576), want)
 
 
 @gpu
