@@ -64,11 +64,11 @@
 //
 // Over the 4-bit cache (fp4kv.cuh) a page stands for the same codes: it comes as it is,
 // 21 KB in one copy into one of two buffers, and eight warps more, 12-19, expand it into a
-// slot; everything behind is as above.  (E2M1 operands would not do: PV wants a page with
-// its keys along the other axis, which exists for 8-bit types only, and the block
-// exponents differ along it.)  Four slots and 20 warps, which share the registers out
-// anew.  Warp 12 loads the query's tile there, as the warps that fill slots see each phase
-// of their barriers.
+// slot; everything behind is as above.  (E2M1 operands would not do: PV sums over the keys,
+// and a block's exponent differs from key to key.)  Four slots and 20 warps, which share
+// the registers out anew (232 bytes a thread are spilled at the 96 of the launch).  Warp 12
+// loads the query's tile there, as the warps that fill slots see each phase of their
+// barriers.
 // What bounds that: the expansion, whose eight warps take 1,500 of the 2,000 cycles that a
 // page takes (980 with the SM to themselves) next to the softmax's 1,550 on the same
 // schedulers; byte selections issue at half the rate of logic instructions, and the ALU

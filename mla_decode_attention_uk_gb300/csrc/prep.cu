@@ -12,11 +12,12 @@
 // columns a lane (three loads of 16 bytes, the third of them RoPE columns: every
 // lane has work, and a head's norm is three shuffles), or a token's latent row.
 // Measured: 7 prompts of 512 to 8190 tokens x 16 heads 58 us, 5.3 TB/s of what has to move
-// (0.79 of a copy; without the next task's loads in flight 68; three CTAs an SM 57, five
-// or six, which spill registers, 92 and more; cosines and sines loaded ahead as well 59, in
-// two CTAs; two to five tasks ahead by asynchronous copies into shared memory 57 to 61: the
-// rest is not for want of loads in flight); one token of 128 sequences x 128 heads 3.7 us,
-// 3.4 TB/s; of two x 16 heads 2.1, a launch.
+// (0.79 of a copy; without the next task's loads in flight 68; four CTAs an SM, which spill 36
+// bytes a thread, 100 with pairs i and i + 32; three 57, five or six, which spill more, 92
+// and more; cosines and sines loaded ahead as well 59, in two CTAs; two to five tasks ahead
+// by asynchronous copies into shared memory 57 to 61: the rest is not for want of loads in
+// flight); one token of 128 sequences x 128 heads 3.7 us, 3.4 TB/s; of two x 16 heads 2.2, a
+// launch.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
