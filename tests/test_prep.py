@@ -577,6 +577,43 @@ def test_queries_are_rotated_before_the_absorb_step_reads_them(B, T, H, in_place
 
 
 @gpu
+@pytest.mark.parametrize("B,T,H", [(1, 1, 16), (8, 2, 32), (128, 1, 128), (200, 8, 64)])
+def test_norms_and_absorb_steps_in_turn_on_one_buffer(B, T, H):
+    # Nothing but the two kernels, each layer's absorb step into a workspace of its own: what
+    # the SMs hold of the buffer is the layer's before.
+    layers = 6
+    d = good_dims(batch=B, q_len=T, num_heads=H)
+    g = torch.Generator(device="cuda").manual_seed(85)
+    rand = lambda *n: torch.randn(*n, generator=g, device="cuda").to(BF)  # noqa: E731
+    queries, w_uk = [rand(B, T, H, 192) for _ in range(layers)], rand(H, 128, 512) / 11
+    lens, cs = torch.full((B,), T, dtype=torch.int32, device="cuda"), cos_sin_table(T).cuda()
+    q_buf, ms = torch.empty_like(queries[0]), [binding.MlaDecode(d) for _ in range(layers)]
+
+    def steps(between=lambda: None):
+        for m, q in zip(ms, queries):
+            binding.norm_rope(d, lens, cs, q=q, q_out=q_buf)
+            between()
+            m.absorb(q_buf, w_uk)
+            between()
+
+    for m in ms:
+        m.plan(lens)
+    torch.cuda.synchronize()
+    steps(torch.cuda.synchronize)
+    want = [m.q_lat().clone() for m in ms]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(10):
+            steps()
+    for k in range(40):
+        for m in ms:
+            m.q_lat().zero_()
+        graph.replay() if k % 2 else steps()
+        assert all(torch.equal(m.q_lat(), w) for m, w in zip(ms, want)), k
+        assert all(m.check() == 0 for m in ms)
+
+
+@gpu
 @pytest.mark.parametrize("H", [16, 128])
 def test_queries_of_prompts_are_rotated_before_the_absorb_step_reads_them(H):
     # Enough tokens for a list of them; the absorb step takes them eight at a time.
